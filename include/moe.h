@@ -398,6 +398,156 @@ moe_status moe_rope_quantize_per_head(const void* x, int32_t x_dtype, const int3
 /* Bytes of workspace moe_rope_quantize_per_head needs.  Host only. */
 moe_status moe_rope_workspace_size(int32_t T, int32_t n_heads, int32_t head_dim, size_t* bytes);
 
+/*
+ * The attention side of a decoder layer whose experts the calls above run:
+ * rotary positions, a paged key/value cache in E4M3 and attention over it
+ * ([post], "Triton JIT recompilation elimination", names the fusion of
+ * rotation and per-head FP8 codes; the calls below are what such codes are
+ * stored in and read by).  The conventions at the top of this file hold for
+ * them; their counts (tokens, sequences, pages) are only kernel arguments.
+ */
+
+/* Rotation of head vectors by position, with one or several axes (text: one;
+ * images and video: time, height, width).  Pair i of a token turns by
+ *   a(t, i) = positions[axis(i)][t] * inv_freq[i],   i < rotary_dim / 2,
+ * formed and reduced in 64 bits, negated when `inverse` (the rotation back,
+ * which is also the rotation's gradient).  The pairs are (x[i],
+ * x[i + rotary_dim/2]), or (x[2i], x[2i+1]) when `interleaved`; (u, v)
+ * becomes (u cos a - v sin a, v cos a + u sin a) in fp32.  Values from
+ * rotary_dim on pass through.
+ *   positions   device int32 [axes][T], |position| < 2^24.
+ *   pair_axis   device int32 [rotary_dim / 2], axis(i) in [0, axes) (a pair
+ *               with any other value is not turned); NULL: axis 0.
+ *   inv_freq    device f32 [rotary_dim / 2].
+ *   axes        1..8.   rotary_dim  a multiple of 16 in [16, head_dim]. */
+typedef struct {
+  const int32_t* positions;
+  const int32_t* pair_axis;
+  const float* inv_freq;
+  int32_t axes, rotary_dim, interleaved, inverse;
+} moe_rotation;
+
+/*
+ * out[t, h, :] = x[t, h, :] rotated.  x and out are [T, n_heads, head_dim]
+ * with strides of their own (elements from token to token and head to head;
+ * the head_dim values of a head are consecutive), so that a head range of a
+ * fused projection is rotated where it lies.  out may be x itself (same
+ * pointer, type and strides); otherwise the two must not overlap.
+ * x          device, x_dtype MOE_BF16 or MOE_F32; strides >= 0.
+ * out        device, out_dtype MOE_BF16 or MOE_F32 (rounded once); strides
+ *            >= head_dim.  (written)
+ * Every pointer 16-byte aligned (index buffers 4), strides in bytes
+ * multiples of 16.  Limits: 1 <= n_heads <= 256; head_dim a multiple of 16 in
+ * [16, 512].  T == 0 is a no-op.  Errors: MOE_ERR_SHAPE, MOE_ERR_DTYPE,
+ * MOE_ERR_NULL, MOE_ERR_ALIGN, MOE_ERR_UNSUPPORTED (out is x with another type or
+ * strides), MOE_ERR_HIP.
+ */
+moe_status moe_rope_axes(const void* x, int32_t x_dtype, int64_t x_stride_t, int64_t x_stride_h,
+                         const moe_rotation* rotation, int32_t T, int32_t n_heads, int32_t head_dim,
+                         void* out, int32_t out_dtype, int64_t out_stride_t, int64_t out_stride_h,
+                         void* stream);
+
+/* A paged key/value cache in E4M3 with one fp32 scale per page and KV head.
+ * Token t of a sequence lies in page block_table[sequence][t / page_size],
+ * slot i = t % page_size; it stands for code * scale.
+ *   k_codes   device uint8 [num_pages][n_kv_heads][page_size][head_dim].
+ *   v_codes   device uint8 [num_pages][n_kv_heads][page_size / 16][head_dim][16]:
+ *             blocks of 16 tokens, channel by channel (value d of slot i at
+ *             [i / 16][d][i % 16]), the order in which attention reads them.
+ *   k_scales, v_scales   device f32 [num_pages][n_kv_heads], positive.
+ * page_size 16, 32, 64 or 128; head_dim a multiple of 16 in [16, 256];
+ * n_kv_heads 1..256; codes 16-byte, scales 4-byte aligned.  Nothing needs
+ * initialising; slots no token was appended to are never used. */
+typedef struct {
+  uint8_t* k_codes;
+  uint8_t* v_codes;
+  float* k_scales;
+  float* v_scales;
+  int32_t num_pages, page_size, n_kv_heads, head_dim;
+} moe_kv_cache;
+
+/* A ragged batch of B sequences over such a cache, T query rows in all.
+ *   cu_q        device int32 [B + 1]: sequence b has rows [cu_q[b], cu_q[b+1])
+ *               of the packed batch, non-decreasing within [0, T]; rows from
+ *               cu_q[B] on belong to no sequence.  NULL: T == B and row b is
+ *               sequence b's one token.
+ *   kv_lens     device int32 [B]: the sequence's tokens in the cache, those of
+ *               its rows included: row cu_q[b] + i stands at token
+ *               kv_lens[b] - rows + i.
+ *   block_table device int32 [B][max_pages]; tokens whose page is outside
+ *               [0, num_pages), or past the table, are not kept by an append
+ *               and not seen by attention.
+ * B <= 65536, T <= 2^28, max_pages >= 1, max_pages * page_size <= 2^30. */
+typedef struct {
+  const int32_t* cu_q;
+  const int32_t* kv_lens;
+  const int32_t* block_table;
+  int32_t B, T, max_pages;
+} moe_kv_batch;
+
+/*
+ * Appends the keys and values of the batch's rows, the keys rotated first
+ * (rotation NULL: as they are; rotation->positions NULL with axes == 1: the
+ * token's own place in its sequence).  For each page and head that gets new
+ * tokens, with amax over these tokens' finite values (keys after rotation):
+ *   need  = the smallest power of two with 448 need >= amax, >= 2^-64;
+ *   scale = max(need, the page's scale) if earlier tokens of the sequence lie
+ *           in the page, else need;
+ *   codes of earlier tokens become E4M3(code * old scale / scale) where the
+ *   scale grew; new codes are E4M3(x / scale), round to nearest even,
+ *   saturating (a NaN saturates too).
+ * Appending the same rows again leaves the cache as it is, bit for bit;
+ * lowering kv_lens and appending anew replaces tokens.  A page that gets new
+ * tokens must belong to one sequence of the batch only.  Slots of no new or
+ * earlier token keep their bytes.
+ * k, v      device [T, n_kv_heads, head_dim] of dtype (MOE_BF16 or MOE_F32),
+ *           strides as in moe_rope_axes.
+ * Errors: MOE_ERR_SHAPE, MOE_ERR_DTYPE, MOE_ERR_NULL, MOE_ERR_ALIGN,
+ * MOE_ERR_HIP.  T == 0 or B == 0 is a no-op.
+ */
+moe_status moe_kv_append(const moe_kv_cache* cache, const moe_kv_batch* batch, const void* k,
+                         int64_t k_stride_t, int64_t k_stride_h, const void* v, int64_t v_stride_t,
+                         int64_t v_stride_h, int32_t dtype, const moe_rotation* rotation, void* stream);
+
+/*
+ * Attention of the batch's rows over the cache.  With G = n_heads /
+ * n_kv_heads query heads per KV head, row i of a sequence at token
+ * p = kv_len - rows + i sees the tokens t < kv_len with t <= p if `causal`
+ * and t > p - window if window > 0;
+ *   s_t = sm_scale * sum_d q[d] k_t[d],   out = sum_t softmax(s)_t v_t,
+ *   lse = log sum_t exp(s_t) (natural).
+ * A row that sees no token gives zeros and lse = -infinity.  bf16 queries:
+ * fp32 scores, sums and softmax, probabilities rounded to bf16 for the second
+ * product.  f32 queries: 24-bit products throughout.  Codes of tokens that no
+ * row sees, and their scales, may hold anything; a NaN code (0x7f, 0xff; an
+ * append makes none) in a token that some row sees makes every row of its
+ * sequence unspecified.
+ * q          device [T, n_heads, head_dim] of q_dtype (MOE_BF16 or MOE_F32),
+ *            strides as in moe_rope_axes (already rotated).
+ * max_q      >= the rows of every sequence (rows of a sequence with more are
+ *            not all written); 1 when cu_q is NULL.
+ * window     0 (none) .. 2^30.
+ * out        device [T, n_heads, head_dim] of q_dtype, dense (written; rows of
+ *            no sequence are left as they were).
+ * lse        device f32 [T, n_heads] or NULL (written likewise).
+ * workspace  device, >= moe_paged_attention_workspace_size() bytes, 16-byte
+ *            aligned; no initialisation, not preserved.
+ * Limits: n_heads a multiple of n_kv_heads, G <= 128.  The result is the same on every
+ * run.  Errors: MOE_ERR_SHAPE, MOE_ERR_DTYPE, MOE_ERR_NULL, MOE_ERR_ALIGN,
+ * MOE_ERR_WORKSPACE, MOE_ERR_HIP.  T == 0 or B == 0 is a no-op.
+ */
+moe_status moe_paged_attention(const moe_kv_cache* cache, const moe_kv_batch* batch, const void* q,
+                               int32_t q_dtype, int64_t q_stride_t, int64_t q_stride_h,
+                               int32_t n_heads, int32_t max_q, float sm_scale, int32_t causal,
+                               int32_t window, void* out, float* lse, void* workspace,
+                               size_t workspace_bytes, void* stream);
+
+/* Bytes of workspace moe_paged_attention needs for T rows in B sequences of
+ * at most max_q rows, over a cache of these sizes (its pointers are not
+ * looked at).  Host only. */
+moe_status moe_paged_attention_workspace_size(const moe_kv_cache* cache, int32_t T, int32_t B,
+                                              int32_t n_heads, int32_t max_q, size_t* bytes);
+
 #ifdef __cplusplus
 }
 #endif

@@ -1,0 +1,162 @@
+// attention.hpp -- what the paged-attention kernels share.
+//
+// Both compute, for a query row r (one head of one token) and the tokens t it
+// sees, with kc, vc the E4M3 codes and ks, vs their page's scales,
+//   s_t = sm_scale ks q.kc_t,  out = sum_t softmax(s)_t vs vc_t
+// in one pass over the tokens with a running maximum m and sum l (base 2:
+// exp2(s log2 e - m)).  Codes are exact in bf16, so both products run on bf16
+// MFMA with fp32 accumulation: q as it is, p = exp2(..) vs rounded to bf16
+// (its sum l is taken from the unrounded fp32 values).  fp32 queries are the
+// sum of three bf16 terms, and so is p: 24 bits, three MFMAs in place of one.
+//
+// Operand layout.  The first product is computed transposed, S^T = K Q^T:
+// MFMA tile j of four takes as its row m the token 16 (m / 4) + 4 j + m % 4
+// of a 64-token tile.  Of the result, lane l then holds tokens
+// 16 (l / 16) + 4 j + i (i = 0..3, j = 0..3) of query l % 16: sixteen
+// consecutive tokens, and as the B operand of O^T = V^T P^T they are exactly
+// the lane's contraction indices when A is a 16-byte load of value codes
+// (paged.hpp).  So probabilities never leave their lane, and neither operand
+// of either product needs a transposition.  The D values of a key are split
+// over the four lane groups in contiguous quarters.
+#pragma once
+
+#include "paged.hpp"
+
+namespace moe {
+
+constexpr float kLog2e = 1.44269504088896340736f;
+constexpr float kLn2 = 0.69314718055994530942f;
+constexpr int kAttnTile = 64;  // tokens of a tile
+constexpr int kAttnGroups = 512;  // workgroups of the few-row kernel: two per CU
+
+struct AttnArgs {
+  PagedArgs c;
+  BatchArgs b;
+  const void* q;
+  long long qs_t, qs_h;  // strides in elements
+  int nH, G;             // query heads, query heads per KV head
+  float scale2;          // sm_scale * log2(e)
+  int causal, window;
+  void* out;             // [T][nH][D]
+  float* lse;            // [T][nH] or NULL
+  float* part_o;         // partial results of sequences that several workgroups share
+  float* part_ml;
+  int W;                 // workgroups per KV head
+};
+
+// Tiles [t0, t0 + n) of tokens that some row of [row0, row0 + rows) of the
+// sequence sees (rows count query tokens here), and the tokens [lo, hi) they see.
+struct View {
+  int lo, hi, t0, n;
+};
+
+__device__ __forceinline__ View view_of(const AttnArgs& a, const Seq& s, int i0, int i1) {
+  View v;
+  const int p0 = s.kv - s.q + i0, p1 = s.kv - s.q + i1 - 1;  // tokens of the first and last query
+  int hi = a.causal && p1 + 1 < s.lim ? p1 + 1 : s.lim;
+  int lo = a.window > 0 && p0 - a.window + 1 > 0 ? p0 - a.window + 1 : 0;
+  if (hi < 0) hi = 0;
+  if (lo > hi) lo = hi;
+  v.lo = lo;
+  v.hi = hi;
+  v.t0 = lo / kAttnTile;
+  v.n = hi > lo ? (hi + kAttnTile - 1) / kAttnTile - v.t0 : 0;
+  return v;
+}
+
+// Two E4M3 codes (byte pair `hi` of w) as packed bf16: exact.
+template <bool HI>
+__device__ __forceinline__ uint32_t codes_bf16x2(int w) {
+  return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((unsigned)w, 1.0f, HI));
+}
+
+// Eight codes (two dwords) as a bf16 MFMA operand.
+__device__ __forceinline__ bf16x8 codes_op(int w0, int w1) {
+  const i32x4 r = {(int)codes_bf16x2<false>(w0), (int)codes_bf16x2<true>(w0), (int)codes_bf16x2<false>(w1),
+                   (int)codes_bf16x2<true>(w1)};
+  return as_bf16x8(r);
+}
+
+// x as NS bf16 terms whose sum is x to 8 NS bits: term k of the eight values.
+template <int NS>
+__device__ __forceinline__ void split_bf16(const float x[8], bf16x8 out[NS]) {
+  float rest[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) rest[i] = x[i];
+#pragma unroll
+  for (int k = 0; k < NS; ++k) {
+    i32x4 w;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t v = pack_bf16x2(rest[2 * i], rest[2 * i + 1]);
+      w[i] = (int)v;
+      if (k + 1 < NS) {
+        rest[2 * i] -= bf16_bits_to_f32(v & 0xffffu);
+        rest[2 * i + 1] -= bf16_bits_to_f32(v >> 16);
+      }
+    }
+    out[k] = as_bf16x8(w);
+  }
+}
+
+template <int NS>
+__device__ __forceinline__ f32x4 mfma_split(const bf16x8 a, const bf16x8 b[NS], f32x4 c) {
+#pragma unroll
+  for (int k = NS - 1; k >= 0; --k) c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b[k], c, 0, 0, 0);
+  return c;
+}
+
+// Page of the 16-token block at token t, clamped to one the cache has; whether
+// the block is seen (tokens [v.lo, v.hi)) and its page is in the cache.
+__device__ __forceinline__ bool attn_page(const AttnArgs& a, const int32_t* table, const View& v, int t, int& page) {
+  const int i = t >> a.c.lS;
+  page = table[i < a.b.max_pages ? i : 0];
+  const bool ok = t < v.hi && t + 16 > v.lo && (unsigned)page < (unsigned)a.c.pages;
+  if (!ok) page = 0;
+  return ok;
+}
+
+// w with its bytes before `skip` and from n on zeroed.
+__device__ __forceinline__ i32x4 keep_bytes(i32x4 w, int skip, int n) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int a = skip - 4 * j, b = n - 4 * j;
+    const uint32_t lo = a <= 0 ? 0xffffffffu : (a >= 4 ? 0u : ~((1u << (8 * a)) - 1u));
+    const uint32_t hi = b >= 4 ? 0xffffffffu : (b <= 0 ? 0u : (1u << (8 * b)) - 1u);
+    w[j] &= (int)(lo & hi);
+  }
+  return w;
+}
+
+// Eight values of a query row as NS bf16 terms (zeros unless live).
+template <int NS>
+__device__ __forceinline__ void load_q8(const AttnArgs& a, size_t at, bool live, bf16x8 out[NS]) {
+  if (NS == 1) {
+    const i32x4 zero = {0, 0, 0, 0};
+    out[0] = as_bf16x8(live ? ld16(reinterpret_cast<const uint16_t*>(a.q) + at) : zero);
+  } else {
+    float x[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) x[k] = live ? reinterpret_cast<const float*>(a.q)[at + k] : 0.0f;
+    split_bf16<NS>(x, out);
+  }
+}
+
+// One row's finished output: o sums, their maximum m (base 2) and sum l.
+template <int NS>
+__device__ __forceinline__ void attn_store4(const AttnArgs& a, size_t row, int d, const float o[4], float l) {
+  const float inv = l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);
+  if (NS == 1) {
+    *reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(a.out) + row * a.c.D + d) =
+        make_uint2(pack_bf16x2(o[0] * inv, o[1] * inv), pack_bf16x2(o[2] * inv, o[3] * inv));
+  } else {
+    *reinterpret_cast<float4*>(reinterpret_cast<float*>(a.out) + row * a.c.D + d) =
+        make_float4(o[0] * inv, o[1] * inv, o[2] * inv, o[3] * inv);
+  }
+}
+
+__device__ __forceinline__ float attn_lse(float m, float l) {
+  return l == 0.0f ? -__builtin_inff() : kLn2 * (m + __builtin_log2f(l));
+}
+
+}  // namespace moe

@@ -71,6 +71,30 @@ int launch_rope_quant(const void* x, int xt, const int32_t* pos, const float* in
                       int nH, int D, int interleaved, int inverse, const float* static_scales,
                       uint8_t* codes, float* scales, void* ws, hipStream_t st);
 
+// Rotary positions with several axes (rope_axes.hip); strides in elements,
+// 16-byte multiples; R = rotary dim, a multiple of 16 up to D.
+int launch_rope_axes(const void* x, int xt, long long xs_t, long long xs_h, const int32_t* pos, int axes,
+                     const int32_t* pair_axis, const float* inv_freq, int T, int nH, int D, int R,
+                     int interleaved, int inverse, void* out, int ot, long long os_t, long long os_h,
+                     hipStream_t st);
+
+// Paged E4M3 cache: append (kv_append.hip) and attention (attn_decode.hip,
+// attn_tile.hip); argument structs in paged.hpp, rotate.hpp, attention.hpp.
+struct PagedArgs;
+struct BatchArgs;
+struct RotateArgs;
+struct AttnArgs;
+int launch_kv_append(const PagedArgs& c, const BatchArgs& b, const void* k, long long ks_t, long long ks_h,
+                     const void* v, long long vs_t, long long vs_h, int xt, const RotateArgs& r,
+                     hipStream_t st);
+// Rows (query tokens times the heads of a KV head) that the few-row kernel
+// takes when asked for `rows`; 0 if it cannot.
+int attn_decode_rows(int D, int rows);
+int launch_attn_decode(const AttnArgs& a, int rows, bool f32, hipStream_t st);
+// Sequences of more than rows_below rows; units: upper bound of their row blocks.
+int attn_tile_rows();
+int launch_attn_tile(const AttnArgs& a, int rows_below, int units, bool f32, hipStream_t st);
+
 // Arguments of the expert GEMMs (device pointers unless noted).
 struct GemmArgs {
   int M, K, N, E, topk, block_m, P;  // host values

@@ -9,7 +9,9 @@
 #include <mutex>
 
 #include "../../include/moe.h"
+#include "attention.hpp"
 #include "launch.hpp"
+#include "rotate.hpp"
 
 namespace {
 
@@ -609,6 +611,235 @@ moe_status moe_quantize_act(const void* x, int32_t x_dtype, int64_t n, const flo
                                 (uint32_t*)(ws + moe::kMaxPartials * sizeof(float)),
                                 (hipStream_t)stream);
   return hip_status(err, "quantisation launch");
+}
+
+}  // extern "C"
+
+// ------------------------------- rotation, paged cache, attention over it
+
+namespace {
+
+bool value_dtype(int dt) { return dt == MOE_F32 || dt == MOE_BF16; }
+
+// Strides of a [T, heads, head_dim] tensor whose heads are read (or written)
+// 16 bytes at a time.
+moe_status check_strides(const char* name, int dt, int64_t st, int64_t sh, int64_t least) {
+  const int64_t unit = 16 / dtype_bytes(dt);
+  if (st < least || sh < least || st > (1LL << 32) || sh > (1LL << 32))
+    return fail(MOE_ERR_SHAPE, "%s strides %lld, %lld must be in [%lld, 2^32]", name, (long long)st, (long long)sh,
+                (long long)least);
+  if (st % unit || sh % unit)
+    return fail(MOE_ERR_ALIGN, "%s strides %lld, %lld must be multiples of 16 bytes", name, (long long)st,
+                (long long)sh);
+  return MOE_OK;
+}
+
+moe_status check_rotation(const moe_rotation* r, int head_dim, bool positions_needed) {
+  if (r->axes < 1 || r->axes > 8) return fail(MOE_ERR_SHAPE, "axes=%d must be in [1, 8]", r->axes);
+  if (r->rotary_dim < 16 || r->rotary_dim > head_dim || r->rotary_dim % 16)
+    return fail(MOE_ERR_SHAPE, "rotary_dim=%d must be a multiple of 16 in [16, head_dim=%d]", r->rotary_dim, head_dim);
+  if (!r->inv_freq) return fail(MOE_ERR_NULL, "inv_freq is NULL");
+  if (!r->positions && (positions_needed || r->axes > 1)) return fail(MOE_ERR_NULL, "positions is NULL");
+  if (!aligned(r->positions, 4) || !aligned(r->pair_axis, 4) || !aligned(r->inv_freq, 4))
+    return fail(MOE_ERR_ALIGN, "positions, pair_axis and inv_freq must be 4-byte aligned");
+  return MOE_OK;
+}
+
+moe::RotateArgs rotate_args(const moe_rotation* r, int T) {
+  moe::RotateArgs a{};
+  if (r)
+    a = moe::RotateArgs{r->positions, r->pair_axis, r->inv_freq, T, r->axes, r->rotary_dim / 2,
+                        r->interleaved ? 1 : 0, r->inverse ? 1 : 0};
+  return a;
+}
+
+moe_status check_cache_dims(const moe_kv_cache* c) {
+  if (!c) return fail(MOE_ERR_NULL, "cache is NULL");
+  if (c->num_pages < 1) return fail(MOE_ERR_SHAPE, "num_pages=%d must be >= 1", c->num_pages);
+  if (c->page_size != 16 && c->page_size != 32 && c->page_size != 64 && c->page_size != 128)
+    return fail(MOE_ERR_SHAPE, "page_size=%d must be 16, 32, 64 or 128", c->page_size);
+  if (c->n_kv_heads < 1 || c->n_kv_heads > 256)
+    return fail(MOE_ERR_SHAPE, "n_kv_heads=%d must be in [1, 256]", c->n_kv_heads);
+  if (c->head_dim < 16 || c->head_dim > 256 || c->head_dim % 16)
+    return fail(MOE_ERR_SHAPE, "head_dim=%d must be a multiple of 16 in [16, 256]", c->head_dim);
+  return MOE_OK;
+}
+
+moe_status check_counts(int32_t T, int32_t B) {
+  if (B < 0 || B > 65536) return fail(MOE_ERR_SHAPE, "B=%d must be in [0, 65536]", B);
+  if (T < 0 || T > (1 << 28)) return fail(MOE_ERR_SHAPE, "T=%d must be in [0, 2^28]", T);
+  return MOE_OK;
+}
+
+moe_status check_cache_batch(const moe_kv_cache* c, const moe_kv_batch* b) {
+  moe_status s = check_cache_dims(c);
+  if (s) return s;
+  if (!b) return fail(MOE_ERR_NULL, "batch is NULL");
+  s = check_counts(b->T, b->B);
+  if (s) return s;
+  if (b->max_pages < 1 || (long long)b->max_pages * c->page_size > (1LL << 30))
+    return fail(MOE_ERR_SHAPE, "max_pages=%d must be >= 1, with max_pages * page_size <= 2^30", b->max_pages);
+  if (!b->cu_q && b->T != b->B)
+    return fail(MOE_ERR_SHAPE, "without cu_q every sequence has one row: T=%d, B=%d", b->T, b->B);
+  if (b->T == 0 || b->B == 0) return MOE_OK;
+  if (!c->k_codes || !c->v_codes || !c->k_scales || !c->v_scales)
+    return fail(MOE_ERR_NULL, "k_codes, v_codes, k_scales and v_scales are required");
+  if (!b->kv_lens || !b->block_table) return fail(MOE_ERR_NULL, "kv_lens and block_table are required");
+  if (!aligned(c->k_codes, 16) || !aligned(c->v_codes, 16))
+    return fail(MOE_ERR_ALIGN, "k_codes and v_codes must be 16-byte aligned");
+  for (const void* q : {(const void*)c->k_scales, (const void*)c->v_scales, (const void*)b->cu_q,
+                        (const void*)b->kv_lens, (const void*)b->block_table})
+    if (!aligned(q, 4)) return fail(MOE_ERR_ALIGN, "scales and index buffers must be 4-byte aligned");
+  return MOE_OK;
+}
+
+moe::PagedArgs paged_args(const moe_kv_cache* c) {
+  return moe::PagedArgs{c->k_codes, c->v_codes, c->k_scales, c->v_scales, c->num_pages,
+                        __builtin_ctz((unsigned)c->page_size), c->n_kv_heads, c->head_dim};
+}
+
+moe::BatchArgs batch_args(const moe_kv_batch* b) {
+  return moe::BatchArgs{b->cu_q, b->kv_lens, b->block_table, b->B, b->max_pages, b->T};
+}
+
+// How a call is shared out: the few-row kernel takes sequences of up to
+// dec_rows rows (0: none) with W workgroups per KV head, the tile kernel the
+// others (tile_units row blocks at most; 0: there are none).
+struct AttnPlan {
+  int dec_rows, W;
+  long long tile_units;
+  size_t part_ml, bytes;
+};
+
+moe_status attn_plan(const moe_kv_cache* c, int32_t T, int32_t B, int32_t n_heads, int32_t max_q, AttnPlan* p) {
+  if (n_heads < 1 || n_heads % c->n_kv_heads || n_heads / c->n_kv_heads > 128)
+    return fail(MOE_ERR_SHAPE, "n_heads=%d must be a multiple of n_kv_heads=%d, at most 128 times it", n_heads,
+                c->n_kv_heads);
+  if (max_q < 1) return fail(MOE_ERR_SHAPE, "max_q=%d must be >= 1", max_q);
+  const int G = n_heads / c->n_kv_heads;
+  const long long rows = (long long)(max_q < T ? max_q : T) * G;
+  *p = AttnPlan{};
+  p->dec_rows = rows <= 64 ? moe::attn_decode_rows(c->head_dim, (int)rows) : 0;
+  const bool all = p->dec_rows > 0;
+  if (!all) p->dec_rows = moe::attn_decode_rows(c->head_dim, G);
+  if (!all) p->tile_units = (long long)T * G / moe::attn_tile_rows() + (B < T ? B : T);
+  if (p->tile_units > (1LL << 30)) return fail(MOE_ERR_SHAPE, "T * n_heads too large");
+  if (p->dec_rows) {
+    p->W = moe::kAttnGroups / c->n_kv_heads > 0 ? moe::kAttnGroups / c->n_kv_heads : 1;
+    const size_t slots = (size_t)c->n_kv_heads * p->W * 2 * p->dec_rows;
+    const int DT = c->head_dim <= 64 ? 64 : (c->head_dim <= 128 ? 128 : 256);
+    p->part_ml = up256(slots * DT * sizeof(float));
+    p->bytes = up256(p->part_ml + slots * 2 * sizeof(float));
+  }
+  return MOE_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+moe_status moe_rope_axes(const void* x, int32_t x_dtype, int64_t x_stride_t, int64_t x_stride_h,
+                         const moe_rotation* rotation, int32_t T, int32_t n_heads, int32_t head_dim,
+                         void* out, int32_t out_dtype, int64_t out_stride_t, int64_t out_stride_h,
+                         void* stream) {
+  moe_status s = check_rope_dims(T, n_heads, head_dim);
+  if (s) return s;
+  if (!value_dtype(x_dtype) || !value_dtype(out_dtype))
+    return fail(MOE_ERR_DTYPE, "x_dtype and out_dtype must be MOE_F32 or MOE_BF16");
+  if (!rotation) return fail(MOE_ERR_NULL, "rotation is NULL");
+  if ((s = check_strides("x", x_dtype, x_stride_t, x_stride_h, 0))) return s;
+  if ((s = check_strides("out", out_dtype, out_stride_t, out_stride_h, head_dim))) return s;
+  if ((s = check_rotation(rotation, head_dim, T > 0))) return s;
+  if (T == 0) return ok();
+  if (!x || !out) return fail(MOE_ERR_NULL, "x and out are required");
+  if (!aligned(x, 16) || !aligned(out, 16)) return fail(MOE_ERR_ALIGN, "x and out must be 16-byte aligned");
+  if (out == x && (x_dtype != out_dtype || x_stride_t != out_stride_t || x_stride_h != out_stride_h))
+    return fail(MOE_ERR_UNSUPPORTED, "in place, out needs the type and strides of x");
+  const int err = moe::launch_rope_axes(x, x_dtype, x_stride_t, x_stride_h, rotation->positions, rotation->axes,
+                                        rotation->pair_axis, rotation->inv_freq, T, n_heads, head_dim,
+                                        rotation->rotary_dim, rotation->interleaved ? 1 : 0,
+                                        rotation->inverse ? 1 : 0, out, out_dtype, out_stride_t, out_stride_h,
+                                        (hipStream_t)stream);
+  return hip_status(err, "rope_axes launch");
+}
+
+moe_status moe_kv_append(const moe_kv_cache* cache, const moe_kv_batch* batch, const void* k,
+                         int64_t k_stride_t, int64_t k_stride_h, const void* v, int64_t v_stride_t,
+                         int64_t v_stride_h, int32_t dtype, const moe_rotation* rotation, void* stream) {
+  moe_status s = check_cache_batch(cache, batch);
+  if (s) return s;
+  if (!value_dtype(dtype)) return fail(MOE_ERR_DTYPE, "dtype must be MOE_F32 or MOE_BF16");
+  if ((s = check_strides("k", dtype, k_stride_t, k_stride_h, 0))) return s;
+  if ((s = check_strides("v", dtype, v_stride_t, v_stride_h, 0))) return s;
+  if (rotation && (s = check_rotation(rotation, cache->head_dim, false))) return s;
+  if (batch->T == 0 || batch->B == 0) return ok();
+  if (!k || !v) return fail(MOE_ERR_NULL, "k and v are required");
+  if (!aligned(k, 16) || !aligned(v, 16)) return fail(MOE_ERR_ALIGN, "k and v must be 16-byte aligned");
+  const int err = moe::launch_kv_append(paged_args(cache), batch_args(batch), k, k_stride_t, k_stride_h, v,
+                                        v_stride_t, v_stride_h, dtype, rotate_args(rotation, batch->T),
+                                        (hipStream_t)stream);
+  return hip_status(err, "kv_append launch");
+}
+
+moe_status moe_paged_attention_workspace_size(const moe_kv_cache* cache, int32_t T, int32_t B,
+                                              int32_t n_heads, int32_t max_q, size_t* bytes) {
+  if (!bytes) return fail(MOE_ERR_NULL, "bytes is NULL");
+  moe_status s = check_cache_dims(cache);
+  if (s) return s;
+  if ((s = check_counts(T, B))) return s;
+  AttnPlan p;
+  if ((s = attn_plan(cache, T, B, n_heads, max_q, &p))) return s;
+  *bytes = p.bytes;
+  return ok();
+}
+
+moe_status moe_paged_attention(const moe_kv_cache* cache, const moe_kv_batch* batch, const void* q,
+                               int32_t q_dtype, int64_t q_stride_t, int64_t q_stride_h,
+                               int32_t n_heads, int32_t max_q, float sm_scale, int32_t causal,
+                               int32_t window, void* out, float* lse, void* workspace,
+                               size_t workspace_bytes, void* stream) {
+  moe_status s = check_cache_batch(cache, batch);
+  if (s) return s;
+  if (!value_dtype(q_dtype)) return fail(MOE_ERR_DTYPE, "q_dtype must be MOE_F32 or MOE_BF16");
+  if ((s = check_strides("q", q_dtype, q_stride_t, q_stride_h, 0))) return s;
+  if (window < 0 || window > (1 << 30)) return fail(MOE_ERR_SHAPE, "window=%d must be in [0, 2^30]", window);
+  if (!(sm_scale - sm_scale == 0.0f)) return fail(MOE_ERR_SHAPE, "sm_scale must be finite");
+  if (!batch->cu_q && max_q != 1) return fail(MOE_ERR_SHAPE, "max_q=%d must be 1 without cu_q", max_q);
+  AttnPlan p;
+  if ((s = attn_plan(cache, batch->T, batch->B, n_heads, max_q, &p))) return s;
+  if (batch->T == 0 || batch->B == 0) return ok();
+  if (!q || !out) return fail(MOE_ERR_NULL, "q and out are required");
+  if (!aligned(q, 16) || !aligned(out, 16) || !aligned(workspace, 16))
+    return fail(MOE_ERR_ALIGN, "q, out and workspace must be 16-byte aligned");
+  if (!aligned(lse, 4)) return fail(MOE_ERR_ALIGN, "lse must be 4-byte aligned");
+  if (p.bytes > 0 && (!workspace || workspace_bytes < p.bytes))
+    return fail(MOE_ERR_WORKSPACE, "workspace of %zu bytes needed, %zu given", p.bytes, workspace_bytes);
+
+  moe::AttnArgs a{};
+  a.c = paged_args(cache);
+  a.b = batch_args(batch);
+  a.q = q;
+  a.qs_t = q_stride_t;
+  a.qs_h = q_stride_h;
+  a.nH = n_heads;
+  a.G = n_heads / cache->n_kv_heads;
+  a.scale2 = sm_scale * moe::kLog2e;
+  a.causal = causal ? 1 : 0;
+  a.window = window;
+  a.out = out;
+  a.lse = lse;
+  if (p.dec_rows) {
+    a.part_o = reinterpret_cast<float*>(workspace);
+    a.part_ml = reinterpret_cast<float*>((char*)workspace + p.part_ml);
+    a.W = p.W;
+    const int err = moe::launch_attn_decode(a, p.dec_rows, q_dtype == MOE_F32, (hipStream_t)stream);
+    if (err) return hip_status(err, "attention launch");
+  }
+  if (p.tile_units) {
+    const int err = moe::launch_attn_tile(a, p.dec_rows, (int)p.tile_units, q_dtype == MOE_F32, (hipStream_t)stream);
+    if (err) return hip_status(err, "attention launch");
+  }
+  return ok();
 }
 
 }  // extern "C"

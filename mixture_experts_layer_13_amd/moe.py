@@ -21,7 +21,8 @@ EXPORTS = ("moe_status_string", "moe_last_error", "moe_align_capacity", "moe_wor
            "moe_route_topk", "moe_align_permute", "moe_fused_forward", "moe_quantize_act",
            "moe_fused_forward_profiled", "moe_fused_forward_noalloc", "moe_route_align", "moe_route_project_topk",
            "moe_route_project_workspace_size", "moe_rope_quantize_per_head", "moe_rope_workspace_size",
-           "moe_fused_forward_persistent")
+           "moe_fused_forward_persistent", "moe_rope_axes", "moe_kv_append", "moe_paged_attention",
+           "moe_paged_attention_workspace_size")
 MOE_QUANT_WORKSPACE_BYTES = 8192
 MOE_WORKSPACE_SCALES_OFFSET = 4096
 MOE_NOALLOC_SCRATCH_BYTES = 64 << 20
@@ -38,6 +39,21 @@ class MoEError(RuntimeError):
 class moe_problem(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int32) for n in
                 ("M", "K", "N", "E", "topk", "block_m", "a_dtype", "w_dtype", "out_dtype")]
+
+
+class moe_rotation(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_void_p) for n in ("positions", "pair_axis", "inv_freq")] +
+                [(n, ctypes.c_int32) for n in ("axes", "rotary_dim", "interleaved", "inverse")])
+
+
+class moe_kv_cache(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_void_p) for n in ("k_codes", "v_codes", "k_scales", "v_scales")] +
+                [(n, ctypes.c_int32) for n in ("num_pages", "page_size", "n_kv_heads", "head_dim")])
+
+
+class moe_kv_batch(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_void_p) for n in ("cu_q", "kv_lens", "block_table")] +
+                [(n, ctypes.c_int32) for n in ("B", "T", "max_pages")])
 
 
 _lib = None
@@ -88,6 +104,19 @@ def lib():
         L.moe_rope_quantize_per_head.restype = ctypes.c_int
         L.moe_rope_workspace_size.argtypes = [i32, i32, i32, ctypes.POINTER(sz)]
         L.moe_rope_workspace_size.restype = ctypes.c_int
+        f32 = ctypes.c_float
+        L.moe_rope_axes.argtypes = [vp, i32, i64, i64, ctypes.POINTER(moe_rotation), i32, i32, i32, vp, i32,
+                                    i64, i64, vp]
+        L.moe_rope_axes.restype = ctypes.c_int
+        L.moe_kv_append.argtypes = [ctypes.POINTER(moe_kv_cache), ctypes.POINTER(moe_kv_batch), vp, i64, i64,
+                                    vp, i64, i64, i32, ctypes.POINTER(moe_rotation), vp]
+        L.moe_kv_append.restype = ctypes.c_int
+        L.moe_paged_attention.argtypes = [ctypes.POINTER(moe_kv_cache), ctypes.POINTER(moe_kv_batch), vp, i32,
+                                          i64, i64, i32, i32, f32, i32, i32, vp, vp, vp, sz, vp]
+        L.moe_paged_attention.restype = ctypes.c_int
+        L.moe_paged_attention_workspace_size.argtypes = [ctypes.POINTER(moe_kv_cache), i32, i32, i32, i32,
+                                                         ctypes.POINTER(sz)]
+        L.moe_paged_attention_workspace_size.restype = ctypes.c_int
         _lib = L
     return _lib
 
@@ -227,6 +256,182 @@ def moe_rope_quantize_per_head(x, positions, inv_freq, interleaved=False, invers
         _ptr(scales), _ptr(workspace), workspace.numel() * workspace.element_size(),
         _stream(stream)))
     return codes, scales
+
+
+def _require(ok, status, detail):
+    if not ok:
+        raise MoEError(status, detail)
+
+
+def _index(t, shape, name, device):
+    """A dense int32 index buffer of this shape (None: any size) on `device`."""
+    _require(t.dtype == torch.int32, MOE_ERR_DTYPE, f"{name} must be int32")
+    _require(t.dim() == len(shape) and all(n is None or n == m for n, m in zip(shape, t.shape)), MOE_ERR_SHAPE,
+             f"{name} has shape {tuple(t.shape)}")
+    _require(t.is_contiguous(), MOE_ERR_UNSUPPORTED, f"{name} must be contiguous")
+    _require(t.device == device, MOE_ERR_UNSUPPORTED, f"{name} is on {t.device}, not on {device}")
+
+
+def _heads(t, shape, name, device):
+    """A [tokens, heads, head_dim] tensor of this shape on `device`, heads contiguous; its two strides."""
+    _require(t.dtype in (torch.bfloat16, torch.float32), MOE_ERR_DTYPE, f"{name} must be bf16 or f32")
+    _require(tuple(t.shape) == tuple(shape), MOE_ERR_SHAPE, f"{name} has shape {tuple(t.shape)}, not {tuple(shape)}")
+    _require(t.stride(2) == 1, MOE_ERR_UNSUPPORTED, f"{name}: the values of a head must be contiguous")
+    _require(t.device == device, MOE_ERR_UNSUPPORTED, f"{name} is on {t.device}, not on {device}")
+    # the strides of a dimension of size one are torch's to choose
+    st = t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2]
+    return st, t.stride(1) if t.shape[1] > 1 else t.shape[2]
+
+
+def _run(device, stream, call):
+    """call(stream handle) with `device` current."""
+    _require(device.type == "cuda", MOE_ERR_UNSUPPORTED, f"tensors are on {device}, not on a GPU")
+    if device.index == torch.cuda.current_device():
+        _check(call(_stream(stream)))
+    else:
+        with torch.cuda.device(device):
+            _check(call(_stream(stream)))
+
+
+def _made(shape, dtype, device, stream):
+    """A tensor made for a call that runs on `stream` (None: the current one)."""
+    t = torch.empty(shape, dtype=dtype, device=device)
+    if stream is not None and t.is_cuda:
+        t.record_stream(stream)
+    return t
+
+
+class Rotation:
+    """Rotary positions (include/moe.h, moe_rotation): positions int32 [T] or
+    [axes, T] (None in an append: the tokens' own places), inv_freq f32
+    [rotary_dim / 2], pair_axis int32 [rotary_dim / 2] or None.  Keeps the
+    tensors; positions may be rewritten in place between calls."""
+
+    def __init__(self, positions, inv_freq, pair_axis=None, interleaved=False, inverse=False):
+        dev = inv_freq.device
+        _require(inv_freq.dtype == torch.float32, MOE_ERR_DTYPE, "inv_freq must be f32")
+        _require(inv_freq.dim() == 1 and inv_freq.is_contiguous(), MOE_ERR_SHAPE, "inv_freq must be a dense vector")
+        axes, self.tokens = 1, None
+        if positions is not None:
+            _index(positions, (None,) * positions.dim(), "positions", dev)
+            _require(positions.dim() in (1, 2), MOE_ERR_SHAPE, "positions must be [T] or [axes, T]")
+            axes = positions.shape[0] if positions.dim() == 2 else 1
+            self.tokens = positions.shape[-1]
+        if pair_axis is not None:
+            _index(pair_axis, (inv_freq.numel(),), "pair_axis", dev)
+        self.positions, self.inv_freq, self.pair_axis, self.device = positions, inv_freq, pair_axis, dev
+        self.struct = moe_rotation(_ptr(positions), _ptr(pair_axis), _ptr(inv_freq), axes, 2 * inv_freq.numel(),
+                                   int(bool(interleaved)), int(bool(inverse)))
+
+    def _for(self, T, device):
+        _require(self.tokens is None or self.tokens == T, MOE_ERR_SHAPE, f"positions of {self.tokens} tokens for {T}")
+        _require(self.device == device, MOE_ERR_UNSUPPORTED, f"the rotation is on {self.device}, not on {device}")
+        return ctypes.byref(self.struct)
+
+
+def moe_rope_axes(x, rotation, out=None, out_dtype=None, stream=None):
+    """x [T, nH, D] bf16/f32, heads contiguous -> x rotated (out may be x)."""
+    T, nH, D = x.shape
+    if out is None:
+        out = _made((T, nH, D), out_dtype or x.dtype, x.device, stream)
+    xs, os = _heads(x, (T, nH, D), "x", x.device), _heads(out, (T, nH, D), "out", x.device)
+    rot = rotation._for(T, x.device)
+    _run(x.device, stream, lambda s: lib().moe_rope_axes(_ptr(x), dtype_code(x.dtype), *xs, rot, T, nH, D, _ptr(out),
+                                                         dtype_code(out.dtype), *os, s))
+    return out
+
+
+class PagedKV:
+    """A paged E4M3 key/value cache (include/moe.h, moe_kv_cache) over the
+    caller's tensors: k_codes [pages, H, S, D] and v_codes [pages, H, S/16, D,
+    16] (float8_e4m3fn or uint8), k_scales and v_scales f32 [pages, H]."""
+
+    def __init__(self, k_codes, v_codes, k_scales, v_scales):
+        _require(k_codes.dim() == 4, MOE_ERR_SHAPE, "k_codes must be [pages, heads, page_size, head_dim]")
+        P, H, S, D = k_codes.shape
+        for t, shape, name in ((k_codes, (P, H, S, D), "k_codes"), (v_codes, (P, H, S // 16, D, 16), "v_codes"),
+                               (k_scales, (P, H), "k_scales"), (v_scales, (P, H), "v_scales")):
+            _require(t.dtype in ((torch.float8_e4m3fn, torch.uint8) if "codes" in name else (torch.float32,)),
+                     MOE_ERR_DTYPE, f"{name} has dtype {t.dtype}")
+            _require(tuple(t.shape) == shape, MOE_ERR_SHAPE, f"{name} has shape {tuple(t.shape)}, not {shape}")
+            _require(t.is_contiguous(), MOE_ERR_UNSUPPORTED, f"{name} must be contiguous")
+            _require(t.device == k_codes.device, MOE_ERR_UNSUPPORTED, f"{name} is on {t.device}")
+        self.k_codes, self.v_codes, self.k_scales, self.v_scales = k_codes, v_codes, k_scales, v_scales
+        self.num_pages, self.n_kv_heads, self.page_size, self.head_dim = P, H, S, D
+        self.device = k_codes.device
+        self.struct = moe_kv_cache(_ptr(k_codes), _ptr(v_codes), _ptr(k_scales), _ptr(v_scales), P, S, H, D)
+
+    def _batch(self, T, kv_lens, block_table, cu_q):
+        _index(kv_lens, (None,), "kv_lens", self.device)
+        B = kv_lens.shape[0]
+        _index(block_table, (B, None), "block_table", self.device)
+        if cu_q is not None:
+            _index(cu_q, (B + 1,), "cu_q", self.device)
+        return moe_kv_batch(_ptr(cu_q), _ptr(kv_lens), _ptr(block_table), B, T, block_table.shape[1])
+
+
+def alloc_kv_cache(num_pages, page_size, n_kv_heads, head_dim, device="cuda"):
+    codes = dict(dtype=torch.float8_e4m3fn, device=device)
+    return PagedKV(torch.empty(num_pages, n_kv_heads, page_size, head_dim, **codes),
+                   torch.empty(num_pages, n_kv_heads, page_size // 16, head_dim, 16, **codes),
+                   torch.empty(num_pages, n_kv_heads, device=device),
+                   torch.empty(num_pages, n_kv_heads, device=device))
+
+
+def moe_kv_append(cache, k, v, kv_lens, block_table, rotation=None, cu_q=None, stream=None):
+    """k, v [T, H, D] bf16/f32 into the cache, k rotated first; kv_lens int32
+    [B] (these rows included), block_table int32 [B, max_pages], cu_q int32
+    [B + 1] or None (one row per sequence)."""
+    T = k.shape[0]
+    shape = (T, cache.n_kv_heads, cache.head_dim)
+    ks, vs = _heads(k, shape, "k", cache.device), _heads(v, shape, "v", cache.device)
+    _require(k.dtype == v.dtype, MOE_ERR_DTYPE, f"k is {k.dtype}, v is {v.dtype}")
+    batch = cache._batch(T, kv_lens, block_table, cu_q)
+    rot = None if rotation is None else rotation._for(T, cache.device)
+    _run(cache.device, stream,
+         lambda s: lib().moe_kv_append(ctypes.byref(cache.struct), ctypes.byref(batch), _ptr(k), *ks, _ptr(v), *vs,
+                                       dtype_code(k.dtype), rot, s))
+
+
+def moe_paged_attention_workspace_size(cache, T, B, n_heads, max_q=1):
+    n = ctypes.c_size_t(0)
+    _check(lib().moe_paged_attention_workspace_size(ctypes.byref(cache.struct), T, B, n_heads, max_q,
+                                                    ctypes.byref(n)))
+    return int(n.value)
+
+
+def moe_paged_attention(cache, q, kv_lens, block_table, cu_q=None, max_q=1, sm_scale=None, causal=True, window=0,
+                        out=None, lse=None, return_lse=False, workspace=None, stream=None):
+    """q [T, nH, D] bf16/f32 (rotated) over the cache -> out [T, nH, D], and
+    with return_lse (or lse given) the log sums lse f32 [T, nH].  max_q: at
+    least the rows of every sequence.  sm_scale None: 1 / sqrt(D)."""
+    T, nH, D = q.shape
+    dev = cache.device
+    qs = _heads(q, (T, nH, cache.head_dim), "q", dev)
+    batch = cache._batch(T, kv_lens, block_table, cu_q)
+    if out is None:
+        out = _made((T, nH, D), q.dtype, dev, stream)
+    _require(out.dtype == q.dtype, MOE_ERR_DTYPE, f"out is {out.dtype}, q is {q.dtype}")
+    _heads(out, (T, nH, D), "out", dev)
+    _require(out.is_contiguous(), MOE_ERR_UNSUPPORTED, "out must be contiguous")
+    if lse is None and return_lse:
+        lse = _made((T, nH), torch.float32, dev, stream)
+    if lse is not None:
+        _require(lse.dtype == torch.float32, MOE_ERR_DTYPE, "lse must be f32")
+        _require(tuple(lse.shape) == (T, nH) and lse.is_contiguous() and lse.device == dev, MOE_ERR_SHAPE,
+                 "lse must be a dense [T, n_heads] on the cache's device")
+    if workspace is None:
+        workspace = _made(max(moe_paged_attention_workspace_size(cache, T, batch.B, nH, max_q), 16), torch.uint8, dev,
+                          stream)
+    _require(workspace.is_contiguous() and workspace.device == dev, MOE_ERR_WORKSPACE,
+             "the workspace must be dense and on the cache's device")
+    scale = D ** -0.5 if sm_scale is None else sm_scale
+    _run(dev, stream,
+         lambda s: lib().moe_paged_attention(ctypes.byref(cache.struct), ctypes.byref(batch), _ptr(q),
+                                             dtype_code(q.dtype), *qs, nH, max_q, scale, int(bool(causal)), window,
+                                             _ptr(out), _ptr(lse), _ptr(workspace),
+                                             workspace.numel() * workspace.element_size(), s))
+    return out if lse is None else (out, lse)
 
 
 @dataclass

@@ -1,0 +1,202 @@
+"""What the rotation, append and attention calls refuse, decided on the host
+before anything is enqueued (no GPU), and the oracle's own closed forms."""
+import ctypes
+
+import numpy as np
+import pytest
+import torch
+
+from mixture_experts_layer_13_amd import moe
+from oracle import attention_oracle as AO
+
+F = 0x7f0000001000
+ODD16, ODD4 = F + 8, F + 2
+BF, F32 = moe.MOE_BF16, moe.MOE_F32
+
+
+def cache(**kw):
+    d = dict(k_codes=F, v_codes=F, k_scales=F, v_scales=F, num_pages=10, page_size=64, n_kv_heads=8, head_dim=128)
+    d.update(kw)
+    return moe.moe_kv_cache(*[d[n] for n, _ in moe.moe_kv_cache._fields_])
+
+
+def batch(**kw):
+    d = dict(cu_q=F, kv_lens=F, block_table=F, B=4, T=9, max_pages=16)
+    d.update(kw)
+    return moe.moe_kv_batch(*[d[n] for n, _ in moe.moe_kv_batch._fields_])
+
+
+def rotation(**kw):
+    d = dict(positions=F, pair_axis=F, inv_freq=F, axes=3, rotary_dim=64, interleaved=0, inverse=0)
+    d.update(kw)
+    return moe.moe_rotation(*[d[n] for n, _ in moe.moe_rotation._fields_])
+
+
+def ref(x):
+    return None if x is None else ctypes.byref(x)
+
+
+def rope(x=F, dt=BF, xs=(4096, 128), rot="default", T=4, nH=32, D=128, out=F + (1 << 30), odt=BF, os=(4096, 128)):
+    rot = rotation() if rot == "default" else rot
+    return moe.lib().moe_rope_axes(x, dt, *xs, ref(rot), T, nH, D, out, odt, *os, None)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(T=-1), moe.MOE_ERR_SHAPE), (dict(nH=0), moe.MOE_ERR_SHAPE), (dict(nH=257), moe.MOE_ERR_SHAPE),
+    (dict(D=120), moe.MOE_ERR_SHAPE), (dict(D=528), moe.MOE_ERR_SHAPE), (dict(dt=2), moe.MOE_ERR_DTYPE),
+    (dict(odt=7), moe.MOE_ERR_DTYPE), (dict(rot=None), moe.MOE_ERR_NULL), (dict(xs=(-8, 128)), moe.MOE_ERR_SHAPE),
+    (dict(xs=(4096, 132)), moe.MOE_ERR_ALIGN), (dict(os=(4096, 120)), moe.MOE_ERR_SHAPE),
+    (dict(os=(4100, 128)), moe.MOE_ERR_ALIGN), (dict(rot=rotation(axes=0)), moe.MOE_ERR_SHAPE),
+    (dict(rot=rotation(axes=9)), moe.MOE_ERR_SHAPE), (dict(rot=rotation(rotary_dim=144)), moe.MOE_ERR_SHAPE),
+    (dict(rot=rotation(rotary_dim=24)), moe.MOE_ERR_SHAPE), (dict(rot=rotation(rotary_dim=0)), moe.MOE_ERR_SHAPE),
+    (dict(rot=rotation(inv_freq=None)), moe.MOE_ERR_NULL), (dict(rot=rotation(positions=None)), moe.MOE_ERR_NULL),
+    (dict(rot=rotation(positions=None, axes=1)), moe.MOE_ERR_NULL), (dict(rot=rotation(positions=ODD4)), moe.MOE_ERR_ALIGN),
+    (dict(x=None), moe.MOE_ERR_NULL), (dict(out=None), moe.MOE_ERR_NULL), (dict(x=ODD16), moe.MOE_ERR_ALIGN),
+    (dict(out=ODD16), moe.MOE_ERR_ALIGN), (dict(out=F, odt=F32), moe.MOE_ERR_UNSUPPORTED),
+    (dict(out=F, os=(8192, 128)), moe.MOE_ERR_UNSUPPORTED), (dict(T=0, x=None, out=None), moe.MOE_OK),
+])
+def test_rope_axes_refusals(kw, status):
+    assert rope(**kw) == status
+    assert (moe.moe_last_error() != "") == (status != moe.MOE_OK)
+
+
+BAD_CACHE = [
+    (dict(num_pages=0), moe.MOE_ERR_SHAPE), (dict(page_size=48), moe.MOE_ERR_SHAPE),
+    (dict(page_size=256), moe.MOE_ERR_SHAPE), (dict(page_size=8), moe.MOE_ERR_SHAPE),
+    (dict(n_kv_heads=0), moe.MOE_ERR_SHAPE), (dict(n_kv_heads=257), moe.MOE_ERR_SHAPE),
+    (dict(head_dim=120), moe.MOE_ERR_SHAPE), (dict(head_dim=272), moe.MOE_ERR_SHAPE),
+    (dict(k_codes=None), moe.MOE_ERR_NULL), (dict(v_scales=None), moe.MOE_ERR_NULL),
+    (dict(v_codes=ODD16), moe.MOE_ERR_ALIGN), (dict(k_scales=ODD4), moe.MOE_ERR_ALIGN),
+]
+BAD_BATCH = [
+    (dict(B=-1), moe.MOE_ERR_SHAPE), (dict(B=65537), moe.MOE_ERR_SHAPE), (dict(T=-1), moe.MOE_ERR_SHAPE),
+    (dict(T=(1 << 28) + 1), moe.MOE_ERR_SHAPE), (dict(max_pages=0), moe.MOE_ERR_SHAPE),
+    (dict(max_pages=(1 << 24) + 1), moe.MOE_ERR_SHAPE), (dict(cu_q=None), moe.MOE_ERR_SHAPE),
+    (dict(kv_lens=None), moe.MOE_ERR_NULL), (dict(block_table=None), moe.MOE_ERR_NULL),
+    (dict(cu_q=ODD4), moe.MOE_ERR_ALIGN), (dict(block_table=ODD4), moe.MOE_ERR_ALIGN),
+]
+
+
+def append(c="default", b="default", k=F, v=F, ks=(2048, 128), vs=(2048, 128), dt=BF, rot=None):
+    c = cache() if c == "default" else c
+    b = batch() if b == "default" else b
+    return moe.lib().moe_kv_append(ref(c), ref(b), k, *ks, v, *vs, dt, ref(rot), None)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(c=None), moe.MOE_ERR_NULL), (dict(b=None), moe.MOE_ERR_NULL), (dict(k=None), moe.MOE_ERR_NULL),
+    (dict(v=None), moe.MOE_ERR_NULL), (dict(v=ODD16), moe.MOE_ERR_ALIGN), (dict(dt=2), moe.MOE_ERR_DTYPE),
+    (dict(ks=(-1, 128)), moe.MOE_ERR_SHAPE), (dict(vs=(2048, 100)), moe.MOE_ERR_ALIGN),
+    (dict(rot=rotation(rotary_dim=256)), moe.MOE_ERR_SHAPE), (dict(rot=rotation(positions=None)), moe.MOE_ERR_NULL),
+    (dict(rot=rotation(inv_freq=None)), moe.MOE_ERR_NULL), (dict(b=batch(T=0), k=None, v=None), moe.MOE_OK),
+    (dict(b=batch(B=0, kv_lens=None)), moe.MOE_OK),
+] + [(dict(c=cache(**kw)), s) for kw, s in BAD_CACHE] + [(dict(b=batch(**kw)), s) for kw, s in BAD_BATCH])
+def test_kv_append_refusals(kw, status):
+    assert append(**kw) == status
+
+
+def attend(c="default", b="default", q=F, dt=BF, qs=(4096, 128), nH=32, max_q=9, scale=0.1, window=0, out=F, lse=None,
+           ws=F, wsb=1 << 40):
+    c = cache() if c == "default" else c
+    b = batch() if b == "default" else b
+    return moe.lib().moe_paged_attention(ref(c), ref(b), q, dt, *qs, nH, max_q, scale, 1, window, out, lse, ws, wsb, None)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(c=None), moe.MOE_ERR_NULL), (dict(b=None), moe.MOE_ERR_NULL), (dict(q=None), moe.MOE_ERR_NULL),
+    (dict(out=None), moe.MOE_ERR_NULL), (dict(ws=None), moe.MOE_ERR_WORKSPACE), (dict(wsb=64), moe.MOE_ERR_WORKSPACE),
+    (dict(dt=2), moe.MOE_ERR_DTYPE), (dict(qs=(4096, 127)), moe.MOE_ERR_ALIGN), (dict(qs=(-8, 128)), moe.MOE_ERR_SHAPE),
+    (dict(nH=0), moe.MOE_ERR_SHAPE), (dict(nH=31), moe.MOE_ERR_SHAPE), (dict(nH=8 * 129), moe.MOE_ERR_SHAPE),
+    (dict(max_q=0), moe.MOE_ERR_SHAPE), (dict(window=-1), moe.MOE_ERR_SHAPE), (dict(window=(1 << 30) + 1), moe.MOE_ERR_SHAPE),
+    (dict(scale=float("nan")), moe.MOE_ERR_SHAPE), (dict(scale=float("inf")), moe.MOE_ERR_SHAPE),
+    (dict(b=batch(cu_q=None, T=4), max_q=2), moe.MOE_ERR_SHAPE), (dict(q=ODD16), moe.MOE_ERR_ALIGN),
+    (dict(out=ODD16), moe.MOE_ERR_ALIGN), (dict(ws=ODD16), moe.MOE_ERR_ALIGN), (dict(lse=ODD4), moe.MOE_ERR_ALIGN),
+    (dict(b=batch(T=0), q=None, out=None, ws=None), moe.MOE_OK),
+] + [(dict(c=cache(**kw)), s) for kw, s in BAD_CACHE] + [(dict(b=batch(**kw)), s) for kw, s in BAD_BATCH])
+def test_attention_refusals(kw, status):
+    assert attend(**kw) == status
+
+
+def test_workspace_size():
+    L, n = moe.lib(), ctypes.c_size_t(0)
+
+    def size(T, B, nH, max_q, **kw):
+        c = cache(k_codes=None, v_codes=None, k_scales=None, v_scales=None, **kw)
+        return L.moe_paged_attention_workspace_size(ref(c), T, B, nH, max_q, ctypes.byref(n)), n.value
+    assert size(1, 1, 32, 1)[0] == moe.MOE_OK and 0 < n.value < 64 << 20
+    assert size(0, 0, 32, 1)[0] == moe.MOE_OK
+    assert size(8192, 1, 32, 8192)[0] == moe.MOE_OK
+    assert size(8, 8, 30, 1)[0] == moe.MOE_ERR_SHAPE
+    assert size(8, 8, 32, 0)[0] == moe.MOE_ERR_SHAPE
+    assert size(-8, 8, 32, 1)[0] == moe.MOE_ERR_SHAPE
+    assert size(8, 8, 32, 1, page_size=5)[0] == moe.MOE_ERR_SHAPE
+    assert L.moe_paged_attention_workspace_size(None, 1, 1, 1, 1, ctypes.byref(n)) == moe.MOE_ERR_NULL
+    assert L.moe_paged_attention_workspace_size(ref(cache()), 1, 1, 8, 1, None) == moe.MOE_ERR_NULL
+
+
+def refused(status, call, *a, **kw):
+    with pytest.raises(moe.MoEError) as e:
+        call(*a, **kw)
+    assert e.value.status == status, e.value
+
+
+def test_binding_refusals():
+    """Types, shapes and strides that the C side cannot see; CPU tensors."""
+    inv = torch.ones(32)
+    pos = torch.zeros(2, 5, dtype=torch.int32)
+    x = torch.zeros(5, 4, 64)
+    E, S, U = moe.MOE_ERR_DTYPE, moe.MOE_ERR_SHAPE, moe.MOE_ERR_UNSUPPORTED
+    refused(E, moe.Rotation, pos.long(), inv)
+    refused(E, moe.Rotation, pos, inv.double())
+    refused(S, moe.Rotation, pos, inv, torch.zeros(31, dtype=torch.int32))
+    refused(U, moe.Rotation, pos.t(), inv)
+    rot = moe.Rotation(pos, inv, torch.zeros(32, dtype=torch.int32))
+    refused(S, moe.moe_rope_axes, x[:4], rot)
+    refused(E, moe.moe_rope_axes, x.half(), rot)
+    refused(U, moe.moe_rope_axes, torch.zeros(5, 64, 4).transpose(1, 2), rot)
+    refused(S, moe.moe_rope_axes, x, rot, out=torch.zeros(5, 4, 32))
+    refused(U, moe.moe_rope_axes, x, rot)  # not on a GPU
+    kc, vc, sc = torch.zeros(3, 4, 16, 64, dtype=torch.uint8), torch.zeros(3, 4, 1, 64, 16, dtype=torch.uint8), torch.ones(3, 4)
+    refused(S, moe.PagedKV, kc, kc, sc, sc)
+    refused(E, moe.PagedKV, kc.int(), vc, sc, sc)
+    refused(E, moe.PagedKV, kc, vc, sc.double(), sc)
+    refused(U, moe.PagedKV, kc.transpose(0, 1).contiguous().transpose(0, 1), vc, sc, sc)
+    cache_ = moe.PagedKV(kc, vc, sc, sc)
+    lens, table = torch.ones(5, dtype=torch.int32), torch.zeros(5, 2, dtype=torch.int32)
+    refused(S, moe.moe_kv_append, cache_, x[:, :3], x[:, :3], lens, table)
+    refused(E, moe.moe_kv_append, cache_, x, x.bfloat16(), lens, table)
+    refused(E, moe.moe_kv_append, cache_, x, x, lens.long(), table)
+    refused(S, moe.moe_kv_append, cache_, x, x, lens, table[:4])
+    refused(S, moe.moe_kv_append, cache_, x, x, lens, table, cu_q=lens)
+    refused(U, moe.moe_kv_append, cache_, x, x, lens, table)
+    refused(S, moe.moe_paged_attention, cache_, x[:, :, :32], lens, table)
+    refused(E, moe.moe_paged_attention, cache_, x, lens, table, out=x.bfloat16())
+    refused(E, moe.moe_paged_attention, cache_, x, lens, table, lse=torch.zeros(5, 4, dtype=torch.float64))
+    refused(U, moe.moe_paged_attention, cache_, x, lens, table)
+
+
+def test_oracle_closed_forms():
+    # E4M3: every code is its own nearest, midpoints go to the even code
+    n = np.array([c for c in range(256) if c & 127 != 127], np.uint8)
+    assert np.array_equal(AO.e4m3_codes(AO.E4M3[n]), n)
+    t = torch.arange(256, dtype=torch.uint8).view(torch.float8_e4m3fn).double().numpy()
+    assert np.array_equal(t, AO.E4M3, equal_nan=True)
+    got = AO.e4m3_codes(AO.MIDS)
+    assert (got % 2 == 0).all() and (np.abs(got.astype(int) - np.arange(126)) <= 1).all()
+    assert AO.E4M3[AO.e4m3_codes(np.array([1e9, -1e9]))].tolist() == [448.0, -448.0]
+    assert [AO.page_scale(a) for a in (0.0, 448.0, 448.5, 1.0)] == [2.0 ** -64, 1.0, 2.0, 2.0 ** -8]
+    # a quarter turn
+    x = np.zeros((1, 1, 4))
+    x[0, 0] = [1, 2, 3, 4]
+    y = AO.rotate(x, np.array([[1]]), np.array([np.pi / 2, 0.0]))
+    assert np.allclose(y[0, 0], [-3, 2, 1, 4])
+    # one token: out is its value, lse its score; equal scores: the mean
+    c = {"k_codes": np.zeros((1, 1, 16, 16), np.uint8), "v_codes": np.zeros((1, 1, 1, 16, 16), np.uint8),
+         "k_scales": np.ones((1, 1), np.float32), "v_scales": np.full((1, 1), 0.5, np.float32)}
+    c = AO.append(c, np.full((2, 1, 16), 1.0), np.stack([np.full((1, 16), 2.0), np.full((1, 16), 4.0)]), [0, 2], [2],
+                  np.array([[0]]))
+    o, l, _ = AO.attention(c, np.full((2, 1, 16), 1.0), [0, 2], [2], np.array([[0]]), 0.25)
+    assert np.allclose(o[0], 2.0) and np.allclose(o[1], 3.0)
+    assert np.allclose(l[:, 0], [4.0, 4.0 + np.log(2)])
+    o, l, _ = AO.attention(c, np.full((3, 1, 16), 1.0), [0, 3], [2], np.array([[0]]), 0.25, window=1)
+    assert (o[0] == 0).all() and l[0, 0] == -np.inf and np.allclose(o[2], 4.0)
