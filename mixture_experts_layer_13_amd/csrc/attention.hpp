@@ -35,7 +35,8 @@ struct AttnArgs {
   const void* q;
   long long qs_t, qs_h;  // strides in elements
   int nH, G;             // query heads, query heads per KV head
-  float scale2;          // sm_scale * log2(e)
+  float scale2;          // |sm_scale| log2(e)
+  int neg;               // sm_scale < 0: the queries change sign
   int causal, window;
   void* out;             // [T][nH][D]
   float* lse;            // [T][nH] or NULL
@@ -106,6 +107,26 @@ __device__ __forceinline__ f32x4 mfma_split(const bf16x8 a, const bf16x8 b[NS], 
   return c;
 }
 
+// Over the four lanes l % 16, + 16, + 32, + 48 that share a query row.
+__device__ __forceinline__ float row_max(float v) {
+  typedef unsigned u32x2 __attribute__((ext_vector_type(2)));
+  u32x2 w = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  v = __builtin_fmaxf(__uint_as_float(w[0]), __uint_as_float(w[1]));
+  w = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return __builtin_fmaxf(__uint_as_float(w[0]), __uint_as_float(w[1]));
+}
+
+__device__ __forceinline__ float row_sum(float v) {
+  v += __shfl_xor(v, 16, 64);
+  return v + __shfl_xor(v, 32, 64);
+}
+
+// A running maximum is replaced only when a score passes it by this much (in
+// powers of two): until then probabilities are at most 2^8, which costs no
+// precision, and neither the maximum over lanes nor the accumulators' scaling
+// is needed.
+constexpr float kMaxSlack = 8.0f;
+
 // Page of the 16-token block at token t, clamped to one the cache has; whether
 // the block is seen (tokens [v.lo, v.hi)) and its page is in the cache.
 __device__ __forceinline__ bool attn_page(const AttnArgs& a, const int32_t* table, const View& v, int t, int& page) {
@@ -133,11 +154,16 @@ template <int NS>
 __device__ __forceinline__ void load_q8(const AttnArgs& a, size_t at, bool live, bf16x8 out[NS]) {
   if (NS == 1) {
     const i32x4 zero = {0, 0, 0, 0};
-    out[0] = as_bf16x8(live ? ld16(reinterpret_cast<const uint16_t*>(a.q) + at) : zero);
+    i32x4 w = live ? ld16(reinterpret_cast<const uint16_t*>(a.q) + at) : zero;
+    if (a.neg) w ^= i32x4{(int)0x80008000, (int)0x80008000, (int)0x80008000, (int)0x80008000};
+    out[0] = as_bf16x8(w);
   } else {
     float x[8];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) x[k] = live ? reinterpret_cast<const float*>(a.q)[at + k] : 0.0f;
+    for (int k = 0; k < 8; ++k) {
+      x[k] = live ? reinterpret_cast<const float*>(a.q)[at + k] : 0.0f;
+      if (a.neg) x[k] = -x[k];
+    }
     split_bf16<NS>(x, out);
   }
 }

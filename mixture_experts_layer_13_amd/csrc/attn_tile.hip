@@ -37,25 +37,29 @@ template <int DT>
 struct TileRaw {
   i32x4 k[DT / 64];
   i32x4 v[DT / 64];
+  float ks, vs;
+  bool gone;
 };
 
+// Two workgroups a CU where the registers allow it: the matrix work of one
+// covers the softmax of the other.
 template <int DT, int NS>
-__global__ __launch_bounds__(kTileThreads) void attn_tile_kernel(TileArgs ta) {
+__global__ __launch_bounds__(kTileThreads, DT <= 128 && NS == 1 ? 2 : 1) void attn_tile_kernel(TileArgs ta) {
   const AttnArgs& a = ta.a;
-  constexpr int KC = DT / 32;  // contraction steps of the first product
+  constexpr int KC = DT / 32;              // contraction steps of the first product
+  constexpr int FR = 4 * KC * 64;          // fragments (16 bytes a lane) of keys, and of values, in a tile
   extern __shared__ __align__(16) uint8_t smem[];
-  bf16x8* kf = reinterpret_cast<bf16x8*>(smem);  // [4 j][KC][64 lanes]
-  bf16x8* vf = kf + 4 * KC * 64;                 // [DT / 16][2][64 lanes]
+  bf16x8* frag = reinterpret_cast<bf16x8*>(smem);  // [2 buffers][keys [4 j][KC] | values [DT / 16][2]][64 lanes]
   __shared__ int scan[kTileWaves];
   __shared__ int found[2];
-  __shared__ float bks[4], bvs[4];
-  __shared__ int bgone[4];
+  __shared__ float bks[2][4], bvs[2][4];
+  __shared__ int bgone[2][4];
   const int lane = threadIdx.x & 63, m = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int h = blockIdx.y;
+  const int h = blockIdx.x % a.c.H;  // heads in turn: with eight, each XCD's L2 keeps one head's codes
 
   // the row block: later blocks, which see more tokens, first
-  const int unit = ta.units - 1 - (int)blockIdx.x;
+  const int unit = ta.units - 1 - (int)(blockIdx.x / a.c.H);
   if (threadIdx.x == 0) found[0] = -1;
   __syncthreads();
   int before = 0;
@@ -71,9 +75,9 @@ __global__ __launch_bounds__(kTileThreads) void attn_tile_kernel(TileArgs ta) {
     before += t;
   }
   __syncthreads();
-  const int b = found[0];
+  const int b = __builtin_amdgcn_readfirstlane(found[0]);
   if (b < 0) return;
-  const int row0 = found[1] * kTileRows;
+  const int row0 = __builtin_amdgcn_readfirstlane(found[1]) * kTileRows;
   const Seq s = load_seq(a.b, a.c.lS, b);
   const int rows = s.q * a.G - row0 < kTileRows ? s.q * a.G - row0 : kTileRows;
   const int i0 = row0 / a.G, i1 = (row0 + rows - 1) / a.G + 1;  // query tokens
@@ -107,14 +111,16 @@ __global__ __launch_bounds__(kTileThreads) void attn_tile_kernel(TileArgs ta) {
   const int all_lo = a.window > 0 ? s.kv - s.q + i1 - a.window : 0;  // tokens [all_lo, all_hi) every row sees
   const int all_hi = a.causal && s.kv - s.q + i0 + 1 < s.lim ? s.kv - s.q + i0 + 1 : s.lim;
 
+  // pages a tile ahead of codes, codes a tile ahead of fragments
+  int pk = 0, pv = 0;
+  bool okv = false;
+  auto pages = [&](int tile) {
+    attn_page(a, table, vw, tile * kAttnTile + 16 * (m >> 2), pk);
+    okv = attn_page(a, table, vw, tile * kAttnTile + 16 * g, pv);
+  };
   TileRaw<DT> raw;
-  float ks = 0.0f, vs = 0.0f;
-  bool gone = true;
   auto load = [&](int tile) {
     const int tk = tile * kAttnTile + 16 * (m >> 2), tv = tile * kAttnTile + 16 * g;
-    int pk, pv;
-    attn_page(a, table, vw, tk, pk);
-    gone = !attn_page(a, table, vw, tv, pv);
     const uint8_t* row = a.c.kc + ((((size_t)pk * a.c.H + h) << lS) + (tk & (S - 1)) + (m & 3) + 4 * wave) * D;
     const size_t at = (size_t)pv * a.c.H + h;
     const uint8_t* blk = a.c.vc + (at << lS) * D + (size_t)((tv & (S - 1)) * D + 16 * m);
@@ -124,21 +130,18 @@ __global__ __launch_bounds__(kTileThreads) void attn_tile_kernel(TileArgs ta) {
       raw.k[c] = ld16(row + (d < D ? d : 0));
       raw.v[c] = ld16(blk + (n < D ? 16 * n : 0));
     }
-    ks = a.c.ks[at];
-    vs = a.c.vs[at];
+    raw.ks = a.c.ks[at];
+    raw.vs = a.c.vs[at];
+    raw.gone = !okv;
   };
-
-  if (vw.n > 0) load(vw.t0);
-  for (int i = 0; i < vw.n; ++i) {
-    const int tile = vw.t0 + i, t0 = tile * kAttnTile;
-    {
-      const int skip = vw.lo - (t0 + 16 * g), n = gone ? 0 : vw.hi - (t0 + 16 * g);
-      if (skip > 0 || n < 16) {
+  auto store = [&](int tile, int buf) {
+    const int skip = vw.lo - (tile * kAttnTile + 16 * g), n = raw.gone ? 0 : vw.hi - (tile * kAttnTile + 16 * g);
+    if (skip > 0 || n < 16) {
 #pragma unroll
-        for (int c = 0; c < DT / 64; ++c) raw.v[c] = keep_bytes(raw.v[c], skip, n);
-      }
+      for (int c = 0; c < DT / 64; ++c) raw.v[c] = keep_bytes(raw.v[c], skip, n);
     }
-    __syncthreads();  // the last tile's operands are read
+    bf16x8* kf = frag + buf * 2 * FR;
+    bf16x8* vf = kf + FR;
 #pragma unroll
     for (int c = 0; c < DT / 64; ++c) {
       kf[(wave * KC + 2 * c) * 64 + lane] = codes_op(raw.k[c][0], raw.k[c][1]);
@@ -147,16 +150,27 @@ __global__ __launch_bounds__(kTileThreads) void attn_tile_kernel(TileArgs ta) {
       vf[((wave + 4 * c) * 2 + 1) * 64 + lane] = codes_op(raw.v[c][2], raw.v[c][3]);
     }
     if (wave == 0 && m == 0) {
-      bks[g] = ks;
-      bvs[g] = gone ? 0.0f : vs;
-      bgone[g] = gone;
+      bks[buf][g] = raw.gone ? 0.0f : raw.ks * a.scale2;
+      bvs[buf][g] = raw.gone ? 1.0f : raw.vs;
+      bgone[buf][g] = raw.gone;
+    }
+  };
+
+  if (vw.n > 0) {
+    pages(vw.t0);
+    load(vw.t0);
+    if (vw.n > 1) pages(vw.t0 + 1);
+    store(vw.t0, 0);
+    if (vw.n > 1) {
+      load(vw.t0 + 1);
+      if (vw.n > 2) pages(vw.t0 + 2);
     }
     __syncthreads();
-    if (i + 1 < vw.n) load(tile + 1);
-    const float f = bks[g] * a.scale2, fv = bvs[g];
-    const bool out = bgone[g] != 0;
-    const bool masked = t0 < all_lo || t0 + kAttnTile > all_hi || (bgone[0] | bgone[1] | bgone[2] | bgone[3]) != 0;
-
+  }
+  for (int i = 0; i < vw.n; ++i) {
+    const int tile = vw.t0 + i, t0 = tile * kAttnTile, buf = i & 1;
+    const bf16x8* kf = frag + buf * 2 * FR;
+    const bf16x8* vf = kf + FR;
     f32x4 sc[kTileRT][4];
 #pragma unroll
     for (int r = 0; r < kTileRT; ++r)
@@ -170,36 +184,62 @@ __global__ __launch_bounds__(kTileThreads) void attn_tile_kernel(TileArgs ta) {
 #pragma unroll
         for (int r = 0; r < kTileRT; ++r) sc[r][j] = mfma_split<NS>(k, q[r][c], sc[r][j]);
       }
+    const float f = bks[buf][g], fv = bvs[buf][g];
+    const bool out = bgone[buf][g] != 0;
+    const bool masked = t0 < all_lo || t0 + kAttnTile > all_hi || __any(out);
+    if (i + 1 < vw.n) {
+      store(tile + 1, buf ^ 1);
+      if (i + 2 < vw.n) {
+        load(tile + 2);
+        if (i + 3 < vw.n) pages(tile + 3);
+      }
+    }
+
+    float top[kTileRT];
+    bool grow = false;
+    if (masked) {
+      const int t = t0 + 16 * g;
+#pragma unroll
+      for (int r = 0; r < kTileRT; ++r)
+#pragma unroll
+        for (int k = 0; k < 16; ++k)
+          if (out || t + k < lo[r] || t + k >= hi[r]) sc[r][k >> 2][k & 3] = -__builtin_inff();
+    }
+#pragma unroll
+    for (int r = 0; r < kTileRT; ++r) {
+      float v = sc[r][0][0];
+#pragma unroll
+      for (int k = 1; k < 16; ++k) v = __builtin_fmaxf(v, sc[r][k >> 2][k & 3]);
+      top[r] = v == -__builtin_inff() ? v : v * f;
+      grow |= top[r] > mx[r] + kMaxSlack;
+    }
+    if (__any(grow)) {
+#pragma unroll
+      for (int r = 0; r < kTileRT; ++r) {
+        const float mn = __builtin_fmaxf(mx[r], row_max(top[r]));
+        const float keep = mn == -__builtin_inff() ? 1.0f : __builtin_amdgcn_exp2f(mx[r] - mn);
+        mx[r] = mn;
+        l[r] *= keep;
+#pragma unroll
+        for (int n = 0; n < DT / 16; ++n) o[r][n] *= keep;
+      }
+    }
+    // p vs = exp2(s f - m + log2 vs); the lane's tokens share f and vs, so
+    // dividing their sum by vs once gives the sum of p
+    const float lv = __builtin_amdgcn_logf(fv), rv = __builtin_amdgcn_exp2f(-lv);
     bf16x8 p[kTileRT][2][NS];
 #pragma unroll
     for (int r = 0; r < kTileRT; ++r) {
-      float x[16], top = -__builtin_inff();
-#pragma unroll
-      for (int k = 0; k < 16; ++k) x[k] = sc[r][k >> 2][k & 3] * f;
-      if (masked) {
-        const int t = t0 + 16 * g;
-#pragma unroll
-        for (int k = 0; k < 16; ++k)
-          if (out || t + k < lo[r] || t + k >= hi[r]) x[k] = -__builtin_inff();
-      }
-#pragma unroll
-      for (int k = 0; k < 16; ++k) top = __builtin_fmaxf(top, x[k]);
-      top = __builtin_fmaxf(top, __shfl_xor(top, 16, 64));
-      top = __builtin_fmaxf(top, __shfl_xor(top, 32, 64));
-      const float mn = __builtin_fmaxf(mx[r], top);
-      const float base = mn == -__builtin_inff() ? 0.0f : mn;
-      const float keep = __builtin_amdgcn_exp2f(mx[r] - base);
-      mx[r] = mn;
-      float sum = 0.0f;
+      const float c = lv - (mx[r] == -__builtin_inff() ? 0.0f : mx[r]);
+      float x[16], sum = 0.0f;
 #pragma unroll
       for (int k = 0; k < 16; ++k) {
-        x[k] = __builtin_amdgcn_exp2f(x[k] - base);
+        const float v = sc[r][k >> 2][k & 3];
+        x[k] = __builtin_amdgcn_exp2f(__builtin_fmaf(v, f, c));
+        if (masked) x[k] = v == -__builtin_inff() ? 0.0f : x[k];
         sum += x[k];
-        x[k] *= fv;
       }
-      l[r] = l[r] * keep + sum;
-#pragma unroll
-      for (int n = 0; n < DT / 16; ++n) o[r][n] *= keep;
+      l[r] += sum * rv;
       split_bf16<NS>(x, p[r][0]);
       split_bf16<NS>(x + 8, p[r][1]);
     }
@@ -211,12 +251,12 @@ __global__ __launch_bounds__(kTileThreads) void attn_tile_kernel(TileArgs ta) {
 #pragma unroll
         for (int r = 0; r < kTileRT; ++r) o[r][n] = mfma_split<NS>(v, p[r][c], o[r][n]);
       }
+    __syncthreads();  // this buffer may be written, the other one read
   }
 
 #pragma unroll
   for (int r = 0; r < kTileRT; ++r) {
-    float sum = l[r] + __shfl_xor(l[r], 16, 64);
-    sum += __shfl_xor(sum, 32, 64);
+    const float sum = row_sum(l[r]);
     const int row = row0 + (wave * kTileRT + r) * 16 + m, i = row / a.G;
     if (i >= s.q) continue;
     const size_t orow = (size_t)(s.q0 + i) * a.nH + h * a.G + row - i * a.G;
@@ -231,8 +271,8 @@ __global__ __launch_bounds__(kTileThreads) void attn_tile_kernel(TileArgs ta) {
 
 template <int DT, int NS>
 static int tile_launch(const TileArgs& t, hipStream_t st) {
-  const size_t lds = (size_t)kAttnTile * DT * 2 * 2;  // keys and values of a tile in bf16
-  if (lds > 65536 - 1024) {
+  const size_t lds = (size_t)kAttnTile * DT * 2 * 2 * 2;  // two tiles' keys and values in bf16
+  if (lds > 32768) {  // with the static part past 64 KB, or near it
     static OncePerDevice once;
     const int err = once.run([&] {
       return (int)hipFuncSetAttribute(reinterpret_cast<const void*>(attn_tile_kernel<DT, NS>),
@@ -240,7 +280,7 @@ static int tile_launch(const TileArgs& t, hipStream_t st) {
     });
     if (err) return err;
   }
-  hipLaunchKernelGGL((attn_tile_kernel<DT, NS>), dim3((unsigned)t.units, (unsigned)t.a.c.H), dim3(kTileThreads), lds, st, t);
+  hipLaunchKernelGGL((attn_tile_kernel<DT, NS>), dim3((unsigned)t.units * t.a.c.H), dim3(kTileThreads), lds, st, t);
   return (int)hipGetLastError();
 }
 

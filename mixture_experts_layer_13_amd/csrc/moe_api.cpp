@@ -723,7 +723,7 @@ moe_status attn_plan(const moe_kv_cache* c, int32_t T, int32_t B, int32_t n_head
   const bool all = p->dec_rows > 0;
   if (!all) p->dec_rows = moe::attn_decode_rows(c->head_dim, G);
   if (!all) p->tile_units = (long long)T * G / moe::attn_tile_rows() + (B < T ? B : T);
-  if (p->tile_units > (1LL << 30)) return fail(MOE_ERR_SHAPE, "T * n_heads too large");
+  if (p->tile_units * c->n_kv_heads > (1LL << 30)) return fail(MOE_ERR_SHAPE, "T * n_heads too large");
   if (p->dec_rows) {
     p->W = moe::kAttnGroups / c->n_kv_heads > 0 ? moe::kAttnGroups / c->n_kv_heads : 1;
     const size_t slots = (size_t)c->n_kv_heads * p->W * 2 * p->dec_rows;
@@ -823,7 +823,8 @@ moe_status moe_paged_attention(const moe_kv_cache* cache, const moe_kv_batch* ba
   a.qs_h = q_stride_h;
   a.nH = n_heads;
   a.G = n_heads / cache->n_kv_heads;
-  a.scale2 = sm_scale * moe::kLog2e;
+  a.scale2 = __builtin_fabsf(sm_scale) * moe::kLog2e;
+  a.neg = sm_scale < 0.0f;
   a.causal = causal ? 1 : 0;
   a.window = window;
   a.out = out;
