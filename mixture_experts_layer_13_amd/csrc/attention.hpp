@@ -43,6 +43,7 @@ struct AttnArgs {
   float* part_o;         // partial results of sequences that several workgroups share
   float* part_ml;
   int W;                 // workgroups per KV head
+  int rows;              // rows of a sequence, at most
 };
 
 // Tiles [t0, t0 + n) of tokens that some row of [row0, row0 + rows) of the
@@ -149,23 +150,70 @@ __device__ __forceinline__ i32x4 keep_bytes(i32x4 w, int skip, int n) {
   return w;
 }
 
-// Eight values of a query row as NS bf16 terms (zeros unless live).
-template <int NS>
-__device__ __forceinline__ void load_q8(const AttnArgs& a, size_t at, bool live, bf16x8 out[NS]) {
-  if (NS == 1) {
-    const i32x4 zero = {0, 0, 0, 0};
-    i32x4 w = live ? ld16(reinterpret_cast<const uint16_t*>(a.q) + at) : zero;
-    if (a.neg) w ^= i32x4{(int)0x80008000, (int)0x80008000, (int)0x80008000, (int)0x80008000};
-    out[0] = as_bf16x8(w);
-  } else {
-    float x[8];
+// A query row's DT / 4 values at d0 as KC B operands of NS bf16 terms each
+// (zeros where the row is not live, or past the head).  Every load is issued
+// before any value is used.
+template <int KC, int NS>
+__device__ __forceinline__ void load_q(const AttnArgs& a, size_t row, int d0, bool live, bf16x8 out[KC][NS]) {
+  constexpr int W = NS == 1 ? 1 : 2;  // 16-byte loads of eight values
+  i32x4 raw[KC][W];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      x[k] = live ? reinterpret_cast<const float*>(a.q)[at + k] : 0.0f;
-      if (a.neg) x[k] = -x[k];
-    }
-    split_bf16<NS>(x, out);
+  for (int c = 0; c < KC; ++c) {
+    const size_t at = row + (d0 + 8 * c < a.c.D ? d0 + 8 * c : 0);
+#pragma unroll
+    for (int k = 0; k < W; ++k)
+      raw[c][k] = NS == 1 ? ld16(reinterpret_cast<const uint16_t*>(a.q) + at)
+                          : ld16(reinterpret_cast<const float*>(a.q) + at + 4 * k);
   }
+  const int sign = a.neg ? (NS == 1 ? (int)0x80008000 : (int)0x80000000) : 0;
+#pragma unroll
+  for (int c = 0; c < KC; ++c) {
+    const bool use = live && d0 + 8 * c < a.c.D;
+#pragma unroll
+    for (int k = 0; k < W; ++k)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) raw[c][k][j] = use ? raw[c][k][j] ^ sign : 0;
+    if (NS == 1) {
+      out[c][0] = as_bf16x8(raw[c][0]);
+    } else {
+      float x[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) x[j] = __int_as_float(raw[c][j >> 2][j & 3]);
+      split_bf16<NS>(x, out[c]);
+    }
+  }
+}
+
+// The largest scaled score of a lane's 16 tokens t.. of one row; masked: those
+// outside [lo, hi), or all if gone, become -infinity first.
+__device__ __forceinline__ float attn_top(f32x4 sc[4], bool masked, bool gone, int t, int lo, int hi, float f) {
+  if (masked) {
+#pragma unroll
+    for (int k = 0; k < 16; ++k)
+      if (gone || t + k < lo || t + k >= hi) sc[k >> 2][k & 3] = -__builtin_inff();
+  }
+  float v = sc[0][0];
+#pragma unroll
+  for (int k = 1; k < 16; ++k) v = __builtin_fmaxf(v, sc[k >> 2][k & 3]);
+  return v == -__builtin_inff() ? v : v * f;
+}
+
+// p vs = exp2(s f - m + log2 vs) of a lane's 16 tokens, as operands; returns
+// their sum.  The lane's tokens lie in one page, so f and vs are the lane's,
+// and dividing the sum by vs once gives the sum of p.  c = log2 vs - m.
+template <int NS>
+__device__ __forceinline__ float attn_probs(const f32x4 sc[4], bool masked, float f, float c, bf16x8 p[2][NS]) {
+  float x[16], sum = 0.0f;
+#pragma unroll
+  for (int k = 0; k < 16; ++k) {
+    const float v = sc[k >> 2][k & 3];
+    x[k] = __builtin_amdgcn_exp2f(__builtin_fmaf(v, f, c));
+    if (masked) x[k] = v == -__builtin_inff() ? 0.0f : x[k];
+    sum += x[k];
+  }
+  split_bf16<NS>(x, p[0]);
+  split_bf16<NS>(x + 8, p[1]);
+  return sum;
 }
 
 // One row's finished output: o sums, their maximum m (base 2) and sum l.

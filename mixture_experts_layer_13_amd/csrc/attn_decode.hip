@@ -10,7 +10,9 @@
 // and accumulators, operands straight from memory (attention.hpp: no LDS, no
 // transposition); they are joined through LDS at the end of a sequence.  A
 // sequence that lies in one run is finished there; the others leave a part
-// per workgroup, which attn_join_kernel joins.
+// per workgroup, which attn_join_kernel joins.  Where the table cannot hold
+// more than kDecOwn tokens a sequence, each has a workgroup of its own
+// instead: no search, no parts, one launch.
 #include "attention.hpp"
 #include "launch.hpp"
 
@@ -19,6 +21,7 @@ namespace moe {
 constexpr int kDecThreads = 256;
 constexpr int kDecWaves = kDecThreads / 64;
 constexpr int kDecMinTiles = kDecWaves;  // a shorter run would leave waves idle
+constexpr int kDecOwn = 1024;            // tokens
 
 // Tiles of sequence b that this kernel works on (0: none, or another kernel's).
 __device__ __forceinline__ int dec_tiles(const AttnArgs& a, int rows_max, int b) {
@@ -41,19 +44,31 @@ struct DecTile {
   bool gone;  // the page of the lane's tokens is not in the cache
 };
 
-// Loads the lane's part of a tile.  Every load is unconditional, from an
+// The lane's part of a tile: its pages (read a tile ahead), then its codes.  Every load is unconditional, from an
 // address clamped into the cache: what a lane must not use (blocks no row
 // sees, pages outside the cache) it hides afterwards, keys by their scores,
 // values by zeros, since a zero probability times a NaN code would be NaN.
+struct DecPages {
+  int k, v;  // pages of the lane's key rows and of its own 16 tokens
+  bool gone;
+};
+
+__device__ __forceinline__ DecPages dec_pages(const AttnArgs& a, const int32_t* table, const View& vw, int tile) {
+  const int lane = threadIdx.x & 63;
+  DecPages p;
+  attn_page(a, table, vw, tile * kAttnTile + 16 * ((lane & 15) >> 2), p.k);
+  p.gone = !attn_page(a, table, vw, tile * kAttnTile + 16 * (lane >> 4), p.v);
+  return p;
+}
+
 template <int DT>
-__device__ __forceinline__ void dec_load(const AttnArgs& a, const int32_t* table, const View& vw, int tile, int h,
+__device__ __forceinline__ void dec_load(const AttnArgs& a, const DecPages& pg, const View& vw, int tile, int h,
                                          DecTile<DT>& r) {
   const int lane = threadIdx.x & 63, m = lane & 15, g = lane >> 4;
   const int D = a.c.D, lS = a.c.lS, S = 1 << lS;
   const int tk = tile * kAttnTile + 16 * (m >> 2), tv = tile * kAttnTile + 16 * g;  // first tokens of the lane's blocks
-  int pk, pv;
-  attn_page(a, table, vw, tk, pk);
-  r.gone = !attn_page(a, table, vw, tv, pv);
+  const int pk = pg.k, pv = pg.v;
+  r.gone = pg.gone;
   {
     const size_t page = ((size_t)pk * a.c.H + h) << lS;
     const uint8_t* row = a.c.kc + (page + (tk & (S - 1)) + (m & 3)) * D;
@@ -75,7 +90,6 @@ __device__ __forceinline__ void dec_load(const AttnArgs& a, const int32_t* table
   if (skip > 0 || n < 16) {
 #pragma unroll
     for (int i = 0; i < DT / 16; ++i) r.v[i] = keep_bytes(r.v[i], skip, n);
-    if (r.gone) r.vs = 0.0f;
   }
 }
 
@@ -85,22 +99,22 @@ struct DecState {
   f32x4 o[NR][DT / 16];
   float m[NR], l[NR];
   int lo[NR], hi[NR];  // tokens that the lane's row sees
+  int all_lo, all_hi;  // tokens that every row sees
 };
 
 // Rows of the sequence into the B operand of the first product.
 template <int DT, int NR, int NS>
 __device__ __forceinline__ void dec_begin(const AttnArgs& a, const Seq& s, int h, DecState<DT, NR, NS>& st) {
   const int lane = threadIdx.x & 63, g = lane >> 4;
+  const int p0 = s.kv - s.q;
+  st.all_lo = a.window > 0 ? s.kv - a.window : 0;
+  st.all_hi = a.causal && p0 + 1 < s.lim ? p0 + 1 : s.lim;
 #pragma unroll
   for (int r = 0; r < NR; ++r) {
     const int row = 16 * r + (lane & 15), i = row / a.G, hd = h * a.G + row - i * a.G;
     const bool live = i < s.q;
     const size_t at = (size_t)(s.q0 + (live ? i : 0)) * a.qs_t + (size_t)(live ? hd : 0) * a.qs_h;
-#pragma unroll
-    for (int c = 0; c < DT / 32; ++c) {
-      const int d = g * (DT / 4) + 8 * c;
-      load_q8<NS>(a, at + d, live && d < a.c.D, st.q[r][c]);
-    }
+    load_q<DT / 32, NS>(a, at, g * (DT / 4), live, st.q[r]);
 #pragma unroll
     for (int n = 0; n < DT / 16; ++n) st.o[r][n] = f32x4{0, 0, 0, 0};
     st.m[r] = -__builtin_inff();
@@ -112,7 +126,7 @@ __device__ __forceinline__ void dec_begin(const AttnArgs& a, const Seq& s, int h
 }
 
 template <int DT, int NR, int NS>
-__device__ __forceinline__ void dec_tile(const AttnArgs& a, const View& vw, int tile, const DecTile<DT>& t,
+__device__ __forceinline__ void dec_tile(const AttnArgs& a, int tile, const DecTile<DT>& t,
                                          DecState<DT, NR, NS>& st) {
   const int lane = threadIdx.x & 63, g = lane >> 4;
   f32x4 s[NR][4];
@@ -128,37 +142,32 @@ __device__ __forceinline__ void dec_tile(const AttnArgs& a, const View& vw, int 
 #pragma unroll
       for (int r = 0; r < NR; ++r) s[r][j] = mfma_split<NS>(k, st.q[r][c], s[r][j]);
     }
-  const int t0 = tile * kAttnTile + 16 * g;
-  const float f = t.ks * a.scale2;
-  bf16x8 p[NR][2][NS];
+  const int t0 = tile * kAttnTile;
+  const bool masked = t0 < st.all_lo || t0 + kAttnTile > st.all_hi || __any(t.gone);
+  const float f = t.gone ? 0.0f : t.ks * a.scale2, fv = t.gone ? 1.0f : t.vs;
+  float top[NR];
+  bool grow = false;
 #pragma unroll
   for (int r = 0; r < NR; ++r) {
-    float x[16], top = -__builtin_inff();
-#pragma unroll
-    for (int k = 0; k < 16; ++k) {
-      x[k] = s[r][k >> 2][k & 3] * f;
-      if (t.gone || t0 + k < st.lo[r] || t0 + k >= st.hi[r]) x[k] = -__builtin_inff();
-      top = __builtin_fmaxf(top, x[k]);
-    }
-    top = __builtin_fmaxf(top, __shfl_xor(top, 16, 64));
-    top = __builtin_fmaxf(top, __shfl_xor(top, 32, 64));
-    const float m = __builtin_fmaxf(st.m[r], top);
-    const float base = m == -__builtin_inff() ? 0.0f : m;
-    const float keep = __builtin_amdgcn_exp2f(st.m[r] - base);
-    st.m[r] = m;
-    float sum = 0.0f;
-#pragma unroll
-    for (int k = 0; k < 16; ++k) {
-      x[k] = __builtin_amdgcn_exp2f(x[k] - base);
-      sum += x[k];
-      x[k] *= t.vs;
-    }
-    st.l[r] = st.l[r] * keep + sum;
-#pragma unroll
-    for (int n = 0; n < DT / 16; ++n) st.o[r][n] *= keep;
-    split_bf16<NS>(x, p[r][0]);
-    split_bf16<NS>(x + 8, p[r][1]);
+    top[r] = attn_top(s[r], masked, t.gone, t0 + 16 * g, st.lo[r], st.hi[r], f);
+    grow |= top[r] > st.m[r] + kMaxSlack;
   }
+  if (__any(grow)) {
+#pragma unroll
+    for (int r = 0; r < NR; ++r) {
+      const float m = __builtin_fmaxf(st.m[r], row_max(top[r]));
+      const float keep = m == -__builtin_inff() ? 1.0f : __builtin_amdgcn_exp2f(st.m[r] - m);
+      st.m[r] = m;
+      st.l[r] *= keep;
+#pragma unroll
+      for (int n = 0; n < DT / 16; ++n) st.o[r][n] *= keep;
+    }
+  }
+  const float lv = __builtin_amdgcn_logf(fv), rv = __builtin_amdgcn_exp2f(-lv);
+  bf16x8 p[NR][2][NS];
+#pragma unroll
+  for (int r = 0; r < NR; ++r)
+    st.l[r] += rv * attn_probs<NS>(s[r], masked, f, lv - (st.m[r] == -__builtin_inff() ? 0.0f : st.m[r]), p[r]);
 #pragma unroll
   for (int n = 0; n < DT / 16; ++n)
 #pragma unroll
@@ -175,10 +184,11 @@ __device__ __forceinline__ size_t part_slot(const AttnArgs& a, int h, int w, int
   return ((size_t)h * a.W + w) * 2 + late;
 }
 
-template <int DT, int NR, int NS>
+// OWN: blockIdx.x is the sequence, which also writes rows that see nothing.
+template <int DT, int NR, int NS, bool OWN>
 __global__ __launch_bounds__(kDecThreads) void attn_decode_kernel(AttnArgs a) {
   constexpr int ROWS = 16 * NR, LD = DT + 4;
-  __shared__ float jo[kDecWaves][16][LD];
+  __shared__ __align__(16) float jo[kDecWaves][16][LD];
   __shared__ float jm[kDecWaves][16], jl[kDecWaves][16];
   __shared__ int scan[kDecWaves];
   __shared__ int found[2];
@@ -186,57 +196,62 @@ __global__ __launch_bounds__(kDecThreads) void attn_decode_kernel(AttnArgs a) {
   const int w = blockIdx.x, h = blockIdx.y;
 
   // the run [begin, end) of this workgroup and the sequence it starts in
-  long long total = 0;
-  for (int base = 0; base < a.b.B; base += kDecThreads) {
-    const int b = base + threadIdx.x;
-    int t;
-    block_scan<kDecThreads>(b < a.b.B ? dec_tiles(a, ROWS, b) : 0, scan, &t);
-    total += t;
-  }
-  const long long run = dec_run(total, a.W);
-  const long long begin = (long long)w * run;
-  if (begin >= total) return;
-  long long end = begin + run;
-  if (end > total) end = total;
-  long long before = 0;
-  for (int base = 0; base < a.b.B && before <= begin; base += kDecThreads) {
-    const int b = base + threadIdx.x;
-    const int n = b < a.b.B ? dec_tiles(a, ROWS, b) : 0;
-    int t;
-    const long long e = before + block_scan<kDecThreads>(n, scan, &t);
-    if (begin >= e - n && begin < e) {
-      found[0] = b;
-      found[1] = (int)(begin - (e - n));
+  int b = w, skip = 0;
+  long long left = 1LL << 40;
+  if (!OWN) {
+    long long total = 0, begin = 0, before = 0;
+    int n = 0, e = 0, t;
+    for (int base = 0; base < a.b.B; base += kDecThreads) {
+      n = base + (int)threadIdx.x < a.b.B ? dec_tiles(a, ROWS, base + threadIdx.x) : 0;
+      e = block_scan<kDecThreads>(n, scan, &t);
+      total += t;
     }
-    before += t;
+    const long long run = dec_run(total, a.W);
+    begin = w * run;
+    if (begin >= total) return;
+    left = total - begin < run ? total - begin : run;
+    for (int base = 0; base < a.b.B && before <= begin; base += kDecThreads) {
+      if (a.b.B > kDecThreads) {  // else the one scan above
+        n = base + (int)threadIdx.x < a.b.B ? dec_tiles(a, ROWS, base + threadIdx.x) : 0;
+        e = block_scan<kDecThreads>(n, scan, &t);
+      }
+      if (begin >= before + e - n && begin < before + e) {
+        found[0] = base + threadIdx.x;
+        found[1] = (int)(begin - (before + e - n));
+      }
+      before += t;
+    }
+    __syncthreads();
+    b = __builtin_amdgcn_readfirstlane(found[0]);
+    skip = __builtin_amdgcn_readfirstlane(found[1]);
   }
-  __syncthreads();
-  int b = found[0], skip = found[1];
-  long long left = end - begin;
 
   while (left > 0 && b < a.b.B) {
     const Seq s = load_seq(a.b, a.c.lS, b);
-    const int n = dec_tiles(a, ROWS, b);
-    if (n == 0) {
+    const View vw = view_of(a, s, 0, s.q);
+    const bool mine = s.q > 0 && s.q <= ROWS / a.G;
+    const int n = mine ? vw.n : 0;
+    if (OWN ? !mine : n == 0) {
+      if (OWN) return;
       ++b;
       continue;
     }
-    const View vw = view_of(a, s, 0, s.q);
     const int count = n - skip < left ? n - skip : (int)left;
     const int32_t* table = a.b.table + (size_t)b * a.b.max_pages;
     DecState<DT, NR, NS> st;
     dec_begin<DT, NR, NS>(a, s, h, st);
+    const int first = vw.t0 + skip;
+    DecPages pages = dec_pages(a, table, vw, first + wave);
     for (int i = wave; i < count; i += kDecWaves) {
       DecTile<DT> t;
-      const int tile = vw.t0 + skip + i;
-      dec_load<DT>(a, table, vw, tile, h, t);
-      dec_tile<DT, NR, NS>(a, vw, tile, t, st);
+      dec_load<DT>(a, pages, vw, first + i, h, t);
+      pages = dec_pages(a, table, vw, first + i + kDecWaves);
+      dec_tile<DT, NR, NS>(a, first + i, t, st);
     }
     const bool whole = skip == 0 && count == n;
 #pragma unroll
     for (int r = 0; r < NR; ++r) {
-      float l = st.l[r] + __shfl_xor(st.l[r], 16, 64);
-      l += __shfl_xor(l, 32, 64);
+      const float l = row_sum(st.l[r]);
       __syncthreads();  // the last join is read
 #pragma unroll
       for (int k = 0; k < DT / 16; ++k)
@@ -279,6 +294,7 @@ __global__ __launch_bounds__(kDecThreads) void attn_decode_kernel(AttnArgs a) {
         }
       }
     }
+    if (OWN) return;
     left -= count;
     skip = 0;
     ++b;
@@ -286,64 +302,102 @@ __global__ __launch_bounds__(kDecThreads) void attn_decode_kernel(AttnArgs a) {
 }
 
 // Joins the parts of a sequence that several workgroups shared, and writes the
-// rows of a sequence that sees nothing: zero, with lse -inf.
-template <int DT, int NR, int NS>
+// rows of a sequence that sees nothing: zero, with lse -inf.  One workgroup
+// per row: its lanes first find the parts' common maximum, then groups of
+// DT / 4 lanes add up every ... th part, and LDS joins the groups.
+template <int DT, int ROWS, int NS>
 __global__ __launch_bounds__(kDecThreads) void attn_join_kernel(AttnArgs a) {
-  constexpr int ROWS = 16 * NR;
+  constexpr int LANES = DT / 4, GROUPS = kDecThreads / LANES;
   __shared__ int scan[kDecWaves];
-  const int b = blockIdx.x, h = blockIdx.y;
+  __shared__ int base[1];
+  __shared__ float weight[kAttnGroups];
+  __shared__ float red[kDecWaves];
+  __shared__ float4 acc[GROUPS][LANES];
+  const int b = blockIdx.x, h = blockIdx.y, row = blockIdx.z;
   const Seq s = load_seq(a.b, a.c.lS, b);
-  if (s.q <= 0 || s.q > ROWS / a.G) return;
+  if (s.q <= 0 || s.q > ROWS / a.G || row >= s.q * a.G) return;
   const int n = view_of(a, s, 0, s.q).n;
   long long total = 0, at = 0;
-  for (int base = 0; base < a.b.B; base += kDecThreads) {
-    const int i = base + threadIdx.x;
+  for (int i0 = 0; i0 < a.b.B; i0 += kDecThreads) {
+    const int i = i0 + threadIdx.x;
     const int v = i < a.b.B ? dec_tiles(a, ROWS, i) : 0;
     int t;
-    block_scan<kDecThreads>(v, scan, &t);
+    const int e = block_scan<kDecThreads>(v, scan, &t);
+    if (i == b) base[0] = e - v;
+    if (b >= i0 && b < i0 + kDecThreads) {
+      __syncthreads();
+      at = total + base[0];
+    }
     total += t;
-    block_scan<kDecThreads>(i < b ? v : 0, scan, &t);
-    at += t;
   }
   const long long run = dec_run(total, a.W);
-  const int w0 = (int)(at / run), w1 = n > 0 ? (int)((at + n - 1) / run) : w0;
-  if (n > 0 && w0 == w1) return;  // finished by its workgroup
-  const int rows = s.q * a.G;
-  for (int i = threadIdx.x; i < rows * (a.c.D / 4); i += kDecThreads) {
-    const int row = i / (a.c.D / 4), d = 4 * (i - row * (a.c.D / 4));
-    float m = -__builtin_inff(), l = 0.0f, o[4] = {0, 0, 0, 0};
-    if (n > 0) {
-      for (int w = w0; w <= w1; ++w) {
-        const float2 ml = *reinterpret_cast<const float2*>(
-            a.part_ml + (part_slot(a, h, w, w == w0) * ROWS + row) * 2);
-        m = __builtin_fmaxf(m, ml.x);
-      }
-      const float base = m == -__builtin_inff() ? 0.0f : m;
-      for (int w = w0; w <= w1; ++w) {
-        const size_t r = part_slot(a, h, w, w == w0) * ROWS + row;
-        const float2 ml = *reinterpret_cast<const float2*>(a.part_ml + r * 2);
-        const float f = __builtin_amdgcn_exp2f(ml.x - base);
-        const float4 v = *reinterpret_cast<const float4*>(a.part_o + r * DT + d);
-        l += f * ml.y;
-        o[0] += f * v.x;
-        o[1] += f * v.y;
-        o[2] += f * v.z;
-        o[3] += f * v.w;
-      }
-    }
-    const int qi = row / a.G;
-    const size_t orow = (size_t)(s.q0 + qi) * a.nH + h * a.G + row - qi * a.G;
-    attn_store4<NS>(a, orow, d, o, l);
-    if (d == 0 && a.lse) a.lse[orow] = attn_lse(m, l);
+  const int w0 = (int)(at / run), parts = n > 0 ? (int)((at + n - 1) / run) - w0 + 1 : 0;
+  if (parts == 1) return;  // finished by its workgroup
+  const size_t slot = (size_t)h * a.W + w0;
+  // part k: slot 1 (begins the sequence) of workgroup w0, slot 0 of the later ones
+  auto part = [&](int k) { return ((slot + k) * 2 + (k == 0 ? 1 : 0)) * ROWS + row; };
+
+  float m = -__builtin_inff();
+  for (int k = threadIdx.x; k < parts; k += kDecThreads) m = __builtin_fmaxf(m, a.part_ml[part(k) * 2]);
+  m = wave_max(m);
+  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = m;
+  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < kDecWaves; ++k) m = __builtin_fmaxf(m, red[k]);
+  const float mm = m == -__builtin_inff() ? 0.0f : m;
+  float l = 0.0f;
+  for (int k = threadIdx.x; k < parts; k += kDecThreads) {
+    const float f = __builtin_amdgcn_exp2f(a.part_ml[part(k) * 2] - mm);
+    weight[k] = f;
+    l += f * a.part_ml[part(k) * 2 + 1];
   }
+  l = wave_sum(l);
+  __syncthreads();  // weights written, maxima read
+  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = l;
+  const int lane = threadIdx.x % LANES, group = threadIdx.x / LANES;
+  float4 o = make_float4(0, 0, 0, 0);
+#pragma unroll 4
+  for (int k = group; k < parts; k += GROUPS) {
+    const float f = weight[k];
+    const float4 v = *reinterpret_cast<const float4*>(a.part_o + part(k) * DT + 4 * lane);
+    o.x += f * v.x;
+    o.y += f * v.y;
+    o.z += f * v.z;
+    o.w += f * v.w;
+  }
+  acc[group][lane] = o;
+  __syncthreads();
+  if (group != 0 || 4 * lane >= a.c.D) return;
+  l = 0.0f;
+#pragma unroll
+  for (int k = 0; k < kDecWaves; ++k) l += red[k];
+  float r[4] = {0, 0, 0, 0};
+  for (int k = 0; k < GROUPS; ++k) {
+    const float4 v = acc[k][lane];
+    r[0] += v.x;
+    r[1] += v.y;
+    r[2] += v.z;
+    r[3] += v.w;
+  }
+  const int qi = row / a.G;
+  const size_t orow = (size_t)(s.q0 + qi) * a.nH + h * a.G + row - qi * a.G;
+  attn_store4<NS>(a, orow, 4 * lane, r, l);
+  if (lane == 0 && a.lse) a.lse[orow] = attn_lse(m, l);
 }
 
 template <int DT, int NR, int NS>
 static int dec_launch(const AttnArgs& a, hipStream_t st) {
-  hipLaunchKernelGGL((attn_decode_kernel<DT, NR, NS>), dim3((unsigned)a.W, (unsigned)a.c.H), dim3(kDecThreads), 0, st, a);
+  const dim3 block(kDecThreads);
+  if (((long long)a.b.max_pages << a.c.lS) <= kDecOwn) {
+    hipLaunchKernelGGL((attn_decode_kernel<DT, NR, NS, true>), dim3((unsigned)a.b.B, (unsigned)a.c.H), block, 0, st, a);
+    return (int)hipGetLastError();
+  }
+  hipLaunchKernelGGL((attn_decode_kernel<DT, NR, NS, false>), dim3((unsigned)a.W, (unsigned)a.c.H), block, 0, st, a);
   const int err = (int)hipGetLastError();
   if (err) return err;
-  hipLaunchKernelGGL((attn_join_kernel<DT, NR, NS>), dim3((unsigned)a.b.B, (unsigned)a.c.H), dim3(kDecThreads), 0, st, a);
+  const int rows = 16 * NR < a.rows ? 16 * NR : a.rows;  // of a sequence, at most
+  hipLaunchKernelGGL((attn_join_kernel<DT, 16 * NR, NS>), dim3((unsigned)a.b.B, (unsigned)a.c.H, (unsigned)rows), block,
+                     0, st, a);
   return (int)hipGetLastError();
 }
 

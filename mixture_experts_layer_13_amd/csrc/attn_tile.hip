@@ -95,11 +95,7 @@ __global__ __launch_bounds__(kTileThreads, DT <= 128 && NS == 1 ? 2 : 1) void at
     const int row = row0 + (wave * kTileRT + r) * 16 + m, i = row / a.G, hd = h * a.G + row - i * a.G;
     const bool live = i < s.q;
     const size_t at = (size_t)(s.q0 + (live ? i : 0)) * a.qs_t + (size_t)(live ? hd : 0) * a.qs_h;
-#pragma unroll
-    for (int c = 0; c < KC; ++c) {
-      const int d = g * (DT / 4) + 8 * c;
-      load_q8<NS>(a, at + d, live && d < D, q[r][c]);
-    }
+    load_q<KC, NS>(a, at, g * (DT / 4), live, q[r]);
 #pragma unroll
     for (int n = 0; n < DT / 16; ++n) o[r][n] = f32x4{0, 0, 0, 0};
     mx[r] = -__builtin_inff();
@@ -197,20 +193,9 @@ __global__ __launch_bounds__(kTileThreads, DT <= 128 && NS == 1 ? 2 : 1) void at
 
     float top[kTileRT];
     bool grow = false;
-    if (masked) {
-      const int t = t0 + 16 * g;
-#pragma unroll
-      for (int r = 0; r < kTileRT; ++r)
-#pragma unroll
-        for (int k = 0; k < 16; ++k)
-          if (out || t + k < lo[r] || t + k >= hi[r]) sc[r][k >> 2][k & 3] = -__builtin_inff();
-    }
 #pragma unroll
     for (int r = 0; r < kTileRT; ++r) {
-      float v = sc[r][0][0];
-#pragma unroll
-      for (int k = 1; k < 16; ++k) v = __builtin_fmaxf(v, sc[r][k >> 2][k & 3]);
-      top[r] = v == -__builtin_inff() ? v : v * f;
+      top[r] = attn_top(sc[r], masked, out, t0 + 16 * g, lo[r], hi[r], f);
       grow |= top[r] > mx[r] + kMaxSlack;
     }
     if (__any(grow)) {
@@ -224,25 +209,11 @@ __global__ __launch_bounds__(kTileThreads, DT <= 128 && NS == 1 ? 2 : 1) void at
         for (int n = 0; n < DT / 16; ++n) o[r][n] *= keep;
       }
     }
-    // p vs = exp2(s f - m + log2 vs); the lane's tokens share f and vs, so
-    // dividing their sum by vs once gives the sum of p
     const float lv = __builtin_amdgcn_logf(fv), rv = __builtin_amdgcn_exp2f(-lv);
     bf16x8 p[kTileRT][2][NS];
 #pragma unroll
-    for (int r = 0; r < kTileRT; ++r) {
-      const float c = lv - (mx[r] == -__builtin_inff() ? 0.0f : mx[r]);
-      float x[16], sum = 0.0f;
-#pragma unroll
-      for (int k = 0; k < 16; ++k) {
-        const float v = sc[r][k >> 2][k & 3];
-        x[k] = __builtin_amdgcn_exp2f(__builtin_fmaf(v, f, c));
-        if (masked) x[k] = v == -__builtin_inff() ? 0.0f : x[k];
-        sum += x[k];
-      }
-      l[r] += sum * rv;
-      split_bf16<NS>(x, p[r][0]);
-      split_bf16<NS>(x + 8, p[r][1]);
-    }
+    for (int r = 0; r < kTileRT; ++r)
+      l[r] += rv * attn_probs<NS>(sc[r], masked, f, lv - (mx[r] == -__builtin_inff() ? 0.0f : mx[r]), p[r]);
 #pragma unroll
     for (int n = 0; n < DT / 16; ++n)
 #pragma unroll

@@ -706,7 +706,7 @@ moe::BatchArgs batch_args(const moe_kv_batch* b) {
 // dec_rows rows (0: none) with W workgroups per KV head, the tile kernel the
 // others (tile_units row blocks at most; 0: there are none).
 struct AttnPlan {
-  int dec_rows, W;
+  int dec_rows, W, rows;
   long long tile_units;
   size_t part_ml, bytes;
 };
@@ -719,6 +719,7 @@ moe_status attn_plan(const moe_kv_cache* c, int32_t T, int32_t B, int32_t n_head
   const int G = n_heads / c->n_kv_heads;
   const long long rows = (long long)(max_q < T ? max_q : T) * G;
   *p = AttnPlan{};
+  p->rows = (int)(rows < (1 << 30) ? rows : 1 << 30);
   p->dec_rows = rows <= 64 ? moe::attn_decode_rows(c->head_dim, (int)rows) : 0;
   const bool all = p->dec_rows > 0;
   if (!all) p->dec_rows = moe::attn_decode_rows(c->head_dim, G);
@@ -833,6 +834,7 @@ moe_status moe_paged_attention(const moe_kv_cache* cache, const moe_kv_batch* ba
     a.part_o = reinterpret_cast<float*>(workspace);
     a.part_ml = reinterpret_cast<float*>((char*)workspace + p.part_ml);
     a.W = p.W;
+    a.rows = p.rows;
     const int err = moe::launch_attn_decode(a, p.dec_rows, q_dtype == MOE_F32, (hipStream_t)stream);
     if (err) return hip_status(err, "attention launch");
   }

@@ -258,39 +258,50 @@ def moe_rope_quantize_per_head(x, positions, inv_freq, interleaved=False, invers
     return codes, scales
 
 
-def _require(ok, status, detail):
-    if not ok:
-        raise MoEError(status, detail)
+_VALUE_CODES = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16}
 
 
 def _index(t, shape, name, device):
-    """A dense int32 index buffer of this shape (None: any size) on `device`."""
-    _require(t.dtype == torch.int32, MOE_ERR_DTYPE, f"{name} must be int32")
-    _require(t.dim() == len(shape) and all(n is None or n == m for n, m in zip(shape, t.shape)), MOE_ERR_SHAPE,
-             f"{name} has shape {tuple(t.shape)}")
-    _require(t.is_contiguous(), MOE_ERR_UNSUPPORTED, f"{name} must be contiguous")
-    _require(t.device == device, MOE_ERR_UNSUPPORTED, f"{name} is on {t.device}, not on {device}")
+    """Address of a dense int32 index buffer of this shape (None: any size) on `device`."""
+    if t.dtype != torch.int32:
+        raise MoEError(MOE_ERR_DTYPE, f"{name} must be int32")
+    if t.dim() != len(shape) or any(n is not None and n != m for n, m in zip(shape, t.shape)):
+        raise MoEError(MOE_ERR_SHAPE, f"{name} has shape {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise MoEError(MOE_ERR_UNSUPPORTED, f"{name} must be contiguous")
+    if t.device != device:
+        raise MoEError(MOE_ERR_UNSUPPORTED, f"{name} is on {t.device}, not on {device}")
+    return t.data_ptr()
 
 
 def _heads(t, shape, name, device):
-    """A [tokens, heads, head_dim] tensor of this shape on `device`, heads contiguous; its two strides."""
-    _require(t.dtype in (torch.bfloat16, torch.float32), MOE_ERR_DTYPE, f"{name} must be bf16 or f32")
-    _require(tuple(t.shape) == tuple(shape), MOE_ERR_SHAPE, f"{name} has shape {tuple(t.shape)}, not {tuple(shape)}")
-    _require(t.stride(2) == 1, MOE_ERR_UNSUPPORTED, f"{name}: the values of a head must be contiguous")
-    _require(t.device == device, MOE_ERR_UNSUPPORTED, f"{name} is on {t.device}, not on {device}")
+    """(address, dtype code, token stride, head stride) of a [tokens, heads,
+    head_dim] tensor of this shape on `device`, the values of a head contiguous."""
+    code = _VALUE_CODES.get(t.dtype)
+    if code is None:
+        raise MoEError(MOE_ERR_DTYPE, f"{name} must be bf16 or f32, not {t.dtype}")
+    if t.shape != shape:
+        raise MoEError(MOE_ERR_SHAPE, f"{name} has shape {tuple(t.shape)}, not {tuple(shape)}")
+    st, sh, sd = t.stride()
+    if sd != 1:
+        raise MoEError(MOE_ERR_UNSUPPORTED, f"{name}: the values of a head must be contiguous")
+    if t.device != device:
+        raise MoEError(MOE_ERR_UNSUPPORTED, f"{name} is on {t.device}, not on {device}")
     # the strides of a dimension of size one are torch's to choose
-    st = t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2]
-    return st, t.stride(1) if t.shape[1] > 1 else t.shape[2]
+    return t.data_ptr(), code, st if shape[0] > 1 else shape[1] * shape[2], sh if shape[1] > 1 else shape[2]
 
 
-def _run(device, stream, call):
-    """call(stream handle) with `device` current."""
-    _require(device.type == "cuda", MOE_ERR_UNSUPPORTED, f"tensors are on {device}, not on a GPU")
-    if device.index == torch.cuda.current_device():
-        _check(call(_stream(stream)))
-    else:
+def _run(device, stream, call, *args):
+    """call(*args, stream handle) with `device` current."""
+    if device.type != "cuda":
+        raise MoEError(MOE_ERR_UNSUPPORTED, f"tensors are on {device}, not on a GPU")
+    if device.index != torch._C._cuda_getDevice():
         with torch.cuda.device(device):
-            _check(call(_stream(stream)))
+            return _run(device, stream, call, *args)
+    handle = torch._C._cuda_getCurrentRawStream(device.index) if stream is None else stream.cuda_stream
+    status = call(*args, handle)
+    if status != MOE_OK:
+        _check(status)
 
 
 def _made(shape, dtype, device, stream):
@@ -309,35 +320,43 @@ class Rotation:
 
     def __init__(self, positions, inv_freq, pair_axis=None, interleaved=False, inverse=False):
         dev = inv_freq.device
-        _require(inv_freq.dtype == torch.float32, MOE_ERR_DTYPE, "inv_freq must be f32")
-        _require(inv_freq.dim() == 1 and inv_freq.is_contiguous(), MOE_ERR_SHAPE, "inv_freq must be a dense vector")
-        axes, self.tokens = 1, None
+        if inv_freq.dtype != torch.float32:
+            raise MoEError(MOE_ERR_DTYPE, "inv_freq must be f32")
+        if inv_freq.dim() != 1 or not inv_freq.is_contiguous():
+            raise MoEError(MOE_ERR_SHAPE, "inv_freq must be a dense vector")
+        half = inv_freq.shape[0]
+        axes, at, self.tokens = 1, None, None
         if positions is not None:
-            _index(positions, (None,) * positions.dim(), "positions", dev)
-            _require(positions.dim() in (1, 2), MOE_ERR_SHAPE, "positions must be [T] or [axes, T]")
-            axes = positions.shape[0] if positions.dim() == 2 else 1
+            dims = positions.dim()
+            if dims not in (1, 2):
+                raise MoEError(MOE_ERR_SHAPE, "positions must be [T] or [axes, T]")
+            at = _index(positions, (None,) * dims, "positions", dev)
+            axes = positions.shape[0] if dims == 2 else 1
             self.tokens = positions.shape[-1]
-        if pair_axis is not None:
-            _index(pair_axis, (inv_freq.numel(),), "pair_axis", dev)
+        axis_at = None if pair_axis is None else _index(pair_axis, (half,), "pair_axis", dev)
         self.positions, self.inv_freq, self.pair_axis, self.device = positions, inv_freq, pair_axis, dev
-        self.struct = moe_rotation(_ptr(positions), _ptr(pair_axis), _ptr(inv_freq), axes, 2 * inv_freq.numel(),
-                                   int(bool(interleaved)), int(bool(inverse)))
+        self.struct = moe_rotation(at, axis_at, inv_freq.data_ptr(), axes, 2 * half, 1 if interleaved else 0,
+                                   1 if inverse else 0)
 
     def _for(self, T, device):
-        _require(self.tokens is None or self.tokens == T, MOE_ERR_SHAPE, f"positions of {self.tokens} tokens for {T}")
-        _require(self.device == device, MOE_ERR_UNSUPPORTED, f"the rotation is on {self.device}, not on {device}")
+        if self.tokens is not None and self.tokens != T:
+            raise MoEError(MOE_ERR_SHAPE, f"positions of {self.tokens} tokens for {T}")
+        if self.device != device:
+            raise MoEError(MOE_ERR_UNSUPPORTED, f"the rotation is on {self.device}, not on {device}")
         return ctypes.byref(self.struct)
 
 
 def moe_rope_axes(x, rotation, out=None, out_dtype=None, stream=None):
     """x [T, nH, D] bf16/f32, heads contiguous -> x rotated (out may be x)."""
-    T, nH, D = x.shape
+    shape, dev = x.shape, x.device
+    if len(shape) != 3:
+        raise MoEError(MOE_ERR_SHAPE, f"x has shape {tuple(shape)}, not [T, heads, head_dim]")
+    T, nH, D = shape
     if out is None:
-        out = _made((T, nH, D), out_dtype or x.dtype, x.device, stream)
-    xs, os = _heads(x, (T, nH, D), "x", x.device), _heads(out, (T, nH, D), "out", x.device)
-    rot = rotation._for(T, x.device)
-    _run(x.device, stream, lambda s: lib().moe_rope_axes(_ptr(x), dtype_code(x.dtype), *xs, rot, T, nH, D, _ptr(out),
-                                                         dtype_code(out.dtype), *os, s))
+        out = _made(shape, out_dtype or x.dtype, dev, stream)
+    xp, xc, xt, xh = _heads(x, shape, "x", dev)
+    op, oc, ot, oh = _heads(out, shape, "out", dev)
+    _run(dev, stream, lib().moe_rope_axes, xp, xc, xt, xh, rotation._for(T, dev), T, nH, D, op, oc, ot, oh)
     return out
 
 
@@ -347,27 +366,32 @@ class PagedKV:
     16] (float8_e4m3fn or uint8), k_scales and v_scales f32 [pages, H]."""
 
     def __init__(self, k_codes, v_codes, k_scales, v_scales):
-        _require(k_codes.dim() == 4, MOE_ERR_SHAPE, "k_codes must be [pages, heads, page_size, head_dim]")
+        if k_codes.dim() != 4:
+            raise MoEError(MOE_ERR_SHAPE, "k_codes must be [pages, heads, page_size, head_dim]")
         P, H, S, D = k_codes.shape
         for t, shape, name in ((k_codes, (P, H, S, D), "k_codes"), (v_codes, (P, H, S // 16, D, 16), "v_codes"),
                                (k_scales, (P, H), "k_scales"), (v_scales, (P, H), "v_scales")):
-            _require(t.dtype in ((torch.float8_e4m3fn, torch.uint8) if "codes" in name else (torch.float32,)),
-                     MOE_ERR_DTYPE, f"{name} has dtype {t.dtype}")
-            _require(tuple(t.shape) == shape, MOE_ERR_SHAPE, f"{name} has shape {tuple(t.shape)}, not {shape}")
-            _require(t.is_contiguous(), MOE_ERR_UNSUPPORTED, f"{name} must be contiguous")
-            _require(t.device == k_codes.device, MOE_ERR_UNSUPPORTED, f"{name} is on {t.device}")
+            if t.dtype not in ((torch.float8_e4m3fn, torch.uint8) if "codes" in name else (torch.float32,)):
+                raise MoEError(MOE_ERR_DTYPE, f"{name} has dtype {t.dtype}")
+            if t.shape != shape:
+                raise MoEError(MOE_ERR_SHAPE, f"{name} has shape {tuple(t.shape)}, not {shape}")
+            if not t.is_contiguous():
+                raise MoEError(MOE_ERR_UNSUPPORTED, f"{name} must be contiguous")
+            if t.device != k_codes.device:
+                raise MoEError(MOE_ERR_UNSUPPORTED, f"{name} is on {t.device}, not on {k_codes.device}")
         self.k_codes, self.v_codes, self.k_scales, self.v_scales = k_codes, v_codes, k_scales, v_scales
         self.num_pages, self.n_kv_heads, self.page_size, self.head_dim = P, H, S, D
         self.device = k_codes.device
-        self.struct = moe_kv_cache(_ptr(k_codes), _ptr(v_codes), _ptr(k_scales), _ptr(v_scales), P, S, H, D)
+        self.struct = moe_kv_cache(k_codes.data_ptr(), v_codes.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr(),
+                                   P, S, H, D)
 
     def _batch(self, T, kv_lens, block_table, cu_q):
-        _index(kv_lens, (None,), "kv_lens", self.device)
+        dev = self.device
+        lens = _index(kv_lens, (None,), "kv_lens", dev)
         B = kv_lens.shape[0]
-        _index(block_table, (B, None), "block_table", self.device)
-        if cu_q is not None:
-            _index(cu_q, (B + 1,), "cu_q", self.device)
-        return moe_kv_batch(_ptr(cu_q), _ptr(kv_lens), _ptr(block_table), B, T, block_table.shape[1])
+        table = _index(block_table, (B, None), "block_table", dev)
+        cu = None if cu_q is None else _index(cu_q, (B + 1,), "cu_q", dev)
+        return moe_kv_batch(cu, lens, table, B, T, block_table.shape[1])
 
 
 def alloc_kv_cache(num_pages, page_size, n_kv_heads, head_dim, device="cuda"):
@@ -382,15 +406,16 @@ def moe_kv_append(cache, k, v, kv_lens, block_table, rotation=None, cu_q=None, s
     """k, v [T, H, D] bf16/f32 into the cache, k rotated first; kv_lens int32
     [B] (these rows included), block_table int32 [B, max_pages], cu_q int32
     [B + 1] or None (one row per sequence)."""
-    T = k.shape[0]
+    T, dev = k.shape[0], cache.device
     shape = (T, cache.n_kv_heads, cache.head_dim)
-    ks, vs = _heads(k, shape, "k", cache.device), _heads(v, shape, "v", cache.device)
-    _require(k.dtype == v.dtype, MOE_ERR_DTYPE, f"k is {k.dtype}, v is {v.dtype}")
+    kp, kc, kt, kh = _heads(k, shape, "k", dev)
+    vp, vc, vt, vh = _heads(v, shape, "v", dev)
+    if kc != vc:
+        raise MoEError(MOE_ERR_DTYPE, f"k is {k.dtype}, v is {v.dtype}")
     batch = cache._batch(T, kv_lens, block_table, cu_q)
-    rot = None if rotation is None else rotation._for(T, cache.device)
-    _run(cache.device, stream,
-         lambda s: lib().moe_kv_append(ctypes.byref(cache.struct), ctypes.byref(batch), _ptr(k), *ks, _ptr(v), *vs,
-                                       dtype_code(k.dtype), rot, s))
+    rot = None if rotation is None else rotation._for(T, dev)
+    _run(dev, stream, lib().moe_kv_append, ctypes.byref(cache.struct), ctypes.byref(batch), kp, kt, kh, vp, vt, vh,
+         kc, rot)
 
 
 def moe_paged_attention_workspace_size(cache, T, B, n_heads, max_q=1):
@@ -405,32 +430,33 @@ def moe_paged_attention(cache, q, kv_lens, block_table, cu_q=None, max_q=1, sm_s
     """q [T, nH, D] bf16/f32 (rotated) over the cache -> out [T, nH, D], and
     with return_lse (or lse given) the log sums lse f32 [T, nH].  max_q: at
     least the rows of every sequence.  sm_scale None: 1 / sqrt(D)."""
-    T, nH, D = q.shape
-    dev = cache.device
-    qs = _heads(q, (T, nH, cache.head_dim), "q", dev)
+    shape, dev = q.shape, cache.device
+    if len(shape) != 3 or shape[2] != cache.head_dim:
+        raise MoEError(MOE_ERR_SHAPE, f"q has shape {tuple(shape)}, not [T, heads, {cache.head_dim}]")
+    T, nH, D = shape
+    qp, qc, qt, qh = _heads(q, shape, "q", dev)
     batch = cache._batch(T, kv_lens, block_table, cu_q)
     if out is None:
-        out = _made((T, nH, D), q.dtype, dev, stream)
-    _require(out.dtype == q.dtype, MOE_ERR_DTYPE, f"out is {out.dtype}, q is {q.dtype}")
-    _heads(out, (T, nH, D), "out", dev)
-    _require(out.is_contiguous(), MOE_ERR_UNSUPPORTED, "out must be contiguous")
-    if lse is None and return_lse:
-        lse = _made((T, nH), torch.float32, dev, stream)
-    if lse is not None:
-        _require(lse.dtype == torch.float32, MOE_ERR_DTYPE, "lse must be f32")
-        _require(tuple(lse.shape) == (T, nH) and lse.is_contiguous() and lse.device == dev, MOE_ERR_SHAPE,
-                 "lse must be a dense [T, n_heads] on the cache's device")
+        out = _made(shape, q.dtype, dev, stream)
+    elif out.dtype != q.dtype:
+        raise MoEError(MOE_ERR_DTYPE, f"out is {out.dtype}, q is {q.dtype}")
+    elif out.shape != shape or not out.is_contiguous() or out.device != dev:
+        raise MoEError(MOE_ERR_SHAPE, f"out must be a dense {tuple(shape)} on the cache's device")
+    if lse is None:
+        if return_lse:
+            lse = _made((T, nH), torch.float32, dev, stream)
+    elif lse.dtype != torch.float32:
+        raise MoEError(MOE_ERR_DTYPE, "lse must be f32")
+    elif lse.shape != (T, nH) or not lse.is_contiguous() or lse.device != dev:
+        raise MoEError(MOE_ERR_SHAPE, f"lse must be a dense {(T, nH)} on the cache's device")
     if workspace is None:
         workspace = _made(max(moe_paged_attention_workspace_size(cache, T, batch.B, nH, max_q), 16), torch.uint8, dev,
                           stream)
-    _require(workspace.is_contiguous() and workspace.device == dev, MOE_ERR_WORKSPACE,
-             "the workspace must be dense and on the cache's device")
-    scale = D ** -0.5 if sm_scale is None else sm_scale
-    _run(dev, stream,
-         lambda s: lib().moe_paged_attention(ctypes.byref(cache.struct), ctypes.byref(batch), _ptr(q),
-                                             dtype_code(q.dtype), *qs, nH, max_q, scale, int(bool(causal)), window,
-                                             _ptr(out), _ptr(lse), _ptr(workspace),
-                                             workspace.numel() * workspace.element_size(), s))
+    elif not workspace.is_contiguous() or workspace.device != dev:
+        raise MoEError(MOE_ERR_WORKSPACE, "the workspace must be dense and on the cache's device")
+    _run(dev, stream, lib().moe_paged_attention, ctypes.byref(cache.struct), ctypes.byref(batch), qp, qc, qt, qh, nH,
+         max_q, D ** -0.5 if sm_scale is None else sm_scale, 1 if causal else 0, window, out.data_ptr(),
+         None if lse is None else lse.data_ptr(), workspace.data_ptr(), workspace.nbytes)
     return out if lse is None else (out, lse)
 
 
