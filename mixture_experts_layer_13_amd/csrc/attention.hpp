@@ -9,20 +9,27 @@
 // (its sum l is taken from the unrounded fp32 values).  fp32 queries are the
 // sum of three bf16 terms, and so is p: 24 bits, three MFMAs in place of one.
 //
-// Operand layout.  The first product is computed transposed, S^T = K Q^T:
-// MFMA tile j of four takes as its row m the token 16 (m / 4) + 4 j + m % 4
-// of a 64-token tile.  Of the result, lane l then holds tokens
-// 16 (l / 16) + 4 j + i (i = 0..3, j = 0..3) of query l % 16: sixteen
-// consecutive tokens, and as the B operand of O^T = V^T P^T they are exactly
-// the lane's contraction indices when A is a 16-byte load of value codes
-// (paged.hpp).  So probabilities never leave their lane, and neither operand
-// of either product needs a transposition.  The D values of a key are split
-// over the four lane groups in contiguous quarters.
+// Operand layout.  The first product is computed transposed, S^T = K Q^T, and
+// the tokens of a 64-token tile are dealt to the rows of its MFMA tiles so
+// that the result leaves every lane with runs of 16 consecutive tokens of one
+// query row: they are exactly the lane's contraction indices as the B operand
+// of O^T = V^T P^T when A is a 16-byte load of value codes (paged.hpp).  So
+// probabilities never leave their lane, and neither operand of either product
+// needs a transposition.
+//   16x16x32 (few rows): tile j of four has as its row m the token
+//   16 (m / 4) + 4 j + m % 4; lane l gets tokens 16 (l / 16) + 4 j + i
+//   (i = 0..3) of query l % 16.
+//   32x32x16 (many rows): tile j of two has as its row m the token
+//   32 (m / 4 % 2) + 16 j + 4 (m / 8) + m % 4; lane l gets tokens
+//   32 (l / 32) + 16 j + i (i = 0..15) of query l % 32.
+// The D values of a key are split over the lane groups in contiguous parts.
 #pragma once
 
 #include "paged.hpp"
 
 namespace moe {
+
+typedef float f32x16 __attribute__((ext_vector_type(16)));
 
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kLn2 = 0.69314718055994530942f;
@@ -107,19 +114,43 @@ __device__ __forceinline__ f32x4 mfma_split(const bf16x8 a, const bf16x8 b[NS], 
   for (int k = NS - 1; k >= 0; --k) c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b[k], c, 0, 0, 0);
   return c;
 }
-
-// Over the four lanes l % 16, + 16, + 32, + 48 that share a query row.
-__device__ __forceinline__ float row_max(float v) {
-  typedef unsigned u32x2 __attribute__((ext_vector_type(2)));
-  u32x2 w = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
-  v = __builtin_fmaxf(__uint_as_float(w[0]), __uint_as_float(w[1]));
-  w = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
-  return __builtin_fmaxf(__uint_as_float(w[0]), __uint_as_float(w[1]));
+template <int NS>
+__device__ __forceinline__ f32x16 mfma_split(const bf16x8 a, const bf16x8 b[NS], f32x16 c) {
+#pragma unroll
+  for (int k = NS - 1; k >= 0; --k) c = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b[k], c, 0, 0, 0);
+  return c;
 }
 
-__device__ __forceinline__ float row_sum(float v) {
-  v += __shfl_xor(v, 16, 64);
-  return v + __shfl_xor(v, 32, 64);
+// Scale of a page's scores; at least the smallest normal number, so that a
+// hidden score, -infinity, stays that.
+__device__ __forceinline__ float score_scale(const AttnArgs& a, float ks) {
+  return __builtin_fmaxf(ks * a.scale2, 0x1p-126f);
+}
+
+// Over lanes l and l ^ 16, and l and l ^ 32 (gfx950 swaps rows and halves of
+// two registers in one instruction each, without LDS).
+typedef unsigned u32x2 __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ u32x2 swap16(float v) {
+  return __builtin_bit_cast(u32x2, __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false));
+}
+__device__ __forceinline__ u32x2 swap32(float v) {
+  return __builtin_bit_cast(u32x2, __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false));
+}
+__device__ __forceinline__ float max16(float v) {
+  const u32x2 w = swap16(v);
+  return __builtin_fmaxf(__uint_as_float(w[0]), __uint_as_float(w[1]));
+}
+__device__ __forceinline__ float max32(float v) {
+  const u32x2 w = swap32(v);
+  return __builtin_fmaxf(__uint_as_float(w[0]), __uint_as_float(w[1]));
+}
+__device__ __forceinline__ float sum16(float v) {
+  const u32x2 w = swap16(v);
+  return __uint_as_float(w[0]) + __uint_as_float(w[1]);
+}
+__device__ __forceinline__ float sum32(float v) {
+  const u32x2 w = swap32(v);
+  return __uint_as_float(w[0]) + __uint_as_float(w[1]);
 }
 
 // A running maximum is replaced only when a score passes it by this much (in
@@ -185,30 +216,29 @@ __device__ __forceinline__ void load_q(const AttnArgs& a, size_t row, int d0, bo
 }
 
 // The largest scaled score of a lane's 16 tokens t.. of one row; masked: those
-// outside [lo, hi), or all if gone, become -infinity first.
-__device__ __forceinline__ float attn_top(f32x4 sc[4], bool masked, bool gone, int t, int lo, int hi, float f) {
+// outside [lo, hi), or all if gone, become -infinity first.  f > 0.
+__device__ __forceinline__ float attn_top(f32x16& sc, bool masked, bool gone, int t, int lo, int hi, float f) {
   if (masked) {
+    const int off = t - lo;
+    const unsigned n = gone || hi <= lo ? 0u : (unsigned)(hi - lo);
 #pragma unroll
-    for (int k = 0; k < 16; ++k)
-      if (gone || t + k < lo || t + k >= hi) sc[k >> 2][k & 3] = -__builtin_inff();
+    for (int k = 0; k < 16; ++k) sc[k] = (unsigned)(off + k) < n ? sc[k] : -__builtin_inff();
   }
-  float v = sc[0][0];
+  float v = sc[0];
 #pragma unroll
-  for (int k = 1; k < 16; ++k) v = __builtin_fmaxf(v, sc[k >> 2][k & 3]);
-  return v == -__builtin_inff() ? v : v * f;
+  for (int k = 1; k < 16; ++k) v = __builtin_fmaxf(v, sc[k]);
+  return v * f;
 }
 
 // p vs = exp2(s f - m + log2 vs) of a lane's 16 tokens, as operands; returns
 // their sum.  The lane's tokens lie in one page, so f and vs are the lane's,
 // and dividing the sum by vs once gives the sum of p.  c = log2 vs - m.
 template <int NS>
-__device__ __forceinline__ float attn_probs(const f32x4 sc[4], bool masked, float f, float c, bf16x8 p[2][NS]) {
+__device__ __forceinline__ float attn_probs(const f32x16& sc, float f, float c, bf16x8 p[2][NS]) {
   float x[16], sum = 0.0f;
 #pragma unroll
   for (int k = 0; k < 16; ++k) {
-    const float v = sc[k >> 2][k & 3];
-    x[k] = __builtin_amdgcn_exp2f(__builtin_fmaf(v, f, c));
-    if (masked) x[k] = v == -__builtin_inff() ? 0.0f : x[k];
+    x[k] = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[k], f, c));
     sum += x[k];
   }
   split_bf16<NS>(x, p[0]);

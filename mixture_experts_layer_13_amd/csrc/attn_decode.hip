@@ -129,22 +129,26 @@ template <int DT, int NR, int NS>
 __device__ __forceinline__ void dec_tile(const AttnArgs& a, int tile, const DecTile<DT>& t,
                                          DecState<DT, NR, NS>& st) {
   const int lane = threadIdx.x & 63, g = lane >> 4;
-  f32x4 s[NR][4];
+  f32x16 s[NR];
 #pragma unroll
-  for (int r = 0; r < NR; ++r)
+  for (int j = 0; j < 4; ++j) {
+    f32x4 x[NR];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) s[r][j] = f32x4{0, 0, 0, 0};
-#pragma unroll
-  for (int j = 0; j < 4; ++j)
+    for (int r = 0; r < NR; ++r) x[r] = f32x4{0, 0, 0, 0};
 #pragma unroll
     for (int c = 0; c < DT / 32; ++c) {
       const bf16x8 k = codes_op(t.k[j][c >> 1][2 * (c & 1)], t.k[j][c >> 1][2 * (c & 1) + 1]);
 #pragma unroll
-      for (int r = 0; r < NR; ++r) s[r][j] = mfma_split<NS>(k, st.q[r][c], s[r][j]);
+      for (int r = 0; r < NR; ++r) x[r] = mfma_split<NS>(k, st.q[r][c], x[r]);
     }
+#pragma unroll
+    for (int r = 0; r < NR; ++r)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) s[r][4 * j + i] = x[r][i];
+  }
   const int t0 = tile * kAttnTile;
   const bool masked = t0 < st.all_lo || t0 + kAttnTile > st.all_hi || __any(t.gone);
-  const float f = t.gone ? 0.0f : t.ks * a.scale2, fv = t.gone ? 1.0f : t.vs;
+  const float f = t.gone ? 1.0f : score_scale(a, t.ks), fv = t.gone ? 1.0f : t.vs;
   float top[NR];
   bool grow = false;
 #pragma unroll
@@ -155,7 +159,7 @@ __device__ __forceinline__ void dec_tile(const AttnArgs& a, int tile, const DecT
   if (__any(grow)) {
 #pragma unroll
     for (int r = 0; r < NR; ++r) {
-      const float m = __builtin_fmaxf(st.m[r], row_max(top[r]));
+      const float m = __builtin_fmaxf(st.m[r], max32(max16(top[r])));
       const float keep = m == -__builtin_inff() ? 1.0f : __builtin_amdgcn_exp2f(st.m[r] - m);
       st.m[r] = m;
       st.l[r] *= keep;
@@ -167,7 +171,7 @@ __device__ __forceinline__ void dec_tile(const AttnArgs& a, int tile, const DecT
   bf16x8 p[NR][2][NS];
 #pragma unroll
   for (int r = 0; r < NR; ++r)
-    st.l[r] += rv * attn_probs<NS>(s[r], masked, f, lv - (st.m[r] == -__builtin_inff() ? 0.0f : st.m[r]), p[r]);
+    st.l[r] += rv * attn_probs<NS>(s[r], f, lv - (st.m[r] == -__builtin_inff() ? 0.0f : st.m[r]), p[r]);
 #pragma unroll
   for (int n = 0; n < DT / 16; ++n)
 #pragma unroll
@@ -251,7 +255,7 @@ __global__ __launch_bounds__(kDecThreads) void attn_decode_kernel(AttnArgs a) {
     const bool whole = skip == 0 && count == n;
 #pragma unroll
     for (int r = 0; r < NR; ++r) {
-      const float l = row_sum(st.l[r]);
+      const float l = sum32(sum16(st.l[r]));
       __syncthreads();  // the last join is read
 #pragma unroll
       for (int k = 0; k < DT / 16; ++k)

@@ -16,8 +16,7 @@ namespace moe {
 
 constexpr int kTileThreads = 256;
 constexpr int kTileWaves = kTileThreads / 64;
-constexpr int kTileRT = 2;                               // 16-row tiles of a wave
-constexpr int kTileRows = 16 * kTileRT * kTileWaves;     // rows of a workgroup
+constexpr int kTileRows = 32 * kTileWaves;  // rows of a workgroup
 
 struct TileArgs {
   AttnArgs a;
@@ -31,8 +30,9 @@ __device__ __forceinline__ int tile_blocks(const TileArgs& t, int b) {
   return rows <= t.rows_below ? 0 : (int)((rows + kTileRows - 1) / kTileRows);
 }
 
-// A thread's raw codes of one tile: keys as S^T tile j = wave, values as
-// channels 16 (wave + 4 i) + m.
+// A thread's raw codes of one tile.  With j = wave % 2: of keys, 32 bytes of
+// its row of MFMA tile j; of values, channels 32 (wave / 2 + 2 i) + l % 32 of
+// the 16 tokens of block 2 (l / 32) + j.
 template <int DT>
 struct TileRaw {
   i32x4 k[DT / 64];
@@ -46,15 +46,15 @@ struct TileRaw {
 template <int DT, int NS>
 __global__ __launch_bounds__(kTileThreads, DT <= 128 && NS == 1 ? 2 : 1) void attn_tile_kernel(TileArgs ta) {
   const AttnArgs& a = ta.a;
-  constexpr int KC = DT / 32;              // contraction steps of the first product
-  constexpr int FR = 4 * KC * 64;          // fragments (16 bytes a lane) of keys, and of values, in a tile
+  constexpr int KC = DT / 16;          // contraction steps of the first product
+  constexpr int FR = 2 * KC * 64;      // fragments (16 bytes a lane) of keys, and of values, in a tile
   extern __shared__ __align__(16) uint8_t smem[];
-  bf16x8* frag = reinterpret_cast<bf16x8*>(smem);  // [2 buffers][keys [4 j][KC] | values [DT / 16][2]][64 lanes]
+  bf16x8* frag = reinterpret_cast<bf16x8*>(smem);  // [2 buffers][keys [2 j][KC] | values [DT / 32][4]][64 lanes]
   __shared__ int scan[kTileWaves];
   __shared__ int found[2];
   __shared__ float bks[2][4], bvs[2][4];
   __shared__ int bgone[2][4];
-  const int lane = threadIdx.x & 63, m = lane & 15, g = lane >> 4;
+  const int lane = threadIdx.x & 63, m = lane & 31, g = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int h = blockIdx.x % a.c.H;  // heads in turn: with eight, each XCD's L2 keeps one head's codes
 
@@ -85,70 +85,76 @@ __global__ __launch_bounds__(kTileThreads, DT <= 128 && NS == 1 ? 2 : 1) void at
   const int32_t* table = a.b.table + (size_t)b * a.b.max_pages;
   const int D = a.c.D, lS = a.c.lS, S = 1 << lS;
 
-  // queries, and what each row sees
-  bf16x8 q[kTileRT][KC][NS];
-  f32x4 o[kTileRT][DT / 16];
-  float mx[kTileRT], l[kTileRT];
-  int lo[kTileRT], hi[kTileRT];
+  // queries, and what the lane's row sees
+  bf16x8 q[KC][NS];
+  f32x16 o[DT / 32];
+  float mx = -__builtin_inff(), l = 0.0f;
+  const int row = row0 + wave * 32 + m, qi = row / a.G, hd = h * a.G + row - qi * a.G;
+  const bool live = qi < s.q;
+  load_q<KC, NS>(a, (size_t)(s.q0 + (live ? qi : 0)) * a.qs_t + (size_t)(live ? hd : 0) * a.qs_h, g * (DT / 2), live, q);
 #pragma unroll
-  for (int r = 0; r < kTileRT; ++r) {
-    const int row = row0 + (wave * kTileRT + r) * 16 + m, i = row / a.G, hd = h * a.G + row - i * a.G;
-    const bool live = i < s.q;
-    const size_t at = (size_t)(s.q0 + (live ? i : 0)) * a.qs_t + (size_t)(live ? hd : 0) * a.qs_h;
-    load_q<KC, NS>(a, at, g * (DT / 4), live, q[r]);
+  for (int n = 0; n < DT / 32; ++n)
 #pragma unroll
-    for (int n = 0; n < DT / 16; ++n) o[r][n] = f32x4{0, 0, 0, 0};
-    mx[r] = -__builtin_inff();
-    l[r] = 0.0f;
-    const int p = s.kv - s.q + i;
-    hi[r] = !live ? 0 : (a.causal && p + 1 < s.lim ? p + 1 : s.lim);
-    lo[r] = a.window > 0 ? p - a.window + 1 : 0;
-  }
-  const int all_lo = a.window > 0 ? s.kv - s.q + i1 - a.window : 0;  // tokens [all_lo, all_hi) every row sees
-  const int all_hi = a.causal && s.kv - s.q + i0 + 1 < s.lim ? s.kv - s.q + i0 + 1 : s.lim;
+    for (int k = 0; k < 16; ++k) o[n][k] = 0.0f;
+  const int p0 = s.kv - s.q;
+  const int hi = !live ? 0 : (a.causal && p0 + qi + 1 < s.lim ? p0 + qi + 1 : s.lim);
+  const int lo = a.window > 0 ? p0 + qi - a.window + 1 : 0;
+  const int all_lo = a.window > 0 ? p0 + i1 - a.window : 0;  // tokens [all_lo, all_hi) every row sees
+  const int all_hi = a.causal && p0 + i0 + 1 < s.lim ? p0 + i0 + 1 : s.lim;
 
   // pages a tile ahead of codes, codes a tile ahead of fragments
+  const int j = wave & 1, bk = 16 * (2 * ((m >> 2) & 1) + j), bv = 16 * (2 * g + j);  // first tokens of the blocks
+  const size_t page_bytes = (size_t)a.c.H * D << lS;
+  const uint8_t* kbase = a.c.kc + (((size_t)h << lS) + 4 * (m >> 3) + (m & 3)) * D;
+  const uint8_t* vbase = a.c.vc + ((size_t)h << lS) * D;
+  int koff[DT / 64], voff[DT / 64];
+#pragma unroll
+  for (int c = 0; c < DT / 64; ++c) {
+    const int d = g * (DT / 2) + (wave >> 1) * (DT / 4) + 16 * c, n = 32 * ((wave >> 1) + 2 * c) + m;
+    koff[c] = d < D ? d : 0;
+    voff[c] = n < D ? 16 * n : 0;
+  }
   int pk = 0, pv = 0;
   bool okv = false;
   auto pages = [&](int tile) {
-    attn_page(a, table, vw, tile * kAttnTile + 16 * (m >> 2), pk);
-    okv = attn_page(a, table, vw, tile * kAttnTile + 16 * g, pv);
+    attn_page(a, table, vw, tile * kAttnTile + bk, pk);
+    okv = attn_page(a, table, vw, tile * kAttnTile + bv, pv);
   };
   TileRaw<DT> raw;
   auto load = [&](int tile) {
-    const int tk = tile * kAttnTile + 16 * (m >> 2), tv = tile * kAttnTile + 16 * g;
-    const uint8_t* row = a.c.kc + ((((size_t)pk * a.c.H + h) << lS) + (tk & (S - 1)) + (m & 3) + 4 * wave) * D;
-    const size_t at = (size_t)pv * a.c.H + h;
-    const uint8_t* blk = a.c.vc + (at << lS) * D + (size_t)((tv & (S - 1)) * D + 16 * m);
+    const int t0 = tile * kAttnTile;
+    const uint8_t* kp = kbase + (size_t)pk * page_bytes + ((t0 + bk) & (S - 1)) * D;
+    const uint8_t* vp = vbase + (size_t)pv * page_bytes + ((t0 + bv) & (S - 1)) * D;
 #pragma unroll
     for (int c = 0; c < DT / 64; ++c) {
-      const int d = g * (DT / 4) + 16 * c, n = 16 * (wave + 4 * c);
-      raw.k[c] = ld16(row + (d < D ? d : 0));
-      raw.v[c] = ld16(blk + (n < D ? 16 * n : 0));
+      raw.k[c] = ld16(kp + koff[c]);
+      raw.v[c] = ld16(vp + voff[c]);
     }
+    const size_t at = (size_t)pv * a.c.H + h;
     raw.ks = a.c.ks[at];
     raw.vs = a.c.vs[at];
     raw.gone = !okv;
   };
   auto store = [&](int tile, int buf) {
-    const int skip = vw.lo - (tile * kAttnTile + 16 * g), n = raw.gone ? 0 : vw.hi - (tile * kAttnTile + 16 * g);
-    if (skip > 0 || n < 16) {
+    const int t0 = tile * kAttnTile;
+    if (t0 < vw.lo || t0 + kAttnTile > vw.hi || __any(raw.gone)) {
+      const int skip = vw.lo - (t0 + bv), n = raw.gone ? 0 : vw.hi - (t0 + bv);
 #pragma unroll
       for (int c = 0; c < DT / 64; ++c) raw.v[c] = keep_bytes(raw.v[c], skip, n);
     }
-    bf16x8* kf = frag + buf * 2 * FR;
-    bf16x8* vf = kf + FR;
+    bf16x8* kf = frag + buf * 2 * FR + (j * KC + (wave >> 1) * (DT / 32)) * 64 + lane;
+    bf16x8* vf = frag + buf * 2 * FR + FR + ((wave >> 1) * 4 + 2 * j) * 64 + lane;
 #pragma unroll
     for (int c = 0; c < DT / 64; ++c) {
-      kf[(wave * KC + 2 * c) * 64 + lane] = codes_op(raw.k[c][0], raw.k[c][1]);
-      kf[(wave * KC + 2 * c + 1) * 64 + lane] = codes_op(raw.k[c][2], raw.k[c][3]);
-      vf[((wave + 4 * c) * 2) * 64 + lane] = codes_op(raw.v[c][0], raw.v[c][1]);
-      vf[((wave + 4 * c) * 2 + 1) * 64 + lane] = codes_op(raw.v[c][2], raw.v[c][3]);
+      kf[(2 * c) * 64] = codes_op(raw.k[c][0], raw.k[c][1]);
+      kf[(2 * c + 1) * 64] = codes_op(raw.k[c][2], raw.k[c][3]);
+      vf[(8 * c) * 64] = codes_op(raw.v[c][0], raw.v[c][1]);
+      vf[(8 * c + 1) * 64] = codes_op(raw.v[c][2], raw.v[c][3]);
     }
-    if (wave == 0 && m == 0) {
-      bks[buf][g] = raw.gone ? 0.0f : raw.ks * a.scale2;
-      bvs[buf][g] = raw.gone ? 1.0f : raw.vs;
-      bgone[buf][g] = raw.gone;
+    if (wave < 2 && m == 0) {
+      bks[buf][2 * g + j] = raw.gone ? 1.0f : score_scale(a, raw.ks);
+      bvs[buf][2 * g + j] = raw.gone ? 1.0f : raw.vs;
+      bgone[buf][2 * g + j] = raw.gone;
     }
   };
 
@@ -165,24 +171,20 @@ __global__ __launch_bounds__(kTileThreads, DT <= 128 && NS == 1 ? 2 : 1) void at
   }
   for (int i = 0; i < vw.n; ++i) {
     const int tile = vw.t0 + i, t0 = tile * kAttnTile, buf = i & 1;
-    const bf16x8* kf = frag + buf * 2 * FR;
+    const bf16x8* kf = frag + buf * 2 * FR + lane;
     const bf16x8* vf = kf + FR;
-    f32x4 sc[kTileRT][4];
+    f32x16 sc[2];
 #pragma unroll
-    for (int r = 0; r < kTileRT; ++r)
+    for (int x = 0; x < 2; ++x)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) sc[r][j] = f32x4{0, 0, 0, 0};
+      for (int k = 0; k < 16; ++k) sc[x][k] = 0.0f;
 #pragma unroll
     for (int c = 0; c < KC; ++c)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const bf16x8 k = kf[(j * KC + c) * 64 + lane];
-#pragma unroll
-        for (int r = 0; r < kTileRT; ++r) sc[r][j] = mfma_split<NS>(k, q[r][c], sc[r][j]);
-      }
-    const float f = bks[buf][g], fv = bvs[buf][g];
-    const bool out = bgone[buf][g] != 0;
-    const bool masked = t0 < all_lo || t0 + kAttnTile > all_hi || __any(out);
+      for (int x = 0; x < 2; ++x) sc[x] = mfma_split<NS>(kf[(x * KC + c) * 64], q[c], sc[x]);
+    const float f0 = bks[buf][2 * g], f1 = bks[buf][2 * g + 1], v0 = bvs[buf][2 * g], v1 = bvs[buf][2 * g + 1];
+    const bool out0 = bgone[buf][2 * g] != 0, out1 = bgone[buf][2 * g + 1] != 0;
+    const bool masked = t0 < all_lo || t0 + kAttnTile > all_hi || __any(out0 || out1);
     if (i + 1 < vw.n) {
       store(tile + 1, buf ^ 1);
       if (i + 2 < vw.n) {
@@ -191,53 +193,41 @@ __global__ __launch_bounds__(kTileThreads, DT <= 128 && NS == 1 ? 2 : 1) void at
       }
     }
 
-    float top[kTileRT];
-    bool grow = false;
+    const int t = t0 + 32 * g;
+    const float top = __builtin_fmaxf(attn_top(sc[0], masked, out0, t, lo, hi, f0),
+                                      attn_top(sc[1], masked, out1, t + 16, lo, hi, f1));
+    if (__any(top > mx + kMaxSlack)) {
+      const float mn = __builtin_fmaxf(mx, max32(top));
+      const float keep = mn == -__builtin_inff() ? 1.0f : __builtin_amdgcn_exp2f(mx - mn);
+      mx = mn;
+      l *= keep;
 #pragma unroll
-    for (int r = 0; r < kTileRT; ++r) {
-      top[r] = attn_top(sc[r], masked, out, t0 + 16 * g, lo[r], hi[r], f);
-      grow |= top[r] > mx[r] + kMaxSlack;
+      for (int n = 0; n < DT / 32; ++n) o[n] *= keep;
     }
-    if (__any(grow)) {
+    const float base = mx == -__builtin_inff() ? 0.0f : mx;
+    const float lv0 = __builtin_amdgcn_logf(v0), lv1 = __builtin_amdgcn_logf(v1);
+    bf16x8 p[2][2][NS];
+    l += __builtin_amdgcn_exp2f(-lv0) * attn_probs<NS>(sc[0], f0, lv0 - base, p[0]);
+    l += __builtin_amdgcn_exp2f(-lv1) * attn_probs<NS>(sc[1], f1, lv1 - base, p[1]);
 #pragma unroll
-      for (int r = 0; r < kTileRT; ++r) {
-        const float mn = __builtin_fmaxf(mx[r], row_max(top[r]));
-        const float keep = mn == -__builtin_inff() ? 1.0f : __builtin_amdgcn_exp2f(mx[r] - mn);
-        mx[r] = mn;
-        l[r] *= keep;
+    for (int c = 0; c < 4; ++c)
 #pragma unroll
-        for (int n = 0; n < DT / 16; ++n) o[r][n] *= keep;
-      }
-    }
-    const float lv = __builtin_amdgcn_logf(fv), rv = __builtin_amdgcn_exp2f(-lv);
-    bf16x8 p[kTileRT][2][NS];
-#pragma unroll
-    for (int r = 0; r < kTileRT; ++r)
-      l[r] += rv * attn_probs<NS>(sc[r], masked, f, lv - (mx[r] == -__builtin_inff() ? 0.0f : mx[r]), p[r]);
-#pragma unroll
-    for (int n = 0; n < DT / 16; ++n)
-#pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        const bf16x8 v = vf[(n * 2 + c) * 64 + lane];
-#pragma unroll
-        for (int r = 0; r < kTileRT; ++r) o[r][n] = mfma_split<NS>(v, p[r][c], o[r][n]);
-      }
+      for (int n = 0; n < DT / 32; ++n) o[n] = mfma_split<NS>(vf[(n * 4 + c) * 64], p[c >> 1][c & 1], o[n]);
     __syncthreads();  // this buffer may be written, the other one read
   }
 
+  l = sum32(l);
+  if (!live) return;
+  const size_t orow = (size_t)(s.q0 + qi) * a.nH + hd;
 #pragma unroll
-  for (int r = 0; r < kTileRT; ++r) {
-    const float sum = row_sum(l[r]);
-    const int row = row0 + (wave * kTileRT + r) * 16 + m, i = row / a.G;
-    if (i >= s.q) continue;
-    const size_t orow = (size_t)(s.q0 + i) * a.nH + h * a.G + row - i * a.G;
+  for (int n = 0; n < DT / 32; ++n)
 #pragma unroll
-    for (int n = 0; n < DT / 16; ++n) {
-      const float v[4] = {o[r][n][0], o[r][n][1], o[r][n][2], o[r][n][3]};
-      if (16 * n < D) attn_store4<NS>(a, orow, 16 * n + 4 * g, v, sum);
+    for (int k = 0; k < 4; ++k) {
+      const float v[4] = {o[n][4 * k], o[n][4 * k + 1], o[n][4 * k + 2], o[n][4 * k + 3]};
+      const int d = 32 * n + 8 * k + 4 * g;
+      if (d < D) attn_store4<NS>(a, orow, d, v, l);
     }
-    if (g == 0 && a.lse) a.lse[orow] = attn_lse(mx[r], sum);
-  }
+  if (g == 0 && a.lse) a.lse[orow] = attn_lse(mx, l);
 }
 
 template <int DT, int NS>
