@@ -159,16 +159,6 @@ __device__ __forceinline__ float sum32(float v) {
 // is needed.
 constexpr float kMaxSlack = 8.0f;
 
-// Page of the 16-token block at token t, clamped to one the cache has; whether
-// the block is seen (tokens [v.lo, v.hi)) and its page is in the cache.
-__device__ __forceinline__ bool attn_page(const AttnArgs& a, const int32_t* table, const View& v, int t, int& page) {
-  const int i = t >> a.c.lS;
-  page = table[i < a.b.max_pages ? i : 0];
-  const bool ok = t < v.hi && t + 16 > v.lo && (unsigned)page < (unsigned)a.c.pages;
-  if (!ok) page = 0;
-  return ok;
-}
-
 // w with its bytes before `skip` and from n on zeroed.
 __device__ __forceinline__ i32x4 keep_bytes(i32x4 w, int skip, int n) {
 #pragma unroll
@@ -215,19 +205,20 @@ __device__ __forceinline__ void load_q(const AttnArgs& a, size_t row, int d0, bo
   }
 }
 
-// The largest scaled score of a lane's 16 tokens t.. of one row; masked: those
-// outside [lo, hi), or all if gone, become -infinity first.  f > 0.
-__device__ __forceinline__ float attn_top(f32x16& sc, bool masked, bool gone, int t, int lo, int hi, float f) {
-  if (masked) {
-    const int off = t - lo;
-    const unsigned n = gone || hi <= lo ? 0u : (unsigned)(hi - lo);
+// Scores of a lane's 16 tokens t.. of one row: -infinity where the row does
+// not see the token (outside [lo, hi), or all if gone).
+__device__ __forceinline__ void attn_hide(f32x16& sc, bool gone, int t, int lo, int hi) {
+  const int off = t - lo;
+  const unsigned n = gone || hi <= lo ? 0u : (unsigned)(hi - lo);
 #pragma unroll
-    for (int k = 0; k < 16; ++k) sc[k] = (unsigned)(off + k) < n ? sc[k] : -__builtin_inff();
-  }
+  for (int k = 0; k < 16; ++k) sc[k] = (unsigned)(off + k) < n ? sc[k] : -__builtin_inff();
+}
+
+__device__ __forceinline__ float attn_top(const f32x16& sc) {
   float v = sc[0];
 #pragma unroll
   for (int k = 1; k < 16; ++k) v = __builtin_fmaxf(v, sc[k]);
-  return v * f;
+  return v;
 }
 
 // p vs = exp2(s f - m + log2 vs) of a lane's 16 tokens, as operands; returns

@@ -49,16 +49,13 @@ struct DecTile {
 // sees, pages outside the cache) it hides afterwards, keys by their scores,
 // values by zeros, since a zero probability times a NaN code would be NaN.
 struct DecPages {
-  int k, v;  // pages of the lane's key rows and of its own 16 tokens
-  bool gone;
+  int k, v;  // as in the table: of the lane's key rows, and of its own 16 tokens
 };
 
-__device__ __forceinline__ DecPages dec_pages(const AttnArgs& a, const int32_t* table, const View& vw, int tile) {
+__device__ __forceinline__ DecPages dec_pages(const AttnArgs& a, const int32_t* table, int tile) {
   const int lane = threadIdx.x & 63;
-  DecPages p;
-  attn_page(a, table, vw, tile * kAttnTile + 16 * ((lane & 15) >> 2), p.k);
-  p.gone = !attn_page(a, table, vw, tile * kAttnTile + 16 * (lane >> 4), p.v);
-  return p;
+  const int ik = (tile * kAttnTile + 16 * ((lane & 15) >> 2)) >> a.c.lS, iv = (tile * kAttnTile + 16 * (lane >> 4)) >> a.c.lS;
+  return DecPages{table[ik < a.b.max_pages ? ik : 0], table[iv < a.b.max_pages ? iv : 0]};
 }
 
 template <int DT>
@@ -67,8 +64,9 @@ __device__ __forceinline__ void dec_load(const AttnArgs& a, const DecPages& pg, 
   const int lane = threadIdx.x & 63, m = lane & 15, g = lane >> 4;
   const int D = a.c.D, lS = a.c.lS, S = 1 << lS;
   const int tk = tile * kAttnTile + 16 * (m >> 2), tv = tile * kAttnTile + 16 * g;  // first tokens of the lane's blocks
-  const int pk = pg.k, pv = pg.v;
-  r.gone = pg.gone;
+  const uint32_t pages = a.c.pages;
+  const uint32_t pk = (uint32_t)pg.k < pages ? pg.k : 0, pv = (uint32_t)pg.v < pages ? pg.v : 0;
+  r.gone = (uint32_t)pg.v >= pages || tv >= vw.hi || tv + 16 <= vw.lo;
   {
     const size_t page = ((size_t)pk * a.c.H + h) << lS;
     const uint8_t* row = a.c.kc + (page + (tk & (S - 1)) + (m & 3)) * D;
@@ -153,7 +151,8 @@ __device__ __forceinline__ void dec_tile(const AttnArgs& a, int tile, const DecT
   bool grow = false;
 #pragma unroll
   for (int r = 0; r < NR; ++r) {
-    top[r] = attn_top(s[r], masked, t.gone, t0 + 16 * g, st.lo[r], st.hi[r], f);
+    if (masked) attn_hide(s[r], t.gone, t0 + 16 * g, st.lo[r], st.hi[r]);
+    top[r] = attn_top(s[r]) * f;
     grow |= top[r] > st.m[r] + kMaxSlack;
   }
   if (__any(grow)) {
@@ -245,11 +244,11 @@ __global__ __launch_bounds__(kDecThreads) void attn_decode_kernel(AttnArgs a) {
     DecState<DT, NR, NS> st;
     dec_begin<DT, NR, NS>(a, s, h, st);
     const int first = vw.t0 + skip;
-    DecPages pages = dec_pages(a, table, vw, first + wave);
+    DecPages pages = dec_pages(a, table, first + wave);
     for (int i = wave; i < count; i += kDecWaves) {
       DecTile<DT> t;
       dec_load<DT>(a, pages, vw, first + i, h, t);
-      pages = dec_pages(a, table, vw, first + i + kDecWaves);
+      pages = dec_pages(a, table, first + i + kDecWaves);
       dec_tile<DT, NR, NS>(a, first + i, t, st);
     }
     const bool whole = skip == 0 && count == n;

@@ -102,11 +102,13 @@ __global__ __launch_bounds__(kTileThreads, DT <= 128 && NS == 1 ? 2 : 1) void at
   const int all_lo = a.window > 0 ? p0 + i1 - a.window : 0;  // tokens [all_lo, all_hi) every row sees
   const int all_hi = a.causal && p0 + i0 + 1 < s.lim ? p0 + i0 + 1 : s.lim;
 
-  // pages a tile ahead of codes, codes a tile ahead of fragments
+  // pages a tile ahead of codes, codes a tile ahead of fragments; past the last
+  // tile all three go on with what is at hand, unused, so that the loop has no
+  // branches (addresses are clamped into the cache)
   const int j = wave & 1, bk = 16 * (2 * ((m >> 2) & 1) + j), bv = 16 * (2 * g + j);  // first tokens of the blocks
-  const size_t page_bytes = (size_t)a.c.H * D << lS;
-  const uint8_t* kbase = a.c.kc + (((size_t)h << lS) + 4 * (m >> 3) + (m & 3)) * D;
-  const uint8_t* vbase = a.c.vc + ((size_t)h << lS) * D;
+  const uint32_t page_bytes = (uint32_t)(a.c.H * D) << lS;                            // at most 2^23
+  const uint8_t* kbase = a.c.kc + (size_t)(((h << lS) + 4 * (m >> 3) + (m & 3)) * D);
+  const uint8_t* vbase = a.c.vc + (size_t)((h << lS) * D);
   int koff[DT / 64], voff[DT / 64];
 #pragma unroll
   for (int c = 0; c < DT / 64; ++c) {
@@ -114,43 +116,47 @@ __global__ __launch_bounds__(kTileThreads, DT <= 128 && NS == 1 ? 2 : 1) void at
     koff[c] = d < D ? d : 0;
     voff[c] = n < D ? 16 * n : 0;
   }
-  int pk = 0, pv = 0;
-  bool okv = false;
+  int pk, pv;  // as in the table
   auto pages = [&](int tile) {
-    attn_page(a, table, vw, tile * kAttnTile + bk, pk);
-    okv = attn_page(a, table, vw, tile * kAttnTile + bv, pv);
+    const int ik = (tile * kAttnTile + bk) >> lS, iv = (tile * kAttnTile + bv) >> lS;
+    pk = table[ik < a.b.max_pages ? ik : 0];
+    pv = table[iv < a.b.max_pages ? iv : 0];
   };
   TileRaw<DT> raw;
   auto load = [&](int tile) {
     const int t0 = tile * kAttnTile;
-    const uint8_t* kp = kbase + (size_t)pk * page_bytes + ((t0 + bk) & (S - 1)) * D;
-    const uint8_t* vp = vbase + (size_t)pv * page_bytes + ((t0 + bv) & (S - 1)) * D;
+    const uint32_t k = (uint32_t)pk < (uint32_t)a.c.pages ? pk : 0, v = (uint32_t)pv < (uint32_t)a.c.pages ? pv : 0;
+    raw.gone = (uint32_t)pv >= (uint32_t)a.c.pages || t0 + bv >= vw.hi || t0 + bv + 16 <= vw.lo;
+    const uint8_t* kp = kbase + (uint64_t)k * page_bytes + ((t0 + bk) & (S - 1)) * D;
+    const uint8_t* vp = vbase + (uint64_t)v * page_bytes + ((t0 + bv) & (S - 1)) * D;
 #pragma unroll
     for (int c = 0; c < DT / 64; ++c) {
       raw.k[c] = ld16(kp + koff[c]);
       raw.v[c] = ld16(vp + voff[c]);
     }
-    const size_t at = (size_t)pv * a.c.H + h;
+    const uint64_t at = (uint64_t)v * (uint32_t)a.c.H + h;
     raw.ks = a.c.ks[at];
     raw.vs = a.c.vs[at];
-    raw.gone = !okv;
   };
-  auto store = [&](int tile, int buf) {
+  auto trim = [&](int tile) {  // zeros for the values of tokens that no row sees
     const int t0 = tile * kAttnTile;
     if (t0 < vw.lo || t0 + kAttnTile > vw.hi || __any(raw.gone)) {
       const int skip = vw.lo - (t0 + bv), n = raw.gone ? 0 : vw.hi - (t0 + bv);
 #pragma unroll
       for (int c = 0; c < DT / 64; ++c) raw.v[c] = keep_bytes(raw.v[c], skip, n);
     }
+  };
+  // one of the DT / 16 fragments that the thread makes of its codes
+  auto store = [&](int buf, int x) {
     bf16x8* kf = frag + buf * 2 * FR + (j * KC + (wave >> 1) * (DT / 32)) * 64 + lane;
     bf16x8* vf = frag + buf * 2 * FR + FR + ((wave >> 1) * 4 + 2 * j) * 64 + lane;
-#pragma unroll
-    for (int c = 0; c < DT / 64; ++c) {
-      kf[(2 * c) * 64] = codes_op(raw.k[c][0], raw.k[c][1]);
-      kf[(2 * c + 1) * 64] = codes_op(raw.k[c][2], raw.k[c][3]);
-      vf[(8 * c) * 64] = codes_op(raw.v[c][0], raw.v[c][1]);
-      vf[(8 * c + 1) * 64] = codes_op(raw.v[c][2], raw.v[c][3]);
-    }
+    const int c = x >> 2, e = 2 * (x & 1);
+    if (x & 2)
+      vf[(8 * c + (x & 1)) * 64] = codes_op(raw.v[c][e], raw.v[c][e + 1]);
+    else
+      kf[(2 * c + (x & 1)) * 64] = codes_op(raw.k[c][e], raw.k[c][e + 1]);
+  };
+  auto store_scales = [&](int buf) {
     if (wave < 2 && m == 0) {
       bks[buf][2 * g + j] = raw.gone ? 1.0f : score_scale(a, raw.ks);
       bvs[buf][2 * g + j] = raw.gone ? 1.0f : raw.vs;
@@ -161,41 +167,60 @@ __global__ __launch_bounds__(kTileThreads, DT <= 128 && NS == 1 ? 2 : 1) void at
   if (vw.n > 0) {
     pages(vw.t0);
     load(vw.t0);
-    if (vw.n > 1) pages(vw.t0 + 1);
-    store(vw.t0, 0);
-    if (vw.n > 1) {
-      load(vw.t0 + 1);
-      if (vw.n > 2) pages(vw.t0 + 2);
-    }
+    pages(vw.t0 + 1);
+    trim(vw.t0);
+#pragma unroll
+    for (int x = 0; x < KC; ++x) store(0, x);
+    store_scales(0);
+    load(vw.t0 + 1);
+    pages(vw.t0 + 2);
     __syncthreads();
   }
   for (int i = 0; i < vw.n; ++i) {
     const int tile = vw.t0 + i, t0 = tile * kAttnTile, buf = i & 1;
     const bf16x8* kf = frag + buf * 2 * FR + lane;
     const bf16x8* vf = kf + FR;
+    const float f0 = bks[buf][2 * g], f1 = bks[buf][2 * g + 1], v0 = bvs[buf][2 * g], v1 = bvs[buf][2 * g + 1];
+    const bool out0 = bgone[buf][2 * g] != 0, out1 = bgone[buf][2 * g + 1] != 0;
+    const bool masked = t0 < all_lo || t0 + kAttnTile > all_hi || __any(out0 || out1);
+    trim(tile + 1);
+
+    // first product: fragments are read AHEAD steps early, and the next
+    // tile's are made from its codes between the steps
+    constexpr int AHEAD = NS == 1 ? 4 : 2;
+    bf16x8 kq[AHEAD][2];
     f32x16 sc[2];
+#pragma unroll
+    for (int c = 0; c < AHEAD; ++c) {
+      kq[c][0] = kf[c * 64];
+      kq[c][1] = kf[(KC + c) * 64];
+    }
 #pragma unroll
     for (int x = 0; x < 2; ++x)
 #pragma unroll
       for (int k = 0; k < 16; ++k) sc[x][k] = 0.0f;
+    __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-    for (int c = 0; c < KC; ++c)
-#pragma unroll
-      for (int x = 0; x < 2; ++x) sc[x] = mfma_split<NS>(kf[(x * KC + c) * 64], q[c], sc[x]);
-    const float f0 = bks[buf][2 * g], f1 = bks[buf][2 * g + 1], v0 = bvs[buf][2 * g], v1 = bvs[buf][2 * g + 1];
-    const bool out0 = bgone[buf][2 * g] != 0, out1 = bgone[buf][2 * g + 1] != 0;
-    const bool masked = t0 < all_lo || t0 + kAttnTile > all_hi || __any(out0 || out1);
-    if (i + 1 < vw.n) {
-      store(tile + 1, buf ^ 1);
-      if (i + 2 < vw.n) {
-        load(tile + 2);
-        if (i + 3 < vw.n) pages(tile + 3);
+    for (int c = 0; c < KC; ++c) {
+      sc[0] = mfma_split<NS>(kq[c % AHEAD][0], q[c], sc[0]);
+      sc[1] = mfma_split<NS>(kq[c % AHEAD][1], q[c], sc[1]);
+      if (c + AHEAD < KC) {
+        kq[c % AHEAD][0] = kf[(c + AHEAD) * 64];
+        kq[c % AHEAD][1] = kf[(KC + c + AHEAD) * 64];
       }
+      store(buf ^ 1, c);
+      __builtin_amdgcn_sched_barrier(0);
     }
+    store_scales(buf ^ 1);
+    load(tile + 2);
+    pages(tile + 3);
 
     const int t = t0 + 32 * g;
-    const float top = __builtin_fmaxf(attn_top(sc[0], masked, out0, t, lo, hi, f0),
-                                      attn_top(sc[1], masked, out1, t + 16, lo, hi, f1));
+    if (masked) {
+      attn_hide(sc[0], out0, t, lo, hi);
+      attn_hide(sc[1], out1, t + 16, lo, hi);
+    }
+    const float top = __builtin_fmaxf(attn_top(sc[0]) * f0, attn_top(sc[1]) * f1);
     if (__any(top > mx + kMaxSlack)) {
       const float mn = __builtin_fmaxf(mx, max32(top));
       const float keep = mn == -__builtin_inff() ? 1.0f : __builtin_amdgcn_exp2f(mx - mn);
