@@ -43,7 +43,9 @@ struct TileRaw {
 
 // Two workgroups a CU where the registers allow it: the matrix work of one
 // covers the softmax of the other.
-template <int DT, int NS>
+// UNI: pages of 64 tokens or more, so that a tile lies in one: its page, scales
+// and addresses are the workgroup's, not the lane's.
+template <int DT, int NS, bool UNI>
 __global__ __launch_bounds__(kTileThreads, DT <= 128 && NS == 1 ? 2 : 1) void attn_tile_kernel(TileArgs ta) {
   const AttnArgs& a = ta.a;
   constexpr int KC = DT / 16;          // contraction steps of the first product
@@ -52,8 +54,8 @@ __global__ __launch_bounds__(kTileThreads, DT <= 128 && NS == 1 ? 2 : 1) void at
   bf16x8* frag = reinterpret_cast<bf16x8*>(smem);  // [2 buffers][keys [2 j][KC] | values [DT / 32][4]][64 lanes]
   __shared__ int scan[kTileWaves];
   __shared__ int found[2];
-  __shared__ float bks[2][4], bvs[2][4];
-  __shared__ int bgone[2][4];
+  __shared__ float bks[2][4], bvs[2][4];  // of the tile's blocks (UNI: not used)
+  __shared__ int bgone[2][4], bany[2][2];
   const int lane = threadIdx.x & 63, m = lane & 31, g = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int h = blockIdx.x % a.c.H;  // heads in turn: with eight, each XCD's L2 keeps one head's codes
@@ -107,28 +109,29 @@ __global__ __launch_bounds__(kTileThreads, DT <= 128 && NS == 1 ? 2 : 1) void at
   // branches (addresses are clamped into the cache)
   const int j = wave & 1, bk = 16 * (2 * ((m >> 2) & 1) + j), bv = 16 * (2 * g + j);  // first tokens of the blocks
   const uint32_t page_bytes = (uint32_t)(a.c.H * D) << lS;                            // at most 2^23
-  const uint8_t* kbase = a.c.kc + (size_t)(((h << lS) + 4 * (m >> 3) + (m & 3)) * D);
+  const uint8_t* kbase = a.c.kc + (size_t)((h << lS) * D);
   const uint8_t* vbase = a.c.vc + (size_t)((h << lS) * D);
-  int koff[DT / 64], voff[DT / 64];
+  uint32_t koff[DT / 64], voff[DT / 64];  // the lane's place in a tile (UNI) or in its block
 #pragma unroll
   for (int c = 0; c < DT / 64; ++c) {
     const int d = g * (DT / 2) + (wave >> 1) * (DT / 4) + 16 * c, n = 32 * ((wave >> 1) + 2 * c) + m;
-    koff[c] = d < D ? d : 0;
-    voff[c] = n < D ? 16 * n : 0;
+    koff[c] = (4 * (m >> 3) + (m & 3) + (UNI ? bk : 0)) * D + (d < D ? d : 0);
+    voff[c] = (UNI ? bv * D : 0) + (n < D ? 16 * n : 0);
   }
-  int pk, pv;  // as in the table
+  int pk, pv;  // as in the table (UNI: pv only)
   auto pages = [&](int tile) {
-    const int ik = (tile * kAttnTile + bk) >> lS, iv = (tile * kAttnTile + bv) >> lS;
-    pk = table[ik < a.b.max_pages ? ik : 0];
+    const int ik = (tile * kAttnTile + (UNI ? 0 : bk)) >> lS, iv = (tile * kAttnTile + (UNI ? 0 : bv)) >> lS;
+    if (!UNI) pk = table[ik < a.b.max_pages ? ik : 0];
     pv = table[iv < a.b.max_pages ? iv : 0];
   };
   TileRaw<DT> raw;
   auto load = [&](int tile) {
     const int t0 = tile * kAttnTile;
-    const uint32_t k = (uint32_t)pk < (uint32_t)a.c.pages ? pk : 0, v = (uint32_t)pv < (uint32_t)a.c.pages ? pv : 0;
-    raw.gone = (uint32_t)pv >= (uint32_t)a.c.pages || t0 + bv >= vw.hi || t0 + bv + 16 <= vw.lo;
-    const uint8_t* kp = kbase + (uint64_t)k * page_bytes + ((t0 + bk) & (S - 1)) * D;
-    const uint8_t* vp = vbase + (uint64_t)v * page_bytes + ((t0 + bv) & (S - 1)) * D;
+    const uint32_t page = UNI ? __builtin_amdgcn_readfirstlane(pv) : pv, pages = a.c.pages;
+    const uint32_t v = page < pages ? page : 0, k = UNI ? v : ((uint32_t)pk < pages ? pk : 0);
+    raw.gone = page >= pages || (!UNI && (t0 + bv >= vw.hi || t0 + bv + 16 <= vw.lo));
+    const uint8_t* kp = kbase + ((uint64_t)k * page_bytes + (uint32_t)(((t0 + (UNI ? 0 : bk)) & (S - 1)) * D));
+    const uint8_t* vp = vbase + ((uint64_t)v * page_bytes + (uint32_t)(((t0 + (UNI ? 0 : bv)) & (S - 1)) * D));
 #pragma unroll
     for (int c = 0; c < DT / 64; ++c) {
       raw.k[c] = ld16(kp + koff[c]);
@@ -140,7 +143,7 @@ __global__ __launch_bounds__(kTileThreads, DT <= 128 && NS == 1 ? 2 : 1) void at
   };
   auto trim = [&](int tile) {  // zeros for the values of tokens that no row sees
     const int t0 = tile * kAttnTile;
-    if (t0 < vw.lo || t0 + kAttnTile > vw.hi || __any(raw.gone)) {
+    if (t0 < vw.lo || t0 + kAttnTile > vw.hi || (UNI ? raw.gone : __any(raw.gone))) {
       const int skip = vw.lo - (t0 + bv), n = raw.gone ? 0 : vw.hi - (t0 + bv);
 #pragma unroll
       for (int c = 0; c < DT / 64; ++c) raw.v[c] = keep_bytes(raw.v[c], skip, n);
@@ -156,11 +159,24 @@ __global__ __launch_bounds__(kTileThreads, DT <= 128 && NS == 1 ? 2 : 1) void at
     else
       kf[(2 * c + (x & 1)) * 64] = codes_op(raw.k[c][e], raw.k[c][e + 1]);
   };
+  // scale of the scores and of the values of the lane's two blocks, and
+  // whether they are hidden: from LDS, or (UNI) from the next tile's load
+  float f0 = 1.0f, f1 = 1.0f, v0 = 1.0f, v1 = 1.0f;
+  bool out0 = false, out1 = false;
   auto store_scales = [&](int buf) {
-    if (wave < 2 && m == 0) {
-      bks[buf][2 * g + j] = raw.gone ? 1.0f : score_scale(a, raw.ks);
-      bvs[buf][2 * g + j] = raw.gone ? 1.0f : raw.vs;
-      bgone[buf][2 * g + j] = raw.gone;
+    const float f = raw.gone ? 1.0f : score_scale(a, raw.ks), v = raw.gone ? 1.0f : raw.vs;
+    if (UNI) {
+      f0 = f1 = f;
+      v0 = v1 = v;
+      out0 = out1 = raw.gone;
+    } else if (wave < 2) {
+      const int any = __any(raw.gone);
+      if (m == 0) {
+        bks[buf][2 * g + j] = f;
+        bvs[buf][2 * g + j] = v;
+        bgone[buf][2 * g + j] = raw.gone;
+        bany[buf][j] = any;
+      }
     }
   };
 
@@ -180,9 +196,6 @@ __global__ __launch_bounds__(kTileThreads, DT <= 128 && NS == 1 ? 2 : 1) void at
     const int tile = vw.t0 + i, t0 = tile * kAttnTile, buf = i & 1;
     const bf16x8* kf = frag + buf * 2 * FR + lane;
     const bf16x8* vf = kf + FR;
-    const float f0 = bks[buf][2 * g], f1 = bks[buf][2 * g + 1], v0 = bvs[buf][2 * g], v1 = bvs[buf][2 * g + 1];
-    const bool out0 = bgone[buf][2 * g] != 0, out1 = bgone[buf][2 * g + 1] != 0;
-    const bool masked = t0 < all_lo || t0 + kAttnTile > all_hi || __any(out0 || out1);
     trim(tile + 1);
 
     // first product: fragments are read AHEAD steps early, and the next
@@ -211,16 +224,22 @@ __global__ __launch_bounds__(kTileThreads, DT <= 128 && NS == 1 ? 2 : 1) void at
       store(buf ^ 1, c);
       __builtin_amdgcn_sched_barrier(0);
     }
+    bool masked = t0 < all_lo || t0 + kAttnTile > all_hi;
+    const float cf0 = UNI ? f0 : bks[buf][2 * g], cf1 = UNI ? f1 : bks[buf][2 * g + 1];
+    const float cv0 = UNI ? v0 : bvs[buf][2 * g], cv1 = UNI ? v1 : bvs[buf][2 * g + 1];
+    const bool cout0 = UNI ? out0 : bgone[buf][2 * g] != 0, cout1 = UNI ? out1 : bgone[buf][2 * g + 1] != 0;
+    masked |= UNI ? out0 : __builtin_amdgcn_readfirstlane(bany[buf][0] | bany[buf][1]) != 0;
     store_scales(buf ^ 1);
     load(tile + 2);
     pages(tile + 3);
 
     const int t = t0 + 32 * g;
     if (masked) {
-      attn_hide(sc[0], out0, t, lo, hi);
-      attn_hide(sc[1], out1, t + 16, lo, hi);
+      attn_hide(sc[0], cout0, t, lo, hi);
+      attn_hide(sc[1], cout1, t + 16, lo, hi);
     }
-    const float top = __builtin_fmaxf(attn_top(sc[0]) * f0, attn_top(sc[1]) * f1);
+    const float top = UNI ? __builtin_fmaxf(attn_top(sc[0]), attn_top(sc[1])) * cf0
+                          : __builtin_fmaxf(attn_top(sc[0]) * cf0, attn_top(sc[1]) * cf1);
     if (__any(top > mx + kMaxSlack)) {
       const float mn = __builtin_fmaxf(mx, max32(top));
       const float keep = mn == -__builtin_inff() ? 1.0f : __builtin_amdgcn_exp2f(mx - mn);
@@ -230,10 +249,12 @@ __global__ __launch_bounds__(kTileThreads, DT <= 128 && NS == 1 ? 2 : 1) void at
       for (int n = 0; n < DT / 32; ++n) o[n] *= keep;
     }
     const float base = mx == -__builtin_inff() ? 0.0f : mx;
-    const float lv0 = __builtin_amdgcn_logf(v0), lv1 = __builtin_amdgcn_logf(v1);
+    const float lv0 = __builtin_amdgcn_logf(cv0), lv1 = UNI ? lv0 : __builtin_amdgcn_logf(cv1);
     bf16x8 p[2][2][NS];
-    l += __builtin_amdgcn_exp2f(-lv0) * attn_probs<NS>(sc[0], f0, lv0 - base, p[0]);
-    l += __builtin_amdgcn_exp2f(-lv1) * attn_probs<NS>(sc[1], f1, lv1 - base, p[1]);
+    const float s0 = attn_probs<NS>(sc[0], cf0, lv0 - base, p[0]);
+    const float s1 = attn_probs<NS>(sc[1], UNI ? cf0 : cf1, lv1 - base, p[1]);
+    l += UNI ? __builtin_amdgcn_exp2f(-lv0) * (s0 + s1)
+             : __builtin_amdgcn_exp2f(-lv0) * s0 + __builtin_amdgcn_exp2f(-lv1) * s1;
 #pragma unroll
     for (int c = 0; c < 4; ++c)
 #pragma unroll
@@ -255,26 +276,32 @@ __global__ __launch_bounds__(kTileThreads, DT <= 128 && NS == 1 ? 2 : 1) void at
   if (g == 0 && a.lse) a.lse[orow] = attn_lse(mx, l);
 }
 
-template <int DT, int NS>
+template <int DT, int NS, bool UNI>
 static int tile_launch(const TileArgs& t, hipStream_t st) {
   const size_t lds = (size_t)kAttnTile * DT * 2 * 2 * 2;  // two tiles' keys and values in bf16
   if (lds > 32768) {  // with the static part past 64 KB, or near it
     static OncePerDevice once;
     const int err = once.run([&] {
-      return (int)hipFuncSetAttribute(reinterpret_cast<const void*>(attn_tile_kernel<DT, NS>),
+      return (int)hipFuncSetAttribute(reinterpret_cast<const void*>(attn_tile_kernel<DT, NS, UNI>),
                                       hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
     });
     if (err) return err;
   }
-  hipLaunchKernelGGL((attn_tile_kernel<DT, NS>), dim3((unsigned)t.units * t.a.c.H), dim3(kTileThreads), lds, st, t);
+  hipLaunchKernelGGL((attn_tile_kernel<DT, NS, UNI>), dim3((unsigned)t.units * t.a.c.H), dim3(kTileThreads), lds, st, t);
   return (int)hipGetLastError();
+}
+
+template <int DT>
+static int tile_pick(const TileArgs& t, bool f32, hipStream_t st) {
+  if (t.a.c.lS >= 6) return f32 ? tile_launch<DT, 3, true>(t, st) : tile_launch<DT, 1, true>(t, st);
+  return f32 ? tile_launch<DT, 3, false>(t, st) : tile_launch<DT, 1, false>(t, st);
 }
 
 int launch_attn_tile(const AttnArgs& a, int rows_below, int units, bool f32, hipStream_t st) {
   const TileArgs t{a, rows_below, units};
-  if (a.c.D <= 64) return f32 ? tile_launch<64, 3>(t, st) : tile_launch<64, 1>(t, st);
-  if (a.c.D <= 128) return f32 ? tile_launch<128, 3>(t, st) : tile_launch<128, 1>(t, st);
-  return f32 ? tile_launch<256, 3>(t, st) : tile_launch<256, 1>(t, st);
+  if (a.c.D <= 64) return tile_pick<64>(t, f32, st);
+  if (a.c.D <= 128) return tile_pick<128>(t, f32, st);
+  return tile_pick<256>(t, f32, st);
 }
 
 int attn_tile_rows() { return kTileRows; }
