@@ -171,35 +171,42 @@ __device__ __forceinline__ i32x4 keep_bytes(i32x4 w, int skip, int n) {
   return w;
 }
 
-// A query row's DT / 4 values at d0 as KC B operands of NS bf16 terms each
-// (zeros where the row is not live, or past the head).  Every load is issued
-// before any value is used.
+// A query row's 8 KC values from d0 on as KC B operands of NS bf16 terms each
+// (zeros where the row is not live, or past the head): first every load, then,
+// once other loads are on their way too, the operands.
 template <int KC, int NS>
-__device__ __forceinline__ void load_q(const AttnArgs& a, size_t row, int d0, bool live, bf16x8 out[KC][NS]) {
-  constexpr int W = NS == 1 ? 1 : 2;  // 16-byte loads of eight values
-  i32x4 raw[KC][W];
+struct QueryRaw {
+  i32x4 w[KC][NS == 1 ? 1 : 2];
+};
+
+template <int KC, int NS>
+__device__ __forceinline__ void load_q(const AttnArgs& a, size_t row, int d0, QueryRaw<KC, NS>& raw) {
 #pragma unroll
   for (int c = 0; c < KC; ++c) {
     const size_t at = row + (d0 + 8 * c < a.c.D ? d0 + 8 * c : 0);
 #pragma unroll
-    for (int k = 0; k < W; ++k)
-      raw[c][k] = NS == 1 ? ld16(reinterpret_cast<const uint16_t*>(a.q) + at)
-                          : ld16(reinterpret_cast<const float*>(a.q) + at + 4 * k);
+    for (int k = 0; k < (NS == 1 ? 1 : 2); ++k)
+      raw.w[c][k] = NS == 1 ? ld16(reinterpret_cast<const uint16_t*>(a.q) + at)
+                            : ld16(reinterpret_cast<const float*>(a.q) + at + 4 * k);
   }
+}
+
+template <int KC, int NS>
+__device__ __forceinline__ void make_q(const AttnArgs& a, const QueryRaw<KC, NS>& raw, int d0, bool live,
+                                       bf16x8 out[KC][NS]) {
   const int sign = a.neg ? (NS == 1 ? (int)0x80008000 : (int)0x80000000) : 0;
 #pragma unroll
   for (int c = 0; c < KC; ++c) {
     const bool use = live && d0 + 8 * c < a.c.D;
-#pragma unroll
-    for (int k = 0; k < W; ++k)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) raw[c][k][j] = use ? raw[c][k][j] ^ sign : 0;
     if (NS == 1) {
-      out[c][0] = as_bf16x8(raw[c][0]);
+      i32x4 w = raw.w[c][0];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) w[j] = use ? w[j] ^ sign : 0;
+      out[c][0] = as_bf16x8(w);
     } else {
       float x[8];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) x[j] = __int_as_float(raw[c][j >> 2][j & 3]);
+      for (int j = 0; j < 8; ++j) x[j] = use ? __int_as_float(raw.w[c][j >> 2][j & 3] ^ sign) : 0.0f;
       split_bf16<NS>(x, out[c]);
     }
   }

@@ -112,7 +112,9 @@ __device__ __forceinline__ void dec_begin(const AttnArgs& a, const Seq& s, int h
     const int row = 16 * r + (lane & 15), i = row / a.G, hd = h * a.G + row - i * a.G;
     const bool live = i < s.q;
     const size_t at = (size_t)(s.q0 + (live ? i : 0)) * a.qs_t + (size_t)(live ? hd : 0) * a.qs_h;
-    load_q<DT / 32, NS>(a, at, g * (DT / 4), live, st.q[r]);
+    QueryRaw<DT / 32, NS> raw;
+    load_q<DT / 32, NS>(a, at, g * (DT / 4), raw);
+    make_q<DT / 32, NS>(a, raw, g * (DT / 4), live, st.q[r]);
 #pragma unroll
     for (int n = 0; n < DT / 16; ++n) st.o[r][n] = f32x4{0, 0, 0, 0};
     st.m[r] = -__builtin_inff();

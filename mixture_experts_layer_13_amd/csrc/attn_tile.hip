@@ -41,6 +41,10 @@ struct TileRaw {
   bool gone;
 };
 
+struct TilePages {
+  int k, v;
+};
+
 // Two workgroups a CU where the registers allow it: the matrix work of one
 // covers the softmax of the other.
 // UNI: pages of 64 tokens or more, so that a tile lies in one: its page, scales
@@ -93,7 +97,8 @@ __global__ __launch_bounds__(kTileThreads, DT <= 128 && NS == 1 ? 2 : 1) void at
   float mx = -__builtin_inff(), l = 0.0f;
   const int row = row0 + wave * 32 + m, qi = row / a.G, hd = h * a.G + row - qi * a.G;
   const bool live = qi < s.q;
-  load_q<KC, NS>(a, (size_t)(s.q0 + (live ? qi : 0)) * a.qs_t + (size_t)(live ? hd : 0) * a.qs_h, g * (DT / 2), live, q);
+  QueryRaw<KC, NS> qraw;
+  load_q<KC, NS>(a, (size_t)(s.q0 + (live ? qi : 0)) * a.qs_t + (size_t)(live ? hd : 0) * a.qs_h, g * (DT / 2), qraw);
 #pragma unroll
   for (int n = 0; n < DT / 32; ++n)
 #pragma unroll
@@ -104,9 +109,9 @@ __global__ __launch_bounds__(kTileThreads, DT <= 128 && NS == 1 ? 2 : 1) void at
   const int all_lo = a.window > 0 ? p0 + i1 - a.window : 0;  // tokens [all_lo, all_hi) every row sees
   const int all_hi = a.causal && p0 + i0 + 1 < s.lim ? p0 + i0 + 1 : s.lim;
 
-  // pages a tile ahead of codes, codes a tile ahead of fragments; past the last
-  // tile all three go on with what is at hand, unused, so that the loop has no
-  // branches (addresses are clamped into the cache)
+  // pages a tile ahead of codes, codes kAhead tiles ahead of fragments; past the
+  // last tile all three go on with what is at hand, unused, so that the loop
+  // has no branches (addresses are clamped into the cache)
   const int j = wave & 1, bk = 16 * (2 * ((m >> 2) & 1) + j), bv = 16 * (2 * g + j);  // first tokens of the blocks
   const uint32_t page_bytes = (uint32_t)(a.c.H * D) << lS;                            // at most 2^23
   const uint8_t* kbase = a.c.kc + (size_t)((h << lS) * D);
@@ -118,17 +123,21 @@ __global__ __launch_bounds__(kTileThreads, DT <= 128 && NS == 1 ? 2 : 1) void at
     koff[c] = (4 * (m >> 3) + (m & 3) + (UNI ? bk : 0)) * D + (d < D ? d : 0);
     voff[c] = (UNI ? bv * D : 0) + (n < D ? 16 * n : 0);
   }
-  int pk, pv;  // as in the table (UNI: pv only)
-  auto pages = [&](int tile) {
+  auto pages = [&](int tile) {  // as in the table (UNI: v only)
     const int ik = (tile * kAttnTile + (UNI ? 0 : bk)) >> lS, iv = (tile * kAttnTile + (UNI ? 0 : bv)) >> lS;
-    if (!UNI) pk = table[ik < a.b.max_pages ? ik : 0];
-    pv = table[iv < a.b.max_pages ? iv : 0];
+    TilePages p{};
+    if (!UNI) p.k = table[ik < a.b.max_pages ? ik : 0];
+    p.v = table[iv < a.b.max_pages ? iv : 0];
+    return p;
   };
-  TileRaw<DT> raw;
-  auto load = [&](int tile) {
+  // two tiles' codes in flight where the registers hold them: the loop is
+  // shorter than a load from memory takes
+  constexpr int kAhead = DT <= 128 && NS == 1 ? 2 : 1;
+  TileRaw<DT> codes[kAhead];
+  auto load = [&](TileRaw<DT>& raw, const TilePages& pg, int tile) {
     const int t0 = tile * kAttnTile;
-    const uint32_t page = UNI ? __builtin_amdgcn_readfirstlane(pv) : pv, pages = a.c.pages;
-    const uint32_t v = page < pages ? page : 0, k = UNI ? v : ((uint32_t)pk < pages ? pk : 0);
+    const uint32_t page = UNI ? __builtin_amdgcn_readfirstlane(pg.v) : pg.v, pages = a.c.pages;
+    const uint32_t v = page < pages ? page : 0, k = UNI ? v : ((uint32_t)pg.k < pages ? pg.k : 0);
     raw.gone = page >= pages || (!UNI && (t0 + bv >= vw.hi || t0 + bv + 16 <= vw.lo));
     const uint8_t* kp = kbase + ((uint64_t)k * page_bytes + (uint32_t)(((t0 + (UNI ? 0 : bk)) & (S - 1)) * D));
     const uint8_t* vp = vbase + ((uint64_t)v * page_bytes + (uint32_t)(((t0 + (UNI ? 0 : bv)) & (S - 1)) * D));
@@ -141,7 +150,7 @@ __global__ __launch_bounds__(kTileThreads, DT <= 128 && NS == 1 ? 2 : 1) void at
     raw.ks = a.c.ks[at];
     raw.vs = a.c.vs[at];
   };
-  auto trim = [&](int tile) {  // zeros for the values of tokens that no row sees
+  auto trim = [&](TileRaw<DT>& raw, int tile) {  // zeros for the values of tokens that no row sees
     const int t0 = tile * kAttnTile;
     if (t0 < vw.lo || t0 + kAttnTile > vw.hi || (UNI ? raw.gone : __any(raw.gone))) {
       const int skip = vw.lo - (t0 + bv), n = raw.gone ? 0 : vw.hi - (t0 + bv);
@@ -150,7 +159,7 @@ __global__ __launch_bounds__(kTileThreads, DT <= 128 && NS == 1 ? 2 : 1) void at
     }
   };
   // one of the DT / 16 fragments that the thread makes of its codes
-  auto store = [&](int buf, int x) {
+  auto store = [&](const TileRaw<DT>& raw, int buf, int x) {
     bf16x8* kf = frag + buf * 2 * FR + (j * KC + (wave >> 1) * (DT / 32)) * 64 + lane;
     bf16x8* vf = frag + buf * 2 * FR + FR + ((wave >> 1) * 4 + 2 * j) * 64 + lane;
     const int c = x >> 2, e = 2 * (x & 1);
@@ -163,7 +172,7 @@ __global__ __launch_bounds__(kTileThreads, DT <= 128 && NS == 1 ? 2 : 1) void at
   // whether they are hidden: from LDS, or (UNI) from the next tile's load
   float f0 = 1.0f, f1 = 1.0f, v0 = 1.0f, v1 = 1.0f;
   bool out0 = false, out1 = false;
-  auto store_scales = [&](int buf) {
+  auto store_scales = [&](const TileRaw<DT>& raw, int buf) {
     const float f = raw.gone ? 1.0f : score_scale(a, raw.ks), v = raw.gone ? 1.0f : raw.vs;
     if (UNI) {
       f0 = f1 = f;
@@ -180,23 +189,30 @@ __global__ __launch_bounds__(kTileThreads, DT <= 128 && NS == 1 ? 2 : 1) void at
     }
   };
 
+  TilePages next{};  // pages of the tile that is loaded next
   if (vw.n > 0) {
-    pages(vw.t0);
-    load(vw.t0);
-    pages(vw.t0 + 1);
-    trim(vw.t0);
+    TileRaw<DT> first;
+    TilePages p[1 + kAhead];
 #pragma unroll
-    for (int x = 0; x < KC; ++x) store(0, x);
-    store_scales(0);
-    load(vw.t0 + 1);
-    pages(vw.t0 + 2);
-    __syncthreads();
+    for (int k = 0; k <= kAhead; ++k) p[k] = pages(vw.t0 + k);
+    next = pages(vw.t0 + 1 + kAhead);
+    load(first, p[0], vw.t0);
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) load(codes[k], p[1 + k], vw.t0 + 1 + k);
+    trim(first, vw.t0);
+#pragma unroll
+    for (int x = 0; x < KC; ++x) store(first, 0, x);
+    store_scales(first, 0);
   }
-  for (int i = 0; i < vw.n; ++i) {
+  make_q<KC, NS>(a, qraw, g * (DT / 2), live, q);
+  __syncthreads();
+
+  // tile i; raw: the codes of tile i + 1, then of tile i + 1 + kAhead
+  auto body = [&](int i, TileRaw<DT>& raw) {
     const int tile = vw.t0 + i, t0 = tile * kAttnTile, buf = i & 1;
     const bf16x8* kf = frag + buf * 2 * FR + lane;
     const bf16x8* vf = kf + FR;
-    trim(tile + 1);
+    trim(raw, tile + 1);
 
     // first product: fragments are read AHEAD steps early, and the next
     // tile's are made from its codes between the steps
@@ -221,7 +237,7 @@ __global__ __launch_bounds__(kTileThreads, DT <= 128 && NS == 1 ? 2 : 1) void at
         kq[c % AHEAD][0] = kf[(c + AHEAD) * 64];
         kq[c % AHEAD][1] = kf[(KC + c + AHEAD) * 64];
       }
-      store(buf ^ 1, c);
+      store(raw, buf ^ 1, c);
       __builtin_amdgcn_sched_barrier(0);
     }
     bool masked = t0 < all_lo || t0 + kAttnTile > all_hi;
@@ -229,9 +245,9 @@ __global__ __launch_bounds__(kTileThreads, DT <= 128 && NS == 1 ? 2 : 1) void at
     const float cv0 = UNI ? v0 : bvs[buf][2 * g], cv1 = UNI ? v1 : bvs[buf][2 * g + 1];
     const bool cout0 = UNI ? out0 : bgone[buf][2 * g] != 0, cout1 = UNI ? out1 : bgone[buf][2 * g + 1] != 0;
     masked |= UNI ? out0 : __builtin_amdgcn_readfirstlane(bany[buf][0] | bany[buf][1]) != 0;
-    store_scales(buf ^ 1);
-    load(tile + 2);
-    pages(tile + 3);
+    store_scales(raw, buf ^ 1);
+    load(raw, next, tile + 1 + kAhead);
+    next = pages(tile + 2 + kAhead);
 
     const int t = t0 + 32 * g;
     if (masked) {
@@ -260,6 +276,10 @@ __global__ __launch_bounds__(kTileThreads, DT <= 128 && NS == 1 ? 2 : 1) void at
 #pragma unroll
       for (int n = 0; n < DT / 32; ++n) o[n] = mfma_split<NS>(vf[(n * 4 + c) * 64], p[c >> 1][c & 1], o[n]);
     __syncthreads();  // this buffer may be written, the other one read
+  };
+  for (int i = 0; i < vw.n; i += kAhead) {
+    body(i, codes[0]);
+    if (kAhead > 1 && i + 1 < vw.n) body(i + 1, codes[kAhead - 1]);
   }
 
   l = sum32(l);
