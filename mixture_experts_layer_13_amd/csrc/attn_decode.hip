@@ -208,7 +208,7 @@ __global__ __launch_bounds__(kDecThreads) void attn_decode_kernel(AttnArgs a) {
     int n = 0, e = 0, t;
     for (int base = 0; base < a.b.B; base += kDecThreads) {
       n = base + (int)threadIdx.x < a.b.B ? dec_tiles(a, ROWS, base + threadIdx.x) : 0;
-      e = block_scan<kDecThreads>(n, scan, &t);
+      e = block_scan<kDecWaves>(n, scan, &t);
       total += t;
     }
     const long long run = dec_run(total, a.W);
@@ -218,7 +218,7 @@ __global__ __launch_bounds__(kDecThreads) void attn_decode_kernel(AttnArgs a) {
     for (int base = 0; base < a.b.B && before <= begin; base += kDecThreads) {
       if (a.b.B > kDecThreads) {  // else the one scan above
         n = base + (int)threadIdx.x < a.b.B ? dec_tiles(a, ROWS, base + threadIdx.x) : 0;
-        e = block_scan<kDecThreads>(n, scan, &t);
+        e = block_scan<kDecWaves>(n, scan, &t);
       }
       if (begin >= before + e - n && begin < before + e) {
         found[0] = base + threadIdx.x;
@@ -327,7 +327,7 @@ __global__ __launch_bounds__(kDecThreads) void attn_join_kernel(AttnArgs a) {
     const int i = i0 + threadIdx.x;
     const int v = i < a.b.B ? dec_tiles(a, ROWS, i) : 0;
     int t;
-    const int e = block_scan<kDecThreads>(v, scan, &t);
+    const int e = block_scan<kDecWaves>(v, scan, &t);
     if (i == b) base[0] = e - v;
     if (b >= i0 && b < i0 + kDecThreads) {
       __syncthreads();

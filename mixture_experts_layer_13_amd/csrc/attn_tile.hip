@@ -73,7 +73,7 @@ __global__ __launch_bounds__(kTileThreads, DT <= 128 && NS == 1 ? 2 : 1) void at
     const int b = base + threadIdx.x;
     const int n = b < a.b.B ? tile_blocks(ta, b) : 0;
     int t;
-    const int e = before + block_scan<kTileThreads>(n, scan, &t);
+    const int e = before + block_scan<kTileWaves>(n, scan, &t);
     if (unit >= e - n && unit < e) {
       found[0] = b;
       found[1] = unit - (e - n);

@@ -14,11 +14,15 @@
 // A scale never shrinks while the page is in use, which makes the append of
 // the same tokens at the same place the same cache bit for bit.
 //
-// One workgroup per (page, head) and per keys or values reads its tokens
-// once, holds them in registers as fp32, reduces the maximum and stores the
-// codes.  Values are stored channel by channel (paged.hpp): through LDS, 16
-// bytes of a channel at a time, where a block of 16 tokens is all new; byte by
-// byte otherwise, which leaves every other token's bytes alone.
+// A workgroup takes one touched page and HG heads (blockDim / HG threads each),
+// keys and values.  It reads its tokens once, 16 values per thread and unit,
+// and has every load in flight before the first is used; meanwhile it computes
+// the tokens' angles into LDS, once for all its heads (the fp64 reduction and
+// sincospi, not the bytes, would bound a prompt's append otherwise); then it
+// rotates, reduces the maxima and stores the codes.  Values are stored channel
+// by channel (paged.hpp): through LDS, four channels by 16 tokens at a time
+// transposed with byte permutes, where a block of 16 tokens is all new; byte
+// by byte otherwise, which leaves every other token's bytes alone.
 #include "launch.hpp"
 #include "paged.hpp"
 #include "rotate.hpp"
@@ -26,6 +30,7 @@
 namespace moe {
 
 constexpr float kMinPageScale = 0x1p-64f;
+constexpr int kAppendThreads = 1024;
 
 struct AppendArgs {
   PagedArgs c;
@@ -34,6 +39,7 @@ struct AppendArgs {
   long long ks_t, ks_h, vs_t, vs_h;  // strides in elements
   RotateArgs r;                      // r.half == 0: no rotation
   int units;                         // upper bound of (sequence, page) pairs
+  int HG, rows;                      // heads of a workgroup; new tokens of a page, at most
 };
 
 // The smallest power of two s with 448 s >= amax: 448 = 1.75 * 2^8, so adding
@@ -48,7 +54,7 @@ __device__ __forceinline__ float page_scale(float amax) {
 __device__ __forceinline__ uint32_t codes4(const float* y, float r) {
   float q[4];
 #pragma unroll
-  for (int j = 0; j < 4; ++j) q[j] = __builtin_fminf(__builtin_fmaxf(y[j] * r, -448.0f), 448.0f);
+  for (int j = 0; j < 4; ++j) q[j] = __builtin_amdgcn_fmed3f(y[j] * r, -448.0f, 448.0f);
   int v = __builtin_amdgcn_cvt_pk_fp8_f32(q[0], q[1], 0, false);
   return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(q[2], q[3], v, true);
 }
@@ -61,15 +67,27 @@ __device__ __forceinline__ uint32_t recode4(uint32_t w, float ratio) {
   return codes4(y, ratio);
 }
 
-// XT: type of k and v; UPT: units of 16 values per thread.
-template <int XT, int THREADS, int UPT>
-__global__ __launch_bounds__(THREADS) void kv_append_kernel(AppendArgs a) {
-  extern __shared__ __align__(16) uint8_t tile[];  // [S][D] codes of values
-  __shared__ int scan[THREADS / 64];
+// 4 x 4 bytes transposed: byte j of out[i] = byte i of in[j].
+__device__ __forceinline__ void transpose4(const uint32_t in[4], uint32_t out[4]) {
+  const uint32_t a = __builtin_amdgcn_perm(in[1], in[0], 0x05010400u), b = __builtin_amdgcn_perm(in[1], in[0], 0x07030602u);
+  const uint32_t c = __builtin_amdgcn_perm(in[3], in[2], 0x05010400u), d = __builtin_amdgcn_perm(in[3], in[2], 0x07030602u);
+  out[0] = __builtin_amdgcn_perm(c, a, 0x05040100u);
+  out[1] = __builtin_amdgcn_perm(c, a, 0x07060302u);
+  out[2] = __builtin_amdgcn_perm(d, b, 0x05040100u);
+  out[3] = __builtin_amdgcn_perm(d, b, 0x07060302u);
+}
+
+// XT: type of k and v; UPT: units of 16 values per thread; CS: angles in LDS.
+template <int XT, int UPT, bool CS>
+__global__ __launch_bounds__(kAppendThreads) void kv_append_kernel(AppendArgs a) {
+  extern __shared__ __align__(16) uint8_t smem[];  // [HG][rows][D] codes of values, then [rows][half] {cos, sin}
+  __shared__ int scan[kAppendThreads / 64];
   __shared__ int found[2];
-  __shared__ float wmax[THREADS / 64];
-  const int S = 1 << a.c.lS, D = a.c.D, h = blockIdx.y;
-  const bool vals = blockIdx.z != 0;
+  __shared__ float wmax[2][kAppendThreads / 64];
+  const int S = 1 << a.c.lS, D = a.c.D, TH = blockDim.x / a.HG;
+  const int sub = threadIdx.x / TH, t = threadIdx.x - sub * TH, h = blockIdx.y * a.HG + sub;
+  uint8_t* tile = smem + (size_t)sub * a.rows * D;
+  float2* cs = reinterpret_cast<float2*>(smem + (size_t)a.HG * a.rows * D);
 
   // the workgroup's sequence and page
   int b = blockIdx.x, rank = 0;
@@ -77,7 +95,7 @@ __global__ __launch_bounds__(THREADS) void kv_append_kernel(AppendArgs a) {
     if (threadIdx.x == 0) found[0] = -1;
     __syncthreads();
     int before = 0;
-    for (int base = 0; base < a.b.B && before <= (int)blockIdx.x; base += THREADS) {
+    for (int base = 0; base < a.b.B && before <= (int)blockIdx.x; base += blockDim.x) {
       int n = 0;
       if (base + (int)threadIdx.x < a.b.B) {
         const Seq s = load_seq(a.b, a.c.lS, base + threadIdx.x);
@@ -85,7 +103,7 @@ __global__ __launch_bounds__(THREADS) void kv_append_kernel(AppendArgs a) {
         if (s.q > 0 && s.lim > p0) n = ((s.lim - 1) >> a.c.lS) - (p0 >> a.c.lS) + 1;
       }
       int total;
-      const int end = before + block_scan<THREADS>(n, scan, &total);
+      const int end = before + block_scan<0>(n, scan, &total);
       if ((int)blockIdx.x >= end - n && (int)blockIdx.x < end) {
         found[0] = base + threadIdx.x;
         found[1] = blockIdx.x - (end - n);
@@ -105,135 +123,186 @@ __global__ __launch_bounds__(THREADS) void kv_append_kernel(AppendArgs a) {
   const int lo = p0 > (pg << a.c.lS) ? p0 : pg << a.c.lS;
   const int hi = s.lim < ((pg + 1) << a.c.lS) ? s.lim : (pg + 1) << a.c.lS;
   const int old = lo & (S - 1);  // earlier tokens in the page
-  const int page = a.b.table[(size_t)b * a.b.max_pages + pg];
-  if ((unsigned)page >= (unsigned)a.c.pages) return;
   const int row0 = s.q0 + lo - start, n = hi - lo;
+  const int page = a.b.table[(size_t)b * a.b.max_pages + pg];
 
-  // the new tokens, in fp32
-  const int upd = D >> 4, units = n * upd;
-  const void* src = vals ? a.v : a.k;
-  const long long st = vals ? a.vs_t : a.ks_t, sh = vals ? a.vs_h : a.ks_h;
-  const int half = vals ? 0 : a.r.half;
-  float x[UPT][16];
-  float amax = 0.0f;
+  // the new tokens: every load first
+  const int upd = D >> 4, units = n * upd, half = a.r.half;
+  RawVec<XT, 8> ka[UPT], kb[UPT], va[UPT], vb[UPT];
+  int tok[UPT], gs[UPT];
 #pragma unroll
   for (int j = 0; j < UPT; ++j) {
-    const int u = j * THREADS + threadIdx.x;
-    if (u >= units) continue;
-    const int tok = u / upd, g = u - tok * upd;
+    const int u = j * TH + t < units ? j * TH + t : 0;
+    tok[j] = u / upd;
+    gs[j] = u - tok[j] * upd;
     int p, q;
-    unit_groups(g, half, a.r.interleaved, p, q);
-    const size_t base = (size_t)(row0 + tok) * st + (size_t)h * sh;
-    i32x4 raw[4];
-    load8<XT>(src, base + p, raw);
-    load8<XT>(src, base + q, raw + 2);
-    unpack8<XT>(raw, x[j]);
-    unpack8<XT>(raw + 2, x[j] + 8);
-    if (g < (half >> 3)) {
-      float2 cs[8];
+    unit_groups<8>(gs[j], half, D, p, q);
+    const size_t krow = (size_t)(row0 + tok[j]) * a.ks_t + (size_t)h * a.ks_h;
+    const size_t vrow = (size_t)(row0 + tok[j]) * a.vs_t + (size_t)h * a.vs_h + 8 * gs[j];
+    ka[j] = load_vec<XT, 8>(a.k, krow + p);
+    kb[j] = load_vec<XT, 8>(a.k, krow + q);
+    va[j] = load_vec<XT, 8>(a.v, vrow);
+    vb[j] = load_vec<XT, 8>(a.v, vrow + (D >> 1));
+  }
+  if ((unsigned)page >= (unsigned)a.c.pages) return;
+  const size_t at = (size_t)page * a.c.H + h;
+  const float kwas = old > 0 ? a.c.ks[at] : 0.0f, vwas = old > 0 ? a.c.vs[at] : 0.0f;
+
+  auto angle = [&](int token, int pair) {
+    const int ax = rotate_axis(a.r, pair);
+    double turns = 0.0;
+    if (ax >= 0) {
+      const int pos = a.r.pos ? a.r.pos[(size_t)ax * a.r.T + row0 + token] : lo + token;
+      turns = (double)pos * ((double)a.r.inv_freq[pair] * kInvTwoPi);
+    }
+    return rotate_cs(turns, a.r.inverse);
+  };
+  if (CS) {
+    for (int i = threadIdx.x; i < n * half; i += blockDim.x) cs[i] = angle(i / half, i % half);
+    __syncthreads();
+  }
+
+  // in fp32, and the largest magnitudes
+  float x[UPT][16], y[UPT][16], kmax = 0.0f, vmax = 0.0f;
+#pragma unroll
+  for (int j = 0; j < UPT; ++j) {
+    unpack_vec(ka[j], x[j]);
+    unpack_vec(kb[j], x[j] + 8);
+    unpack_vec(va[j], y[j]);
+    unpack_vec(vb[j], y[j] + 8);
+    if (gs[j] < (half >> 3)) {
+      float2 w[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const int pr = 8 * g + i, ax = rotate_axis(a.r, pr);
-        double turns = 0.0;
-        if (ax >= 0) {
-          const int pos = a.r.pos ? a.r.pos[(size_t)ax * a.r.T + row0 + tok] : lo + tok;
-          turns = (double)pos * (double)a.r.inv_freq[pr] * kInvTwoPi;
-        }
-        cs[i] = rotate_cs(turns, a.r.inverse);
+        const int pair = unit_pair<8>(gs[j], i, half, a.r.interleaved);
+        w[i] = CS ? cs[tok[j] * half + pair] : angle(tok[j], pair);
       }
-      rotate_unit(x[j], x[j] + 8, cs, a.r.interleaved);
+      rotate_unit<8>(x[j], x[j] + 8, w, a.r.interleaved);
     }
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
-      const float m = __builtin_fabsf(x[j][i]);
-      amax = __builtin_fmaxf(amax, m < __builtin_inff() ? m : 0.0f);
+      kmax = __builtin_fmaxf(kmax, __builtin_fabsf(x[j][i]));
+      vmax = __builtin_fmaxf(vmax, __builtin_fabsf(y[j][i]));
     }
   }
-  amax = wave_max(amax);
-  if ((threadIdx.x & 63) == 0) wmax[threadIdx.x >> 6] = amax;
-  __syncthreads();
+  if (__any(kmax == __builtin_inff() || vmax == __builtin_inff())) {  // then of the finite ones
+    kmax = vmax = 0.0f;
 #pragma unroll
-  for (int w = 0; w < THREADS / 64; ++w) amax = __builtin_fmaxf(amax, wmax[w]);
+    for (int j = 0; j < UPT; ++j)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const float k = __builtin_fabsf(x[j][i]), v = __builtin_fabsf(y[j][i]);
+        kmax = __builtin_fmaxf(kmax, k < __builtin_inff() ? k : 0.0f);
+        vmax = __builtin_fmaxf(vmax, v < __builtin_inff() ? v : 0.0f);
+      }
+  }
+  kmax = wave_max(kmax);
+  vmax = wave_max(vmax);
+  if ((threadIdx.x & 63) == 0) {
+    wmax[0][threadIdx.x >> 6] = kmax;
+    wmax[1][threadIdx.x >> 6] = vmax;
+  }
+  __syncthreads();
+  for (int w = 0; w < TH >> 6; ++w) {
+    kmax = __builtin_fmaxf(kmax, wmax[0][sub * (TH >> 6) + w]);
+    vmax = __builtin_fmaxf(vmax, wmax[1][sub * (TH >> 6) + w]);
+  }
 
-  float* scale = (vals ? a.c.vs : a.c.ks) + (size_t)page * a.c.H + h;
-  uint8_t* codes = (vals ? a.c.vc : a.c.kc) + ((size_t)page * a.c.H + h) * ((size_t)D << a.c.lS);
-  const float was = old > 0 ? *scale : 0.0f;
-  const float need = page_scale(amax);
-  const float now = was > need ? was : need;
-  const float rcp = 1.0f / now;
-  if (old > 0 && now != was) {
-    // recode what was there: whole 16-byte groups of keys; of values, the
-    // bytes of earlier tokens (bytes past them go back unchanged, before the
-    // new ones are stored)
-    const float ratio = was / now;
-    const int groups = vals ? ((old + 15) >> 4) * D : (old * D) >> 4;
-    for (int i = threadIdx.x; i < groups; i += THREADS) {
-      uint4 w = *reinterpret_cast<uint4*>(codes + 16 * (size_t)i);
+  uint8_t* kc = a.c.kc + at * ((size_t)D << a.c.lS);
+  uint8_t* vc = a.c.vc + at * ((size_t)D << a.c.lS);
+  const float kneed = page_scale(kmax), vneed = page_scale(vmax);
+  const float know = kwas > kneed ? kwas : kneed, vnow = vwas > vneed ? vwas : vneed;
+  if (old > 0 && know != kwas) {  // recode what was there
+    const float ratio = kwas / know;
+    for (int i = t; i < (old * D) >> 4; i += TH) {
+      uint4 w = *reinterpret_cast<uint4*>(kc + 16 * (size_t)i);
+      *reinterpret_cast<uint4*>(kc + 16 * (size_t)i) =
+          make_uint4(recode4(w.x, ratio), recode4(w.y, ratio), recode4(w.z, ratio), recode4(w.w, ratio));
+    }
+  }
+  if (old > 0 && vnow != vwas) {
+    // the bytes of earlier tokens; those past them go back unchanged, before
+    // the new ones are stored
+    const float ratio = vwas / vnow;
+    for (int i = t; i < ((old + 15) >> 4) * D; i += TH) {
+      uint4 w = *reinterpret_cast<uint4*>(vc + 16 * (size_t)i);
       uint32_t* c = reinterpret_cast<uint32_t*>(&w);
-      const int keep = vals ? old - 16 * (i / D) : 16;  // bytes of earlier tokens
+      const int keep = old - 16 * (i / D);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const int k = keep - 4 * j;
         const uint32_t mask = k >= 4 ? 0xffffffffu : (k <= 0 ? 0u : (1u << (8 * k)) - 1u);
         c[j] = (recode4(c[j], ratio) & mask) | (c[j] & ~mask);
       }
-      *reinterpret_cast<uint4*>(codes + 16 * (size_t)i) = w;
+      *reinterpret_cast<uint4*>(vc + 16 * (size_t)i) = w;
     }
   }
-  __syncthreads();  // every thread has read *scale; recoded bytes are stored
-  if (threadIdx.x == 0) *scale = now;
-
+  const float kr = 1.0f / know, vr = 1.0f / vnow;
 #pragma unroll
   for (int j = 0; j < UPT; ++j) {
-    const int u = j * THREADS + threadIdx.x;
-    if (u >= units) continue;
-    const int tok = u / upd, g = u - tok * upd;
+    if (j * TH + t >= units) continue;
     int p, q;
-    unit_groups(g, half, a.r.interleaved, p, q);
-    uint32_t w[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) w[i] = codes4(x[j] + 4 * i, rcp);
-    uint8_t* row = (vals ? tile + (size_t)tok * D : codes + (size_t)(old + tok) * D);
-    *reinterpret_cast<uint2*>(row + p) = make_uint2(w[0], w[1]);
-    *reinterpret_cast<uint2*>(row + q) = make_uint2(w[2], w[3]);
+    unit_groups<8>(gs[j], half, D, p, q);
+    uint8_t* row = kc + (size_t)(old + tok[j]) * D;
+    *reinterpret_cast<uint2*>(row + p) = make_uint2(codes4(x[j], kr), codes4(x[j] + 4, kr));
+    *reinterpret_cast<uint2*>(row + q) = make_uint2(codes4(x[j] + 8, kr), codes4(x[j] + 12, kr));
+    row = tile + (size_t)tok[j] * D + 8 * gs[j];
+    *reinterpret_cast<uint2*>(row) = make_uint2(codes4(y[j], vr), codes4(y[j] + 4, vr));
+    *reinterpret_cast<uint2*>(row + (D >> 1)) = make_uint2(codes4(y[j] + 8, vr), codes4(y[j] + 12, vr));
   }
-  if (!vals) return;
-  __syncthreads();
-  // values: one 16-byte group (block of 16 tokens, channel) per thread and step
-  const int blk0 = old >> 4, blks = ((old + n - 1) >> 4) - blk0 + 1;
-  for (int i = threadIdx.x; i < blks * D; i += THREADS) {
-    const int blk = blk0 + i / D, d = i % D;
-    uint8_t* to = codes + ((size_t)blk * D + d) * 16;
-    const int t0 = 16 * blk - old;  // first token of the block, among the new ones
+  if (t == 0) {  // every thread of the head has long read the old ones
+    a.c.ks[at] = know;
+    a.c.vs[at] = vnow;
+  }
+  __syncthreads();  // the values' codes are in LDS, the recoded bytes in the page
+  const int blk0 = old >> 4, blks = ((old + n - 1) >> 4) - blk0 + 1, quads = D >> 2;
+  for (int i = t; i < blks * quads; i += TH) {
+    const int blk = i / quads, d = 4 * (i - blk * quads), t0 = 16 * (blk0 + blk) - old;  // its first token, among the new
+    uint8_t* to = vc + ((size_t)(blk0 + blk) * D + d) * 16;
     if (t0 >= 0 && t0 + 16 <= n) {
-      uint32_t w[4] = {0, 0, 0, 0};
+      uint32_t in[4][4], w[4][4];
 #pragma unroll
-      for (int k = 0; k < 16; ++k) w[k >> 2] |= (uint32_t)tile[(size_t)(t0 + k) * D + d] << (8 * (k & 3));
-      *reinterpret_cast<uint4*>(to) = make_uint4(w[0], w[1], w[2], w[3]);
+      for (int k = 0; k < 16; ++k) in[k >> 2][k & 3] = *reinterpret_cast<uint32_t*>(tile + (size_t)(t0 + k) * D + d);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) transpose4(in[k], w[k]);
+#pragma unroll
+      for (int c = 0; c < 4; ++c) *reinterpret_cast<uint4*>(to + 16 * c) = make_uint4(w[0][c], w[1][c], w[2][c], w[3][c]);
     } else {
-      for (int k = t0 < 0 ? -t0 : 0; k < 16 && t0 + k < n; ++k) to[k] = tile[(size_t)(t0 + k) * D + d];
+      for (int k = t0 < 0 ? -t0 : 0; k < 16 && t0 + k < n; ++k)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) to[16 * c + k] = tile[(size_t)(t0 + k) * D + d + c];
     }
   }
-}
-
-template <int XT, int THREADS, int UPT>
-static int append_launch(const AppendArgs& a, int rows, hipStream_t st) {
-  const size_t lds = (size_t)rows * a.c.D;  // at most 32 KB
-  hipLaunchKernelGGL((kv_append_kernel<XT, THREADS, UPT>), dim3((unsigned)a.units, (unsigned)a.c.H, 2), dim3(THREADS),
-                     lds, st, a);
-  return (int)hipGetLastError();
 }
 
 template <int XT>
-static int append_pick(const AppendArgs& a, hipStream_t st) {
-  const int S = 1 << a.c.lS;
-  const int rows = a.b.cu_q ? S : 1;  // new tokens of a page, at most
-  const int units = rows * (a.c.D / 16);
-  if (units <= 64) return append_launch<XT, 64, 1>(a, rows, st);
-  if (units <= 256) return append_launch<XT, 256, 1>(a, rows, st);
-  if (units <= 512) return append_launch<XT, 256, 2>(a, rows, st);
-  if (units <= 1024) return append_launch<XT, 512, 2>(a, rows, st);
-  return append_launch<XT, 1024, 2>(a, rows, st);  // S <= 128, D <= 256: at most 2048 units
+static int append_pick(AppendArgs& a, hipStream_t st) {
+  a.rows = a.b.cu_q ? 1 << a.c.lS : 1;  // new tokens of a page, at most
+  const int units = a.rows * (a.c.D / 16);
+  int TH = 64;  // threads of a head: two units each, at most
+  while (2 * TH < units) TH *= 2;
+  const size_t angles = (size_t)a.rows * a.r.half * sizeof(float2);
+  const size_t most = 60 << 10;  // LDS of a workgroup
+  const bool cs = angles > 0 && (size_t)a.rows * a.c.D + angles <= most;
+  // heads of a workgroup: they share the angles, as long as every CU has work
+  a.HG = 1;
+  while (cs && a.HG < 4 && a.c.H % (2 * a.HG) == 0 && 2 * a.HG * TH <= kAppendThreads &&
+         (size_t)2 * a.HG * a.rows * a.c.D + angles <= most &&
+         (long long)a.units * a.c.H / (2 * a.HG) >= 2 * device_cu_count())
+    a.HG *= 2;
+  const size_t lds = (size_t)a.HG * a.rows * a.c.D + (cs ? angles : 0);
+  const dim3 grid((unsigned)a.units, (unsigned)(a.c.H / a.HG)), block((unsigned)(TH * a.HG));
+  if (units <= TH) {
+    if (cs)
+      hipLaunchKernelGGL((kv_append_kernel<XT, 1, true>), grid, block, lds, st, a);
+    else
+      hipLaunchKernelGGL((kv_append_kernel<XT, 1, false>), grid, block, lds, st, a);
+  } else if (cs) {
+    hipLaunchKernelGGL((kv_append_kernel<XT, 2, true>), grid, block, lds, st, a);
+  } else {
+    hipLaunchKernelGGL((kv_append_kernel<XT, 2, false>), grid, block, lds, st, a);
+  }
+  return (int)hipGetLastError();
 }
 
 int launch_kv_append(const PagedArgs& c, const BatchArgs& b, const void* k, long long ks_t, long long ks_h,

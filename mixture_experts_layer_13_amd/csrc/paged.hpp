@@ -52,12 +52,12 @@ __device__ __forceinline__ Seq load_seq(const BatchArgs& a, int lS, int b) {
   return s;
 }
 
-// Inclusive prefix sum over the workgroup's threads; *total the whole sum.
-// scratch: one int per wave in LDS.  Ends with a barrier, so that it can be
-// called again at once.
-template <int THREADS>
+// Inclusive prefix sum over the workgroup's threads (WAVES waves; 0: as many
+// as the launch has); *total the whole sum.  scratch: one int per wave in LDS.
+// Ends with a barrier, so that it can be called again at once.
+template <int WAVES>
 __device__ __forceinline__ int block_scan(int v, int* scratch, int* total) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, waves = WAVES ? WAVES : (int)blockDim.x >> 6;
 #pragma unroll
   for (int o = 1; o < 64; o <<= 1) {
     const int up = __shfl_up(v, o, 64);
@@ -66,8 +66,7 @@ __device__ __forceinline__ int block_scan(int v, int* scratch, int* total) {
   if (lane == 63) scratch[wave] = v;
   __syncthreads();
   int before = 0, all = 0;
-#pragma unroll
-  for (int w = 0; w < THREADS / 64; ++w) {
+  for (int w = 0; w < waves; ++w) {
     const int x = scratch[w];
     before += w < wave ? x : 0;
     all += x;

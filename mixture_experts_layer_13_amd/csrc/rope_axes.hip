@@ -5,10 +5,10 @@
 // projection is rotated where it lies, and out may be x.
 //
 // Bytes bound it: x is read and out written once.  A workgroup takes `tb`
-// tokens; its threads issue the loads of up to kUnits units of 16 values
-// each, compute the tokens' angles into LDS while these are in flight (one
-// fp64 product and one sincospi per token and pair, shared by every head),
-// and after one barrier rotate and store.  Each thread reads both halves of
+// tokens; its threads issue the loads of up to kRaUnits pairs of 16-byte
+// vectors each, compute the tokens' angles into LDS while these are in flight
+// (once per token and pair, for every head), and after one barrier rotate and
+// store.  Each thread reads both halves of
 // its pairs before it writes them, which is what allows out == x.
 #include "launch.hpp"
 #include "rotate.hpp"
@@ -16,7 +16,7 @@
 namespace moe {
 
 constexpr int kRaThreads = 256;
-constexpr int kRaUnits = 4;           // units of 16 values a thread holds at once
+constexpr int kRaUnits = 4;           // pairs of vectors a thread holds at once
 constexpr int kRaMaxAngles = 4096;    // LDS: {cos, sin} of at most this many (token, pair)
 
 struct RopeAxesArgs {
@@ -27,17 +27,21 @@ struct RopeAxesArgs {
   RotateArgs r;
 };
 
-template <int OT>
-__device__ __forceinline__ void store8(void* base, size_t idx, const float v[8]) {
+template <int OT, int E>
+__device__ __forceinline__ void store_vec(void* base, size_t idx, const float* v) {
   if (OT == DT_BF16) {
-    uint32_t w[4];
+    uint32_t w[E / 2];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) w[j] = pack_bf16x2(v[2 * j], v[2 * j + 1]);
-    *reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(base) + idx) = make_uint4(w[0], w[1], w[2], w[3]);
+    for (int j = 0; j < E / 2; ++j) w[j] = pack_bf16x2(v[2 * j], v[2 * j + 1]);
+    uint16_t* p = reinterpret_cast<uint16_t*>(base) + idx;
+    if (E == 8)
+      *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[E / 2 - 2], w[E / 2 - 1]);
+    else
+      *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
   } else {
-    float* p = reinterpret_cast<float*>(base) + idx;
-    *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
-    *reinterpret_cast<float4*>(p + 4) = make_float4(v[4], v[5], v[6], v[7]);
+#pragma unroll
+    for (int j = 0; j < E; j += 4)
+      *reinterpret_cast<float4*>(reinterpret_cast<float*>(base) + idx + j) = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
   }
 }
 
@@ -46,9 +50,10 @@ __global__ __launch_bounds__(kRaThreads) void rope_axes_kernel(RopeAxesArgs a) {
   __shared__ float2 cs[kRaMaxAngles];
   const int t0 = blockIdx.x * a.tb;
   const int tn = a.T - t0 < a.tb ? a.T - t0 : a.tb;
-  const int upd = a.D >> 4, upt = a.nH * upd, units = tn * upt;
+  constexpr int E = XT == DT_BF16 ? 8 : 4;  // values of a 16-byte load
+  const int upd = a.D / (2 * E), upt = a.nH * upd, units = tn * upt;
   for (int base = 0; base < units; base += kRaThreads * kRaUnits) {
-    i32x4 raw[kRaUnits][4];
+    RawVec<XT, E> ra[kRaUnits], rb[kRaUnits];
     int tok[kRaUnits], hd[kRaUnits], gs[kRaUnits];
 #pragma unroll
     for (int s = 0; s < kRaUnits; ++s) {
@@ -59,17 +64,17 @@ __global__ __launch_bounds__(kRaThreads) void rope_axes_kernel(RopeAxesArgs a) {
       hd[s] = r / upd;
       gs[s] = r - hd[s] * upd;
       int p, q;
-      unit_groups(gs[s], a.r.half, a.r.interleaved, p, q);
+      unit_groups<E>(gs[s], a.r.half, a.D, p, q);
       const size_t row = (size_t)(t0 + tok[s]) * a.xs_t + (size_t)hd[s] * a.xs_h;
-      load8<XT>(a.x, row + p, raw[s]);
-      load8<XT>(a.x, row + q, raw[s] + 2);
+      ra[s] = load_vec<XT, E>(a.x, row + p);
+      rb[s] = load_vec<XT, E>(a.x, row + q);
     }
     if (base == 0) {
       for (int i = threadIdx.x; i < tn * a.r.half; i += kRaThreads) {
         const int t = i / a.r.half, pr = i - t * a.r.half, ax = rotate_axis(a.r, pr);
         double turns = 0.0;
         if (ax >= 0)
-          turns = (double)a.r.pos[(size_t)ax * a.r.T + t0 + t] * (double)a.r.inv_freq[pr] * kInvTwoPi;
+          turns = (double)a.r.pos[(size_t)ax * a.r.T + t0 + t] * ((double)a.r.inv_freq[pr] * kInvTwoPi);
         cs[i] = rotate_cs(turns, a.r.inverse);
       }
       __syncthreads();
@@ -77,15 +82,20 @@ __global__ __launch_bounds__(kRaThreads) void rope_axes_kernel(RopeAxesArgs a) {
 #pragma unroll
     for (int s = 0; s < kRaUnits; ++s) {
       if (base + s * kRaThreads + (int)threadIdx.x >= units) continue;
-      float va[8], vb[8];
-      unpack8<XT>(raw[s], va);
-      unpack8<XT>(raw[s] + 2, vb);
-      if (gs[s] < (a.r.half >> 3)) rotate_unit(va, vb, cs + tok[s] * a.r.half + 8 * gs[s], a.r.interleaved);
+      float va[E], vb[E];
+      unpack_vec(ra[s], va);
+      unpack_vec(rb[s], vb);
+      if (gs[s] < a.r.half / E) {
+        float2 w[E];
+#pragma unroll
+        for (int i = 0; i < E; ++i) w[i] = cs[tok[s] * a.r.half + unit_pair<E>(gs[s], i, a.r.half, a.r.interleaved)];
+        rotate_unit<E>(va, vb, w, a.r.interleaved);
+      }
       int p, q;
-      unit_groups(gs[s], a.r.half, a.r.interleaved, p, q);
+      unit_groups<E>(gs[s], a.r.half, a.D, p, q);
       const size_t row = (size_t)(t0 + tok[s]) * a.os_t + (size_t)hd[s] * a.os_h;
-      store8<OT>(a.out, row + p, va);
-      store8<OT>(a.out, row + q, vb);
+      store_vec<OT, E>(a.out, row + p, va);
+      store_vec<OT, E>(a.out, row + q, vb);
     }
   }
 }
@@ -107,7 +117,7 @@ int launch_rope_axes(const void* x, int xt, long long xs_t, long long xs_h, cons
   a.r = RotateArgs{pos, pair_axis, inv_freq, T, axes, R / 2, interleaved, inverse};
   // tokens per workgroup: enough units for its threads, unless that would
   // leave compute units without a workgroup
-  const int upt = nH * (D / 16);
+  const int upt = nH * (D / (xt == DT_BF16 ? 16 : 8));
   int tb = 1;
   while (tb < 64 && 2 * tb * upt <= kRaThreads * kRaUnits && 2 * tb * (R / 2) <= kRaMaxAngles &&
          (T + 2 * tb - 1) / (2 * tb) >= 2 * device_cu_count())

@@ -22,12 +22,29 @@ struct RotateArgs {
 
 constexpr double kInvTwoPi = 0.15915494309189533577;
 
-// {cos, sin} of turns * 2 pi, the turn given in fp64.
+// {cos, sin} of turns * 2 pi.  The turn's fraction t in [-1/2, 1/2] is the
+// quarter q = rint(4 t) plus r in [-1/8, 1/8] (the subtraction is exact), and
+// sin and cos of 2 pi r are their Taylor series in r to the powers 9 and 10
+// (first terms left out: 3e-9 and 2e-10 of the result), with coefficients
+// (2 pi)^n / n!.  About 30 instructions, half of what sincospi of the math
+// library takes; within 2 ulp.
 __device__ __forceinline__ float2 rotate_cs(double turns, int inverse) {
-  const float frac = (float)(turns - __builtin_rint(turns));
-  float s, c;
-  sincospif(2.0f * frac, &s, &c);
-  return make_float2(c, inverse ? -s : s);
+  const float t = (float)(turns - __builtin_rint(turns));
+  const float q = __builtin_rintf(4.0f * t), r = __builtin_fmaf(-0.25f, q, t), z = r * r;
+  float s = __builtin_fmaf(z, 42.058693944897654f, -76.705859753061386f);
+  s = __builtin_fmaf(z, s, 81.605249276075051f);
+  s = __builtin_fmaf(z, s, -41.341702240399755f);
+  s = r * __builtin_fmaf(z, s, 6.2831853071795865f);
+  float c = __builtin_fmaf(z, -26.426256783374398f, 60.244641371876661f);
+  c = __builtin_fmaf(z, c, -85.456817206693723f);
+  c = __builtin_fmaf(z, c, 64.939394022668296f);
+  c = __builtin_fmaf(z, c, -19.739208802178716f);
+  c = __builtin_fmaf(z, c, 1.0f);
+  // a quarter on: (c, s) -> (-s, c); q and q + 4 are the same
+  const int k = (int)q;
+  const float co = k & 1 ? s : c, si = k & 1 ? c : s;
+  const uint32_t nc = (uint32_t)((k + 1) & 2) << 30, ns = ((uint32_t)(k & 2) << 30) ^ ((uint32_t)inverse << 31);
+  return make_float2(__uint_as_float(__float_as_uint(co) ^ nc), __uint_as_float(__float_as_uint(si) ^ ns));
 }
 
 // Axis of pair i; -1 (the pair is left unturned) when the map names none.
@@ -37,52 +54,39 @@ __device__ __forceinline__ int rotate_axis(const RotateArgs& r, int i) {
   return (unsigned)a < (unsigned)r.axes ? a : -1;
 }
 
-// Raw bits of 8 consecutive values at p: one 16-byte load for bf16, two for f32.
-template <int XT>
-__device__ __forceinline__ void load8(const void* base, size_t idx, i32x4 raw[2]) {
-  if (XT == DT_BF16) {
-    raw[0] = ld16(reinterpret_cast<const uint16_t*>(base) + idx);
+// A head's values are handled as pairs of vectors of E values: vector g of a
+// half and its counterpart half a stretch on, for the rotated values
+// (stretch 2 half) and the passed ones behind them alike.  With halves pairing
+// the two vectors hold the members of pairs E g..; interleaved, each holds E/2
+// whole pairs, from E g / 2 and half / 2 + E g / 2 on.  Either way consecutive
+// g are consecutive in memory.  First indices of pair-of-vectors g's two.
+template <int E>
+__device__ __forceinline__ void unit_groups(int g, int half, int D, int& p, int& q) {
+  const int rot = half / E;
+  if (g < rot) {
+    p = E * g;
+    q = half + E * g;
   } else {
-    raw[0] = ld16(reinterpret_cast<const float*>(base) + idx);
-    raw[1] = ld16(reinterpret_cast<const float*>(base) + idx + 4);
+    p = 2 * half + E * (g - rot);
+    q = p + (D >> 1) - half;
   }
 }
 
-template <int XT>
-__device__ __forceinline__ void unpack8(const i32x4 raw[2], float v[8]) {
-  if (XT == DT_BF16) {
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      v[2 * j] = bf16_bits_to_f32((uint32_t)raw[0][j] & 0xffffu);
-      v[2 * j + 1] = bf16_bits_to_f32((uint32_t)raw[0][j] >> 16);
-    }
-  } else {
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      v[j] = __int_as_float(raw[0][j]);
-      v[4 + j] = __int_as_float(raw[1][j]);
-    }
-  }
+// Pair of {cos, sin} number i (0..E-1) of unit g.
+template <int E>
+__device__ __forceinline__ int unit_pair(int g, int i, int half, int interleaved) {
+  return interleaved ? (i < E / 2 ? E / 2 * g + i : half / 2 + E / 2 * (g - 1) + i) : E * g + i;
 }
 
-// A unit is 16 values of one head: with halves pairing the first D/16 units'
-// rotated part pairs values 8g.. with half + 8g.., interleaved and
-// pass-through units are 16 consecutive values.  First indices of its two
-// groups of 8 (rot_units = half / 8 units are rotated).
-__device__ __forceinline__ void unit_groups(int g, int half, int interleaved, int& p, int& q) {
-  const bool halves = !interleaved && g < (half >> 3);
-  p = halves ? 8 * g : 16 * g;
-  q = halves ? half + 8 * g : 16 * g + 8;
-}
-
-// Rotates a unit's 16 values in place (a = first group of 8, b = second);
-// cs[j] is {cos, sin} of pair 8g + j.
-__device__ __forceinline__ void rotate_unit(float a[8], float b[8], const float2* cs, int interleaved) {
+// Rotates a unit in place (a: first vector, b: second); cs[i] is {cos, sin} of
+// its pair number i.
+template <int E>
+__device__ __forceinline__ void rotate_unit(float* a, float* b, const float2* cs, int interleaved) {
   if (interleaved) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
+    for (int j = 0; j < E / 2; ++j) {
       const float u0 = a[2 * j], v0 = a[2 * j + 1], u1 = b[2 * j], v1 = b[2 * j + 1];
-      const float2 c0 = cs[j], c1 = cs[4 + j];
+      const float2 c0 = cs[j], c1 = cs[E / 2 + j];
       a[2 * j] = __builtin_fmaf(u0, c0.x, -(v0 * c0.y));
       a[2 * j + 1] = __builtin_fmaf(v0, c0.x, u0 * c0.y);
       b[2 * j] = __builtin_fmaf(u1, c1.x, -(v1 * c1.y));
@@ -90,10 +94,38 @@ __device__ __forceinline__ void rotate_unit(float a[8], float b[8], const float2
     }
   } else {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
+    for (int j = 0; j < E; ++j) {
       const float u = a[j], v = b[j];
       a[j] = __builtin_fmaf(u, cs[j].x, -(v * cs[j].y));
       b[j] = __builtin_fmaf(v, cs[j].x, u * cs[j].y);
+    }
+  }
+}
+
+// Values idx.. of the tensor at base: E of them (a multiple of a 16-byte load).
+template <int XT, int E>
+struct RawVec {
+  i32x4 w[E * (XT == DT_BF16 ? 2 : 4) / 16];
+};
+
+template <int XT, int E>
+__device__ __forceinline__ RawVec<XT, E> load_vec(const void* base, size_t idx) {
+  RawVec<XT, E> r;
+  const char* at = reinterpret_cast<const char*>(base) + idx * (XT == DT_BF16 ? 2 : 4);
+#pragma unroll
+  for (int k = 0; k < (int)(sizeof(r.w) / 16); ++k) r.w[k] = ld16(at + 16 * k);
+  return r;
+}
+
+template <int XT, int E>
+__device__ __forceinline__ void unpack_vec(const RawVec<XT, E>& r, float* v) {
+#pragma unroll
+  for (int j = 0; j < E; ++j) {
+    if (XT == DT_BF16) {
+      const uint32_t w = (uint32_t)r.w[j >> 3][(j >> 1) & 3];
+      v[j] = __uint_as_float(j & 1 ? w & 0xffff0000u : w << 16);
+    } else {
+      v[j] = __int_as_float(r.w[j >> 2][j & 3]);
     }
   }
 }
