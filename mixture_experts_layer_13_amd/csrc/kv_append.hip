@@ -14,15 +14,13 @@
 // A scale never shrinks while the page is in use, which makes the append of
 // the same tokens at the same place the same cache bit for bit.
 //
-// A workgroup takes one touched page and HG heads (blockDim / HG threads each),
-// keys and values.  It reads its tokens once, 16 values per thread and unit,
-// and has every load in flight before the first is used; meanwhile it computes
-// the tokens' angles into LDS, once for all its heads (the fp64 reduction and
-// sincospi, not the bytes, would bound a prompt's append otherwise); then it
-// rotates, reduces the maxima and stores the codes.  Values are stored channel
-// by channel (paged.hpp): through LDS, four channels by 16 tokens at a time
-// transposed with byte permutes, where a block of 16 tokens is all new; byte
-// by byte otherwise, which leaves every other token's bytes alone.
+// A workgroup takes one touched page and head, keys and values.  It reads its
+// tokens once, 16 values per thread and unit, with every load in flight before
+// the first is used, rotates keys in registers (a thread owns whole pairs),
+// reduces the maxima and stores the codes.  Values are stored channel by
+// channel (paged.hpp): through LDS, four channels by 16 tokens at a time
+// transposed with byte permutes, where a block of 16 tokens is all new; byte by
+// byte otherwise, which leaves every other token's bytes alone.
 #include "launch.hpp"
 #include "paged.hpp"
 #include "rotate.hpp"
@@ -39,7 +37,8 @@ struct AppendArgs {
   long long ks_t, ks_h, vs_t, vs_h;  // strides in elements
   RotateArgs r;                      // r.half == 0: no rotation
   int units;                         // upper bound of (sequence, page) pairs
-  int HG, rows;                      // heads of a workgroup; new tokens of a page, at most
+  uint32_t upd_magic;                // t / (D / 16) = t upd_magic >> 20 for t < 1024
+  int unit_toks, unit_rest;          // threads / (D / 16), and the remainder
 };
 
 // The smallest power of two s with 448 s >= amax: 448 = 1.75 * 2^8, so adding
@@ -77,36 +76,33 @@ __device__ __forceinline__ void transpose4(const uint32_t in[4], uint32_t out[4]
   out[3] = __builtin_amdgcn_perm(d, b, 0x07060302u);
 }
 
-// XT: type of k and v; UPT: units of 16 values per thread; CS: angles in LDS.
-template <int XT, int UPT, bool CS>
+// XT: type of k and v; UPT: units of 16 values per thread.
+template <int XT, int UPT>
 __global__ __launch_bounds__(kAppendThreads) void kv_append_kernel(AppendArgs a) {
-  extern __shared__ __align__(16) uint8_t smem[];  // [HG][rows][D] codes of values, then [rows][half] {cos, sin}
+  extern __shared__ __align__(16) uint8_t tile[];  // [rows][D] codes of values
   __shared__ int scan[kAppendThreads / 64];
   __shared__ int found[2];
   __shared__ float wmax[2][kAppendThreads / 64];
-  const int S = 1 << a.c.lS, D = a.c.D, TH = blockDim.x / a.HG;
-  const int sub = threadIdx.x / TH, t = threadIdx.x - sub * TH, h = blockIdx.y * a.HG + sub;
-  uint8_t* tile = smem + (size_t)sub * a.rows * D;
-  float2* cs = reinterpret_cast<float2*>(smem + (size_t)a.HG * a.rows * D);
+  const int S = 1 << a.c.lS, D = a.c.D, TH = blockDim.x, t = threadIdx.x, unit = blockIdx.x, h = blockIdx.y;
 
   // the workgroup's sequence and page
-  int b = blockIdx.x, rank = 0;
+  int b = unit, rank = 0;
   if (a.b.cu_q) {
-    if (threadIdx.x == 0) found[0] = -1;
+    if (t == 0) found[0] = -1;
     __syncthreads();
     int before = 0;
-    for (int base = 0; base < a.b.B && before <= (int)blockIdx.x; base += blockDim.x) {
+    for (int base = 0; base < a.b.B && before <= unit; base += TH) {
       int n = 0;
-      if (base + (int)threadIdx.x < a.b.B) {
-        const Seq s = load_seq(a.b, a.c.lS, base + threadIdx.x);
+      if (base + t < a.b.B) {
+        const Seq s = load_seq(a.b, a.c.lS, base + t);
         const int p0 = s.kv - s.q > 0 ? s.kv - s.q : 0;
         if (s.q > 0 && s.lim > p0) n = ((s.lim - 1) >> a.c.lS) - (p0 >> a.c.lS) + 1;
       }
       int total;
       const int end = before + block_scan<0>(n, scan, &total);
-      if ((int)blockIdx.x >= end - n && (int)blockIdx.x < end) {
-        found[0] = base + threadIdx.x;
-        found[1] = blockIdx.x - (end - n);
+      if (unit >= end - n && unit < end) {
+        found[0] = base + t;
+        found[1] = unit - (end - n);
       }
       before += total;
     }
@@ -127,20 +123,24 @@ __global__ __launch_bounds__(kAppendThreads) void kv_append_kernel(AppendArgs a)
   const int page = a.b.table[(size_t)b * a.b.max_pages + pg];
 
   // the new tokens: every load first
-  const int upd = D >> 4, units = n * upd, half = a.r.half;
+  const int upd = D >> 4, units = n * upd, half = a.r.half, first = (int)((t * a.upd_magic) >> 20);
   RawVec<XT, 8> ka[UPT], kb[UPT], va[UPT], vb[UPT];
-  int tok[UPT], gs[UPT];
+  int tok[UPT], gs[UPT], at_p[UPT], at_q[UPT], pos[UPT];
 #pragma unroll
   for (int j = 0; j < UPT; ++j) {
-    const int u = j * TH + t < units ? j * TH + t : 0;
-    tok[j] = u / upd;
-    gs[j] = u - tok[j] * upd;
-    int p, q;
-    unit_groups<8>(gs[j], half, D, p, q);
+    // unit j TH + t; past the last, the same values of token 0, which change no maximum
+    int k = first + j * a.unit_toks, g = t - first * upd + j * a.unit_rest;
+    k += g >= upd;
+    g -= g >= upd ? upd : 0;
+    tok[j] = k < n ? k : 0;
+    gs[j] = g;
+    unit_groups<8>(gs[j], half, D, at_p[j], at_q[j]);
+    pos[j] = lo + tok[j];
+    if (half && a.r.pos) pos[j] = a.r.pos[row0 + tok[j]];  // on the first axis
     const size_t krow = (size_t)(row0 + tok[j]) * a.ks_t + (size_t)h * a.ks_h;
     const size_t vrow = (size_t)(row0 + tok[j]) * a.vs_t + (size_t)h * a.vs_h + 8 * gs[j];
-    ka[j] = load_vec<XT, 8>(a.k, krow + p);
-    kb[j] = load_vec<XT, 8>(a.k, krow + q);
+    ka[j] = load_vec<XT, 8>(a.k, krow + at_p[j]);
+    kb[j] = load_vec<XT, 8>(a.k, krow + at_q[j]);
     va[j] = load_vec<XT, 8>(a.v, vrow);
     vb[j] = load_vec<XT, 8>(a.v, vrow + (D >> 1));
   }
@@ -148,37 +148,31 @@ __global__ __launch_bounds__(kAppendThreads) void kv_append_kernel(AppendArgs a)
   const size_t at = (size_t)page * a.c.H + h;
   const float kwas = old > 0 ? a.c.ks[at] : 0.0f, vwas = old > 0 ? a.c.vs[at] : 0.0f;
 
-  auto angle = [&](int token, int pair) {
-    const int ax = rotate_axis(a.r, pair);
-    double turns = 0.0;
-    if (ax >= 0) {
-      const int pos = a.r.pos ? a.r.pos[(size_t)ax * a.r.T + row0 + token] : lo + token;
-      turns = (double)pos * ((double)a.r.inv_freq[pair] * kInvTwoPi);
-    }
-    return rotate_cs(turns, a.r.inverse);
-  };
-  if (CS) {
-    for (int i = threadIdx.x; i < n * half; i += blockDim.x) cs[i] = angle(i / half, i % half);
-    __syncthreads();
-  }
-
   // in fp32, and the largest magnitudes
   float x[UPT][16], y[UPT][16], kmax = 0.0f, vmax = 0.0f;
+  TurnFreq freq[8];
 #pragma unroll
   for (int j = 0; j < UPT; ++j) {
+    float2 cs[8];
+    const bool turn = gs[j] < (half >> 3);
+    if (turn) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int pair = unit_pair<8>(gs[j], i, half, a.r.interleaved);
+        if (XT == DT_F32 || j == 0 || a.unit_rest) freq[i] = turn_freq(a.r.inv_freq[pair]);  // else the same pairs as before
+        int p = pos[j];
+        if (a.r.pair_axis) {
+          const int ax = rotate_axis(a.r, pair);
+          p = ax < 0 ? 0 : (a.r.pos ? a.r.pos[(size_t)ax * a.r.T + row0 + tok[j]] : p);
+        }
+        cs[i] = rotate_cs(p, freq[i], a.r.inverse);
+      }
+    }
     unpack_vec(ka[j], x[j]);
     unpack_vec(kb[j], x[j] + 8);
     unpack_vec(va[j], y[j]);
     unpack_vec(vb[j], y[j] + 8);
-    if (gs[j] < (half >> 3)) {
-      float2 w[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int pair = unit_pair<8>(gs[j], i, half, a.r.interleaved);
-        w[i] = CS ? cs[tok[j] * half + pair] : angle(tok[j], pair);
-      }
-      rotate_unit<8>(x[j], x[j] + 8, w, a.r.interleaved);
-    }
+    if (turn) rotate_unit<8>(x[j], x[j] + 8, cs, a.r.interleaved);
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
       kmax = __builtin_fmaxf(kmax, __builtin_fabsf(x[j][i]));
@@ -198,14 +192,14 @@ __global__ __launch_bounds__(kAppendThreads) void kv_append_kernel(AppendArgs a)
   }
   kmax = wave_max(kmax);
   vmax = wave_max(vmax);
-  if ((threadIdx.x & 63) == 0) {
-    wmax[0][threadIdx.x >> 6] = kmax;
-    wmax[1][threadIdx.x >> 6] = vmax;
+  if ((t & 63) == 0) {
+    wmax[0][t >> 6] = kmax;
+    wmax[1][t >> 6] = vmax;
   }
   __syncthreads();
   for (int w = 0; w < TH >> 6; ++w) {
-    kmax = __builtin_fmaxf(kmax, wmax[0][sub * (TH >> 6) + w]);
-    vmax = __builtin_fmaxf(vmax, wmax[1][sub * (TH >> 6) + w]);
+    kmax = __builtin_fmaxf(kmax, wmax[0][w]);
+    vmax = __builtin_fmaxf(vmax, wmax[1][w]);
   }
 
   uint8_t* kc = a.c.kc + at * ((size_t)D << a.c.lS);
@@ -241,28 +235,26 @@ __global__ __launch_bounds__(kAppendThreads) void kv_append_kernel(AppendArgs a)
 #pragma unroll
   for (int j = 0; j < UPT; ++j) {
     if (j * TH + t >= units) continue;
-    int p, q;
-    unit_groups<8>(gs[j], half, D, p, q);
-    uint8_t* row = kc + (size_t)(old + tok[j]) * D;
-    *reinterpret_cast<uint2*>(row + p) = make_uint2(codes4(x[j], kr), codes4(x[j] + 4, kr));
-    *reinterpret_cast<uint2*>(row + q) = make_uint2(codes4(x[j] + 8, kr), codes4(x[j] + 12, kr));
-    row = tile + (size_t)tok[j] * D + 8 * gs[j];
+    uint8_t* row = kc + (old + tok[j]) * D;
+    *reinterpret_cast<uint2*>(row + at_p[j]) = make_uint2(codes4(x[j], kr), codes4(x[j] + 4, kr));
+    *reinterpret_cast<uint2*>(row + at_q[j]) = make_uint2(codes4(x[j] + 8, kr), codes4(x[j] + 12, kr));
+    row = tile + tok[j] * D + 8 * gs[j];
     *reinterpret_cast<uint2*>(row) = make_uint2(codes4(y[j], vr), codes4(y[j] + 4, vr));
     *reinterpret_cast<uint2*>(row + (D >> 1)) = make_uint2(codes4(y[j] + 8, vr), codes4(y[j] + 12, vr));
   }
-  if (t == 0) {  // every thread of the head has long read the old ones
+  if (t == 0) {  // every thread has read the old ones, before the barrier above
     a.c.ks[at] = know;
     a.c.vs[at] = vnow;
   }
-  __syncthreads();  // the values' codes are in LDS, the recoded bytes in the page
+  __syncthreads();  // the codes are in LDS, the recoded bytes in the page
   const int blk0 = old >> 4, blks = ((old + n - 1) >> 4) - blk0 + 1, quads = D >> 2;
   for (int i = t; i < blks * quads; i += TH) {
     const int blk = i / quads, d = 4 * (i - blk * quads), t0 = 16 * (blk0 + blk) - old;  // its first token, among the new
-    uint8_t* to = vc + ((size_t)(blk0 + blk) * D + d) * 16;
+    uint8_t* to = vc + ((blk0 + blk) * D + d) * 16;
     if (t0 >= 0 && t0 + 16 <= n) {
       uint32_t in[4][4], w[4][4];
 #pragma unroll
-      for (int k = 0; k < 16; ++k) in[k >> 2][k & 3] = *reinterpret_cast<uint32_t*>(tile + (size_t)(t0 + k) * D + d);
+      for (int k = 0; k < 16; ++k) in[k >> 2][k & 3] = *reinterpret_cast<uint32_t*>(tile + (t0 + k) * D + d);
 #pragma unroll
       for (int k = 0; k < 4; ++k) transpose4(in[k], w[k]);
 #pragma unroll
@@ -270,38 +262,26 @@ __global__ __launch_bounds__(kAppendThreads) void kv_append_kernel(AppendArgs a)
     } else {
       for (int k = t0 < 0 ? -t0 : 0; k < 16 && t0 + k < n; ++k)
 #pragma unroll
-        for (int c = 0; c < 4; ++c) to[16 * c + k] = tile[(size_t)(t0 + k) * D + d + c];
+        for (int c = 0; c < 4; ++c) to[16 * c + k] = tile[(t0 + k) * D + d + c];
     }
   }
 }
 
 template <int XT>
 static int append_pick(AppendArgs& a, hipStream_t st) {
-  a.rows = a.b.cu_q ? 1 << a.c.lS : 1;  // new tokens of a page, at most
-  const int units = a.rows * (a.c.D / 16);
-  int TH = 64;  // threads of a head: two units each, at most
+  const int rows = a.b.cu_q ? 1 << a.c.lS : 1;  // new tokens of a page, at most
+  const int units = rows * (a.c.D / 16);
+  int TH = 64;  // two units a thread, at most
   while (2 * TH < units) TH *= 2;
-  const size_t angles = (size_t)a.rows * a.r.half * sizeof(float2);
-  const size_t most = 60 << 10;  // LDS of a workgroup
-  const bool cs = angles > 0 && (size_t)a.rows * a.c.D + angles <= most;
-  // heads of a workgroup: they share the angles, as long as every CU has work
-  a.HG = 1;
-  while (cs && a.HG < 4 && a.c.H % (2 * a.HG) == 0 && 2 * a.HG * TH <= kAppendThreads &&
-         (size_t)2 * a.HG * a.rows * a.c.D + angles <= most &&
-         (long long)a.units * a.c.H / (2 * a.HG) >= 2 * device_cu_count())
-    a.HG *= 2;
-  const size_t lds = (size_t)a.HG * a.rows * a.c.D + (cs ? angles : 0);
-  const dim3 grid((unsigned)a.units, (unsigned)(a.c.H / a.HG)), block((unsigned)(TH * a.HG));
-  if (units <= TH) {
-    if (cs)
-      hipLaunchKernelGGL((kv_append_kernel<XT, 1, true>), grid, block, lds, st, a);
-    else
-      hipLaunchKernelGGL((kv_append_kernel<XT, 1, false>), grid, block, lds, st, a);
-  } else if (cs) {
-    hipLaunchKernelGGL((kv_append_kernel<XT, 2, true>), grid, block, lds, st, a);
-  } else {
-    hipLaunchKernelGGL((kv_append_kernel<XT, 2, false>), grid, block, lds, st, a);
-  }
+  a.upd_magic = (1u << 20) / (a.c.D / 16) + 1;
+  a.unit_toks = TH / (a.c.D / 16);
+  a.unit_rest = TH % (a.c.D / 16);
+  const size_t lds = (size_t)rows * a.c.D;  // at most 32 KB
+  const dim3 grid((unsigned)a.units, (unsigned)a.c.H), block((unsigned)TH);
+  if (units <= TH)
+    hipLaunchKernelGGL((kv_append_kernel<XT, 1>), grid, block, lds, st, a);
+  else
+    hipLaunchKernelGGL((kv_append_kernel<XT, 2>), grid, block, lds, st, a);
   return (int)hipGetLastError();
 }
 

@@ -72,10 +72,8 @@ __global__ __launch_bounds__(kRaThreads) void rope_axes_kernel(RopeAxesArgs a) {
     if (base == 0) {
       for (int i = threadIdx.x; i < tn * a.r.half; i += kRaThreads) {
         const int t = i / a.r.half, pr = i - t * a.r.half, ax = rotate_axis(a.r, pr);
-        double turns = 0.0;
-        if (ax >= 0)
-          turns = (double)a.r.pos[(size_t)ax * a.r.T + t0 + t] * ((double)a.r.inv_freq[pr] * kInvTwoPi);
-        cs[i] = rotate_cs(turns, a.r.inverse);
+        const int pos = ax >= 0 ? a.r.pos[(size_t)ax * a.r.T + t0 + t] : 0;
+        cs[i] = rotate_cs(pos, turn_freq(a.r.inv_freq[pr]), a.r.inverse);
       }
       __syncthreads();
     }

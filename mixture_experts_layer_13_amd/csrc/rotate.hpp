@@ -3,9 +3,10 @@
 //
 // Pair i of a token turns by positions[axis(i)][token] * inv_freq[i] radians.
 // In fp32 that product is off by half an ulp of the angle: 2^-8 rad at
-// position 2^17 times inv_freq 1, and more beyond.  So it is formed and
-// reduced in fp64 as turns (|position| < 2^24: the error stays below 2^-26
-// rad), and only the fraction of a turn, at most 1/2, goes on in fp32.
+// position 2^17 times inv_freq 1, and more beyond.  So it is formed as turns
+// from a frequency of two fp32 terms, and the whole turns are taken off the
+// leading product inside a fused multiply-add (|position| < 2^24 is exact in
+// fp32): only the fraction of a turn, at most 1/2, is ever rounded.
 #pragma once
 
 #include "common.hpp"
@@ -22,29 +23,28 @@ struct RotateArgs {
 
 constexpr double kInvTwoPi = 0.15915494309189533577;
 
-// {cos, sin} of turns * 2 pi.  The turn's fraction t in [-1/2, 1/2] is the
-// quarter q = rint(4 t) plus r in [-1/8, 1/8] (the subtraction is exact), and
-// sin and cos of 2 pi r are their Taylor series in r to the powers 9 and 10
-// (first terms left out: 3e-9 and 2e-10 of the result), with coefficients
-// (2 pi)^n / n!.  About 30 instructions, half of what sincospi of the math
-// library takes; within 2 ulp.
-__device__ __forceinline__ float2 rotate_cs(double turns, int inverse) {
-  const float t = (float)(turns - __builtin_rint(turns));
-  const float q = __builtin_rintf(4.0f * t), r = __builtin_fmaf(-0.25f, q, t), z = r * r;
-  float s = __builtin_fmaf(z, 42.058693944897654f, -76.705859753061386f);
-  s = __builtin_fmaf(z, s, 81.605249276075051f);
-  s = __builtin_fmaf(z, s, -41.341702240399755f);
-  s = r * __builtin_fmaf(z, s, 6.2831853071795865f);
-  float c = __builtin_fmaf(z, -26.426256783374398f, 60.244641371876661f);
-  c = __builtin_fmaf(z, c, -85.456817206693723f);
-  c = __builtin_fmaf(z, c, 64.939394022668296f);
-  c = __builtin_fmaf(z, c, -19.739208802178716f);
-  c = __builtin_fmaf(z, c, 1.0f);
-  // a quarter on: (c, s) -> (-s, c); q and q + 4 are the same
-  const int k = (int)q;
-  const float co = k & 1 ? s : c, si = k & 1 ? c : s;
-  const uint32_t nc = (uint32_t)((k + 1) & 2) << 30, ns = ((uint32_t)(k & 2) << 30) ^ ((uint32_t)inverse << 31);
-  return make_float2(__uint_as_float(__float_as_uint(co) ^ nc), __uint_as_float(__float_as_uint(si) ^ ns));
+// A frequency in turns per position, as two terms.
+struct TurnFreq {
+  float hi, lo;
+};
+
+__device__ __forceinline__ TurnFreq turn_freq(float inv_freq) {
+  // 1 / (2 pi) as two fp32 terms; the first product's rounding is recovered
+  constexpr float h = 0.15915494f, l = (float)(kInvTwoPi - (double)h);
+  const float hi = inv_freq * h;
+  return TurnFreq{hi, __builtin_fmaf(inv_freq, l, __builtin_fmaf(inv_freq, h, -hi))};
+}
+
+// {cos, sin} of the angle of position pos.  gfx950's sine and cosine take
+// turns, and on [-1/2, 1/2] are within 2^-22.9 of the exact values (measured
+// at every multiple of 2^-25 there); rounding the fraction adds at most
+// 2^-23.3, and the two products and the sum of a rotation 2^-24 each, so that a
+// rotated value is within 2^-21.7 (|u| + |v|).  A polynomial of the same error
+// takes five times as long, and an append was bound by it.
+__device__ __forceinline__ float2 rotate_cs(int pos, TurnFreq f, int inverse) {
+  const float x = (float)pos;
+  const float t = __builtin_fmaf(x, f.lo, __builtin_fmaf(x, f.hi, -__builtin_rintf(x * f.hi)));
+  return make_float2(__builtin_amdgcn_cosf(t), __builtin_amdgcn_sinf(inverse ? -t : t));
 }
 
 // Axis of pair i; -1 (the pair is left unturned) when the map names none.

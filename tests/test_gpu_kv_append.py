@@ -139,6 +139,25 @@ def test_token_by_token_equals_at_once():
         assert (near > 0).mean() < 0.01
 
 
+@pytest.mark.parametrize("n", [1, 33, 40, 63])
+def test_scale_is_of_these_tokens_only(n):
+    """Threads without a token of their own add nothing to the maximum: token
+    0's pairs turn to (1.7, 1.7) exactly where another angle would give up to
+    2.4, over the border at 448 * 2^-8 = 1.75; the other tokens are small."""
+    D, S, invf = 128, 64, A.inv_freq(128)
+    pos = torch.arange(1000, 1000 + n, dtype=torch.int32)
+    x = torch.full((n, 1, D), 1e-3, dtype=torch.float64)
+    x[0] = 1.7
+    x = torch.from_numpy(AO.rotate(x.numpy(), pos[None].numpy(), invf.numpy(), None, False, True))
+    for dt in ("f32", "bf16"):
+        k = x.to(A.DT[dt])
+        cache = moe.alloc_kv_cache(1, S, 1, D)
+        moe.moe_kv_append(cache, k.cuda(), k.cuda(), A.i32([n]), A.i32([[0]]), cu_q=A.i32([0, n]),
+                          rotation=moe.Rotation(pos.cuda(), invf.cuda()))
+        torch.cuda.synchronize()
+        assert float(cache.k_scales[0, 0]) == 2.0 ** -8, (dt, float(cache.k_scales[0, 0]))
+
+
 def test_extremes():
     """Zeros, the type's largest, infinities and NaN: the scale is that of the
     finite values, infinities saturate, and no code is a NaN."""
