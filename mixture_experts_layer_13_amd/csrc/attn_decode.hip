@@ -23,16 +23,20 @@ constexpr int kDecWaves = kDecThreads / 64;
 constexpr int kDecMinTiles = kDecWaves;  // a shorter run would leave waves idle
 constexpr int kDecOwn = 1024;            // tokens
 
-// Tiles of sequence b that this kernel works on (0: none, or another kernel's).
+__device__ __forceinline__ int dec_slots(int tiles) { return (tiles + kDecMinTiles - 1) / kDecMinTiles * kDecMinTiles; }
+
+// Tiles of sequence b that this kernel works on (0: none, or another kernel's),
+// rounded up to the shortest run: runs and sequences then both begin at
+// multiples of it, and a shortest run never spans two sequences.
 __device__ __forceinline__ int dec_tiles(const AttnArgs& a, int rows_max, int b) {
   const Seq s = load_seq(a.b, a.c.lS, b);
   if (s.q <= 0 || s.q > rows_max / a.G) return 0;
-  return view_of(a, s, 0, s.q).n;
+  return dec_slots(view_of(a, s, 0, s.q).n);
 }
 
 __device__ __forceinline__ long long dec_run(long long total, int W) {
   const long long per = (total + W - 1) / W;
-  return per < kDecMinTiles ? kDecMinTiles : per;
+  return per < kDecMinTiles ? kDecMinTiles : (per + kDecMinTiles - 1) / kDecMinTiles * kDecMinTiles;
 }
 
 // Raw codes of one tile, and the scales of the lane's own 16 tokens.
@@ -300,7 +304,7 @@ __global__ __launch_bounds__(kDecThreads) void attn_decode_kernel(AttnArgs a) {
       }
     }
     if (OWN) return;
-    left -= count;
+    left -= dec_slots(n) - skip;
     skip = 0;
     ++b;
   }
@@ -336,7 +340,7 @@ __global__ __launch_bounds__(kDecThreads) void attn_join_kernel(AttnArgs a) {
     total += t;
   }
   const long long run = dec_run(total, a.W);
-  const int w0 = (int)(at / run), parts = n > 0 ? (int)((at + n - 1) / run) - w0 + 1 : 0;
+  const int w0 = (int)(at / run), parts = n > 0 ? (int)((at + dec_slots(n) - 1) / run) - w0 + 1 : 0;
   if (parts == 1) return;  // finished by its workgroup
   const size_t slot = (size_t)h * a.W + w0;
   // part k: slot 1 (begins the sequence) of workgroup w0, slot 0 of the later ones
