@@ -34,7 +34,11 @@ typedef float f32x16 __attribute__((ext_vector_type(16)));
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kLn2 = 0.69314718055994530942f;
 constexpr int kAttnTile = 64;  // tokens of a tile
-constexpr int kAttnGroups = 512;  // workgroups of the few-row kernel: two per CU
+// Workgroups of the few-row kernel: one per CU, or two where a tile is half as
+// large (64 sequences of 8192 tokens, D 128: 175 us with one, 184 with two;
+// D 64: 106 and 97).
+constexpr int kAttnGroups = 512;  // at most
+constexpr int attn_groups(int D) { return D <= 64 ? 512 : 256; }
 
 struct AttnArgs {
   PagedArgs c;

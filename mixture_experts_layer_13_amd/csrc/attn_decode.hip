@@ -22,6 +22,7 @@ constexpr int kDecThreads = 256;
 constexpr int kDecWaves = kDecThreads / 64;
 constexpr int kDecMinTiles = kDecWaves;  // a shorter run would leave waves idle
 constexpr int kDecOwn = 1024;            // tokens
+constexpr long long kCacheBytes = 256LL << 20;  // last-level cache of the MI355X
 
 __device__ __forceinline__ int dec_slots(int tiles) { return (tiles + kDecMinTiles - 1) / kDecMinTiles * kDecMinTiles; }
 
@@ -62,37 +63,42 @@ __device__ __forceinline__ DecPages dec_pages(const AttnArgs& a, const int32_t* 
   return DecPages{table[ik < a.b.max_pages ? ik : 0], table[iv < a.b.max_pages ? iv : 0]};
 }
 
-template <int DT>
-__device__ __forceinline__ void dec_load(const AttnArgs& a, const DecPages& pg, const View& vw, int tile, int h,
-                                         DecTile<DT>& r) {
-  const int lane = threadIdx.x & 63, m = lane & 15, g = lane >> 4;
-  const int D = a.c.D, lS = a.c.lS, S = 1 << lS;
-  const int tk = tile * kAttnTile + 16 * (m >> 2), tv = tile * kAttnTile + 16 * g;  // first tokens of the lane's blocks
-  const uint32_t pages = a.c.pages;
-  const uint32_t pk = (uint32_t)pg.k < pages ? pg.k : 0, pv = (uint32_t)pg.v < pages ? pg.v : 0;
-  r.gone = (uint32_t)pg.v >= pages || tv >= vw.hi || tv + 16 <= vw.lo;
-  {
-    const size_t page = ((size_t)pk * a.c.H + h) << lS;
-    const uint8_t* row = a.c.kc + (page + (tk & (S - 1)) + (m & 3)) * D;
+// A load of codes: past the caches where the pool is larger than they are (it
+// keeps the table, the queries and other kernels' data in them).
+template <bool STREAM>
+__device__ __forceinline__ i32x4 ld_codes(const uint8_t* p) {
+  const i32x4* q = reinterpret_cast<const i32x4*>(p);
+  return STREAM ? __builtin_nontemporal_load(q) : *q;
+}
+
+template <int DT, bool STREAM>
+__device__ __forceinline__ void dec_load_k(const AttnArgs& a, const DecPages& pg, int tile, int h, DecTile<DT>& r) {
+  const int lane = threadIdx.x & 63, m = lane & 15, g = lane >> 4, D = a.c.D, lS = a.c.lS;
+  const int t = tile * kAttnTile + 16 * (m >> 2);  // first token of the lane's block
+  const uint32_t page = (uint32_t)pg.k < (uint32_t)a.c.pages ? pg.k : 0;
+  const uint8_t* row = a.c.kc + ((((size_t)page * a.c.H + h) << lS) + (t & ((1 << lS) - 1)) + (m & 3)) * D;
 #pragma unroll
-    for (int c = 0; c < DT / 64; ++c) {
-      const int d = g * (DT / 4) + 16 * c;
-      const uint8_t* at = row + (d < D ? d : 0);
+  for (int c = 0; c < DT / 64; ++c) {
+    const int d = g * (DT / 4) + 16 * c;
+    const uint8_t* at = row + (d < D ? d : 0);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) r.k[j][c] = ld16(at + 4 * j * D);
-    }
+    for (int j = 0; j < 4; ++j) r.k[j][c] = ld_codes<STREAM>(at + 4 * j * D);
   }
-  const size_t at = (size_t)pv * a.c.H + h;
-  const uint8_t* blk = a.c.vc + (at << lS) * D + (size_t)((tv & (S - 1)) * D + 16 * m);
+}
+
+template <int DT, bool STREAM>
+__device__ __forceinline__ void dec_load_v(const AttnArgs& a, const DecPages& pg, const View& vw, int tile, int h,
+                                           DecTile<DT>& r) {
+  const int lane = threadIdx.x & 63, m = lane & 15, g = lane >> 4, D = a.c.D, lS = a.c.lS;
+  const int t = tile * kAttnTile + 16 * g;  // first token of the lane's block
+  const uint32_t page = (uint32_t)pg.v < (uint32_t)a.c.pages ? pg.v : 0;
+  r.gone = (uint32_t)pg.v >= (uint32_t)a.c.pages || t >= vw.hi || t + 16 <= vw.lo;
+  const size_t at = (size_t)page * a.c.H + h;
+  const uint8_t* blk = a.c.vc + (at << lS) * D + (size_t)((t & ((1 << lS) - 1)) * D + 16 * m);
 #pragma unroll
-  for (int i = 0; i < DT / 16; ++i) r.v[i] = ld16(blk + (16 * i < D ? 256 * i : 0));
+  for (int i = 0; i < DT / 16; ++i) r.v[i] = ld_codes<STREAM>(blk + (16 * i < D ? 256 * i : 0));
   r.ks = a.c.ks[at];
   r.vs = a.c.vs[at];
-  const int skip = vw.lo - tv, n = r.gone ? 0 : vw.hi - tv;
-  if (skip > 0 || n < 16) {
-#pragma unroll
-    for (int i = 0; i < DT / 16; ++i) r.v[i] = keep_bytes(r.v[i], skip, n);
-  }
 }
 
 template <int DT, int NR, int NS>
@@ -129,9 +135,20 @@ __device__ __forceinline__ void dec_begin(const AttnArgs& a, const Seq& s, int h
   }
 }
 
-template <int DT, int NR, int NS>
-__device__ __forceinline__ void dec_tile(const AttnArgs& a, int tile, const DecTile<DT>& t,
-                                         DecState<DT, NR, NS>& st) {
+// Whether a tile's keys (values) are loaded in the place of the last one's as
+// soon as these are used, under the other product's work, or both at once when
+// the last tile is done.  1.07 GB of codes, 16 query heads: D 256 260 us and
+// 282; D 64 95 and 97; D 128 182 and 175, its loads being long enough to keep
+// memory busy and the loop shorter without.
+template <int DT>
+constexpr bool dec_early() {
+  return DT != 128;
+}
+
+// The tile in t, and the next one's loads if dec_early() and next >= 0.
+template <int DT, int NR, int NS, bool STREAM>
+__device__ __forceinline__ void dec_tile(const AttnArgs& a, const View& vw, int tile, int next, const DecPages& pg, int h,
+                                         DecTile<DT>& t, DecState<DT, NR, NS>& st) {
   const int lane = threadIdx.x & 63, g = lane >> 4;
   f32x16 s[NR];
 #pragma unroll
@@ -150,6 +167,7 @@ __device__ __forceinline__ void dec_tile(const AttnArgs& a, int tile, const DecT
 #pragma unroll
       for (int i = 0; i < 4; ++i) s[r][4 * j + i] = x[r][i];
   }
+  if (dec_early<DT>() && next >= 0) dec_load_k<DT, STREAM>(a, pg, next, h, t);
   const int t0 = tile * kAttnTile;
   const bool masked = t0 < st.all_lo || t0 + kAttnTile > st.all_hi || __any(t.gone);
   const float f = t.gone ? 1.0f : score_scale(a, t.ks), fv = t.gone ? 1.0f : t.vs;
@@ -177,6 +195,11 @@ __device__ __forceinline__ void dec_tile(const AttnArgs& a, int tile, const DecT
 #pragma unroll
   for (int r = 0; r < NR; ++r)
     st.l[r] += rv * attn_probs<NS>(s[r], f, lv - (st.m[r] == -__builtin_inff() ? 0.0f : st.m[r]), p[r]);
+  const int skip = vw.lo - (t0 + 16 * g), n_seen = t.gone ? 0 : vw.hi - (t0 + 16 * g);
+  if (__any(skip > 0 || n_seen < 16)) {
+#pragma unroll
+    for (int i = 0; i < DT / 16; ++i) t.v[i] = keep_bytes(t.v[i], skip, n_seen);
+  }
 #pragma unroll
   for (int n = 0; n < DT / 16; ++n)
 #pragma unroll
@@ -185,6 +208,7 @@ __device__ __forceinline__ void dec_tile(const AttnArgs& a, int tile, const DecT
 #pragma unroll
       for (int r = 0; r < NR; ++r) st.o[r][n] = mfma_split<NS>(v, p[r][c], st.o[r][n]);
     }
+  if (dec_early<DT>() && next >= 0) dec_load_v<DT, STREAM>(a, pg, vw, next, h, t);
 }
 
 // Slot of a workgroup's part: a run holds at most one sequence that began
@@ -194,7 +218,8 @@ __device__ __forceinline__ size_t part_slot(const AttnArgs& a, int h, int w, int
 }
 
 // OWN: blockIdx.x is the sequence, which also writes rows that see nothing.
-template <int DT, int NR, int NS, bool OWN>
+// STREAM: codes are read past the caches.
+template <int DT, int NR, int NS, bool OWN, bool STREAM>
 __global__ __launch_bounds__(kDecThreads) void attn_decode_kernel(AttnArgs a) {
   constexpr int ROWS = 16 * NR, LD = DT + 4;
   __shared__ __align__(16) float jo[kDecWaves][16][LD];
@@ -250,12 +275,25 @@ __global__ __launch_bounds__(kDecThreads) void attn_decode_kernel(AttnArgs a) {
     DecState<DT, NR, NS> st;
     dec_begin<DT, NR, NS>(a, s, h, st);
     const int first = vw.t0 + skip;
-    DecPages pages = dec_pages(a, table, first + wave);
-    for (int i = wave; i < count; i += kDecWaves) {
+    if (wave < count) {
       DecTile<DT> t;
-      dec_load<DT>(a, pages, vw, first + i, h, t);
-      pages = dec_pages(a, table, first + i + kDecWaves);
-      dec_tile<DT, NR, NS>(a, first + i, t, st);
+      DecPages pages = dec_pages(a, table, first + wave);
+      DecPages after = dec_pages(a, table, first + wave + kDecWaves);
+      dec_load_k<DT, STREAM>(a, pages, first + wave, h, t);
+      dec_load_v<DT, STREAM>(a, pages, vw, first + wave, h, t);
+      for (int i = wave; i < count; i += kDecWaves) {
+        if (dec_early<DT>()) {
+          pages = after;
+          after = dec_pages(a, table, first + i + 2 * kDecWaves);
+        } else if (i != wave) {
+          pages = after;
+          after = dec_pages(a, table, first + i + kDecWaves);
+          dec_load_k<DT, STREAM>(a, pages, first + i, h, t);
+          dec_load_v<DT, STREAM>(a, pages, vw, first + i, h, t);
+        }
+        const int next = dec_early<DT>() && i + kDecWaves < count ? first + i + kDecWaves : -1;
+        dec_tile<DT, NR, NS, STREAM>(a, vw, first + i, next, pages, h, t, st);
+      }
     }
     const bool whole = skip == 0 && count == n;
 #pragma unroll
@@ -396,12 +434,18 @@ __global__ __launch_bounds__(kDecThreads) void attn_join_kernel(AttnArgs a) {
 
 template <int DT, int NR, int NS>
 static int dec_launch(const AttnArgs& a, hipStream_t st) {
-  const dim3 block(kDecThreads);
+  const dim3 block(kDecThreads), grid((unsigned)a.W, (unsigned)a.c.H);
   if (((long long)a.b.max_pages << a.c.lS) <= kDecOwn) {
-    hipLaunchKernelGGL((attn_decode_kernel<DT, NR, NS, true>), dim3((unsigned)a.b.B, (unsigned)a.c.H), block, 0, st, a);
+    hipLaunchKernelGGL((attn_decode_kernel<DT, NR, NS, true, false>), dim3((unsigned)a.b.B, (unsigned)a.c.H), block, 0, st, a);
     return (int)hipGetLastError();
   }
-  hipLaunchKernelGGL((attn_decode_kernel<DT, NR, NS, false>), dim3((unsigned)a.W, (unsigned)a.c.H), block, 0, st, a);
+  // 64 sequences of 8192 tokens (1.07 GB): 176 us past the caches, 192 through
+  // them; 21 MB in all, which the last-level cache holds: 22.6 and 20.2
+  const long long pool = 2LL * a.c.pages * a.c.H * a.c.D << a.c.lS;
+  if (pool > kCacheBytes)
+    hipLaunchKernelGGL((attn_decode_kernel<DT, NR, NS, false, true>), grid, block, 0, st, a);
+  else
+    hipLaunchKernelGGL((attn_decode_kernel<DT, NR, NS, false, false>), grid, block, 0, st, a);
   const int err = (int)hipGetLastError();
   if (err) return err;
   const int rows = 16 * NR < a.rows ? 16 * NR : a.rows;  // of a sequence, at most

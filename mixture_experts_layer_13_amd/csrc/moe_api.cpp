@@ -726,7 +726,7 @@ moe_status attn_plan(const moe_kv_cache* c, int32_t T, int32_t B, int32_t n_head
   if (!all) p->tile_units = (long long)T * G / moe::attn_tile_rows() + (B < T ? B : T);
   if (p->tile_units * c->n_kv_heads > (1LL << 30)) return fail(MOE_ERR_SHAPE, "T * n_heads too large");
   if (p->dec_rows) {
-    p->W = moe::kAttnGroups / c->n_kv_heads > 0 ? moe::kAttnGroups / c->n_kv_heads : 1;
+    p->W = moe::attn_groups(c->head_dim) / c->n_kv_heads > 0 ? moe::attn_groups(c->head_dim) / c->n_kv_heads : 1;
     const size_t slots = (size_t)c->n_kv_heads * p->W * 2 * p->dec_rows;
     const int DT = c->head_dim <= 64 ? 64 : (c->head_dim <= 128 ? 128 : 256);
     p->part_ml = up256(slots * DT * sizeof(float));
