@@ -1,351 +1,14 @@
-// attn_decode.hip -- attention over the paged E4M3 cache for few query rows:
-// one token per sequence, or a few, times the query heads that share a KV
-// head, up to 16 NR rows.
-//
-// The cache's bytes bound it: every code is read once, for all the rows that
-// share the KV head.  The tiles of all sequences are laid end to end, and W
-// workgroups per KV head take equal runs of them, so that a ragged batch, or
-// one long sequence, fills the chip as evenly as equal ones.  Within a run the
-// four waves take every fourth tile, each with its own running maximum, sum
-// and accumulators, operands straight from memory (attention.hpp: no LDS, no
-// transposition); they are joined through LDS at the end of a sequence.  A
-// sequence that lies in one run is finished there; the others leave a part
-// per workgroup, which attn_join_kernel joins.  Where the table cannot hold
-// more than kDecOwn tokens a sequence, each has a workgroup of its own
-// instead: no search, no parts, one launch.
-#include "attention.hpp"
+// attn_decode.hip -- the few-row attention (attn_decode.hpp) as a launch of its
+// own, and the join of the parts that its workgroups leave.
+#include "attn_decode.hpp"
 #include "launch.hpp"
 
 namespace moe {
 
-constexpr int kDecThreads = 256;
-constexpr int kDecWaves = kDecThreads / 64;
-constexpr int kDecMinTiles = kDecWaves;  // a shorter run would leave waves idle
-constexpr int kDecOwn = 1024;            // tokens
-constexpr long long kCacheBytes = 256LL << 20;  // last-level cache of the MI355X
-
-__device__ __forceinline__ int dec_slots(int tiles) { return (tiles + kDecMinTiles - 1) / kDecMinTiles * kDecMinTiles; }
-
-// Tiles of sequence b that this kernel works on (0: none, or another kernel's),
-// rounded up to the shortest run: runs and sequences then both begin at
-// multiples of it, and a shortest run never spans two sequences.
-__device__ __forceinline__ int dec_tiles(const AttnArgs& a, int rows_max, int b) {
-  const Seq s = load_seq(a.b, a.c.lS, b);
-  if (s.q <= 0 || s.q > rows_max / a.G) return 0;
-  return dec_slots(view_of(a, s, 0, s.q).n);
-}
-
-__device__ __forceinline__ long long dec_run(long long total, int W) {
-  const long long per = (total + W - 1) / W;
-  return per < kDecMinTiles ? kDecMinTiles : (per + kDecMinTiles - 1) / kDecMinTiles * kDecMinTiles;
-}
-
-// Raw codes of one tile, and the scales of the lane's own 16 tokens.
-template <int DT>
-struct DecTile {
-  i32x4 k[4][DT / 64];
-  i32x4 v[DT / 16];
-  float ks, vs;
-  bool gone;  // the page of the lane's tokens is not in the cache
-};
-
-// The lane's part of a tile: its pages (read a tile ahead), then its codes.  Every load is unconditional, from an
-// address clamped into the cache: what a lane must not use (blocks no row
-// sees, pages outside the cache) it hides afterwards, keys by their scores,
-// values by zeros, since a zero probability times a NaN code would be NaN.
-struct DecPages {
-  int k, v;  // as in the table: of the lane's key rows, and of its own 16 tokens
-};
-
-__device__ __forceinline__ DecPages dec_pages(const AttnArgs& a, const int32_t* table, int tile) {
-  const int lane = threadIdx.x & 63;
-  const int ik = (tile * kAttnTile + 16 * ((lane & 15) >> 2)) >> a.c.lS, iv = (tile * kAttnTile + 16 * (lane >> 4)) >> a.c.lS;
-  return DecPages{table[ik < a.b.max_pages ? ik : 0], table[iv < a.b.max_pages ? iv : 0]};
-}
-
-// A load of codes: past the caches where the pool is larger than they are (it
-// keeps the table, the queries and other kernels' data in them).
-template <bool STREAM>
-__device__ __forceinline__ i32x4 ld_codes(const uint8_t* p) {
-  const i32x4* q = reinterpret_cast<const i32x4*>(p);
-  return STREAM ? __builtin_nontemporal_load(q) : *q;
-}
-
-template <int DT, bool STREAM>
-__device__ __forceinline__ void dec_load_k(const AttnArgs& a, const DecPages& pg, int tile, int h, DecTile<DT>& r) {
-  const int lane = threadIdx.x & 63, m = lane & 15, g = lane >> 4, D = a.c.D, lS = a.c.lS;
-  const int t = tile * kAttnTile + 16 * (m >> 2);  // first token of the lane's block
-  const uint32_t page = (uint32_t)pg.k < (uint32_t)a.c.pages ? pg.k : 0;
-  const uint8_t* row = a.c.kc + ((((size_t)page * a.c.H + h) << lS) + (t & ((1 << lS) - 1)) + (m & 3)) * D;
-#pragma unroll
-  for (int c = 0; c < DT / 64; ++c) {
-    const int d = g * (DT / 4) + 16 * c;
-    const uint8_t* at = row + (d < D ? d : 0);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) r.k[j][c] = ld_codes<STREAM>(at + 4 * j * D);
-  }
-}
-
-template <int DT, bool STREAM>
-__device__ __forceinline__ void dec_load_v(const AttnArgs& a, const DecPages& pg, const View& vw, int tile, int h,
-                                           DecTile<DT>& r) {
-  const int lane = threadIdx.x & 63, m = lane & 15, g = lane >> 4, D = a.c.D, lS = a.c.lS;
-  const int t = tile * kAttnTile + 16 * g;  // first token of the lane's block
-  const uint32_t page = (uint32_t)pg.v < (uint32_t)a.c.pages ? pg.v : 0;
-  r.gone = (uint32_t)pg.v >= (uint32_t)a.c.pages || t >= vw.hi || t + 16 <= vw.lo;
-  const size_t at = (size_t)page * a.c.H + h;
-  const uint8_t* blk = a.c.vc + (at << lS) * D + (size_t)((t & ((1 << lS) - 1)) * D + 16 * m);
-#pragma unroll
-  for (int i = 0; i < DT / 16; ++i) r.v[i] = ld_codes<STREAM>(blk + (16 * i < D ? 256 * i : 0));
-  r.ks = a.c.ks[at];
-  r.vs = a.c.vs[at];
-}
-
-template <int DT, int NR, int NS>
-struct DecState {
-  bf16x8 q[NR][DT / 32][NS];
-  f32x4 o[NR][DT / 16];
-  float m[NR], l[NR];
-  int lo[NR], hi[NR];  // tokens that the lane's row sees
-  int all_lo, all_hi;  // tokens that every row sees
-};
-
-// Rows of the sequence into the B operand of the first product.
-template <int DT, int NR, int NS>
-__device__ __forceinline__ void dec_begin(const AttnArgs& a, const Seq& s, int h, DecState<DT, NR, NS>& st) {
-  const int lane = threadIdx.x & 63, g = lane >> 4;
-  const int p0 = s.kv - s.q;
-  st.all_lo = a.window > 0 ? s.kv - a.window : 0;
-  st.all_hi = a.causal && p0 + 1 < s.lim ? p0 + 1 : s.lim;
-#pragma unroll
-  for (int r = 0; r < NR; ++r) {
-    const int row = 16 * r + (lane & 15), i = row / a.G, hd = h * a.G + row - i * a.G;
-    const bool live = i < s.q;
-    const size_t at = (size_t)(s.q0 + (live ? i : 0)) * a.qs_t + (size_t)(live ? hd : 0) * a.qs_h;
-    QueryRaw<DT / 32, NS> raw;
-    load_q<DT / 32, NS>(a, at, g * (DT / 4), raw);
-    make_q<DT / 32, NS>(a, raw, g * (DT / 4), live, st.q[r]);
-#pragma unroll
-    for (int n = 0; n < DT / 16; ++n) st.o[r][n] = f32x4{0, 0, 0, 0};
-    st.m[r] = -__builtin_inff();
-    st.l[r] = 0.0f;
-    const int p = s.kv - s.q + i;
-    st.hi[r] = !live ? 0 : (a.causal && p + 1 < s.lim ? p + 1 : s.lim);
-    st.lo[r] = a.window > 0 ? p - a.window + 1 : 0;
-  }
-}
-
-// Whether a tile's keys (values) are loaded in the place of the last one's as
-// soon as these are used, under the other product's work, or both at once when
-// the last tile is done.  1.07 GB of codes, 16 query heads: D 256 260 us and
-// 282; D 64 95 and 97; D 128 182 and 175, its loads being long enough to keep
-// memory busy and the loop shorter without.
-template <int DT>
-constexpr bool dec_early() {
-  return DT != 128;
-}
-
-// The tile in t, and the next one's loads if dec_early() and next >= 0.
-template <int DT, int NR, int NS, bool STREAM>
-__device__ __forceinline__ void dec_tile(const AttnArgs& a, const View& vw, int tile, int next, const DecPages& pg, int h,
-                                         DecTile<DT>& t, DecState<DT, NR, NS>& st) {
-  const int lane = threadIdx.x & 63, g = lane >> 4;
-  f32x16 s[NR];
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    f32x4 x[NR];
-#pragma unroll
-    for (int r = 0; r < NR; ++r) x[r] = f32x4{0, 0, 0, 0};
-#pragma unroll
-    for (int c = 0; c < DT / 32; ++c) {
-      const bf16x8 k = codes_op(t.k[j][c >> 1][2 * (c & 1)], t.k[j][c >> 1][2 * (c & 1) + 1]);
-#pragma unroll
-      for (int r = 0; r < NR; ++r) x[r] = mfma_split<NS>(k, st.q[r][c], x[r]);
-    }
-#pragma unroll
-    for (int r = 0; r < NR; ++r)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) s[r][4 * j + i] = x[r][i];
-  }
-  if (dec_early<DT>() && next >= 0) dec_load_k<DT, STREAM>(a, pg, next, h, t);
-  const int t0 = tile * kAttnTile;
-  const bool masked = t0 < st.all_lo || t0 + kAttnTile > st.all_hi || __any(t.gone);
-  const float f = t.gone ? 1.0f : score_scale(a, t.ks), fv = t.gone ? 1.0f : t.vs;
-  float top[NR];
-  bool grow = false;
-#pragma unroll
-  for (int r = 0; r < NR; ++r) {
-    if (masked) attn_hide(s[r], t.gone, t0 + 16 * g, st.lo[r], st.hi[r]);
-    top[r] = attn_top(s[r]) * f;
-    grow |= top[r] > st.m[r] + kMaxSlack;
-  }
-  if (__any(grow)) {
-#pragma unroll
-    for (int r = 0; r < NR; ++r) {
-      const float m = __builtin_fmaxf(st.m[r], max32(max16(top[r])));
-      const float keep = m == -__builtin_inff() ? 1.0f : __builtin_amdgcn_exp2f(st.m[r] - m);
-      st.m[r] = m;
-      st.l[r] *= keep;
-#pragma unroll
-      for (int n = 0; n < DT / 16; ++n) st.o[r][n] *= keep;
-    }
-  }
-  const float lv = __builtin_amdgcn_logf(fv), rv = __builtin_amdgcn_exp2f(-lv);
-  bf16x8 p[NR][2][NS];
-#pragma unroll
-  for (int r = 0; r < NR; ++r)
-    st.l[r] += rv * attn_probs<NS>(s[r], f, lv - (st.m[r] == -__builtin_inff() ? 0.0f : st.m[r]), p[r]);
-  const int skip = vw.lo - (t0 + 16 * g), n_seen = t.gone ? 0 : vw.hi - (t0 + 16 * g);
-  if (__any(skip > 0 || n_seen < 16)) {
-#pragma unroll
-    for (int i = 0; i < DT / 16; ++i) t.v[i] = keep_bytes(t.v[i], skip, n_seen);
-  }
-#pragma unroll
-  for (int n = 0; n < DT / 16; ++n)
-#pragma unroll
-    for (int c = 0; c < 2; ++c) {
-      const bf16x8 v = codes_op(t.v[n][2 * c], t.v[n][2 * c + 1]);
-#pragma unroll
-      for (int r = 0; r < NR; ++r) st.o[r][n] = mfma_split<NS>(v, p[r][c], st.o[r][n]);
-    }
-  if (dec_early<DT>() && next >= 0) dec_load_v<DT, STREAM>(a, pg, vw, next, h, t);
-}
-
-// Slot of a workgroup's part: a run holds at most one sequence that began
-// before it (slot 0) and one that goes on after it (slot 1).
-__device__ __forceinline__ size_t part_slot(const AttnArgs& a, int h, int w, int late) {
-  return ((size_t)h * a.W + w) * 2 + late;
-}
-
-// OWN: blockIdx.x is the sequence, which also writes rows that see nothing.
-// STREAM: codes are read past the caches.
 template <int DT, int NR, int NS, bool OWN, bool STREAM>
 __global__ __launch_bounds__(kDecThreads) void attn_decode_kernel(AttnArgs a) {
-  constexpr int ROWS = 16 * NR, LD = DT + 4;
-  __shared__ __align__(16) float jo[kDecWaves][16][LD];
-  __shared__ float jm[kDecWaves][16], jl[kDecWaves][16];
-  __shared__ int scan[kDecWaves];
-  __shared__ int found[2];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, g = lane >> 4;
-  const int w = blockIdx.x, h = blockIdx.y;
-
-  // the run [begin, end) of this workgroup and the sequence it starts in
-  int b = w, skip = 0;
-  long long left = 1LL << 40;
-  if (!OWN) {
-    long long total = 0, begin = 0, before = 0;
-    int n = 0, e = 0, t;
-    for (int base = 0; base < a.b.B; base += kDecThreads) {
-      n = base + (int)threadIdx.x < a.b.B ? dec_tiles(a, ROWS, base + threadIdx.x) : 0;
-      e = block_scan<kDecWaves>(n, scan, &t);
-      total += t;
-    }
-    const long long run = dec_run(total, a.W);
-    begin = w * run;
-    if (begin >= total) return;
-    left = total - begin < run ? total - begin : run;
-    for (int base = 0; base < a.b.B && before <= begin; base += kDecThreads) {
-      if (a.b.B > kDecThreads) {  // else the one scan above
-        n = base + (int)threadIdx.x < a.b.B ? dec_tiles(a, ROWS, base + threadIdx.x) : 0;
-        e = block_scan<kDecWaves>(n, scan, &t);
-      }
-      if (begin >= before + e - n && begin < before + e) {
-        found[0] = base + threadIdx.x;
-        found[1] = (int)(begin - (before + e - n));
-      }
-      before += t;
-    }
-    __syncthreads();
-    b = __builtin_amdgcn_readfirstlane(found[0]);
-    skip = __builtin_amdgcn_readfirstlane(found[1]);
-  }
-
-  while (left > 0 && b < a.b.B) {
-    const Seq s = load_seq(a.b, a.c.lS, b);
-    const View vw = view_of(a, s, 0, s.q);
-    const bool mine = s.q > 0 && s.q <= ROWS / a.G;
-    const int n = mine ? vw.n : 0;
-    if (OWN ? !mine : n == 0) {
-      if (OWN) return;
-      ++b;
-      continue;
-    }
-    const int count = n - skip < left ? n - skip : (int)left;
-    const int32_t* table = a.b.table + (size_t)b * a.b.max_pages;
-    DecState<DT, NR, NS> st;
-    dec_begin<DT, NR, NS>(a, s, h, st);
-    const int first = vw.t0 + skip;
-    if (wave < count) {
-      DecTile<DT> t;
-      DecPages pages = dec_pages(a, table, first + wave);
-      DecPages after = dec_pages(a, table, first + wave + kDecWaves);
-      dec_load_k<DT, STREAM>(a, pages, first + wave, h, t);
-      dec_load_v<DT, STREAM>(a, pages, vw, first + wave, h, t);
-      for (int i = wave; i < count; i += kDecWaves) {
-        if (dec_early<DT>()) {
-          pages = after;
-          after = dec_pages(a, table, first + i + 2 * kDecWaves);
-        } else if (i != wave) {
-          pages = after;
-          after = dec_pages(a, table, first + i + kDecWaves);
-          dec_load_k<DT, STREAM>(a, pages, first + i, h, t);
-          dec_load_v<DT, STREAM>(a, pages, vw, first + i, h, t);
-        }
-        const int next = dec_early<DT>() && i + kDecWaves < count ? first + i + kDecWaves : -1;
-        dec_tile<DT, NR, NS, STREAM>(a, vw, first + i, next, pages, h, t, st);
-      }
-    }
-    const bool whole = skip == 0 && count == n;
-#pragma unroll
-    for (int r = 0; r < NR; ++r) {
-      const float l = sum32(sum16(st.l[r]));
-      __syncthreads();  // the last join is read
-#pragma unroll
-      for (int k = 0; k < DT / 16; ++k)
-        *reinterpret_cast<f32x4*>(&jo[wave][lane & 15][16 * k + 4 * g]) = st.o[r][k];
-      if (g == 0) {
-        jm[wave][lane] = st.m[r];
-        jl[wave][lane] = l;
-      }
-      __syncthreads();
-      const int col = threadIdx.x >> 4, row = 16 * r + col, qi = row / a.G;
-      if (qi < s.q) {
-        float m = -__builtin_inff();
-#pragma unroll
-        for (int k = 0; k < kDecWaves; ++k) m = __builtin_fmaxf(m, jm[k][col]);
-        const float base = m == -__builtin_inff() ? 0.0f : m;
-        float f[kDecWaves], sum = 0.0f;
-#pragma unroll
-        for (int k = 0; k < kDecWaves; ++k) {
-          f[k] = __builtin_amdgcn_exp2f(jm[k][col] - base);
-          sum += f[k] * jl[k][col];
-        }
-        const size_t orow = (size_t)(s.q0 + qi) * a.nH + h * a.G + row - qi * a.G;
-        const size_t slot = part_slot(a, h, w, skip == 0);
-        for (int d = 4 * (threadIdx.x & 15); d < a.c.D; d += 64) {
-          float o[4] = {0, 0, 0, 0};
-#pragma unroll
-          for (int k = 0; k < kDecWaves; ++k)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) o[j] += f[k] * jo[k][col][d + j];
-          if (whole)
-            attn_store4<NS>(a, orow, d, o, sum);
-          else
-            *reinterpret_cast<float4*>(a.part_o + (slot * ROWS + row) * DT + d) = make_float4(o[0], o[1], o[2], o[3]);
-        }
-        if ((threadIdx.x & 15) == 0) {
-          if (!whole)
-            *reinterpret_cast<float2*>(a.part_ml + (slot * ROWS + row) * 2) = make_float2(m, sum);
-          else if (a.lse)
-            a.lse[orow] = attn_lse(m, sum);
-        }
-      }
-    }
-    if (OWN) return;
-    left -= dec_slots(n) - skip;
-    skip = 0;
-    ++b;
-  }
+  __shared__ __align__(16) DecShared<DT> sh;
+  attn_decode_run<DT, NR, NS, OWN, STREAM>(a, blockIdx.x, blockIdx.y, sh);
 }
 
 // Joins the parts of a sequence that several workgroups shared, and writes the
@@ -433,6 +96,14 @@ __global__ __launch_bounds__(kDecThreads) void attn_join_kernel(AttnArgs a) {
 }
 
 template <int DT, int NR, int NS>
+static int join_launch(const AttnArgs& a, hipStream_t st) {
+  const int rows = 16 * NR < a.rows ? 16 * NR : a.rows;  // of a sequence, at most
+  hipLaunchKernelGGL((attn_join_kernel<DT, 16 * NR, NS>), dim3((unsigned)a.b.B, (unsigned)a.c.H, (unsigned)rows),
+                     dim3(kDecThreads), 0, st, a);
+  return (int)hipGetLastError();
+}
+
+template <int DT, int NR, int NS>
 static int dec_launch(const AttnArgs& a, hipStream_t st) {
   const dim3 block(kDecThreads), grid((unsigned)a.W, (unsigned)a.c.H);
   if (((long long)a.b.max_pages << a.c.lS) <= kDecOwn) {
@@ -447,11 +118,7 @@ static int dec_launch(const AttnArgs& a, hipStream_t st) {
   else
     hipLaunchKernelGGL((attn_decode_kernel<DT, NR, NS, false, false>), grid, block, 0, st, a);
   const int err = (int)hipGetLastError();
-  if (err) return err;
-  const int rows = 16 * NR < a.rows ? 16 * NR : a.rows;  // of a sequence, at most
-  hipLaunchKernelGGL((attn_join_kernel<DT, 16 * NR, NS>), dim3((unsigned)a.b.B, (unsigned)a.c.H, (unsigned)rows), block,
-                     0, st, a);
-  return (int)hipGetLastError();
+  return err ? err : join_launch<DT, NR, NS>(a, st);
 }
 
 template <int NS>
@@ -470,6 +137,12 @@ int attn_decode_rows(int D, int rows) {
   const int most = D <= 64 ? 64 : (D <= 128 ? 32 : 16);
   if (rows > most) return 0;
   return rows <= 16 ? 16 : (rows <= 32 ? 32 : 64);
+}
+
+int launch_attn_join16(const AttnArgs& a, bool f32, hipStream_t st) {
+  if (a.c.D <= 64) return f32 ? join_launch<64, 1, 3>(a, st) : join_launch<64, 1, 1>(a, st);
+  if (a.c.D <= 128) return f32 ? join_launch<128, 1, 3>(a, st) : join_launch<128, 1, 1>(a, st);
+  return f32 ? join_launch<256, 1, 3>(a, st) : join_launch<256, 1, 1>(a, st);
 }
 
 int launch_attn_decode(const AttnArgs& a, int rows, bool f32, hipStream_t st) {

@@ -9,7 +9,7 @@
 // contiguous; the next tile's codes are already in flight in registers while
 // the waves work on this one.  Operand layout, transposed first product and
 // running softmax: attention.hpp.
-#include "attention.hpp"
+#include "attn_decode.hpp"
 #include "launch.hpp"
 
 namespace moe {
@@ -20,8 +20,9 @@ constexpr int kTileRows = 32 * kTileWaves;  // rows of a workgroup
 
 struct TileArgs {
   AttnArgs a;
-  int rows_below;  // sequences of at most this many rows are another kernel's
+  int rows_below;  // sequences of at most this many rows are not worked on here
   int units;       // upper bound of (sequence, row block) pairs
+  int decode;      // workgroups, before those, that take the sequences of up to 16 rows
 };
 
 __device__ __forceinline__ int tile_blocks(const TileArgs& t, int b) {
@@ -56,16 +57,24 @@ __global__ __launch_bounds__(kTileThreads, DT <= 128 && NS == 1 ? 2 : 1) void at
   constexpr int FR = 2 * KC * 64;      // fragments (16 bytes a lane) of keys, and of values, in a tile
   extern __shared__ __align__(16) uint8_t smem[];
   bf16x8* frag = reinterpret_cast<bf16x8*>(smem);  // [2 buffers][keys [2 j][KC] | values [DT / 32][4]][64 lanes]
+  if ((int)blockIdx.x < ta.decode) {
+    // single tokens among the prompts: in the same launch, beside the row
+    // blocks (a batch of 12 chunks and single tokens: 7 us of 55)
+    attn_decode_run<DT, 1, NS, false, false>(a, blockIdx.x / a.c.H, blockIdx.x % a.c.H,
+                                             *reinterpret_cast<DecShared<DT>*>(smem));
+    return;
+  }
+  const int block = blockIdx.x - ta.decode;
   __shared__ int scan[kTileWaves];
   __shared__ int found[2];
   __shared__ float bks[2][4], bvs[2][4];  // of the tile's blocks (UNI: not used)
   __shared__ int bgone[2][4], bany[2][2];
   const int lane = threadIdx.x & 63, m = lane & 31, g = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int h = blockIdx.x % a.c.H;  // heads in turn: with eight, each XCD's L2 keeps one head's codes
+  const int h = block % a.c.H;  // heads in turn: with eight, each XCD's L2 keeps one head's codes
 
   // the row block: later blocks, which see more tokens, first
-  const int unit = ta.units - 1 - (int)(blockIdx.x / a.c.H);
+  const int unit = ta.units - 1 - block / a.c.H;
   if (threadIdx.x == 0) found[0] = -1;
   __syncthreads();
   int before = 0;
@@ -307,7 +316,7 @@ static int tile_launch(const TileArgs& t, hipStream_t st) {
     });
     if (err) return err;
   }
-  hipLaunchKernelGGL((attn_tile_kernel<DT, NS, UNI>), dim3((unsigned)t.units * t.a.c.H), dim3(kTileThreads), lds, st, t);
+  hipLaunchKernelGGL((attn_tile_kernel<DT, NS, UNI>), dim3((unsigned)(t.decode + t.units * t.a.c.H)), dim3(kTileThreads), lds, st, t);
   return (int)hipGetLastError();
 }
 
@@ -318,10 +327,17 @@ static int tile_pick(const TileArgs& t, bool f32, hipStream_t st) {
 }
 
 int launch_attn_tile(const AttnArgs& a, int rows_below, int units, bool f32, hipStream_t st) {
-  const TileArgs t{a, rows_below, units};
-  if (a.c.D <= 64) return tile_pick<64>(t, f32, st);
-  if (a.c.D <= 128) return tile_pick<128>(t, f32, st);
-  return tile_pick<256>(t, f32, st);
+  // few-row sequences of up to 16 rows run in this launch too; wider ones
+  // need more registers than a tile and have a launch of their own
+  const bool both = rows_below == 16;
+  const TileArgs t{a, rows_below, units, both ? a.W * a.c.H : 0};
+  int err = rows_below > 16 ? launch_attn_decode(a, rows_below, f32, st) : 0;
+  if (err) return err;
+  if (a.c.D <= 64)
+    err = tile_pick<64>(t, f32, st);
+  else
+    err = a.c.D <= 128 ? tile_pick<128>(t, f32, st) : tile_pick<256>(t, f32, st);
+  return err || !both ? err : launch_attn_join16(a, f32, st);
 }
 
 int attn_tile_rows() { return kTileRows; }

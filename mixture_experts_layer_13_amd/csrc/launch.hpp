@@ -91,7 +91,9 @@ int launch_kv_append(const PagedArgs& c, const BatchArgs& b, const void* k, long
 // takes when asked for `rows`; 0 if it cannot.
 int attn_decode_rows(int D, int rows);
 int launch_attn_decode(const AttnArgs& a, int rows, bool f32, hipStream_t st);
-// Sequences of more than rows_below rows; units: upper bound of their row blocks.
+int launch_attn_join16(const AttnArgs& a, bool f32, hipStream_t st);
+// The whole of a batch with sequences of more than rows_below rows among them
+// (units: upper bound of their row blocks); the others are the few-row kernel's.
 int attn_tile_rows();
 int launch_attn_tile(const AttnArgs& a, int rows_below, int units, bool f32, hipStream_t st);
 

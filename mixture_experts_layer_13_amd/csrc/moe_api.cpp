@@ -836,14 +836,11 @@ moe_status moe_paged_attention(const moe_kv_cache* cache, const moe_kv_batch* ba
     a.part_ml = reinterpret_cast<float*>((char*)workspace + p.part_ml);
     a.W = p.W;
     a.rows = p.rows;
-    const int err = moe::launch_attn_decode(a, p.dec_rows, q_dtype == MOE_F32, (hipStream_t)stream);
-    if (err) return hip_status(err, "attention launch");
   }
-  if (p.tile_units) {
-    const int err = moe::launch_attn_tile(a, p.dec_rows, (int)p.tile_units, q_dtype == MOE_F32, (hipStream_t)stream);
-    if (err) return hip_status(err, "attention launch");
-  }
-  return ok();
+  const bool f32 = q_dtype == MOE_F32;
+  const int err = p.tile_units ? moe::launch_attn_tile(a, p.dec_rows, (int)p.tile_units, f32, (hipStream_t)stream)
+                               : moe::launch_attn_decode(a, p.dec_rows, f32, (hipStream_t)stream);
+  return hip_status(err, "attention launch");
 }
 
 }  // extern "C"
