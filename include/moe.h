@@ -435,7 +435,7 @@ typedef struct {
  * pointer, type and strides); otherwise the two must not overlap.
  * x          device, x_dtype MOE_BF16 or MOE_F32; strides >= 0.
  * out        device, out_dtype MOE_BF16 or MOE_F32 (rounded once); strides
- *            >= head_dim.  (written)
+ *            >= head_dim, no two heads overlapping.  (written)
  * Every pointer 16-byte aligned (index buffers 4), strides in bytes
  * multiples of 16.  Limits: 1 <= n_heads <= 256; head_dim a multiple of 16 in
  * [16, 512].  T == 0 is a no-op.  Errors: MOE_ERR_SHAPE, MOE_ERR_DTYPE,
@@ -454,7 +454,8 @@ moe_status moe_rope_axes(const void* x, int32_t x_dtype, int64_t x_stride_t, int
  *   v_codes   device uint8 [num_pages][n_kv_heads][page_size / 16][head_dim][16]:
  *             blocks of 16 tokens, channel by channel (value d of slot i at
  *             [i / 16][d][i % 16]), the order in which attention reads them.
- *   k_scales, v_scales   device f32 [num_pages][n_kv_heads], positive.
+ *   k_scales, v_scales   device f32 [num_pages][n_kv_heads]; of pages that hold
+ *             tokens, within 2^-64 and 2^64.
  * page_size 16, 32, 64 or 128; head_dim a multiple of 16 in [16, 256];
  * n_kv_heads 1..256; codes 16-byte, scales 4-byte aligned.  Nothing needs
  * initialising; slots no token was appended to are never used. */
@@ -490,7 +491,8 @@ typedef struct {
  * (rotation NULL: as they are; rotation->positions NULL with axes == 1: the
  * token's own place in its sequence).  For each page and head that gets new
  * tokens, with amax over these tokens' finite values (keys after rotation):
- *   need  = the smallest power of two with 448 need >= amax, >= 2^-64;
+ *   need  = the smallest power of two with 448 need >= amax, within 2^-64 and
+ *           2^64;
  *   scale = max(need, the page's scale) if earlier tokens of the sequence lie
  *           in the page, else need;
  *   codes of earlier tokens become E4M3(code * old scale / scale) where the
@@ -532,8 +534,8 @@ moe_status moe_kv_append(const moe_kv_cache* cache, const moe_kv_batch* batch, c
  * lse        device f32 [T, n_heads] or NULL (written likewise).
  * workspace  device, >= moe_paged_attention_workspace_size() bytes, 16-byte
  *            aligned; no initialisation, not preserved.
- * Limits: n_heads a multiple of n_kv_heads, G <= 128.  The result is the same on every
- * run.  Errors: MOE_ERR_SHAPE, MOE_ERR_DTYPE, MOE_ERR_NULL, MOE_ERR_ALIGN,
+ * Limits: n_heads a multiple of n_kv_heads, G <= 128; at most 2^24 row blocks
+ * (128 rows of a KV head).  The result is the same on every run.  Errors: MOE_ERR_SHAPE, MOE_ERR_DTYPE, MOE_ERR_NULL, MOE_ERR_ALIGN,
  * MOE_ERR_WORKSPACE, MOE_ERR_HIP.  T == 0 or B == 0 is a no-op.
  */
 moe_status moe_paged_attention(const moe_kv_cache* cache, const moe_kv_batch* batch, const void* q,

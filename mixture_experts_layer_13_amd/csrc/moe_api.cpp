@@ -724,7 +724,9 @@ moe_status attn_plan(const moe_kv_cache* c, int32_t T, int32_t B, int32_t n_head
   const bool all = p->dec_rows > 0;
   if (!all) p->dec_rows = moe::attn_decode_rows(c->head_dim, G);
   if (!all) p->tile_units = (long long)T * G / moe::attn_tile_rows() + (B < T ? B : T);
-  if (p->tile_units * c->n_kv_heads > (1LL << 30)) return fail(MOE_ERR_SHAPE, "T * n_heads too large");
+  // the grid: at most 2^32 threads
+  if (p->tile_units * c->n_kv_heads > (1LL << 24) - 1024)
+    return fail(MOE_ERR_SHAPE, "T=%d rows of %d heads are too many for one call", T, n_heads);
   if (p->dec_rows) {
     p->W = moe::attn_groups(c->head_dim) / c->n_kv_heads > 0 ? moe::attn_groups(c->head_dim) / c->n_kv_heads : 1;
     const size_t slots = (size_t)c->n_kv_heads * p->W * 2 * p->dec_rows;
@@ -752,6 +754,10 @@ moe_status moe_rope_axes(const void* x, int32_t x_dtype, int64_t x_stride_t, int
   if ((s = check_strides("out", out_dtype, out_stride_t, out_stride_h, head_dim))) return s;
   if ((s = check_rotation(rotation, head_dim, T > 0))) return s;
   if (T == 0) return ok();
+  if (out_stride_t < (n_heads - 1) * out_stride_h + head_dim && out_stride_h < (T - 1) * out_stride_t + head_dim &&
+      T > 1 && n_heads > 1)
+    return fail(MOE_ERR_SHAPE, "out strides %lld, %lld make its heads overlap", (long long)out_stride_t,
+                (long long)out_stride_h);
   if (!x || !out) return fail(MOE_ERR_NULL, "x and out are required");
   if (!aligned(x, 16) || !aligned(out, 16)) return fail(MOE_ERR_ALIGN, "x and out must be 16-byte aligned");
   if (out == x && (x_dtype != out_dtype || x_stride_t != out_stride_t || x_stride_h != out_stride_h))

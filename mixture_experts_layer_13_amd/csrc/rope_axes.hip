@@ -17,6 +17,7 @@ namespace moe {
 
 constexpr int kRaThreads = 256;
 constexpr int kRaUnits = 4;           // pairs of vectors a thread holds at once
+constexpr int kRaMaxGrid = 1 << 20;   // workgroups of a launch; each takes every kRaMaxGrid-th run of tokens
 constexpr int kRaMaxAngles = 4096;    // LDS: {cos, sin} of at most this many (token, pair)
 
 struct RopeAxesArgs {
@@ -48,53 +49,55 @@ __device__ __forceinline__ void store_vec(void* base, size_t idx, const float* v
 template <int XT, int OT>
 __global__ __launch_bounds__(kRaThreads) void rope_axes_kernel(RopeAxesArgs a) {
   __shared__ float2 cs[kRaMaxAngles];
-  const int t0 = blockIdx.x * a.tb;
-  const int tn = a.T - t0 < a.tb ? a.T - t0 : a.tb;
   constexpr int E = XT == DT_BF16 ? 8 : 4;  // values of a 16-byte load
-  const int upd = a.D / (2 * E), upt = a.nH * upd, units = tn * upt;
-  for (int base = 0; base < units; base += kRaThreads * kRaUnits) {
-    RawVec<XT, E> ra[kRaUnits], rb[kRaUnits];
-    int tok[kRaUnits], hd[kRaUnits], gs[kRaUnits];
+  const int upd = a.D / (2 * E), upt = a.nH * upd;
+  for (long long t0 = (long long)blockIdx.x * a.tb; t0 < a.T; t0 += (long long)gridDim.x * a.tb) {
+    const int tn = a.T - t0 < a.tb ? (int)(a.T - t0) : a.tb, units = tn * upt;
+    for (int base = 0; base < units; base += kRaThreads * kRaUnits) {
+      RawVec<XT, E> ra[kRaUnits], rb[kRaUnits];
+      int tok[kRaUnits], hd[kRaUnits], gs[kRaUnits];
 #pragma unroll
-    for (int s = 0; s < kRaUnits; ++s) {
-      const int u = base + s * kRaThreads + threadIdx.x;
-      const int uu = u < units ? u : 0;
-      tok[s] = uu / upt;
-      const int r = uu - tok[s] * upt;
-      hd[s] = r / upd;
-      gs[s] = r - hd[s] * upd;
-      int p, q;
-      unit_groups<E>(gs[s], a.r.half, a.D, p, q);
-      const size_t row = (size_t)(t0 + tok[s]) * a.xs_t + (size_t)hd[s] * a.xs_h;
-      ra[s] = load_vec<XT, E>(a.x, row + p);
-      rb[s] = load_vec<XT, E>(a.x, row + q);
-    }
-    if (base == 0) {
-      for (int i = threadIdx.x; i < tn * a.r.half; i += kRaThreads) {
-        const int t = i / a.r.half, pr = i - t * a.r.half, ax = rotate_axis(a.r, pr);
-        const int pos = ax >= 0 ? a.r.pos[(size_t)ax * a.r.T + t0 + t] : 0;
-        cs[i] = rotate_cs(pos, turn_freq(a.r.inv_freq[pr]), a.r.inverse);
+      for (int s = 0; s < kRaUnits; ++s) {
+        const int u = base + s * kRaThreads + threadIdx.x;
+        const int uu = u < units ? u : 0;
+        tok[s] = uu / upt;
+        const int r = uu - tok[s] * upt;
+        hd[s] = r / upd;
+        gs[s] = r - hd[s] * upd;
+        int p, q;
+        unit_groups<E>(gs[s], a.r.half, a.D, p, q);
+        const size_t row = (size_t)(t0 + tok[s]) * a.xs_t + (size_t)hd[s] * a.xs_h;
+        ra[s] = load_vec<XT, E>(a.x, row + p);
+        rb[s] = load_vec<XT, E>(a.x, row + q);
       }
-      __syncthreads();
-    }
-#pragma unroll
-    for (int s = 0; s < kRaUnits; ++s) {
-      if (base + s * kRaThreads + (int)threadIdx.x >= units) continue;
-      float va[E], vb[E];
-      unpack_vec(ra[s], va);
-      unpack_vec(rb[s], vb);
-      if (gs[s] < a.r.half / E) {
-        float2 w[E];
-#pragma unroll
-        for (int i = 0; i < E; ++i) w[i] = cs[tok[s] * a.r.half + unit_pair<E>(gs[s], i, a.r.half, a.r.interleaved)];
-        rotate_unit<E>(va, vb, w, a.r.interleaved);
+      if (base == 0) {
+        for (int i = threadIdx.x; i < tn * a.r.half; i += kRaThreads) {
+          const int t = i / a.r.half, pr = i - t * a.r.half, ax = rotate_axis(a.r, pr);
+          const int pos = ax >= 0 ? a.r.pos[(size_t)ax * a.r.T + t0 + t] : 0;
+          cs[i] = rotate_cs(pos, turn_freq(a.r.inv_freq[pr]), a.r.inverse);
+        }
+        __syncthreads();
       }
-      int p, q;
-      unit_groups<E>(gs[s], a.r.half, a.D, p, q);
-      const size_t row = (size_t)(t0 + tok[s]) * a.os_t + (size_t)hd[s] * a.os_h;
-      store_vec<OT, E>(a.out, row + p, va);
-      store_vec<OT, E>(a.out, row + q, vb);
+#pragma unroll
+      for (int s = 0; s < kRaUnits; ++s) {
+        if (base + s * kRaThreads + (int)threadIdx.x >= units) continue;
+        float va[E], vb[E];
+        unpack_vec(ra[s], va);
+        unpack_vec(rb[s], vb);
+        if (gs[s] < a.r.half / E) {
+          float2 w[E];
+#pragma unroll
+          for (int i = 0; i < E; ++i) w[i] = cs[tok[s] * a.r.half + unit_pair<E>(gs[s], i, a.r.half, a.r.interleaved)];
+          rotate_unit<E>(va, vb, w, a.r.interleaved);
+        }
+        int p, q;
+        unit_groups<E>(gs[s], a.r.half, a.D, p, q);
+        const size_t row = (size_t)(t0 + tok[s]) * a.os_t + (size_t)hd[s] * a.os_h;
+        store_vec<OT, E>(a.out, row + p, va);
+        store_vec<OT, E>(a.out, row + q, vb);
+      }
     }
+    __syncthreads();  // the angles are read
   }
 }
 
@@ -121,7 +124,8 @@ int launch_rope_axes(const void* x, int xt, long long xs_t, long long xs_h, cons
          (T + 2 * tb - 1) / (2 * tb) >= 2 * device_cu_count())
     tb *= 2;
   a.tb = tb;
-  const dim3 grid((unsigned)((T + tb - 1) / tb)), block(kRaThreads);
+  const long long groups = ((long long)T + tb - 1) / tb;
+  const dim3 grid((unsigned)(groups < kRaMaxGrid ? groups : kRaMaxGrid)), block(kRaThreads);
   if (xt == DT_BF16 && ot == DT_BF16)
     hipLaunchKernelGGL((rope_axes_kernel<DT_BF16, DT_BF16>), grid, block, 0, st, a);
   else if (xt == DT_BF16)

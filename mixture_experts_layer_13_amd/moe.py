@@ -642,3 +642,39 @@ class FusedMoE:
                               self.alignment, self.out, self.workspace, self.w13_scale,
                               self.w2_scale, self.a1_scale, self.a2_scale, stream, events)
         return self.out
+
+
+class PagedAttention:
+    """The attention of a decoder layer ahead of its experts: queries and keys
+    rotated, keys and values into the paged cache, attention over it (the calls
+    moe_rope_axes, moe_kv_append and moe_paged_attention), with the buffers
+    allocated once for at most max_tokens rows in max_seqs sequences of at most
+    max_q rows.  Nothing is allocated or synchronised per call, so the sequence
+    can be captured into a HIP graph; lengths, tables and positions are read on
+    the device and may change between replays."""
+
+    def __init__(self, cache, n_heads, inv_freq, max_tokens, max_seqs=None, max_q=1, pair_axis=None,
+                 interleaved=False, sm_scale=None, causal=True, window=0, dtype=torch.bfloat16):
+        self.cache, self.n_heads, self.max_q = cache, n_heads, max_q
+        self.inv_freq, self.pair_axis, self.interleaved = inv_freq, pair_axis, interleaved
+        self.sm_scale, self.causal, self.window = sm_scale, causal, window
+        shape = (max_tokens, n_heads, cache.head_dim)
+        self.q = torch.empty(shape, dtype=dtype, device=cache.device)
+        self.out = torch.empty(shape, dtype=dtype, device=cache.device)
+        n = moe_paged_attention_workspace_size(cache, max_tokens, max_seqs or max_tokens, n_heads, max_q)
+        self.workspace = torch.empty(max(n, 16), dtype=torch.uint8, device=cache.device)
+
+    def __call__(self, q, k, v, positions, kv_lens, block_table, cu_q=None, stream=None):
+        """q [T, n_heads, D], k and v [T, n_kv_heads, D]; positions int32 [T] or
+        [axes, T]; kv_lens counts these rows.  Returns out [T, n_heads, D], this
+        object's buffer."""
+        T = q.shape[0]
+        if T > self.out.shape[0]:
+            raise MoEError(MOE_ERR_SHAPE, f"T={T} rows, buffers for {self.out.shape[0]}")
+        rotation = Rotation(positions, self.inv_freq, self.pair_axis, self.interleaved)
+        moe_rope_axes(q, rotation, out=self.q[:T], stream=stream)
+        moe_kv_append(self.cache, k, v, kv_lens, block_table, rotation=rotation, cu_q=cu_q, stream=stream)
+        return moe_paged_attention(self.cache, self.q[:T], kv_lens, block_table, cu_q=cu_q,
+                                   max_q=1 if cu_q is None else self.max_q, sm_scale=self.sm_scale,
+                                   causal=self.causal, window=self.window, out=self.out[:T],
+                                   workspace=self.workspace, stream=stream)

@@ -6,7 +6,7 @@ out as include/moe.h documents: k_codes [P, H, S, D] and v_codes
 import numpy as np
 
 E4M3_MAX = 448.0
-MIN_SCALE = 2.0 ** -64
+MIN_SCALE, MAX_SCALE = 2.0 ** -64, 2.0 ** 64
 
 
 def _table():
@@ -69,7 +69,7 @@ def pair_of(D, half, interleaved):
 
 def page_scale(amax):
     s = MIN_SCALE
-    while E4M3_MAX * s < amax:
+    while E4M3_MAX * s < amax and s < MAX_SCALE:
         s *= 2
     return s
 

@@ -53,7 +53,9 @@ def rope(x=F, dt=BF, xs=(4096, 128), rot="default", T=4, nH=32, D=128, out=F + (
     (dict(rot=rotation(positions=None, axes=1)), moe.MOE_ERR_NULL), (dict(rot=rotation(positions=ODD4)), moe.MOE_ERR_ALIGN),
     (dict(x=None), moe.MOE_ERR_NULL), (dict(out=None), moe.MOE_ERR_NULL), (dict(x=ODD16), moe.MOE_ERR_ALIGN),
     (dict(out=ODD16), moe.MOE_ERR_ALIGN), (dict(out=F, odt=F32), moe.MOE_ERR_UNSUPPORTED),
-    (dict(out=F, os=(8192, 128)), moe.MOE_ERR_UNSUPPORTED), (dict(T=0, x=None, out=None), moe.MOE_OK),
+    (dict(out=F, os=(8192, 128)), moe.MOE_ERR_UNSUPPORTED), (dict(os=(2048, 128)), moe.MOE_ERR_SHAPE),
+    (dict(os=(128, 128)), moe.MOE_ERR_SHAPE), (dict(os=(128, 384)), moe.MOE_ERR_SHAPE),
+    (dict(T=1, os=(128, 128), xs=(128, 128), x=None), moe.MOE_ERR_NULL),  # one token: no overlap (dict(T=0, x=None, out=None), moe.MOE_OK),
 ])
 def test_rope_axes_refusals(kw, status):
     assert rope(**kw) == status
@@ -111,6 +113,7 @@ def attend(c="default", b="default", q=F, dt=BF, qs=(4096, 128), nH=32, max_q=9,
     (dict(scale=float("nan")), moe.MOE_ERR_SHAPE), (dict(scale=float("inf")), moe.MOE_ERR_SHAPE),
     (dict(b=batch(cu_q=None, T=4), max_q=2), moe.MOE_ERR_SHAPE), (dict(q=ODD16), moe.MOE_ERR_ALIGN),
     (dict(out=ODD16), moe.MOE_ERR_ALIGN), (dict(ws=ODD16), moe.MOE_ERR_ALIGN), (dict(lse=ODD4), moe.MOE_ERR_ALIGN),
+    (dict(b=batch(T=1 << 28), max_q=1 << 28, c=cache(n_kv_heads=1), nH=32), moe.MOE_ERR_SHAPE),
     (dict(b=batch(T=0), q=None, out=None, ws=None), moe.MOE_OK),
 ] + [(dict(c=cache(**kw)), s) for kw, s in BAD_CACHE] + [(dict(b=batch(**kw)), s) for kw, s in BAD_BATCH])
 def test_attention_refusals(kw, status):
