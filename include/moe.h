@@ -455,7 +455,7 @@ moe_status moe_rope_axes(const void* x, int32_t x_dtype, int64_t x_stride_t, int
  *             blocks of 16 tokens, channel by channel (value d of slot i at
  *             [i / 16][d][i % 16]), the order in which attention reads them.
  *   k_scales, v_scales   device f32 [num_pages][n_kv_heads]; of pages that hold
- *             tokens, within 2^-64 and 2^64.
+ *             tokens, within 2^-64 and 2^48.
  * page_size 16, 32, 64 or 128; head_dim a multiple of 16 in [16, 256];
  * n_kv_heads 1..256; codes 16-byte, scales 4-byte aligned.  Nothing needs
  * initialising; slots no token was appended to are never used. */
@@ -492,7 +492,7 @@ typedef struct {
  * token's own place in its sequence).  For each page and head that gets new
  * tokens, with amax over these tokens' finite values (keys after rotation):
  *   need  = the smallest power of two with 448 need >= amax, within 2^-64 and
- *           2^64;
+ *           2^48;
  *   scale = max(need, the page's scale) if earlier tokens of the sequence lie
  *           in the page, else need;
  *   codes of earlier tokens become E4M3(code * old scale / scale) where the
@@ -519,8 +519,8 @@ moe_status moe_kv_append(const moe_kv_cache* cache, const moe_kv_batch* batch, c
  *   s_t = sm_scale * sum_d q[d] k_t[d],   out = sum_t softmax(s)_t v_t,
  *   lse = log sum_t exp(s_t) (natural).
  * A row that sees no token gives zeros and lse = -infinity.  bf16 queries:
- * fp32 scores, sums and softmax, probabilities rounded to bf16 for the second
- * product.  f32 queries: 24-bit products throughout.  Codes of tokens that no
+ * fp32 scores, sums and softmax, probabilities rounded to 11 bits (fp16) for
+ * the second product.  f32 queries: 24-bit products throughout.  Codes of tokens that no
  * row sees, and their scales, may hold anything; a NaN code (0x7f, 0xff; an
  * append makes none) in a token that some row sees makes every row of its
  * sequence unspecified.

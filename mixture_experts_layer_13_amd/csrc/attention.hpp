@@ -3,11 +3,16 @@
 // Both compute, for a query row r (one head of one token) and the tokens t it
 // sees, with kc, vc the E4M3 codes and ks, vs their page's scales,
 //   s_t = sm_scale ks q.kc_t,  out = sum_t softmax(s)_t vs vc_t
-// in one pass over the tokens with a running maximum m and sum l (base 2:
-// exp2(s log2 e - m)).  Codes are exact in bf16, so both products run on bf16
-// MFMA with fp32 accumulation: q as it is, p = exp2(..) vs rounded to bf16
-// (its sum l is taken from the unrounded fp32 values).  fp32 queries are the
-// sum of three bf16 terms, and so is p: 24 bits, three MFMAs in place of one.
+// in one pass over the tokens with, in base 2 and fp32, a running maximum m of
+// s + log2 vs and sums l of exp2(s - m) and o of exp2(s + log2 vs - m) vc:
+// out = o / l, lse = m + log2 l.  Taking vs into the maximum is what lets the
+// second product's operands, x = exp2(s + log2 vs - m) and the codes, be fp16
+// without any bound on the scales: x is at most 2^8 (kMaxSlack), the row's
+// largest at least about 1, so x has 11 bits down to 2^-14 of it and an error
+// of 2^-25 of it below; as bf16 it would have 8.  Codes are exact in both, and
+// bf16 queries go into bf16 MFMA as they are; both accumulate in fp32.  fp32
+// queries, and their x, are the sum of three bf16 terms: 24 bits, three MFMAs
+// in place of one.
 //
 // Operand layout.  The first product is computed transposed, S^T = K Q^T, and
 // the tokens of a 64-token tile are dealt to the rows of its MFMA tiles so
@@ -90,6 +95,22 @@ __device__ __forceinline__ bf16x8 codes_op(int w0, int w1) {
   return as_bf16x8(r);
 }
 
+// The second product's operands, as bits: fp16 for bf16 queries (NS 1), bf16
+// terms for fp32 ones.
+typedef _Float16 f16x2_t __attribute__((ext_vector_type(2)));
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+
+template <int NS>
+__device__ __forceinline__ bf16x8 value_op(int w0, int w1) {
+  if (NS > 1) return codes_op(w0, w1);
+  const i32x4 r = {
+      __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8((unsigned)w0, 1.0f, false)),
+      __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8((unsigned)w0, 1.0f, true)),
+      __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8((unsigned)w1, 1.0f, false)),
+      __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8((unsigned)w1, 1.0f, true))};
+  return as_bf16x8(r);
+}
+
 // x as NS bf16 terms whose sum is x to 8 NS bits: term k of the eight values.
 template <int NS>
 __device__ __forceinline__ void split_bf16(const float x[8], bf16x8 out[NS]) {
@@ -123,6 +144,19 @@ __device__ __forceinline__ f32x16 mfma_split(const bf16x8 a, const bf16x8 b[NS],
 #pragma unroll
   for (int k = NS - 1; k >= 0; --k) c = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b[k], c, 0, 0, 0);
   return c;
+}
+
+// The second product: a value fragment and x, operands of value_op and
+// attn_probs.
+template <int NS>
+__device__ __forceinline__ f32x4 mfma_value(const bf16x8 a, const bf16x8 b[NS], f32x4 c) {
+  if (NS > 1) return mfma_split<NS>(a, b, c);
+  return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b[0]), c, 0, 0, 0);
+}
+template <int NS>
+__device__ __forceinline__ f32x16 mfma_value(const bf16x8 a, const bf16x8 b[NS], f32x16 c) {
+  if (NS > 1) return mfma_split<NS>(a, b, c);
+  return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b[0]), c, 0, 0, 0);
 }
 
 // Scale of a page's scores; at least the smallest normal number, so that a
@@ -232,9 +266,9 @@ __device__ __forceinline__ float attn_top(const f32x16& sc) {
   return v;
 }
 
-// p vs = exp2(s f - m + log2 vs) of a lane's 16 tokens, as operands; returns
-// their sum.  The lane's tokens lie in one page, so f and vs are the lane's,
-// and dividing the sum by vs once gives the sum of p.  c = log2 vs - m.
+// x = exp2(s f + c), c = log2 vs - m, of a lane's 16 tokens, as operands;
+// returns their sum.  The lane's tokens lie in one page, so f and vs are the
+// lane's, and dividing the sum by vs once gives that of exp2(s f - m).
 template <int NS>
 __device__ __forceinline__ float attn_probs(const f32x16& sc, float f, float c, bf16x8 p[2][NS]) {
   float x[16], sum = 0.0f;
@@ -243,8 +277,20 @@ __device__ __forceinline__ float attn_probs(const f32x16& sc, float f, float c, 
     x[k] = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[k], f, c));
     sum += x[k];
   }
-  split_bf16<NS>(x, p[0]);
-  split_bf16<NS>(x + 8, p[1]);
+  if (NS > 1) {
+    split_bf16<NS>(x, p[0]);
+    split_bf16<NS>(x + 8, p[1]);
+  } else {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      i32x4 w;
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        w[k] = __builtin_bit_cast(
+            int, __builtin_convertvector((f32x2_t{x[8 * h + 2 * k], x[8 * h + 2 * k + 1]}), f16x2_t));
+      p[h][0] = as_bf16x8(w);
+    }
+  }
   return sum;
 }
 

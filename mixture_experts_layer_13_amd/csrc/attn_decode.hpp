@@ -172,12 +172,13 @@ __device__ __forceinline__ void dec_tile(const AttnArgs& a, const View& vw, int 
   const int t0 = tile * kAttnTile;
   const bool masked = t0 < st.all_lo || t0 + kAttnTile > st.all_hi || __any(t.gone);
   const float f = t.gone ? 1.0f : score_scale(a, t.ks), fv = t.gone ? 1.0f : t.vs;
+  const float lv = __builtin_amdgcn_logf(fv), rv = __builtin_amdgcn_exp2f(-lv);
   float top[NR];
   bool grow = false;
 #pragma unroll
   for (int r = 0; r < NR; ++r) {
     if (masked) attn_hide(s[r], t.gone, t0 + 16 * g, st.lo[r], st.hi[r]);
-    top[r] = attn_top(s[r]) * f;
+    top[r] = __builtin_fmaf(attn_top(s[r]), f, lv);
     grow |= top[r] > st.m[r] + kMaxSlack;
   }
   if (__any(grow)) {
@@ -191,7 +192,6 @@ __device__ __forceinline__ void dec_tile(const AttnArgs& a, const View& vw, int 
       for (int n = 0; n < DT / 16; ++n) st.o[r][n] *= keep;
     }
   }
-  const float lv = __builtin_amdgcn_logf(fv), rv = __builtin_amdgcn_exp2f(-lv);
   bf16x8 p[NR][2][NS];
 #pragma unroll
   for (int r = 0; r < NR; ++r)
@@ -205,9 +205,9 @@ __device__ __forceinline__ void dec_tile(const AttnArgs& a, const View& vw, int 
   for (int n = 0; n < DT / 16; ++n)
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
-      const bf16x8 v = codes_op(t.v[n][2 * c], t.v[n][2 * c + 1]);
+      const bf16x8 v = value_op<NS>(t.v[n][2 * c], t.v[n][2 * c + 1]);
 #pragma unroll
-      for (int r = 0; r < NR; ++r) st.o[r][n] = mfma_split<NS>(v, p[r][c], st.o[r][n]);
+      for (int r = 0; r < NR; ++r) st.o[r][n] = mfma_value<NS>(v, p[r][c], st.o[r][n]);
     }
   if (dec_early<DT>() && next >= 0) dec_load_v<DT, STREAM>(a, pg, vw, next, h, t);
 }

@@ -173,7 +173,7 @@ __global__ __launch_bounds__(kTileThreads, DT <= 128 && NS == 1 ? 2 : 1) void at
     bf16x8* vf = frag + buf * 2 * FR + FR + ((wave >> 1) * 4 + 2 * j) * 64 + lane;
     const int c = x >> 2, e = 2 * (x & 1);
     if (x & 2)
-      vf[(8 * c + (x & 1)) * 64] = codes_op(raw.v[c][e], raw.v[c][e + 1]);
+      vf[(8 * c + (x & 1)) * 64] = value_op<NS>(raw.v[c][e], raw.v[c][e + 1]);
     else
       kf[(2 * c + (x & 1)) * 64] = codes_op(raw.k[c][e], raw.k[c][e + 1]);
   };
@@ -263,8 +263,10 @@ __global__ __launch_bounds__(kTileThreads, DT <= 128 && NS == 1 ? 2 : 1) void at
       attn_hide(sc[0], cout0, t, lo, hi);
       attn_hide(sc[1], cout1, t + 16, lo, hi);
     }
-    const float top = UNI ? __builtin_fmaxf(attn_top(sc[0]), attn_top(sc[1])) * cf0
-                          : __builtin_fmaxf(attn_top(sc[0]) * cf0, attn_top(sc[1]) * cf1);
+    const float lv0 = __builtin_amdgcn_logf(cv0), lv1 = UNI ? lv0 : __builtin_amdgcn_logf(cv1);
+    const float top = UNI ? __builtin_fmaf(__builtin_fmaxf(attn_top(sc[0]), attn_top(sc[1])), cf0, lv0)
+                          : __builtin_fmaxf(__builtin_fmaf(attn_top(sc[0]), cf0, lv0),
+                                            __builtin_fmaf(attn_top(sc[1]), cf1, lv1));
     if (__any(top > mx + kMaxSlack)) {
       const float mn = __builtin_fmaxf(mx, max32(top));
       const float keep = mn == -__builtin_inff() ? 1.0f : __builtin_amdgcn_exp2f(mx - mn);
@@ -274,7 +276,6 @@ __global__ __launch_bounds__(kTileThreads, DT <= 128 && NS == 1 ? 2 : 1) void at
       for (int n = 0; n < DT / 32; ++n) o[n] *= keep;
     }
     const float base = mx == -__builtin_inff() ? 0.0f : mx;
-    const float lv0 = __builtin_amdgcn_logf(cv0), lv1 = UNI ? lv0 : __builtin_amdgcn_logf(cv1);
     bf16x8 p[2][2][NS];
     const float s0 = attn_probs<NS>(sc[0], cf0, lv0 - base, p[0]);
     const float s1 = attn_probs<NS>(sc[1], UNI ? cf0 : cf1, lv1 - base, p[1]);
@@ -283,7 +284,7 @@ __global__ __launch_bounds__(kTileThreads, DT <= 128 && NS == 1 ? 2 : 1) void at
 #pragma unroll
     for (int c = 0; c < 4; ++c)
 #pragma unroll
-      for (int n = 0; n < DT / 32; ++n) o[n] = mfma_split<NS>(vf[(n * 4 + c) * 64], p[c >> 1][c & 1], o[n]);
+      for (int n = 0; n < DT / 32; ++n) o[n] = mfma_value<NS>(vf[(n * 4 + c) * 64], p[c >> 1][c & 1], o[n]);
     __syncthreads();  // this buffer may be written, the other one read
   };
   for (int i = 0; i < vw.n; i += kAhead) {

@@ -4,8 +4,8 @@
 // Per touched page and head, over the page's new tokens (keys after the
 // rotation, in fp32: rotation and code are one rounding):
 //   need = the smallest power of two with 448 need >= max |x|, kept within
-//          2^-64 and 2^64, so that products and sums of codes, scales and
-//          probabilities stay finite in fp32 (values past 8e21 saturate);
+//          2^-64 and 2^48, so that the attention's sums of codes, scales and
+//          probabilities stay in fp32's range (values past 1.2e17 saturate);
 //   s'   = max(need, s) if earlier tokens of the sequence lie in the page,
 //          else need;
 //   codes of earlier tokens: E4M3(code * s / s'); new: E4M3(x / s').
@@ -29,7 +29,7 @@
 
 namespace moe {
 
-constexpr float kMinPageScale = 0x1p-64f, kMaxPageScale = 0x1p+64f;
+constexpr float kMinPageScale = 0x1p-64f, kMaxPageScale = 0x1p+48f;
 constexpr int kAppendThreads = 1024;
 
 struct AppendArgs {
@@ -47,7 +47,7 @@ struct AppendArgs {
 // the distance from 1.75 to 2 carries into the exponent exactly above it.
 __device__ __forceinline__ float page_scale(float amax) {
   const uint32_t e = (__float_as_uint(amax) + 0x1fffffu) >> 23;  // 448 * 2^(e - 135)
-  return e <= 8u + 63u ? kMinPageScale : (e >= 8u + 191u ? kMaxPageScale : __uint_as_float((e - 8u) << 23));
+  return e <= 8u + 63u ? kMinPageScale : (e >= 8u + 175u ? kMaxPageScale : __uint_as_float((e - 8u) << 23));
 }
 
 // Four codes of y / s (r = 1 / s, exact: s is a power of two).  Saturates;

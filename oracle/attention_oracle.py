@@ -6,7 +6,7 @@ out as include/moe.h documents: k_codes [P, H, S, D] and v_codes
 import numpy as np
 
 E4M3_MAX = 448.0
-MIN_SCALE, MAX_SCALE = 2.0 ** -64, 2.0 ** 64
+MIN_SCALE, MAX_SCALE = 2.0 ** -64, 2.0 ** 48
 
 
 def _table():
@@ -115,28 +115,31 @@ def append(cache, k, v, cu, kv_lens, table, touched=None):
 
 
 def gather(cache, table_row, n, h, hidden):
-    """Keys and values [n, D] of a sequence's tokens in fp64; hidden[t] for tokens of no page."""
+    """Keys and values [n, D] of a sequence's tokens in fp64, and the values'
+    scales [n]; hidden[t] for tokens of no page."""
     P, H, S, D = cache["k_codes"].shape
-    k, v = np.zeros((n, D)), np.zeros((n, D))
+    k, v, vs = np.zeros((n, D)), np.zeros((n, D)), np.zeros(n)
     for t in range(n):
         page = int(table_row[t // S]) if t // S < len(table_row) else -1
         if not 0 <= page < P:
             hidden[t] = True
             continue
         k[t] = E4M3[cache["k_codes"][page, h, t % S]] * float(cache["k_scales"][page, h])
-        v[t] = E4M3[_v_slot(cache, page, h, t % S)] * float(cache["v_scales"][page, h])
-    return k, v
+        vs[t] = float(cache["v_scales"][page, h])
+        v[t] = E4M3[_v_slot(cache, page, h, t % S)] * vs[t]
+    return k, v, vs
 
 
 def attention(cache, q, cu, kv_lens, table, scale, causal=True, window=0):
     """(out [T, nH, D], lse [T, nH], bound) in fp64; rows of no sequence are
     NaN.  bound: per row, the largest scale * sum |q||k| over the tokens it
-    sees, sum p|v| per value, and how many it sees."""
+    sees, sum p|v| per value, how many it sees, and the largest p times its
+    value's scale."""
     T, nH, D = q.shape
     H, S = cache["k_codes"].shape[1], cache["k_codes"].shape[2]
     G = nH // H
     out, lse = np.full((T, nH, D), np.nan), np.full((T, nH), np.nan)
-    reach, mass, seen = np.zeros((T, nH)), np.zeros((T, nH, D)), np.zeros((T, nH))
+    reach, mass, seen, heavy = np.zeros((T, nH)), np.zeros((T, nH, D)), np.zeros((T, nH)), np.zeros((T, nH))
     q = q.astype(np.float64)
     for b in range(len(kv_lens)):
         n = min(max(int(kv_lens[b]), 0), table.shape[1] * S)
@@ -146,14 +149,14 @@ def attention(cache, q, cu, kv_lens, table, scale, causal=True, window=0):
         for h in range(H):
             hidden = np.zeros(n, bool)
             with np.errstate(invalid="ignore"):
-                k, v = gather(cache, table[b], n, h, hidden)
+                k, v, vs = gather(cache, table[b], n, h, hidden)
             sees = np.broadcast_to(~hidden[None], (rows, n)).copy()
             if causal:
                 sees &= t <= pos
             if window:
                 sees &= t > pos - window
             used = sees.any(0)
-            k[~used], v[~used] = 0.0, 0.0
+            k[~used], v[~used], vs[~used] = 0.0, 0.0, 0.0
             for g in range(h * G, h * G + G):
                 x = q[cu[b]:cu[b + 1], g]
                 with np.errstate(invalid="ignore", divide="ignore"):
@@ -167,4 +170,5 @@ def attention(cache, q, cu, kv_lens, table, scale, causal=True, window=0):
                 mass[cu[b]:cu[b + 1], g] = p @ np.abs(v)
                 reach[cu[b]:cu[b + 1], g] = np.where(sees, np.abs(x) @ np.abs(k).T * abs(scale), 0).max(1, initial=0)
                 seen[cu[b]:cu[b + 1], g] = sees.sum(1)
-    return out, lse, (reach, mass, seen)
+                heavy[cu[b]:cu[b + 1], g] = (p * vs).max(1, initial=0)
+    return out, lse, (reach, mass, seen, heavy)

@@ -160,7 +160,7 @@ def test_scale_is_of_these_tokens_only(n):
 
 def test_extremes():
     """Zeros, the type's largest, infinities and NaN: the scale is that of the
-    finite values within 2^-64 and 2^64, what is past it saturates, and no code
+    finite values within 2^-64 and 2^48, what is past it saturates, and no code
     is a NaN."""
     H, D, S = 6, 32, 16
     x = torch.zeros(4, H, D)
@@ -175,7 +175,7 @@ def test_extremes():
     torch.cuda.synchronize()
     g = A.host_cache(cache)
     assert np.array_equal(g["k_scales"][1], g["v_scales"][1])
-    assert g["k_scales"][1].tolist() == [2.0 ** -64, 2.0 ** 64, 2.0 ** -64, 2.0 ** -7, 1.0, 2.0]
+    assert g["k_scales"][1].tolist() == [2.0 ** -64, 2.0 ** 48, 2.0 ** -64, 2.0 ** -7, 1.0, 2.0]
     codes = g["k_codes"][1, :, :4]
     assert not ((codes & 127) == 127).any() and (codes[0] == 0).all() and (codes[2] == 0).all()
     val = AO.E4M3[codes]
