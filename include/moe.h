@@ -454,8 +454,8 @@ moe_status moe_rope_axes(const void* x, int32_t x_dtype, int64_t x_stride_t, int
  *   v_codes   device uint8 [num_pages][n_kv_heads][page_size / 16][head_dim][16]:
  *             blocks of 16 tokens, channel by channel (value d of slot i at
  *             [i / 16][d][i % 16]), the order in which attention reads them.
- *   k_scales, v_scales   device f32 [num_pages][n_kv_heads]; of pages that hold
- *             tokens, within 2^-64 and 2^48.
+ *   k_scales, v_scales   device f32 [num_pages][n_kv_heads], within 2^-64 and
+ *             2^48 (attention takes others as the nearest of these).
  * page_size 16, 32, 64 or 128; head_dim a multiple of 16 in [16, 256];
  * n_kv_heads 1..256; codes 16-byte, scales 4-byte aligned.  Nothing needs
  * initialising; slots no token was appended to are never used. */
@@ -519,10 +519,11 @@ moe_status moe_kv_append(const moe_kv_cache* cache, const moe_kv_batch* batch, c
  *   s_t = sm_scale * sum_d q[d] k_t[d],   out = sum_t softmax(s)_t v_t,
  *   lse = log sum_t exp(s_t) (natural).
  * A row that sees no token gives zeros and lse = -infinity.  bf16 queries:
- * fp32 scores, sums and softmax, probabilities rounded to 11 bits (fp16) for
- * the second product.  f32 queries: 24-bit products throughout.  Codes of tokens that no
- * row sees, and their scales, may hold anything; a NaN code (0x7f, 0xff; an
- * append makes none) in a token that some row sees makes every row of its
+ * fp32 scores, sums and softmax; probabilities times v_scales, over the row's
+ * largest, rounded to 11 bits (fp16, whose smallest step is here 2^-31) for the
+ * second product.  f32 queries: 24-bit products throughout.  Codes of tokens
+ * that no row sees, and their scales, may hold anything; a NaN code (0x7f, 0xff;
+ * an append makes none) in a token that some row sees makes every row of its
  * sequence unspecified.
  * q          device [T, n_heads, head_dim] of q_dtype (MOE_BF16 or MOE_F32),
  *            strides as in moe_rope_axes (already rotated).
@@ -532,10 +533,13 @@ moe_status moe_kv_append(const moe_kv_cache* cache, const moe_kv_batch* batch, c
  * out        device [T, n_heads, head_dim] of q_dtype, dense (written; rows of
  *            no sequence are left as they were).
  * lse        device f32 [T, n_heads] or NULL (written likewise).
+ * sm_scale   within -2^64 and 2^64.
  * workspace  device, >= moe_paged_attention_workspace_size() bytes, 16-byte
  *            aligned; no initialisation, not preserved.
  * Limits: n_heads a multiple of n_kv_heads, G <= 128; at most 2^24 row blocks
- * (128 rows of a KV head).  The result is the same on every run.  Errors: MOE_ERR_SHAPE, MOE_ERR_DTYPE, MOE_ERR_NULL, MOE_ERR_ALIGN,
+ * (128 rows of a KV head).  The result is the same on every run.  Calls that
+ * may overlap in time, graph replays among them, need workspaces of their own.
+ * Errors: MOE_ERR_SHAPE, MOE_ERR_DTYPE, MOE_ERR_NULL, MOE_ERR_ALIGN,
  * MOE_ERR_WORKSPACE, MOE_ERR_HIP.  T == 0 or B == 0 is a no-op.
  */
 moe_status moe_paged_attention(const moe_kv_cache* cache, const moe_kv_batch* batch, const void* q,
@@ -544,8 +548,8 @@ moe_status moe_paged_attention(const moe_kv_cache* cache, const moe_kv_batch* ba
                                int32_t window, void* out, float* lse, void* workspace,
                                size_t workspace_bytes, void* stream);
 
-/* Bytes of workspace moe_paged_attention needs for T rows in B sequences of
- * at most max_q rows, over a cache of these sizes (its pointers are not
+/* Bytes of workspace moe_paged_attention needs for at most T rows in at most B
+ * sequences of at most max_q rows, over a cache of these sizes (its pointers are not
  * looked at).  Host only. */
 moe_status moe_paged_attention_workspace_size(const moe_kv_cache* cache, int32_t T, int32_t B,
                                               int32_t n_heads, int32_t max_q, size_t* bytes);

@@ -7,9 +7,9 @@
 // s + log2 vs and sums l of exp2(s - m) and o of exp2(s + log2 vs - m) vc:
 // out = o / l, lse = m + log2 l.  Taking vs into the maximum is what lets the
 // second product's operands, x = exp2(s + log2 vs - m) and the codes, be fp16
-// without any bound on the scales: x is at most 2^8 (kMaxSlack), the row's
-// largest at least about 1, so x has 11 bits down to 2^-14 of it and an error
-// of 2^-25 of it below; as bf16 it would have 8.  Codes are exact in both, and
+// whatever the scales: x is at most 2^15, a row's largest at least 2^7 (kMaxLow,
+// kMaxSlack), so x has 11 bits down to 2^-21 of the largest and an error of
+// 2^-32 of it below; as bf16 it would have 8 bits.  Codes are exact in both, and
 // bf16 queries go into bf16 MFMA as they are; both accumulate in fp32.  fp32
 // queries, and their x, are the sum of three bf16 terms: 24 bits, three MFMAs
 // in place of one.
@@ -58,6 +58,7 @@ struct AttnArgs {
   float* lse;            // [T][nH] or NULL
   float* part_o;         // partial results of sequences that several workgroups share
   float* part_ml;
+  int2* part_seq;        // [H][W]: sequence that begins in the workgroup's run and goes on after it, and its parts
   int W;                 // workgroups per KV head
   int rows;              // rows of a sequence, at most
 };
@@ -159,10 +160,16 @@ __device__ __forceinline__ f32x16 mfma_value(const bf16x8 a, const bf16x8 b[NS],
   return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b[0]), c, 0, 0, 0);
 }
 
+// A page's scale, within the bounds that an append keeps (a scale of zero, or
+// none at all, then makes no infinity or NaN of its own).
+__device__ __forceinline__ float page_scale_of(float s) {
+  return __builtin_fminf(__builtin_fmaxf(s, kMinPageScale), kMaxPageScale);
+}
+
 // Scale of a page's scores; at least the smallest normal number, so that a
 // hidden score, -infinity, stays that.
 __device__ __forceinline__ float score_scale(const AttnArgs& a, float ks) {
-  return __builtin_fmaxf(ks * a.scale2, 0x1p-126f);
+  return __builtin_fmaxf(page_scale_of(ks) * a.scale2, 0x1p-126f);
 }
 
 // Over lanes l and l ^ 16, and l and l ^ 32 (gfx950 swaps rows and halves of
@@ -191,11 +198,11 @@ __device__ __forceinline__ float sum32(float v) {
   return __uint_as_float(w[0]) + __uint_as_float(w[1]);
 }
 
-// A running maximum is replaced only when a score passes it by this much (in
-// powers of two): until then probabilities are at most 2^8, which costs no
-// precision, and neither the maximum over lanes nor the accumulators' scaling
-// is needed.
-constexpr float kMaxSlack = 8.0f;
+// The running m is put kMaxLow (in powers of two) below the maximum, and
+// replaced only when a score passes it by kMaxSlack: until then neither the
+// maximum over lanes nor the accumulators' scaling is needed, and x stays below
+// fp16's largest value.
+constexpr float kMaxLow = 7.0f, kMaxSlack = 15.0f;
 
 // w with its bytes before `skip` and from n on zeroed.
 __device__ __forceinline__ i32x4 keep_bytes(i32x4 w, int skip, int n) {
@@ -294,7 +301,7 @@ __device__ __forceinline__ float attn_probs(const f32x16& sc, float f, float c, 
   return sum;
 }
 
-// One row's finished output: o sums, their maximum m (base 2) and sum l.
+// Four values of a row's output from its sums o and l.
 template <int NS>
 __device__ __forceinline__ void attn_store4(const AttnArgs& a, size_t row, int d, const float o[4], float l) {
   const float inv = l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);

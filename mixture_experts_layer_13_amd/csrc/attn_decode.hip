@@ -11,44 +11,45 @@ __global__ __launch_bounds__(kDecThreads) void attn_decode_kernel(AttnArgs a) {
   attn_decode_run<DT, NR, NS, OWN, STREAM>(a, blockIdx.x, blockIdx.y, sh);
 }
 
-// Joins the parts of a sequence that several workgroups shared, and writes the
-// rows of a sequence that sees nothing: zero, with lse -inf.  One workgroup
-// per row: its lanes first find the parts' common maximum, then groups of
-// DT / 4 lanes add up every ... th part, and LDS joins the groups.
+// Joins the parts of the sequence, if any, that began in workgroup blockIdx.x's
+// run and went on into the next ones.  One workgroup per row: its lanes find
+// the parts' common maximum, groups of DT / 4 lanes add up every GROUPS-th
+// part, and LDS joins the groups.  Latency bounds it (4 us, most of it the
+// launch and two trips to memory): what follows the header, the parts'
+// maxima, sums and first kJoinAhead values of each lane, is loaded at once.
+constexpr int kJoinAhead = 4;
 template <int DT, int ROWS, int NS>
 __global__ __launch_bounds__(kDecThreads) void attn_join_kernel(AttnArgs a) {
-  constexpr int LANES = DT / 4, GROUPS = kDecThreads / LANES;
-  __shared__ int scan[kDecWaves];
-  __shared__ int base[1];
+  constexpr int LANES = DT / 4, GROUPS = kDecThreads / LANES, ML = kAttnGroups / kDecThreads;
   __shared__ float weight[kAttnGroups];
   __shared__ float red[kDecWaves];
   __shared__ float4 acc[GROUPS][LANES];
-  const int b = blockIdx.x, h = blockIdx.y, row = blockIdx.z;
-  const Seq s = load_seq(a.b, a.c.lS, b);
-  if (s.q <= 0 || s.q > ROWS / a.G || row >= s.q * a.G) return;
-  const int n = view_of(a, s, 0, s.q).n;
-  long long total = 0, at = 0;
-  for (int i0 = 0; i0 < a.b.B; i0 += kDecThreads) {
-    const int i = i0 + threadIdx.x;
-    const int v = i < a.b.B ? dec_tiles(a, ROWS, i) : 0;
-    int t;
-    const int e = block_scan<kDecWaves>(v, scan, &t);
-    if (i == b) base[0] = e - v;
-    if (b >= i0 && b < i0 + kDecThreads) {
-      __syncthreads();
-      at = total + base[0];
-    }
-    total += t;
-  }
-  const long long run = dec_run(total, a.W);
-  const int w0 = (int)(at / run), parts = n > 0 ? (int)((at + dec_slots(n) - 1) / run) - w0 + 1 : 0;
-  if (parts == 1) return;  // finished by its workgroup
+  const int w0 = blockIdx.x, h = blockIdx.y, row = blockIdx.z;
+  const int2 shared = a.part_seq[h * a.W + w0];
+  const int b = shared.x, parts = shared.y;
+  if (b < 0) return;
   const size_t slot = (size_t)h * a.W + w0;
   // part k: slot 1 (begins the sequence) of workgroup w0, slot 0 of the later ones
   auto part = [&](int k) { return ((slot + k) * 2 + (k == 0 ? 1 : 0)) * ROWS + row; };
+  const int lane = threadIdx.x % LANES, group = threadIdx.x / LANES;
+  const Seq s = load_seq(a.b, a.c.lS, b);
+  float2 ml[ML];
+#pragma unroll
+  for (int j = 0; j < ML; ++j) {
+    const int k = threadIdx.x + j * kDecThreads;
+    ml[j] = k < parts ? *reinterpret_cast<const float2*>(a.part_ml + part(k) * 2) : make_float2(-__builtin_inff(), 0.0f);
+  }
+  float4 first[kJoinAhead];
+#pragma unroll
+  for (int j = 0; j < kJoinAhead; ++j) {
+    const int k = group + j * GROUPS;
+    first[j] = *reinterpret_cast<const float4*>(a.part_o + part(k < parts ? k : 0) * DT + 4 * lane);
+  }
+  if (row >= s.q * a.G) return;
 
-  float m = -__builtin_inff();
-  for (int k = threadIdx.x; k < parts; k += kDecThreads) m = __builtin_fmaxf(m, a.part_ml[part(k) * 2]);
+  float m = ml[0].x;
+#pragma unroll
+  for (int j = 1; j < ML; ++j) m = __builtin_fmaxf(m, ml[j].x);
   m = wave_max(m);
   if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = m;
   __syncthreads();
@@ -56,25 +57,28 @@ __global__ __launch_bounds__(kDecThreads) void attn_join_kernel(AttnArgs a) {
   for (int k = 0; k < kDecWaves; ++k) m = __builtin_fmaxf(m, red[k]);
   const float mm = m == -__builtin_inff() ? 0.0f : m;
   float l = 0.0f;
-  for (int k = threadIdx.x; k < parts; k += kDecThreads) {
-    const float f = __builtin_amdgcn_exp2f(a.part_ml[part(k) * 2] - mm);
-    weight[k] = f;
-    l += f * a.part_ml[part(k) * 2 + 1];
+#pragma unroll
+  for (int j = 0; j < ML; ++j) {
+    const float f = __builtin_amdgcn_exp2f(ml[j].x - mm);
+    weight[threadIdx.x + j * kDecThreads] = f;  // 0 past the last part
+    l += f * ml[j].y;
   }
   l = wave_sum(l);
   __syncthreads();  // weights written, maxima read
   if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = l;
-  const int lane = threadIdx.x % LANES, group = threadIdx.x / LANES;
   float4 o = make_float4(0, 0, 0, 0);
-#pragma unroll 4
-  for (int k = group; k < parts; k += GROUPS) {
-    const float f = weight[k];
-    const float4 v = *reinterpret_cast<const float4*>(a.part_o + part(k) * DT + 4 * lane);
+  auto add = [&](float f, const float4& v) {
     o.x += f * v.x;
     o.y += f * v.y;
     o.z += f * v.z;
     o.w += f * v.w;
-  }
+  };
+#pragma unroll
+  for (int j = 0; j < kJoinAhead; ++j)
+    if (group + j * GROUPS < parts) add(weight[group + j * GROUPS], first[j]);
+#pragma unroll 4
+  for (int k = group + kJoinAhead * GROUPS; k < parts; k += GROUPS)
+    add(weight[k], *reinterpret_cast<const float4*>(a.part_o + part(k) * DT + 4 * lane));
   acc[group][lane] = o;
   __syncthreads();
   if (group != 0 || 4 * lane >= a.c.D) return;
@@ -98,7 +102,7 @@ __global__ __launch_bounds__(kDecThreads) void attn_join_kernel(AttnArgs a) {
 template <int DT, int NR, int NS>
 static int join_launch(const AttnArgs& a, hipStream_t st) {
   const int rows = 16 * NR < a.rows ? 16 * NR : a.rows;  // of a sequence, at most
-  hipLaunchKernelGGL((attn_join_kernel<DT, 16 * NR, NS>), dim3((unsigned)a.b.B, (unsigned)a.c.H, (unsigned)rows),
+  hipLaunchKernelGGL((attn_join_kernel<DT, 16 * NR, NS>), dim3((unsigned)a.W, (unsigned)a.c.H, (unsigned)rows),
                      dim3(kDecThreads), 0, st, a);
   return (int)hipGetLastError();
 }

@@ -171,7 +171,7 @@ __device__ __forceinline__ void dec_tile(const AttnArgs& a, const View& vw, int 
   if (dec_early<DT>() && next >= 0) dec_load_k<DT, STREAM>(a, pg, next, h, t);
   const int t0 = tile * kAttnTile;
   const bool masked = t0 < st.all_lo || t0 + kAttnTile > st.all_hi || __any(t.gone);
-  const float f = t.gone ? 1.0f : score_scale(a, t.ks), fv = t.gone ? 1.0f : t.vs;
+  const float f = t.gone ? 1.0f : score_scale(a, t.ks), fv = t.gone ? 1.0f : page_scale_of(t.vs);
   const float lv = __builtin_amdgcn_logf(fv), rv = __builtin_amdgcn_exp2f(-lv);
   float top[NR];
   bool grow = false;
@@ -184,7 +184,7 @@ __device__ __forceinline__ void dec_tile(const AttnArgs& a, const View& vw, int 
   if (__any(grow)) {
 #pragma unroll
     for (int r = 0; r < NR; ++r) {
-      const float m = __builtin_fmaxf(st.m[r], max32(max16(top[r])));
+      const float m = __builtin_fmaxf(st.m[r], max32(max16(top[r])) - kMaxLow);
       const float keep = m == -__builtin_inff() ? 1.0f : __builtin_amdgcn_exp2f(st.m[r] - m);
       st.m[r] = m;
       st.l[r] *= keep;
@@ -226,6 +226,24 @@ struct DecShared {
   int scan[kDecWaves], found[2];
 };
 
+// The rows of sequence b, if this kernel's, that see no token: zero, with lse
+// -infinity.  By one thread: they are few.
+__device__ __forceinline__ bool dec_empty(const AttnArgs& a, const Seq& s, int rows_max) {
+  return s.q > 0 && s.q <= rows_max / a.G && view_of(a, s, 0, s.q).n == 0;
+}
+template <int NS>
+__device__ __forceinline__ void dec_clear(const AttnArgs& a, int rows_max, int b, int h) {
+  const Seq s = load_seq(a.b, a.c.lS, b);
+  if (!dec_empty(a, s, rows_max)) return;
+  const float zero[4] = {0, 0, 0, 0};
+  for (int i = 0; i < s.q; ++i)
+    for (int g = 0; g < a.G; ++g) {
+      const size_t row = (size_t)(s.q0 + i) * a.nH + h * a.G + g;
+      for (int d = 0; d < a.c.D; d += 4) attn_store4<NS>(a, row, d, zero, 0.0f);
+      if (a.lse) a.lse[row] = -__builtin_inff();
+    }
+}
+
 // Workgroup w of KV head h.  OWN: w is the sequence, whose workgroup then also
 // writes rows that see nothing.  STREAM: codes are read past the caches.
 template <int DT, int NR, int NS, bool OWN, bool STREAM>
@@ -238,7 +256,8 @@ __device__ __forceinline__ void attn_decode_run(const AttnArgs& a, int w, int h,
 
   // the run [begin, end) of this workgroup and the sequence it starts in
   int b = w, skip = 0;
-  long long left = 1LL << 40;
+  long long left = 1LL << 40, run = 0;
+  int2 shared = make_int2(-1, 0);
   if (!OWN) {
     long long total = 0, begin = 0, before = 0;
     int n = 0, e = 0, t;
@@ -246,10 +265,15 @@ __device__ __forceinline__ void attn_decode_run(const AttnArgs& a, int w, int h,
       n = base + (int)threadIdx.x < a.b.B ? dec_tiles(a, ROWS, base + threadIdx.x) : 0;
       e = block_scan<kDecWaves>(n, sh.scan, &t);
       total += t;
+      const int own = base + (int)threadIdx.x;  // of the sequences that see nothing, every W-th is this workgroup's
+      if (own < a.b.B && n == 0 && own % a.W == w) dec_clear<NS>(a, ROWS, own, h);
     }
-    const long long run = dec_run(total, a.W);
+    run = dec_run(total, a.W);
     begin = w * run;
-    if (begin >= total) return;
+    if (begin >= total) {
+      if (threadIdx.x == 0) a.part_seq[h * a.W + w] = shared;
+      return;
+    }
     left = total - begin < run ? total - begin : run;
     for (int base = 0; base < a.b.B && before <= begin; base += kDecThreads) {
       if (a.b.B > kDecThreads) {  // else the one scan above
@@ -303,6 +327,10 @@ __device__ __forceinline__ void attn_decode_run(const AttnArgs& a, int w, int h,
       }
     }
     const bool whole = skip == 0 && count == n;
+    if (!OWN && skip == 0 && !whole) {  // so this run is not the last, and its length is `run`
+      const long long at = run - left;
+      shared = make_int2(b, (int)((at + dec_slots(n) - 1) / run) + 1);
+    }
 #pragma unroll
     for (int r = 0; r < NR; ++r) {
       const float l = sum32(sum16(st.l[r]));
@@ -353,6 +381,7 @@ __device__ __forceinline__ void attn_decode_run(const AttnArgs& a, int w, int h,
     skip = 0;
     ++b;
   }
+  if (threadIdx.x == 0) a.part_seq[h * a.W + w] = shared;
 }
 
 }  // namespace moe

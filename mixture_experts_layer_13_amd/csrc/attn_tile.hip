@@ -4,7 +4,7 @@
 // A workgroup takes 128 consecutive rows of one sequence and KV head (the
 // query heads of a token are consecutive rows, so all of them use the same
 // keys and values) and walks the 64-token tiles that they see.  A tile's codes
-// are converted to bf16 once and put into LDS in MFMA operand order, 16 bytes
+// are converted to MFMA operands once and put into LDS in operand order, 16 bytes
 // per lane and fragment, so that both the writes and the reads of a wave are
 // contiguous; the next tile's codes are already in flight in registers while
 // the waves work on this one.  Operand layout, transposed first product and
@@ -182,7 +182,7 @@ __global__ __launch_bounds__(kTileThreads, DT <= 128 && NS == 1 ? 2 : 1) void at
   float f0 = 1.0f, f1 = 1.0f, v0 = 1.0f, v1 = 1.0f;
   bool out0 = false, out1 = false;
   auto store_scales = [&](const TileRaw<DT>& raw, int buf) {
-    const float f = raw.gone ? 1.0f : score_scale(a, raw.ks), v = raw.gone ? 1.0f : raw.vs;
+    const float f = raw.gone ? 1.0f : score_scale(a, raw.ks), v = raw.gone ? 1.0f : page_scale_of(raw.vs);
     if (UNI) {
       f0 = f1 = f;
       v0 = v1 = v;
@@ -268,7 +268,7 @@ __global__ __launch_bounds__(kTileThreads, DT <= 128 && NS == 1 ? 2 : 1) void at
                           : __builtin_fmaxf(__builtin_fmaf(attn_top(sc[0]), cf0, lv0),
                                             __builtin_fmaf(attn_top(sc[1]), cf1, lv1));
     if (__any(top > mx + kMaxSlack)) {
-      const float mn = __builtin_fmaxf(mx, max32(top));
+      const float mn = __builtin_fmaxf(mx, max32(top) - kMaxLow);
       const float keep = mn == -__builtin_inff() ? 1.0f : __builtin_amdgcn_exp2f(mx - mn);
       mx = mn;
       l *= keep;

@@ -29,7 +29,6 @@
 
 namespace moe {
 
-constexpr float kMinPageScale = 0x1p-64f, kMaxPageScale = 0x1p+48f;
 constexpr int kAppendThreads = 1024;
 
 struct AppendArgs {

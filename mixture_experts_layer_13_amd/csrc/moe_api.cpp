@@ -3,6 +3,7 @@
 // returns a non-zero status has enqueued nothing.
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
 #include <cstdarg>
 #include <cstdio>
 #include <cstring>
@@ -708,8 +709,19 @@ moe::BatchArgs batch_args(const moe_kv_batch* b) {
 struct AttnPlan {
   int dec_rows, W, rows;
   long long tile_units;
-  size_t part_ml, bytes;
+  size_t part_ml, part_seq, bytes;
 };
+
+int attn_width(const moe_kv_cache* c) { return std::max(1, moe::attn_groups(c->head_dim) / c->n_kv_heads); }
+
+// Places of the parts in the workspace, for sequences of up to dec_rows rows.
+void attn_layout(const moe_kv_cache* c, int dec_rows, AttnPlan* p) {
+  const size_t groups = (size_t)c->n_kv_heads * attn_width(c), slots = groups * 2 * dec_rows;
+  const int DT = c->head_dim <= 64 ? 64 : (c->head_dim <= 128 ? 128 : 256);
+  p->part_ml = up256(slots * DT * sizeof(float));
+  p->part_seq = up256(p->part_ml + slots * 2 * sizeof(float));
+  p->bytes = up256(p->part_seq + groups * 2 * sizeof(int32_t));
+}
 
 moe_status attn_plan(const moe_kv_cache* c, int32_t T, int32_t B, int32_t n_heads, int32_t max_q, AttnPlan* p) {
   if (n_heads < 1 || n_heads % c->n_kv_heads || n_heads / c->n_kv_heads > 128)
@@ -728,11 +740,8 @@ moe_status attn_plan(const moe_kv_cache* c, int32_t T, int32_t B, int32_t n_head
   if (p->tile_units * c->n_kv_heads > (1LL << 24) - 1024)
     return fail(MOE_ERR_SHAPE, "T=%d rows of %d heads are too many for one call", T, n_heads);
   if (p->dec_rows) {
-    p->W = moe::attn_groups(c->head_dim) / c->n_kv_heads > 0 ? moe::attn_groups(c->head_dim) / c->n_kv_heads : 1;
-    const size_t slots = (size_t)c->n_kv_heads * p->W * 2 * p->dec_rows;
-    const int DT = c->head_dim <= 64 ? 64 : (c->head_dim <= 128 ? 128 : 256);
-    p->part_ml = up256(slots * DT * sizeof(float));
-    p->bytes = up256(p->part_ml + slots * 2 * sizeof(float));
+    p->W = attn_width(c);
+    attn_layout(c, p->dec_rows, p);
   }
   return MOE_OK;
 }
@@ -796,7 +805,13 @@ moe_status moe_paged_attention_workspace_size(const moe_kv_cache* cache, int32_t
   if ((s = check_counts(T, B))) return s;
   AttnPlan p;
   if ((s = attn_plan(cache, T, B, n_heads, max_q, &p))) return s;
-  *bytes = p.bytes;
+  // enough for fewer tokens or rows too, whose sequences may go another way
+  const int G = n_heads / cache->n_kv_heads;
+  int rows = 0;
+  for (int q = 1; q == 1 || (q <= std::min(max_q, T) && q * G <= 64); ++q)
+    rows = std::max(rows, moe::attn_decode_rows(cache->head_dim, q * G));
+  if (rows) attn_layout(cache, rows, &p);
+  *bytes = rows ? p.bytes : 0;
   return ok();
 }
 
@@ -810,7 +825,7 @@ moe_status moe_paged_attention(const moe_kv_cache* cache, const moe_kv_batch* ba
   if (!value_dtype(q_dtype)) return fail(MOE_ERR_DTYPE, "q_dtype must be MOE_F32 or MOE_BF16");
   if ((s = check_strides("q", q_dtype, q_stride_t, q_stride_h, 0))) return s;
   if (window < 0 || window > (1 << 30)) return fail(MOE_ERR_SHAPE, "window=%d must be in [0, 2^30]", window);
-  if (!(sm_scale - sm_scale == 0.0f)) return fail(MOE_ERR_SHAPE, "sm_scale must be finite");
+  if (!(__builtin_fabsf(sm_scale) <= 0x1p+64f)) return fail(MOE_ERR_SHAPE, "sm_scale must be within -2^64 and 2^64");
   if (!batch->cu_q && max_q != 1) return fail(MOE_ERR_SHAPE, "max_q=%d must be 1 without cu_q", max_q);
   AttnPlan p;
   if ((s = attn_plan(cache, batch->T, batch->B, n_heads, max_q, &p))) return s;
@@ -840,6 +855,7 @@ moe_status moe_paged_attention(const moe_kv_cache* cache, const moe_kv_batch* ba
   if (p.dec_rows) {
     a.part_o = reinterpret_cast<float*>(workspace);
     a.part_ml = reinterpret_cast<float*>((char*)workspace + p.part_ml);
+    a.part_seq = reinterpret_cast<int2*>((char*)workspace + p.part_seq);
     a.W = p.W;
     a.rows = p.rows;
   }

@@ -18,6 +18,9 @@ struct PagedArgs {
   int pages, lS, H, D;  // page size S = 1 << lS
 };
 
+// Bounds of a page's scale.
+constexpr float kMinPageScale = 0x1p-64f, kMaxPageScale = 0x1p+48f;
+
 struct BatchArgs {
   const int32_t* cu_q;     // [B + 1] first query row of each sequence, or NULL (row b)
   const int32_t* kv_lens;  // [B] cached tokens, the queries' own among them

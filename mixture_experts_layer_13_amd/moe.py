@@ -305,10 +305,14 @@ def _run(device, stream, call, *args):
 
 
 def _made(shape, dtype, device, stream):
-    """A tensor made for a call that runs on `stream` (None: the current one)."""
-    t = torch.empty(shape, dtype=dtype, device=device)
-    if stream is not None and t.is_cuda:
-        t.record_stream(stream)
+    """A tensor made for a call that runs on `stream` (None: the current one):
+    from that stream's memory, so that nothing still at work on another one
+    holds it, and not given back before the current stream is done with it."""
+    if stream is None or device.type != "cuda":
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    t.record_stream(torch.cuda.current_stream(device))
     return t
 
 
@@ -425,17 +429,20 @@ def moe_paged_attention_workspace_size(cache, T, B, n_heads, max_q=1):
     return int(n.value)
 
 
-def moe_paged_attention(cache, q, kv_lens, block_table, cu_q=None, max_q=1, sm_scale=None, causal=True, window=0,
+def moe_paged_attention(cache, q, kv_lens, block_table, cu_q=None, max_q=None, sm_scale=None, causal=True, window=0,
                         out=None, lse=None, return_lse=False, workspace=None, stream=None):
     """q [T, nH, D] bf16/f32 (rotated) over the cache -> out [T, nH, D], and
     with return_lse (or lse given) the log sums lse f32 [T, nH].  max_q: at
-    least the rows of every sequence.  sm_scale None: 1 / sqrt(D)."""
+    least the rows of every sequence (None: T, or 1 without cu_q).  sm_scale
+    None: 1 / sqrt(D)."""
     shape, dev = q.shape, cache.device
     if len(shape) != 3 or shape[2] != cache.head_dim:
         raise MoEError(MOE_ERR_SHAPE, f"q has shape {tuple(shape)}, not [T, heads, {cache.head_dim}]")
     T, nH, D = shape
     qp, qc, qt, qh = _heads(q, shape, "q", dev)
     batch = cache._batch(T, kv_lens, block_table, cu_q)
+    if max_q is None:
+        max_q = 1 if cu_q is None else max(T, 1)
     if out is None:
         out = _made(shape, q.dtype, dev, stream)
     elif out.dtype != q.dtype:
@@ -649,19 +656,19 @@ class PagedAttention:
     rotated, keys and values into the paged cache, attention over it (the calls
     moe_rope_axes, moe_kv_append and moe_paged_attention), with the buffers
     allocated once for at most max_tokens rows in max_seqs sequences of at most
-    max_q rows.  Nothing is allocated or synchronised per call, so the sequence
+    max_q rows (None: as many as there are).  Nothing is allocated or synchronised per call, so the sequence
     can be captured into a HIP graph; lengths, tables and positions are read on
     the device and may change between replays."""
 
-    def __init__(self, cache, n_heads, inv_freq, max_tokens, max_seqs=None, max_q=1, pair_axis=None,
+    def __init__(self, cache, n_heads, inv_freq, max_tokens, max_seqs=None, max_q=None, pair_axis=None,
                  interleaved=False, sm_scale=None, causal=True, window=0, dtype=torch.bfloat16):
-        self.cache, self.n_heads, self.max_q = cache, n_heads, max_q
+        self.cache, self.n_heads, self.max_q = cache, n_heads, max_q or max_tokens
         self.inv_freq, self.pair_axis, self.interleaved = inv_freq, pair_axis, interleaved
         self.sm_scale, self.causal, self.window = sm_scale, causal, window
         shape = (max_tokens, n_heads, cache.head_dim)
         self.q = torch.empty(shape, dtype=dtype, device=cache.device)
         self.out = torch.empty(shape, dtype=dtype, device=cache.device)
-        n = moe_paged_attention_workspace_size(cache, max_tokens, max_seqs or max_tokens, n_heads, max_q)
+        n = moe_paged_attention_workspace_size(cache, max_tokens, max_seqs or max_tokens, n_heads, self.max_q)
         self.workspace = torch.empty(max(n, 16), dtype=torch.uint8, device=cache.device)
 
     def __call__(self, q, k, v, positions, kv_lens, block_table, cu_q=None, stream=None):

@@ -104,8 +104,8 @@ def check_attention(out, lse, ref, dtype, D, label):
     rounded: 2 u reach) every p is off by a factor within 2 e + 8 u.  Numerator
     and denominator are fp32 sums over `seen` tokens: (seen + 8) u each.  bf16
     queries: x = p vs over the row's largest p vs (`heavy`) is rounded to fp16,
-    by at most 2^-11 of itself, or 2^-25 where it is below 2^-14, which makes
-    at most seen 448 2^-25 heavy of the output; that is rounded by 2^-8.  fp32
+    by at most 2^-11 of itself, or 2^-32 where it is below 2^-21, which makes
+    at most seen 448 2^-32 heavy of the output; that is rounded by 2^-8.  fp32
     queries: 24 bits of p and of the output (u)."""
     o64, l64, (reach, mass, seen, heavy) = ref
     live = ~np.isnan(l64)
@@ -114,7 +114,7 @@ def check_attention(out, lse, ref, dtype, D, label):
     rel = 2 * (2 * e + 8 * u) + 2 * (seen + 8) * u
     h = HALF_STEP[dtype]
     p = 2.0 ** -11 if dtype == "bf16" else h
-    floor = (seen * 448 * 2.0 ** -25 * heavy if dtype == "bf16" else 0 * seen)[:, :, None]
+    floor = (seen * 448 * 2.0 ** -32 * heavy if dtype == "bf16" else 0 * seen)[:, :, None]
     tol = ((rel + p)[:, :, None] * mass + floor) * (1 + h) + h * np.abs(o64) + 1e-30
     got, glse = f64(out), f64(lse)
     assert np.isfinite(got[live]).all(), label

@@ -111,6 +111,7 @@ def attend(c="default", b="default", q=F, dt=BF, qs=(4096, 128), nH=32, max_q=9,
     (dict(nH=0), moe.MOE_ERR_SHAPE), (dict(nH=31), moe.MOE_ERR_SHAPE), (dict(nH=8 * 129), moe.MOE_ERR_SHAPE),
     (dict(max_q=0), moe.MOE_ERR_SHAPE), (dict(window=-1), moe.MOE_ERR_SHAPE), (dict(window=(1 << 30) + 1), moe.MOE_ERR_SHAPE),
     (dict(scale=float("nan")), moe.MOE_ERR_SHAPE), (dict(scale=float("inf")), moe.MOE_ERR_SHAPE),
+    (dict(scale=-2.0 ** 64 * 1.001), moe.MOE_ERR_SHAPE),
     (dict(b=batch(cu_q=None, T=4), max_q=2), moe.MOE_ERR_SHAPE), (dict(q=ODD16), moe.MOE_ERR_ALIGN),
     (dict(out=ODD16), moe.MOE_ERR_ALIGN), (dict(ws=ODD16), moe.MOE_ERR_ALIGN), (dict(lse=ODD4), moe.MOE_ERR_ALIGN),
     (dict(b=batch(T=1 << 28), max_q=1 << 28, c=cache(n_kv_heads=1), nH=32), moe.MOE_ERR_SHAPE),
@@ -133,6 +134,10 @@ def test_workspace_size():
     assert size(8, 8, 32, 0)[0] == moe.MOE_ERR_SHAPE
     assert size(-8, 8, 32, 1)[0] == moe.MOE_ERR_SHAPE
     assert size(8, 8, 32, 1, page_size=5)[0] == moe.MOE_ERR_SHAPE
+    for D, G in ((64, 8), (64, 3), (64, 40), (128, 4), (128, 20), (256, 16), (256, 17)):  # enough for less, too
+        most = size(600, 9, 2 * G, 600, head_dim=D, n_kv_heads=2)[1]
+        assert all(size(T, 2, 2 * G, m, head_dim=D, n_kv_heads=2)[1] <= most
+                   for T in (0, 1, 2, 3, 5, 8, 16, 17, 64, 65, 599) for m in (1, 2, 4, 7, 16, 33, 600))
     assert L.moe_paged_attention_workspace_size(None, 1, 1, 1, 1, ctypes.byref(n)) == moe.MOE_ERR_NULL
     assert L.moe_paged_attention_workspace_size(ref(cache()), 1, 1, 8, 1, None) == moe.MOE_ERR_NULL
 

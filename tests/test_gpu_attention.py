@@ -111,6 +111,53 @@ def test_many_sequences():
     run(q, [n + int(r.randint(0, 50)) for n in q], 1, 4, 32, 16, "bf16")
 
 
+@pytest.mark.parametrize("q", [[0, 1], [1, 40]])
+def test_sequences_that_see_nothing(q):
+    """Padding of a batch: sequences without tokens before, between and behind
+    the others, in a table long enough for workgroups to share sequences."""
+    kv = [0] * 40 + [1500] + [0] * 270 + [70, 0, 2100] + [0] * 30
+    rows = [1] * 40 + [1] + [q[i % 2] for i in range(270)] + [1, q[1], 1] + [1] * 30
+    run(rows, kv, 2, 4, 32, 16, "bf16")
+    table = np.full((5, 100), 7, np.int32)
+    run([1, q[1], 1, 1, 2], [0] * 5, 2, 4, 32, 16, "f32", table=table, pages=8)
+
+
+@pytest.mark.parametrize("q", [1, 40])
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_many_small_probabilities_beside_a_large_one(q, dt):
+    """20000 tokens, each 2^-22.2 of one that has no value itself: their sum is
+    the output, and fp16 has its smallest step at 2^-24."""
+    n, H, D, S = 20000, 1, 64, 64
+    P, table = A.tables([n], S, 1)
+    host = A.random_cache(P, H, S, D, 2)
+    host["k_codes"][:] = 0
+    host["v_codes"] = (host["v_codes"] & 7) | 0x58  # 16 to 30
+    host["k_codes"][table[0, 0], 0, 5, 9] = 0x38  # 1
+    host["v_codes"][table[0, 0], 0, 0, :, 5] = 0
+    host["k_scales"][:], host["v_scales"][:] = 1, 0.25
+    x = torch.zeros(q, 2, D, dtype=A.DT[dt])
+    x[:, :, 9] = 1
+    scale = 22.2 * np.log(2)
+    ref = AO.attention(host, A.f64(x), [0, q], [n], table, scale, False)
+    out, lse = attend(host, table, x, [q], [n], causal=False, scale=scale)
+    torch.cuda.synchronize()
+    A.check_attention(out, lse, ref, dt, D, f"small beside large q{q} {dt}")
+
+
+@pytest.mark.parametrize("q", [[1, 1], [40, 30]])
+def test_scales_outside_their_bounds_count_as_the_nearest(q):
+    kv = [100, 64]
+    host, tab, x = make(q, kv, 1, 4, 64, 16, "bf16")
+    used = [p for row in tab for p in row if p >= 0]
+    host["v_scales"][used[0]], host["k_scales"][used[1]], host["v_scales"][used[2]] = 0, 0, -1
+    ref = {n: a.copy() for n, a in host.items()}
+    ref["v_scales"][used[0]] = ref["k_scales"][used[1]] = ref["v_scales"][used[2]] = AO.MIN_SCALE
+    out, lse = attend(host, tab, x, q, kv)
+    want = AO.attention(ref, A.f64(x), A.offsets(q), kv, tab, 64 ** -0.5)
+    torch.cuda.synchronize()
+    A.check_attention(out, lse, want, "bf16", 64, f"scales outside their bounds q{q}")
+
+
 @pytest.mark.parametrize("scale", [0.0, -0.3, 3.0])
 def test_scales(scale):
     run([1, 1], [130, 7], 1, 4, 64, 16, "f32", scale=scale)
@@ -199,6 +246,23 @@ def test_strides_streams_and_graphs(q):
             e = attend(host, tab, wide[:, 3:11].contiguous(), q, [n - step for n in kv], window=window)
             torch.cuda.synchronize()
             assert torch.equal(out, e[0]) and torch.equal(lse, e[1]), step
+
+
+def test_defaults_hold_for_any_rows():
+    """Without max_q every sequence is worked on; a layer's buffers do for fewer
+    rows than they were made for, whichever kernel takes these."""
+    H, G, D, S = 1, 8, 64, 16
+    for q in ([300, 1], [4], [1, 8, 2], [2, 1]):
+        kv = [n + 31 for n in q]
+        host, tab, x = make(q, kv, H, G, D, S, "bf16")
+        want = attend(host, tab, x, q, kv)[0]
+        cache, lens, table, cu = A.device_cache(host), A.i32(kv), A.i32(tab), A.i32(A.offsets(q))
+        got = moe.moe_paged_attention(cache, x.cuda(), lens, table, cu_q=cu)
+        size = moe.moe_paged_attention_workspace_size(cache, 512, 8, H * G, 512)
+        ws = torch.empty(size, dtype=torch.uint8, device="cuda")
+        again = moe.moe_paged_attention(cache, x.cuda(), lens, table, cu_q=cu, max_q=512, workspace=ws)
+        torch.cuda.synchronize()
+        assert torch.equal(got, want) and torch.equal(again, want), q
 
 
 def test_two_calls_at_once():
