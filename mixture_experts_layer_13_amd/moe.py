@@ -261,11 +261,12 @@ def moe_rope_quantize_per_head(x, positions, inv_freq, interleaved=False, invers
 _VALUE_CODES = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16}
 
 
-def _index(t, shape, name, device):
-    """Address of a dense int32 index buffer of this shape (None: any size) on `device`."""
-    if t.dtype != torch.int32:
+def _index(t, dims, first, name, device):
+    """Address of a dense int32 index buffer of this many dimensions, the first
+    of this size (None: any), on `device`."""
+    if t.dtype is not torch.int32:
         raise MoEError(MOE_ERR_DTYPE, f"{name} must be int32")
-    if t.dim() != len(shape) or any(n is not None and n != m for n, m in zip(shape, t.shape)):
+    if t.dim() != dims or (first is not None and t.size(0) != first):
         raise MoEError(MOE_ERR_SHAPE, f"{name} has shape {tuple(t.shape)}")
     if not t.is_contiguous():
         raise MoEError(MOE_ERR_UNSUPPORTED, f"{name} must be contiguous")
@@ -304,15 +305,16 @@ def _run(device, stream, call, *args):
         _check(status)
 
 
-def _made(shape, dtype, device, stream):
-    """A tensor made for a call that runs on `stream` (None: the current one):
-    from that stream's memory, so that nothing still at work on another one
-    holds it, and not given back before the current stream is done with it."""
-    if stream is None or device.type != "cuda":
-        return torch.empty(shape, dtype=dtype, device=device)
+def _made(like, shape, dtype, stream):
+    """A tensor of `like`'s device (and type, if dtype is None) made for a call
+    that runs on `stream` (None: the current one): from that stream's memory,
+    so that nothing still at work on another one holds it, and not given back
+    before the current stream is done with it."""
+    if stream is None or not like.is_cuda:
+        return like.new_empty(shape) if dtype is None else like.new_empty(shape, dtype=dtype)
     with torch.cuda.stream(stream):
-        t = torch.empty(shape, dtype=dtype, device=device)
-    t.record_stream(torch.cuda.current_stream(device))
+        t = like.new_empty(shape, dtype=dtype or like.dtype)
+    t.record_stream(torch.cuda.current_stream(like.device))
     return t
 
 
@@ -324,20 +326,20 @@ class Rotation:
 
     def __init__(self, positions, inv_freq, pair_axis=None, interleaved=False, inverse=False):
         dev = inv_freq.device
-        if inv_freq.dtype != torch.float32:
+        if inv_freq.dtype is not torch.float32:
             raise MoEError(MOE_ERR_DTYPE, "inv_freq must be f32")
         if inv_freq.dim() != 1 or not inv_freq.is_contiguous():
             raise MoEError(MOE_ERR_SHAPE, "inv_freq must be a dense vector")
-        half = inv_freq.shape[0]
+        half = inv_freq.size(0)
         axes, at, self.tokens = 1, None, None
         if positions is not None:
             dims = positions.dim()
             if dims not in (1, 2):
                 raise MoEError(MOE_ERR_SHAPE, "positions must be [T] or [axes, T]")
-            at = _index(positions, (None,) * dims, "positions", dev)
-            axes = positions.shape[0] if dims == 2 else 1
-            self.tokens = positions.shape[-1]
-        axis_at = None if pair_axis is None else _index(pair_axis, (half,), "pair_axis", dev)
+            at = _index(positions, dims, None, "positions", dev)
+            axes = positions.size(0) if dims == 2 else 1
+            self.tokens = positions.size(-1)
+        axis_at = None if pair_axis is None else _index(pair_axis, 1, half, "pair_axis", dev)
         self.positions, self.inv_freq, self.pair_axis, self.device = positions, inv_freq, pair_axis, dev
         self.struct = moe_rotation(at, axis_at, inv_freq.data_ptr(), axes, 2 * half, 1 if interleaved else 0,
                                    1 if inverse else 0)
@@ -357,7 +359,7 @@ def moe_rope_axes(x, rotation, out=None, out_dtype=None, stream=None):
         raise MoEError(MOE_ERR_SHAPE, f"x has shape {tuple(shape)}, not [T, heads, head_dim]")
     T, nH, D = shape
     if out is None:
-        out = _made(shape, out_dtype or x.dtype, dev, stream)
+        out = _made(x, shape, out_dtype, stream)
     xp, xc, xt, xh = _heads(x, shape, "x", dev)
     op, oc, ot, oh = _heads(out, shape, "out", dev)
     _run(dev, stream, lib().moe_rope_axes, xp, xc, xt, xh, rotation._for(T, dev), T, nH, D, op, oc, ot, oh)
@@ -391,11 +393,11 @@ class PagedKV:
 
     def _batch(self, T, kv_lens, block_table, cu_q):
         dev = self.device
-        lens = _index(kv_lens, (None,), "kv_lens", dev)
-        B = kv_lens.shape[0]
-        table = _index(block_table, (B, None), "block_table", dev)
-        cu = None if cu_q is None else _index(cu_q, (B + 1,), "cu_q", dev)
-        return moe_kv_batch(cu, lens, table, B, T, block_table.shape[1])
+        lens = _index(kv_lens, 1, None, "kv_lens", dev)
+        B = kv_lens.size(0)
+        table = _index(block_table, 2, B, "block_table", dev)
+        cu = None if cu_q is None else _index(cu_q, 1, B + 1, "cu_q", dev)
+        return moe_kv_batch(cu, lens, table, B, T, block_table.size(1))
 
 
 def alloc_kv_cache(num_pages, page_size, n_kv_heads, head_dim, device="cuda"):
@@ -444,21 +446,21 @@ def moe_paged_attention(cache, q, kv_lens, block_table, cu_q=None, max_q=None, s
     if max_q is None:
         max_q = 1 if cu_q is None else max(T, 1)
     if out is None:
-        out = _made(shape, q.dtype, dev, stream)
+        out = _made(q, shape, None, stream)
     elif out.dtype != q.dtype:
         raise MoEError(MOE_ERR_DTYPE, f"out is {out.dtype}, q is {q.dtype}")
     elif out.shape != shape or not out.is_contiguous() or out.device != dev:
         raise MoEError(MOE_ERR_SHAPE, f"out must be a dense {tuple(shape)} on the cache's device")
     if lse is None:
         if return_lse:
-            lse = _made((T, nH), torch.float32, dev, stream)
+            lse = _made(q, (T, nH), torch.float32, stream)
     elif lse.dtype != torch.float32:
         raise MoEError(MOE_ERR_DTYPE, "lse must be f32")
     elif lse.shape != (T, nH) or not lse.is_contiguous() or lse.device != dev:
         raise MoEError(MOE_ERR_SHAPE, f"lse must be a dense {(T, nH)} on the cache's device")
     if workspace is None:
-        workspace = _made(max(moe_paged_attention_workspace_size(cache, T, batch.B, nH, max_q), 16), torch.uint8, dev,
-                          stream)
+        size = moe_paged_attention_workspace_size(cache, T, batch.B, nH, max_q)
+        workspace = _made(q, (max(size, 16),), torch.uint8, stream)
     elif not workspace.is_contiguous() or workspace.device != dev:
         raise MoEError(MOE_ERR_WORKSPACE, "the workspace must be dense and on the cache's device")
     _run(dev, stream, lib().moe_paged_attention, ctypes.byref(cache.struct), ctypes.byref(batch), qp, qc, qt, qh, nH,
