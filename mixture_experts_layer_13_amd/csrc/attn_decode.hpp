@@ -13,6 +13,12 @@
 // per workgroup, which attn_join_kernel joins.  Where the table cannot hold
 // more than kDecOwn tokens a sequence, each has a workgroup of its own
 // instead: no search, no parts, one launch.
+// Measured, 32 query and 8 KV heads of 128, bf16: 64 sequences of 4096 to 12288
+// tokens (1.075 GB) 170 us, 6.3 TB/s; 131071 tokens (268 MB) 49.7 us with the
+// join, 5.4 TB/s; 1000 tokens, a workgroup a head, 10 us: a chain of table,
+// codes and four tiles.  16 sequences of up to 5001 tokens, one KV head of 256,
+// f32: 20 us for 21 MB, one tile a wave: search, codes, and the three products
+// per term, in turn.
 #pragma once
 
 #include "attention.hpp"
@@ -50,10 +56,11 @@ struct DecTile {
   bool gone;  // the page of the lane's tokens is not in the cache
 };
 
-// The lane's part of a tile: its pages (read a tile ahead), then its codes.  Every load is unconditional, from an
-// address clamped into the cache: what a lane must not use (blocks no row
-// sees, pages outside the cache) it hides afterwards, keys by their scores,
-// values by zeros, since a zero probability times a NaN code would be NaN.
+// The lane's part of a tile: its pages (read a tile ahead), then its codes.
+// Every load is unconditional, from an address clamped into the cache: what a
+// lane must not use (blocks no row sees, pages outside the cache) it hides
+// afterwards, keys by their scores, values by zeros, since a zero probability
+// times a NaN code would be NaN.
 struct DecPages {
   int k, v;  // as in the table: of the lane's key rows, and of its own 16 tokens
 };
