@@ -14,8 +14,8 @@
 // more than kDecOwn tokens a sequence, each has a workgroup of its own
 // instead: no search, no parts, one launch.
 // Measured, 32 query and 8 KV heads of 128, bf16: 64 sequences of 4096 to 12288
-// tokens (1.075 GB) 170 us, 6.3 TB/s; 131071 tokens (268 MB) 49.7 us with the
-// join, 5.4 TB/s; 1000 tokens, a workgroup a head, 10 us: a chain of table,
+// tokens (1.075 GB) 169 us, 6.35 TB/s; 131071 tokens (268 MB) 48.5 us with the
+// join, 5.5 TB/s; 1000 tokens, a workgroup a head, 10 us: a chain of table,
 // codes and four tiles.  16 sequences of up to 5001 tokens, one KV head of 256,
 // f32: 20 us for 21 MB, one tile a wave: search, codes, and the three products
 // per term, in turn.
@@ -79,19 +79,26 @@ __device__ __forceinline__ i32x4 ld_codes(const uint8_t* p) {
   return STREAM ? __builtin_nontemporal_load(q) : *q;
 }
 
-template <int DT, bool STREAM>
-__device__ __forceinline__ void dec_load_k(const AttnArgs& a, const DecPages& pg, int tile, int h, DecTile<DT>& r) {
-  const int lane = threadIdx.x & 63, m = lane & 15, g = lane >> 4, D = a.c.D, lS = a.c.lS;
+__device__ __forceinline__ const uint8_t* dec_k_row(const AttnArgs& a, const DecPages& pg, int tile, int h) {
+  const int lane = threadIdx.x & 63, m = lane & 15, D = a.c.D, lS = a.c.lS;
   const int t = tile * kAttnTile + 16 * (m >> 2);  // first token of the lane's block
   const uint32_t page = (uint32_t)pg.k < (uint32_t)a.c.pages ? pg.k : 0;
-  const uint8_t* row = a.c.kc + ((((size_t)page * a.c.H + h) << lS) + (t & ((1 << lS) - 1)) + (m & 3)) * D;
+  return a.c.kc + ((((size_t)page * a.c.H + h) << lS) + (t & ((1 << lS) - 1)) + (m & 3)) * D;
+}
+template <int DT, bool STREAM>
+__device__ __forceinline__ void dec_load_kj(const AttnArgs& a, const uint8_t* row, int j, DecTile<DT>& r) {
+  const int g = (threadIdx.x & 63) >> 4, D = a.c.D;
 #pragma unroll
   for (int c = 0; c < DT / 64; ++c) {
     const int d = g * (DT / 4) + 16 * c;
-    const uint8_t* at = row + (d < D ? d : 0);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) r.k[j][c] = ld_codes<STREAM>(at + 4 * j * D);
+    r.k[j][c] = ld_codes<STREAM>(row + (d < D ? d : 0) + 4 * j * D);
   }
+}
+template <int DT, bool STREAM>
+__device__ __forceinline__ void dec_load_k(const AttnArgs& a, const DecPages& pg, int tile, int h, DecTile<DT>& r) {
+  const uint8_t* row = dec_k_row(a, pg, tile, h);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) dec_load_kj<DT, STREAM>(a, row, j, r);
 }
 
 template <int DT, bool STREAM>
@@ -103,10 +110,10 @@ __device__ __forceinline__ void dec_load_v(const AttnArgs& a, const DecPages& pg
   r.gone = (uint32_t)pg.v >= (uint32_t)a.c.pages || t >= vw.hi || t + 16 <= vw.lo;
   const size_t at = (size_t)page * a.c.H + h;
   const uint8_t* blk = a.c.vc + (at << lS) * D + (size_t)((t & ((1 << lS) - 1)) * D + 16 * m);
+  r.ks = a.c.ks[at];  // used before the values: loaded before them
+  r.vs = a.c.vs[at];
 #pragma unroll
   for (int i = 0; i < DT / 16; ++i) r.v[i] = ld_codes<STREAM>(blk + (16 * i < D ? 256 * i : 0));
-  r.ks = a.c.ks[at];
-  r.vs = a.c.vs[at];
 }
 
 template <int DT, int NR, int NS>
@@ -144,10 +151,11 @@ __device__ __forceinline__ void dec_begin(const AttnArgs& a, const Seq& s, int h
 }
 
 // Whether a tile's keys (values) are loaded in the place of the last one's as
-// soon as these are used, under the other product's work, or both at once when
-// the last tile is done.  1.07 GB of codes, 16 query heads: D 256 260 us and
-// 282; D 64 95 and 97; D 128 182 and 175, its loads being long enough to keep
-// memory busy and the loop shorter without.
+// soon as these are used, keys by quarters, under the rest of the work, or both
+// at once when the last tile is done.  1.07 GB of codes, 16 query heads: D 256
+// 222 us and 282 (keys not by quarters: 247); D 64 93 and 97; D 128 178 and
+// 170, its loads being long enough to keep memory busy and the loop shorter
+// without.
 template <int DT>
 constexpr bool dec_early() {
   return DT != 128;
@@ -159,6 +167,7 @@ __device__ __forceinline__ void dec_tile(const AttnArgs& a, const View& vw, int 
                                          DecTile<DT>& t, DecState<DT, NR, NS>& st) {
   const int lane = threadIdx.x & 63, g = lane >> 4;
   f32x16 s[NR];
+  const uint8_t* krow = dec_early<DT>() ? dec_k_row(a, pg, next >= 0 ? next : tile, h) : nullptr;
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     f32x4 x[NR];
@@ -174,8 +183,12 @@ __device__ __forceinline__ void dec_tile(const AttnArgs& a, const View& vw, int 
     for (int r = 0; r < NR; ++r)
 #pragma unroll
       for (int i = 0; i < 4; ++i) s[r][4 * j + i] = x[r][i];
+    if (dec_early<DT>() && next >= 0) {
+      __builtin_amdgcn_sched_barrier(0);
+      dec_load_kj<DT, STREAM>(a, krow, j, t);
+      __builtin_amdgcn_sched_barrier(0);
+    }
   }
-  if (dec_early<DT>() && next >= 0) dec_load_k<DT, STREAM>(a, pg, next, h, t);
   const int t0 = tile * kAttnTile;
   const bool masked = t0 < st.all_lo || t0 + kAttnTile > st.all_hi || __any(t.gone);
   const float f = t.gone ? 1.0f : score_scale(a, t.ks), fv = t.gone ? 1.0f : page_scale_of(t.vs);
