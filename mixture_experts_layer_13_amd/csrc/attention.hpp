@@ -27,7 +27,8 @@
 //   32x32x16 (many rows): tile j of two has as its row m the token
 //   32 (m / 4 % 2) + 16 j + 4 (m / 8) + m % 4; lane l gets tokens
 //   32 (l / 32) + 16 j + i (i = 0..15) of query l % 32.
-// The D values of a key are split over the lane groups in contiguous parts.
+// The D values of a key are dealt to the lane groups in turn, 16 at a time, as
+// they are loaded.
 #pragma once
 
 #include "paged.hpp"
@@ -40,8 +41,8 @@ constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kLn2 = 0.69314718055994530942f;
 constexpr int kAttnTile = 64;  // tokens of a tile
 // Workgroups of the few-row kernel: one per CU, or two where a tile is half as
-// large (64 sequences of 8192 tokens, D 128: 175 us with one, 184 with two;
-// D 64: 106 and 97).
+// large (64 sequences of 8192 tokens, D 128: 169 us with one, 173 with two;
+// D 64: 113 and 93).
 constexpr int kAttnGroups = 512;  // at most
 constexpr int attn_groups(int D) { return D <= 64 ? 512 : 256; }
 
@@ -216,19 +217,25 @@ __device__ __forceinline__ i32x4 keep_bytes(i32x4 w, int skip, int n) {
   return w;
 }
 
-// A query row's 8 KC values from d0 on as KC B operands of NS bf16 terms each
-// (zeros where the row is not live, or past the head): first every load, then,
-// once other loads are on their way too, the operands.
+// The lane's values of a query row as KC B operands of 8 values and NS bf16
+// terms each (zeros where the row is not live, or past the head): first every
+// load, then, once other loads are on their way too, the operands.  Values come
+// in 16s, STEP apart, from d0 on.
+template <int STEP>
+constexpr int q_place(int d0, int c) {
+  return d0 + STEP * (c >> 1) + 8 * (c & 1);
+}
 template <int KC, int NS>
 struct QueryRaw {
   i32x4 w[KC][NS == 1 ? 1 : 2];
 };
 
-template <int KC, int NS>
+template <int STEP, int KC, int NS>
 __device__ __forceinline__ void load_q(const AttnArgs& a, size_t row, int d0, QueryRaw<KC, NS>& raw) {
 #pragma unroll
   for (int c = 0; c < KC; ++c) {
-    const size_t at = row + (d0 + 8 * c < a.c.D ? d0 + 8 * c : 0);
+    const int d = q_place<STEP>(d0, c);
+    const size_t at = row + (d < a.c.D ? d : 0);
 #pragma unroll
     for (int k = 0; k < (NS == 1 ? 1 : 2); ++k)
       raw.w[c][k] = NS == 1 ? ld16(reinterpret_cast<const uint16_t*>(a.q) + at)
@@ -236,13 +243,13 @@ __device__ __forceinline__ void load_q(const AttnArgs& a, size_t row, int d0, Qu
   }
 }
 
-template <int KC, int NS>
+template <int STEP, int KC, int NS>
 __device__ __forceinline__ void make_q(const AttnArgs& a, const QueryRaw<KC, NS>& raw, int d0, bool live,
                                        bf16x8 out[KC][NS]) {
   const int sign = a.neg ? (NS == 1 ? (int)0x80008000 : (int)0x80000000) : 0;
 #pragma unroll
   for (int c = 0; c < KC; ++c) {
-    const bool use = live && d0 + 8 * c < a.c.D;
+    const bool use = live && q_place<STEP>(d0, c) < a.c.D;
     if (NS == 1) {
       i32x4 w = raw.w[c][0];
 #pragma unroll

@@ -109,20 +109,22 @@ static int join_launch(const AttnArgs& a, hipStream_t st) {
 
 template <int DT, int NR, int NS>
 static int dec_launch(const AttnArgs& a, hipStream_t st) {
-  const dim3 block(kDecThreads), grid((unsigned)a.W, (unsigned)a.c.H);
-  if (((long long)a.b.max_pages << a.c.lS) <= kDecOwn) {
-    hipLaunchKernelGGL((attn_decode_kernel<DT, NR, NS, true, false>), dim3((unsigned)a.b.B, (unsigned)a.c.H), block, 0, st, a);
-    return (int)hipGetLastError();
-  }
-  // 64 sequences of 8192 tokens (1.07 GB): 176 us past the caches, 192 through
-  // them; 21 MB in all, which the last-level cache holds: 22.6 and 20.2
+  const bool own = (long long)a.b.max_pages << a.c.lS <= (a.b.B >= a.W ? 2 * kDecOwn : kDecOwn);
+  const dim3 block(kDecThreads), grid((unsigned)(own ? a.b.B : a.W), (unsigned)a.c.H);
+  // 64 sequences of 8192 tokens (1.07 GB): 169 us past the caches, 190 through
+  // them; 500 of 500 to 900 (726 MB): 126 and 138; 21 MB in all, which the
+  // last-level cache holds: 22.8 and 20.6
   const long long pool = 2LL * a.c.pages * a.c.H * a.c.D << a.c.lS;
-  if (pool > kCacheBytes)
+  if (own && pool > kCacheBytes)
+    hipLaunchKernelGGL((attn_decode_kernel<DT, NR, NS, true, true>), grid, block, 0, st, a);
+  else if (own)
+    hipLaunchKernelGGL((attn_decode_kernel<DT, NR, NS, true, false>), grid, block, 0, st, a);
+  else if (pool > kCacheBytes)
     hipLaunchKernelGGL((attn_decode_kernel<DT, NR, NS, false, true>), grid, block, 0, st, a);
   else
     hipLaunchKernelGGL((attn_decode_kernel<DT, NR, NS, false, false>), grid, block, 0, st, a);
   const int err = (int)hipGetLastError();
-  return err ? err : join_launch<DT, NR, NS>(a, st);
+  return err || own ? err : join_launch<DT, NR, NS>(a, st);
 }
 
 template <int NS>

@@ -11,13 +11,13 @@
 // transposition); they are joined through LDS at the end of a sequence.  A
 // sequence that lies in one run is finished there; the others leave a part
 // per workgroup, which attn_join_kernel joins.  Where the table cannot hold
-// more than kDecOwn tokens a sequence, each has a workgroup of its own
+// many tokens a sequence (kDecOwn), each has a workgroup of its own
 // instead: no search, no parts, one launch.
 // Measured, 32 query and 8 KV heads of 128, bf16: 64 sequences of 4096 to 12288
 // tokens (1.075 GB) 169 us, 6.35 TB/s; 131071 tokens (268 MB) 48.5 us with the
 // join, 5.5 TB/s; 1000 tokens, a workgroup a head, 10 us: a chain of table,
 // codes and four tiles.  16 sequences of up to 5001 tokens, one KV head of 256,
-// f32: 20 us for 21 MB, one tile a wave: search, codes, and the three products
+// f32: 19 us for 21 MB, one tile a wave: search, codes, and the three products
 // per term, in turn.
 #pragma once
 
@@ -28,7 +28,11 @@ namespace moe {
 constexpr int kDecThreads = 256;
 constexpr int kDecWaves = kDecThreads / 64;
 constexpr int kDecMinTiles = kDecWaves;  // a shorter run would leave waves idle
-constexpr int kDecOwn = 1024;            // tokens
+// Tokens up to which a sequence has a workgroup of its own, 8 KV heads of 128:
+// one sequence of 1000 tokens 11.2 us, shared out 13.7; of 1900 14.3 and 14.0.
+// Twice as many where these fill the chip: 64 sequences of 1500 to 1900 tokens
+// 43 and 50 us, of 2100 to 4000 77 and 73.
+constexpr int kDecOwn = 1024;
 constexpr long long kCacheBytes = 256LL << 20;  // last-level cache of the MI355X
 
 __device__ __forceinline__ int dec_slots(int tiles) { return (tiles + kDecMinTiles - 1) / kDecMinTiles * kDecMinTiles; }
@@ -79,26 +83,21 @@ __device__ __forceinline__ i32x4 ld_codes(const uint8_t* p) {
   return STREAM ? __builtin_nontemporal_load(q) : *q;
 }
 
-__device__ __forceinline__ const uint8_t* dec_k_row(const AttnArgs& a, const DecPages& pg, int tile, int h) {
-  const int lane = threadIdx.x & 63, m = lane & 15, D = a.c.D, lS = a.c.lS;
-  const int t = tile * kAttnTile + 16 * (m >> 2);  // first token of the lane's block
-  const uint32_t page = (uint32_t)pg.k < (uint32_t)a.c.pages ? pg.k : 0;
-  return a.c.kc + ((((size_t)page * a.c.H + h) << lS) + (t & ((1 << lS) - 1)) + (m & 3)) * D;
-}
-template <int DT, bool STREAM>
-__device__ __forceinline__ void dec_load_kj(const AttnArgs& a, const uint8_t* row, int j, DecTile<DT>& r) {
-  const int g = (threadIdx.x & 63) >> 4, D = a.c.D;
-#pragma unroll
-  for (int c = 0; c < DT / 64; ++c) {
-    const int d = g * (DT / 4) + 16 * c;
-    r.k[j][c] = ld_codes<STREAM>(row + (d < D ? d : 0) + 4 * j * D);
-  }
-}
 template <int DT, bool STREAM>
 __device__ __forceinline__ void dec_load_k(const AttnArgs& a, const DecPages& pg, int tile, int h, DecTile<DT>& r) {
-  const uint8_t* row = dec_k_row(a, pg, tile, h);
+  const int lane = threadIdx.x & 63, m = lane & 15, g = lane >> 4, D = a.c.D, lS = a.c.lS;
+  const int t = tile * kAttnTile + 16 * (m >> 2);  // first token of the lane's block
+  const uint32_t page = (uint32_t)pg.k < (uint32_t)a.c.pages ? pg.k : 0;
+  const uint8_t* row = a.c.kc + ((((size_t)page * a.c.H + h) << lS) + (t & ((1 << lS) - 1)) + (m & 3)) * D;
 #pragma unroll
-  for (int j = 0; j < 4; ++j) dec_load_kj<DT, STREAM>(a, row, j, r);
+  for (int c = 0; c < DT / 64; ++c) {
+    // the four lanes of a row read 64 consecutive bytes: with a quarter of the
+    // row each, 1.07 GB of heads of 256 took 220 us and now 172
+    const int d = 64 * c + 16 * g;
+    const uint8_t* at = row + (d < D ? d : 0);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) r.k[j][c] = ld_codes<STREAM>(at + 4 * j * D);
+  }
 }
 
 template <int DT, bool STREAM>
@@ -138,8 +137,8 @@ __device__ __forceinline__ void dec_begin(const AttnArgs& a, const Seq& s, int h
     const bool live = i < s.q;
     const size_t at = (size_t)(s.q0 + (live ? i : 0)) * a.qs_t + (size_t)(live ? hd : 0) * a.qs_h;
     QueryRaw<DT / 32, NS> raw;
-    load_q<DT / 32, NS>(a, at, g * (DT / 4), raw);
-    make_q<DT / 32, NS>(a, raw, g * (DT / 4), live, st.q[r]);
+    load_q<64, DT / 32, NS>(a, at, 16 * g, raw);
+    make_q<64, DT / 32, NS>(a, raw, 16 * g, live, st.q[r]);
 #pragma unroll
     for (int n = 0; n < DT / 16; ++n) st.o[r][n] = f32x4{0, 0, 0, 0};
     st.m[r] = -__builtin_inff();
@@ -150,24 +149,12 @@ __device__ __forceinline__ void dec_begin(const AttnArgs& a, const Seq& s, int h
   }
 }
 
-// Whether a tile's keys (values) are loaded in the place of the last one's as
-// soon as these are used, keys by quarters, under the rest of the work, or both
-// at once when the last tile is done.  1.07 GB of codes, 16 query heads: D 256
-// 222 us and 282 (keys not by quarters: 247); D 64 93 and 97; D 128 178 and
-// 170, its loads being long enough to keep memory busy and the loop shorter
-// without.
-template <int DT>
-constexpr bool dec_early() {
-  return DT != 128;
-}
-
-// The tile in t, and the next one's loads if dec_early() and next >= 0.
-template <int DT, int NR, int NS, bool STREAM>
-__device__ __forceinline__ void dec_tile(const AttnArgs& a, const View& vw, int tile, int next, const DecPages& pg, int h,
-                                         DecTile<DT>& t, DecState<DT, NR, NS>& st) {
+// The tile in t.
+template <int DT, int NR, int NS>
+__device__ __forceinline__ void dec_tile(const AttnArgs& a, const View& vw, int tile, DecTile<DT>& t,
+                                         DecState<DT, NR, NS>& st) {
   const int lane = threadIdx.x & 63, g = lane >> 4;
   f32x16 s[NR];
-  const uint8_t* krow = dec_early<DT>() ? dec_k_row(a, pg, next >= 0 ? next : tile, h) : nullptr;
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     f32x4 x[NR];
@@ -183,11 +170,6 @@ __device__ __forceinline__ void dec_tile(const AttnArgs& a, const View& vw, int 
     for (int r = 0; r < NR; ++r)
 #pragma unroll
       for (int i = 0; i < 4; ++i) s[r][4 * j + i] = x[r][i];
-    if (dec_early<DT>() && next >= 0) {
-      __builtin_amdgcn_sched_barrier(0);
-      dec_load_kj<DT, STREAM>(a, krow, j, t);
-      __builtin_amdgcn_sched_barrier(0);
-    }
   }
   const int t0 = tile * kAttnTile;
   const bool masked = t0 < st.all_lo || t0 + kAttnTile > st.all_hi || __any(t.gone);
@@ -229,7 +211,6 @@ __device__ __forceinline__ void dec_tile(const AttnArgs& a, const View& vw, int 
 #pragma unroll
       for (int r = 0; r < NR; ++r) st.o[r][n] = mfma_value<NS>(v, p[r][c], st.o[r][n]);
     }
-  if (dec_early<DT>() && next >= 0) dec_load_v<DT, STREAM>(a, pg, vw, next, h, t);
 }
 
 // Slot of a workgroup's part: a run holds at most one sequence that began
@@ -328,22 +309,17 @@ __device__ __forceinline__ void attn_decode_run(const AttnArgs& a, int w, int h,
     const int first = vw.t0 + skip;
     if (wave < count) {
       DecTile<DT> t;
-      DecPages pages = dec_pages(a, table, first + wave);
-      DecPages after = dec_pages(a, table, first + wave + kDecWaves);
-      dec_load_k<DT, STREAM>(a, pages, first + wave, h, t);
-      dec_load_v<DT, STREAM>(a, pages, vw, first + wave, h, t);
+      DecPages after = dec_pages(a, table, first + wave);
       for (int i = wave; i < count; i += kDecWaves) {
-        if (dec_early<DT>()) {
-          pages = after;
-          after = dec_pages(a, table, first + i + 2 * kDecWaves);
-        } else if (i != wave) {
-          pages = after;
-          after = dec_pages(a, table, first + i + kDecWaves);
-          dec_load_k<DT, STREAM>(a, pages, first + i, h, t);
-          dec_load_v<DT, STREAM>(a, pages, vw, first + i, h, t);
-        }
-        const int next = dec_early<DT>() && i + kDecWaves < count ? first + i + kDecWaves : -1;
-        dec_tile<DT, NR, NS, STREAM>(a, vw, first + i, next, pages, h, t, st);
+        const DecPages pages = after;
+        after = dec_pages(a, table, first + i + kDecWaves);  // ahead of the codes, not behind them
+        dec_load_k<DT, STREAM>(a, pages, first + i, h, t);
+        dec_load_v<DT, STREAM>(a, pages, vw, first + i, h, t);
+        // the three terms of f32 fill the registers, and the compiler would
+        // load the values behind the first product: 1.07 GB, D 256, 224 us
+        // against 180 (bf16 without: 172, with: 178)
+        if (NS > 1) __builtin_amdgcn_sched_barrier(0);
+        dec_tile<DT, NR, NS>(a, vw, first + i, t, st);
       }
     }
     const bool whole = skip == 0 && count == n;

@@ -40,7 +40,7 @@ __device__ __forceinline__ int tile_blocks(const TileArgs& t, int b) {
   return rows <= t.rows_below ? 0 : (int)((rows + kTileRows - 1) / kTileRows);
 }
 
-// A thread's raw codes of one tile.  With j = wave % 2: of keys, 32 bytes of
+// A thread's raw codes of one tile.  With j = wave % 2: of keys, DT / 4 bytes of
 // its row of MFMA tile j; of values, channels 32 (wave / 2 + 2 i) + l % 32 of
 // the 16 tokens of block 2 (l / 32) + j.
 template <int DT>
@@ -116,7 +116,7 @@ __global__ __launch_bounds__(kTileThreads, DT <= 128 && NS == 1 ? 2 : 1) void at
   const int row = row0 + wave * 32 + m, qi = row / a.G, hd = h * a.G + row - qi * a.G;
   const bool live = qi < s.q;
   QueryRaw<KC, NS> qraw;
-  load_q<KC, NS>(a, (size_t)(s.q0 + (live ? qi : 0)) * a.qs_t + (size_t)(live ? hd : 0) * a.qs_h, g * (DT / 2), qraw);
+  load_q<32, KC, NS>(a, (size_t)(s.q0 + (live ? qi : 0)) * a.qs_t + (size_t)(live ? hd : 0) * a.qs_h, 16 * g, qraw);
 #pragma unroll
   for (int n = 0; n < DT / 32; ++n)
 #pragma unroll
@@ -137,7 +137,7 @@ __global__ __launch_bounds__(kTileThreads, DT <= 128 && NS == 1 ? 2 : 1) void at
   uint32_t koff[DT / 64], voff[DT / 64];  // the lane's place in a tile (UNI) or in its block
 #pragma unroll
   for (int c = 0; c < DT / 64; ++c) {
-    const int d = g * (DT / 2) + (wave >> 1) * (DT / 4) + 16 * c, n = 32 * ((wave >> 1) + 2 * c) + m;
+    const int d = 32 * ((wave >> 1) * (DT / 64) + c) + 16 * g, n = 32 * ((wave >> 1) + 2 * c) + m;
     koff[c] = (4 * (m >> 3) + (m & 3) + (UNI ? bk : 0)) * D + (d < D ? d : 0);
     voff[c] = (UNI ? bv * D : 0) + (n < D ? 16 * n : 0);
   }
@@ -222,7 +222,7 @@ __global__ __launch_bounds__(kTileThreads, DT <= 128 && NS == 1 ? 2 : 1) void at
     for (int x = 0; x < KC; ++x) store(first, 0, x);
     store_scales(first, 0);
   }
-  make_q<KC, NS>(a, qraw, g * (DT / 2), live, q);
+  make_q<32, KC, NS>(a, qraw, 16 * g, live, q);
   __syncthreads();
 
   // tile i; raw: the codes of tile i + 1, then of tile i + 1 + kAhead

@@ -103,6 +103,16 @@ def test_long_sequence_is_shared_out():
     run([1], [30000], 1, 8, 128, 128, "f32")
 
 
+@pytest.mark.parametrize("extra", [0, 1])
+def test_tables_on_both_sides_of_a_workgroup_of_its_own(extra):
+    """Tables of 1024 and 2048 tokens, and of one page more, with few sequences and with many."""
+    for kv, cap in (([1000, 3, 0, 777], 1024), ([1500, 0, 2047, 63] * 20, 2048)):
+        P, small = A.tables(kv, 32, 1)
+        table = np.full((len(kv), cap // 32 + extra), -1, np.int32)
+        table[:, :small.shape[1]] = small
+        run([1] * len(kv), kv, 8, 2, 16, 32, "bf16", table=table, pages=P)
+
+
 def test_many_sequences():
     r = np.random.RandomState(1)
     kv = r.randint(0, 90, 600).tolist()
@@ -275,6 +285,29 @@ def test_two_calls_at_once():
     got = [[moe.moe_paged_attention(cache, xd, lens, table, stream=s) for _ in range(4)] for s in streams]
     torch.cuda.synchronize()
     assert all(torch.equal(o, want) for side in got for o in side)
+
+
+@pytest.mark.parametrize("cap", [100, 40])
+def test_a_pool_larger_than_the_caches(cap):
+    """Few tokens of a pool of over 256 MB, shared out and by workgroups of their own."""
+    H, D, S, kv = 2, 64, 16, [300, 0, 611, 64]
+    small, table = A.tables(kv, S, 1)
+    host = A.poison_unseen(A.random_cache(small, H, S, D, 2), kv, table, [1] * 4)
+    P = (1 << 28) // (2 * H * S * D) + 1000
+    where = np.random.RandomState(3).permutation(P)[:small]
+    kc = torch.full((P, H, S, D), 0x7F, dtype=torch.uint8, device="cuda")
+    vc = torch.full((P, H, S // 16, D, 16), 0x7F, dtype=torch.uint8, device="cuda")
+    sc = torch.full((2, P, H), float("nan"), device="cuda")
+    at = torch.from_numpy(where).cuda()
+    for t, n in ((kc, "k_codes"), (vc, "v_codes"), (sc[0], "k_scales"), (sc[1], "v_scales")):
+        t[at] = torch.from_numpy(host[n]).cuda()
+    wide = np.full((4, cap), -1, np.int32)
+    wide[:, :table.shape[1]] = np.where(table < 0, -1, where[table])
+    x = A.values((4, H * 4, D), "bf16", 4)
+    out, lse = moe.moe_paged_attention(moe.PagedKV(kc, vc, sc[0], sc[1]), x.cuda(), A.i32(kv), A.i32(wide), return_lse=True)
+    torch.cuda.synchronize()
+    ref = AO.attention(host, A.f64(x), A.offsets([1] * 4), kv, table, D ** -0.5)
+    A.check_attention(out, lse, ref, "bf16", D, f"large pool, table of {cap * S}")
 
 
 @pytest.mark.parametrize("q", [1, 100])
