@@ -410,7 +410,8 @@ moe_status moe_rope_workspace_size(int32_t T, int32_t n_heads, int32_t head_dim,
 /* Rotation of head vectors by position, with one or several axes (text: one;
  * images and video: time, height, width).  Pair i of a token turns by
  *   a(t, i) = positions[axis(i)][t] * inv_freq[i],   i < rotary_dim / 2,
- * formed and reduced in 64 bits, negated when `inverse` (the rotation back,
+ * formed from a frequency of two fp32 terms, whole turns taken off before
+ * anything is rounded (fp32 would be off by 2^-8 at an angle of 2^17), negated when `inverse` (the rotation back,
  * which is also the rotation's gradient).  The pairs are (x[i],
  * x[i + rotary_dim/2]), or (x[2i], x[2i+1]) when `interleaved`; (u, v)
  * becomes (u cos a - v sin a, v cos a + u sin a) in fp32.  Values from

@@ -10,12 +10,13 @@
 // the waves work on this one.  Operand layout, transposed first product and
 // running softmax: attention.hpp.
 // Measured, a causal prompt of 8192 tokens, 32 query and 8 KV heads of 128,
-// bf16, page 64: 530 us, 1.03 PFLOP/s (a library product of 8192^3: 1.23).  The
+// bf16, page 64: 530 to 558 us by the card's clock, 1.0 PFLOP/s (a library
+// product of 8192^3: 1.23).  The
 // matrix pipe is busy for half of the cycles and the VALU for as much again
 // (per score a multiply-add, an exponential of four issue slots, a sum, half a
-// conversion, and the maximum), at a clock of 1.9 to 2.0 GHz under this load;
+// conversion, and the maximum), at a clock of 1.75 to 2.0 GHz under this load;
 // the two overlap as far as two workgroups a CU allow.  Pages below 64 tokens
-// 575 us.  Twelve chunks of up to 701 tokens over up to 6001, window 1024,
+// 560 to 577 us.  Twelve chunks of up to 701 tokens over up to 6001, window 1024,
 // 16 / 4 heads of 64, page 16: 48 us, two or three workgroups a CU, so that a
 // third of the chip waits for the CUs with three; the VALU bounds those.
 #include "attn_decode.hpp"
