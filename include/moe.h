@@ -501,7 +501,8 @@ typedef struct {
  *   saturating (a NaN saturates too).
  * Appending the same rows again leaves the cache as it is, bit for bit;
  * lowering kv_lens and appending anew replaces tokens.  A page that gets new
- * tokens must belong to one sequence of the batch only.  Slots of no new or
+ * tokens must belong to one sequence of the batch only, and stand in its table
+ * once.  k and v must not overlap the cache.  Slots of no new or
  * earlier token keep their bytes.
  * k, v      device [T, n_kv_heads, head_dim] of dtype (MOE_BF16 or MOE_F32),
  *           strides as in moe_rope_axes.
@@ -532,7 +533,7 @@ moe_status moe_kv_append(const moe_kv_cache* cache, const moe_kv_batch* batch, c
  *            not all written); 1 when cu_q is NULL.
  * window     0 (none) .. 2^30.
  * out        device [T, n_heads, head_dim] of q_dtype, dense (written; rows of
- *            no sequence are left as they were).
+ *            no sequence are left as they were); overlaps no other argument.
  * lse        device f32 [T, n_heads] or NULL (written likewise).
  * sm_scale   within -2^64 and 2^64.
  * workspace  device, >= moe_paged_attention_workspace_size() bytes, 16-byte
