@@ -88,12 +88,13 @@ template <int XT, int UPT>
 __global__ __launch_bounds__(kAppendThreads) void kv_append_kernel(AppendArgs a) {
   extern __shared__ __align__(16) uint8_t tile[];  // [rows][D] codes of values
   __shared__ int scan[kAppendThreads / 64];
-  __shared__ int found[2];
+  __shared__ int found[6];
   __shared__ float wmax[2][kAppendThreads / 64];
   const int S = 1 << a.c.lS, D = a.c.D, TH = blockDim.x, t = threadIdx.x, unit = blockIdx.x, h = blockIdx.y;
 
   // the workgroup's sequence and page
   int b = unit, rank = 0;
+  Seq s;
   if (a.b.cu_q) {
     if (t == 0) found[0] = -1;
     __syncthreads();
@@ -101,7 +102,7 @@ __global__ __launch_bounds__(kAppendThreads) void kv_append_kernel(AppendArgs a)
     for (int base = 0; base < a.b.B && before <= unit; base += TH) {
       int n = 0;
       if (base + t < a.b.B) {
-        const Seq s = load_seq(a.b, a.c.lS, base + t);
+        s = load_seq(a.b, a.c.lS, base + t);
         const int p0 = s.kv - s.q > 0 ? s.kv - s.q : 0;
         if (s.q > 0 && s.lim > p0) n = ((s.lim - 1) >> a.c.lS) - (p0 >> a.c.lS) + 1;
       }
@@ -110,6 +111,10 @@ __global__ __launch_bounds__(kAppendThreads) void kv_append_kernel(AppendArgs a)
       if (unit >= end - n && unit < end) {
         found[0] = base + t;
         found[1] = unit - (end - n);
+        found[2] = s.q0;
+        found[3] = s.q;
+        found[4] = s.kv;
+        found[5] = s.lim;
       }
       before += total;
     }
@@ -117,8 +122,10 @@ __global__ __launch_bounds__(kAppendThreads) void kv_append_kernel(AppendArgs a)
     b = found[0];
     rank = found[1];
     if (b < 0) return;
+    s = Seq{found[2], found[3], found[4], found[5]};
+  } else {
+    s = load_seq(a.b, a.c.lS, b);
   }
-  const Seq s = load_seq(a.b, a.c.lS, b);
   const int start = s.kv - s.q;  // token of the sequence's first row; rows of negative tokens are not kept
   const int p0 = start > 0 ? start : 0;
   if (s.q == 0 || s.lim <= p0) return;
