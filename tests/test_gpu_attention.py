@@ -128,6 +128,9 @@ def test_sequences_that_see_nothing(q):
     kv = [0] * 40 + [1500] + [0] * 270 + [70, 0, 2100] + [0] * 30
     rows = [1] * 40 + [1] + [q[i % 2] for i in range(270)] + [1, q[1], 1] + [1] * 30
     run(rows, kv, 2, 4, 32, 16, "bf16")
+    # eight workgroups a head, one of which goes from one sequence over the gap to the next
+    kv = [0] * 3 + [900] + [0] * 200 + [700] + [0] * 70 + [2100] + [0] * 2
+    run([1] * len(kv), kv, 64, 1, 16, 16, "bf16")
     table = np.full((5, 100), 7, np.int32)
     run([1, q[1], 1, 1, 2], [0] * 5, 2, 4, 32, 16, "f32", table=table, pages=8)
 
