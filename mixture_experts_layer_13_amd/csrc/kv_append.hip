@@ -25,7 +25,7 @@
 // byte otherwise, which leaves every other token's bytes alone.
 // Measured, page 64, 8 heads of 128, bf16: 65536 tokens at 4.43 TB/s (a copy:
 // 5.43), bytes and the conversions' VALU together; 8192 tokens (50 MB) in
-// 17.6 us, since its 1032 workgroups are all resident at once and load, then
+// 17.3 us, since its 1032 workgroups are all resident at once and load, then
 // store, in step; one token of each of 64 sequences in 5 us, a chain of table,
 // token, barrier and store.  Keys and values in workgroups of their own take
 // 19 to 21 us for the 8192 tokens, a workgroup over all heads 26.
