@@ -10,7 +10,7 @@
 // the waves work on this one.  Operand layout, transposed first product and
 // running softmax: attention.hpp.
 // Measured, a causal prompt of 8192 tokens, 32 query and 8 KV heads of 128,
-// bf16, page 64: 530 to 558 us by the card's clock, 1.0 PFLOP/s (a library
+// bf16, page 64: 530 to 562 us by the card's clock, 1.0 PFLOP/s (a library
 // product of 8192^3: 1.23).  The
 // matrix pipe is busy for half of the cycles and the VALU for as much again
 // (per score a multiply-add, an exponential of four issue slots, a sum, half a
