@@ -208,3 +208,9 @@ def test_oracle_closed_forms():
     assert np.allclose(l[:, 0], [4.0, 4.0 + np.log(2)])
     o, l, _ = AO.attention(c, np.full((3, 1, 16), 1.0), [0, 3], [2], np.array([[0]]), 0.25, window=1)
     assert (o[0] == 0).all() and l[0, 0] == -np.inf and np.allclose(o[2], 4.0)
+
+
+def test_rotation_of_no_tokens():
+    """T == 0 is a no-op whatever the pointers; it leaves no error behind."""
+    assert rope(T=0, x=None, out=None) == moe.MOE_OK
+    assert moe.moe_last_error() == ""
