@@ -635,12 +635,13 @@ moe_status check_strides(const char* name, int dt, int64_t st, int64_t sh, int64
   return MOE_OK;
 }
 
-moe_status check_rotation(const moe_rotation* r, int head_dim, bool positions_needed) {
+// any: the call has tokens; without, positions may be an empty tensor's, NULL.
+moe_status check_rotation(const moe_rotation* r, int head_dim, bool any, bool positions_needed) {
   if (r->axes < 1 || r->axes > 8) return fail(MOE_ERR_SHAPE, "axes=%d must be in [1, 8]", r->axes);
   if (r->rotary_dim < 16 || r->rotary_dim > head_dim || r->rotary_dim % 16)
     return fail(MOE_ERR_SHAPE, "rotary_dim=%d must be a multiple of 16 in [16, head_dim=%d]", r->rotary_dim, head_dim);
   if (!r->inv_freq) return fail(MOE_ERR_NULL, "inv_freq is NULL");
-  if (!r->positions && (positions_needed || r->axes > 1)) return fail(MOE_ERR_NULL, "positions is NULL");
+  if (!r->positions && any && (positions_needed || r->axes > 1)) return fail(MOE_ERR_NULL, "positions is NULL");
   if (!aligned(r->positions, 4) || !aligned(r->pair_axis, 4) || !aligned(r->inv_freq, 4))
     return fail(MOE_ERR_ALIGN, "positions, pair_axis and inv_freq must be 4-byte aligned");
   return MOE_OK;
@@ -761,7 +762,7 @@ moe_status moe_rope_axes(const void* x, int32_t x_dtype, int64_t x_stride_t, int
   if (!rotation) return fail(MOE_ERR_NULL, "rotation is NULL");
   if ((s = check_strides("x", x_dtype, x_stride_t, x_stride_h, 0))) return s;
   if ((s = check_strides("out", out_dtype, out_stride_t, out_stride_h, head_dim))) return s;
-  if ((s = check_rotation(rotation, head_dim, T > 0))) return s;
+  if ((s = check_rotation(rotation, head_dim, T > 0, true))) return s;
   if (T == 0) return ok();
   if (out_stride_t < (n_heads - 1) * out_stride_h + head_dim && out_stride_h < (T - 1) * out_stride_t + head_dim &&
       T > 1 && n_heads > 1)
@@ -787,7 +788,7 @@ moe_status moe_kv_append(const moe_kv_cache* cache, const moe_kv_batch* batch, c
   if (!value_dtype(dtype)) return fail(MOE_ERR_DTYPE, "dtype must be MOE_F32 or MOE_BF16");
   if ((s = check_strides("k", dtype, k_stride_t, k_stride_h, 0))) return s;
   if ((s = check_strides("v", dtype, v_stride_t, v_stride_h, 0))) return s;
-  if (rotation && (s = check_rotation(rotation, cache->head_dim, false))) return s;
+  if (rotation && (s = check_rotation(rotation, cache->head_dim, batch->T > 0 && batch->B > 0, false))) return s;
   if (batch->T == 0 || batch->B == 0) return ok();
   if (!k || !v) return fail(MOE_ERR_NULL, "k and v are required");
   if (!aligned(k, 16) || !aligned(v, 16)) return fail(MOE_ERR_ALIGN, "k and v must be 16-byte aligned");

@@ -214,3 +214,13 @@ def test_rotation_of_no_tokens():
     """T == 0 is a no-op whatever the pointers; it leaves no error behind."""
     assert rope(T=0, x=None, out=None) == moe.MOE_OK
     assert moe.moe_last_error() == ""
+
+
+def test_no_tokens_and_several_axes():
+    """Positions [axes][0] have no address: an empty tensor's is NULL."""
+    none = rotation(positions=None)
+    assert none.axes == 3
+    assert rope(T=0, x=None, out=None, rot=none) == moe.MOE_OK
+    assert append(b=batch(T=0), k=None, v=None, rot=none) == moe.MOE_OK
+    assert append(b=batch(B=0), rot=none) == moe.MOE_OK
+    assert rope(rot=none) == append(rot=none) == moe.MOE_ERR_NULL
