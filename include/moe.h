@@ -439,9 +439,9 @@ typedef struct {
  *            >= head_dim, no two heads overlapping.  (written)
  * Every pointer 16-byte aligned (index buffers 4), strides in bytes
  * multiples of 16.  Limits: 1 <= n_heads <= 256; head_dim a multiple of 16 in
- * [16, 512].  T == 0 is a no-op.  Errors: MOE_ERR_SHAPE, MOE_ERR_DTYPE,
- * MOE_ERR_NULL, MOE_ERR_ALIGN, MOE_ERR_UNSUPPORTED (out is x with another type or
- * strides), MOE_ERR_HIP.
+ * [16, 512]; T n_heads head_dim <= 2^34.  T == 0 is a no-op.  Errors:
+ * MOE_ERR_SHAPE, MOE_ERR_DTYPE, MOE_ERR_NULL, MOE_ERR_ALIGN,
+ * MOE_ERR_UNSUPPORTED (out is x with another type or strides), MOE_ERR_HIP.
  */
 moe_status moe_rope_axes(const void* x, int32_t x_dtype, int64_t x_stride_t, int64_t x_stride_h,
                          const moe_rotation* rotation, int32_t T, int32_t n_heads, int32_t head_dim,

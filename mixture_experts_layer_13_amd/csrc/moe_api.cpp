@@ -635,6 +635,18 @@ moe_status check_strides(const char* name, int dt, int64_t st, int64_t sh, int64
   return MOE_OK;
 }
 
+// Whether no two heads of a [T, heads, D] tensor overlap (strides of at least
+// D).  Heads dh apart in the one direction and dt in the other are
+// |dh sh - dt st| apart: for each dh the nearest two dt decide.
+bool heads_apart(int T, int64_t st, int heads, int64_t sh, int D) {
+  for (int64_t dh = 1; dh < heads; ++dh) {
+    const int64_t at = dh * sh, dt = at / st;
+    if (dt < T && at - dt * st < D) return false;
+    if (dt + 1 < T && (dt + 1) * st - at < D) return false;
+  }
+  return true;
+}
+
 // any: the call has tokens; without, positions may be an empty tensor's, NULL.
 moe_status check_rotation(const moe_rotation* r, int head_dim, bool any, bool positions_needed) {
   if (r->axes < 1 || r->axes > 8) return fail(MOE_ERR_SHAPE, "axes=%d must be in [1, 8]", r->axes);
@@ -764,8 +776,7 @@ moe_status moe_rope_axes(const void* x, int32_t x_dtype, int64_t x_stride_t, int
   if ((s = check_strides("out", out_dtype, out_stride_t, out_stride_h, head_dim))) return s;
   if ((s = check_rotation(rotation, head_dim, T > 0, true))) return s;
   if (T == 0) return ok();
-  if (out_stride_t < (n_heads - 1) * out_stride_h + head_dim && out_stride_h < (T - 1) * out_stride_t + head_dim &&
-      T > 1 && n_heads > 1)
+  if (!heads_apart(T, out_stride_t, n_heads, out_stride_h, head_dim))
     return fail(MOE_ERR_SHAPE, "out strides %lld, %lld make its heads overlap", (long long)out_stride_t,
                 (long long)out_stride_h);
   if (!x || !out) return fail(MOE_ERR_NULL, "x and out are required");

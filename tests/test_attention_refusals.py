@@ -224,3 +224,19 @@ def test_no_tokens_and_several_axes():
     assert append(b=batch(T=0), k=None, v=None, rot=none) == moe.MOE_OK
     assert append(b=batch(B=0), rot=none) == moe.MOE_OK
     assert rope(rot=none) == append(rot=none) == moe.MOE_ERR_NULL
+
+
+@pytest.mark.parametrize("T,nH,os,apart", [
+    (3, 2, (256, 384), True),       # a head's tokens between the other's: 0 256 512, 384 640 896
+    (100, 2, (256, 384), True), (5, 3, (384, 512), True), (5, 3, (384, 640), True), (9, 256, (128, 1152), True),
+    (3, 2, (256, 520), False), (2, 2, (256, 520), True), (3, 2, (256, 320), False), (4, 2, (256, 512), False),
+    (3, 2, (256, 512), False), (2, 2, (256, 512), True), (10, 3, (384, 448), False), (1 << 19, 256, (1 << 32, 128), True),
+    (9, 256, (1152, 128), False), (9, 9, (1152, 128), True), (9, 256, (128, 1144), False),
+])
+def test_out_heads_apart_or_refused(T, nH, os, apart):
+    """Strides whose heads lie apart are taken however they interleave."""
+    if T <= 1000:  # by going through them
+        at = sorted(t * os[0] + h * os[1] for t in range(T) for h in range(nH))
+        assert all(b - a >= 128 for a, b in zip(at, at[1:])) == apart
+    status = rope(T=T, nH=nH, os=os, x=None)  # NULL: past the check of the strides, and nothing enqueued
+    assert status == (moe.MOE_ERR_NULL if apart else moe.MOE_ERR_SHAPE), moe.moe_last_error()

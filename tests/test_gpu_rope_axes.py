@@ -149,3 +149,16 @@ def test_empty_graph_and_other_stream():
         g.replay()
         torch.cuda.synchronize()
         assert torch.equal(out, moe.moe_rope_axes(x, rot)), k
+
+
+def test_heads_between_tokens():
+    """An output whose heads lie between another head's tokens."""
+    T, D = 33, 64
+    x = A.values((T, 2, D), "bf16", 4).cuda()
+    rot = moe.Rotation(torch.arange(T, dtype=torch.int32, device="cuda"), A.inv_freq(D).cuda())
+    buf = torch.full((2 * T + 4, D), 7.0, dtype=torch.bfloat16, device="cuda")
+    out = buf.as_strided((T, 2, D), (2 * D, 3 * D, 1))
+    moe.moe_rope_axes(x, rot, out=out)
+    torch.cuda.synchronize()
+    assert torch.equal(out, moe.moe_rope_axes(x, rot))
+    assert (buf[1] == 7).all() and (buf[2 * T] == 7).all() and (buf[2 * T + 2:] == 7).all()
