@@ -26,6 +26,7 @@ EXPORTS = ("moe_status_string", "moe_last_error", "moe_align_capacity", "moe_wor
 MOE_QUANT_WORKSPACE_BYTES = 8192
 MOE_WORKSPACE_SCALES_OFFSET = 4096
 MOE_NOALLOC_SCRATCH_BYTES = 64 << 20
+MOE_MAX_SEQS = 65536  # sequences of an append's or attention's batch
 MOE_FUSED_SYNC_BYTES = 32768
 MOE_FUSED_SYNC_ERROR_OFFSET = 128
 
@@ -670,7 +671,8 @@ class PagedAttention:
         shape = (max_tokens, n_heads, cache.head_dim)
         self.q = torch.empty(shape, dtype=dtype, device=cache.device)
         self.out = torch.empty(shape, dtype=dtype, device=cache.device)
-        n = moe_paged_attention_workspace_size(cache, max_tokens, max_seqs or max_tokens, n_heads, self.max_q)
+        seqs = max_seqs or min(max_tokens, MOE_MAX_SEQS)
+        n = moe_paged_attention_workspace_size(cache, max_tokens, seqs, n_heads, self.max_q)
         self.workspace = torch.empty(max(n, 16), dtype=torch.uint8, device=cache.device)
 
     def __call__(self, q, k, v, positions, kv_lens, block_table, cu_q=None, stream=None):

@@ -240,3 +240,12 @@ def test_out_heads_apart_or_refused(T, nH, os, apart):
         assert all(b - a >= 128 for a, b in zip(at, at[1:])) == apart
     status = rope(T=T, nH=nH, os=os, x=None)  # NULL: past the check of the strides, and nothing enqueued
     assert status == (moe.MOE_ERR_NULL if apart else moe.MOE_ERR_SHAPE), moe.moe_last_error()
+
+
+def test_layer_buffers_for_more_tokens_than_sequences_can_be():
+    """A call has at most 65536 sequences; a layer's rows are not bound by that."""
+    kc, vc, sc = torch.zeros(3, 1, 16, 16, dtype=torch.uint8), torch.zeros(3, 1, 1, 16, 16, dtype=torch.uint8), torch.ones(3, 1)
+    layer = moe.PagedAttention(moe.PagedKV(kc, vc, sc, sc), 1, torch.ones(8), max_tokens=70000)
+    assert layer.out.shape[0] == 70000
+    assert layer.workspace.nbytes >= moe.moe_paged_attention_workspace_size(layer.cache, 70000, 65536, 1, 70000)
+    refused(moe.MOE_ERR_SHAPE, moe.PagedAttention, layer.cache, 1, torch.ones(8), 70000, max_seqs=65537)
