@@ -661,7 +661,9 @@ class PagedAttention:
     allocated once for at most max_tokens rows in max_seqs sequences of at most
     max_q rows (None: as many as there are).  Nothing is allocated or synchronised per call, so the sequence
     can be captured into a HIP graph; lengths, tables and positions are read on
-    the device and may change between replays."""
+    the device and may change between replays.  The rotated queries, out and the
+    workspace are the object's: calls of one object, and replays of graphs that
+    hold them, must not overlap in time, and out holds until the next."""
 
     def __init__(self, cache, n_heads, inv_freq, max_tokens, max_seqs=None, max_q=None, pair_axis=None,
                  interleaved=False, sm_scale=None, causal=True, window=0, dtype=torch.bfloat16):
