@@ -340,3 +340,29 @@ def test_offsets_past_32_bits(q):
     ref = AO.attention(small, A.f64(x), [0, q], [n], low, D ** -0.5)
     A.check_attention(out, lse, ref, "bf16", D, f"past 32 bits q{q}")
     assert int(kc[:-3].max()) == 0 and int(vc[:-3].max()) == 0
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_parts_of_more_than_256_workgroups(dt):
+    """One sequence over 313 workgroups of one KV head: the join's second half."""
+    run([1], [80003], 1, 4, 64, 64, dt)
+
+
+@pytest.mark.parametrize("bad", [float("inf"), float("nan")])
+def test_a_bad_query_of_a_prompt_shows_in_its_row(bad):
+    """The last row of the first sequence sees 90 tokens, the first of the
+    second sequence 32, keys of both signs among them: no softmax is left."""
+    q, kv = [70, 33], [90, 64]
+    host, tab, x = make(q, kv, 1, 4, 64, 16, "bf16")
+    clean = attend(host, tab, x, q, kv)
+    for row in (69, 70):
+        y = x.clone()
+        y[row, 1, 7] = bad
+        want = AO.attention(host, A.f64(y), A.offsets(q), kv, tab, 64 ** -0.5)
+        assert np.isnan(want[0][row, 1]).all()  # the formula's, too
+        out, lse = attend(host, tab, y, q, kv)
+        torch.cuda.synchronize()
+        assert not torch.isfinite(out[row, 1]).any() and not torch.isfinite(lse[row, 1])
+        keep = torch.ones(lse.shape, dtype=torch.bool, device="cuda")
+        keep[row, 1] = False
+        assert torch.equal(out[keep], clean[0][keep]) and torch.equal(lse[keep], clean[1][keep])
