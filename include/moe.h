@@ -410,16 +410,16 @@ moe_status moe_rope_workspace_size(int32_t T, int32_t n_heads, int32_t head_dim,
 /* Rotation of head vectors by position, with one or several axes (text: one;
  * images and video: time, height, width).  Pair i of a token turns by
  *   a(t, i) = positions[axis(i)][t] * inv_freq[i],   i < rotary_dim / 2,
- * formed from a frequency of two fp32 terms, whole turns taken off before
- * anything is rounded (fp32 would be off by 2^-8 at an angle of 2^17), negated when `inverse` (the rotation back,
- * which is also the rotation's gradient).  The pairs are (x[i],
+ * whose fraction of a turn is formed in whole numbers of 2^-32 before anything is
+ * rounded (fp32 would be off by 2^-8 at an angle of 2^17), negated when `inverse`
+ * (the rotation back, which is also the rotation's gradient).  The pairs are (x[i],
  * x[i + rotary_dim/2]), or (x[2i], x[2i+1]) when `interleaved`; (u, v)
- * becomes (u cos a - v sin a, v cos a + u sin a) in fp32.  Values from
- * rotary_dim on pass through.
- *   positions   device int32 [axes][T], |position| < 2^24.
+ * becomes (u cos a - v sin a, v cos a + u sin a) in fp32, within 2^-21.6
+ * (|u| + |v|).  Values from rotary_dim on pass through.
+ *   positions   device int32 [axes][T], any values.
  *   pair_axis   device int32 [rotary_dim / 2], axis(i) in [0, axes) (a pair
- *               with any other value is not turned); NULL: axis 0.
- *   inv_freq    device f32 [rotary_dim / 2].
+ *               with any other value has the angle 0); NULL: axis 0.
+ *   inv_freq    device f32 [rotary_dim / 2], within -2^32 and 2^32.
  *   axes        1..8.   rotary_dim  a multiple of 16 in [16, head_dim]. */
 typedef struct {
   const int32_t* positions;

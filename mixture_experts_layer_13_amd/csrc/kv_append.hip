@@ -90,7 +90,12 @@ __global__ __launch_bounds__(kAppendThreads) void kv_append_kernel(AppendArgs a)
   __shared__ int scan[kAppendThreads / 64];
   __shared__ int found[6];
   __shared__ float wmax[2][kAppendThreads / 64];
+  __shared__ TurnFreq turns[128];
   const int S = 1 << a.c.lS, D = a.c.D, TH = blockDim.x, t = threadIdx.x, unit = blockIdx.x, h = blockIdx.y;
+  const int half = a.r.half;  // at most 128: two for each of 64 threads
+  float inv[2];
+#pragma unroll
+  for (int j = 0; j < 2; ++j) inv[j] = t + j * TH < half ? a.r.inv_freq[t + j * TH] : 0.0f;
 
   // the workgroup's sequence and page
   int b = unit, rank = 0;
@@ -137,7 +142,7 @@ __global__ __launch_bounds__(kAppendThreads) void kv_append_kernel(AppendArgs a)
   const int page = a.b.table[(size_t)b * a.b.max_pages + pg];
 
   // the new tokens: every load first
-  const int upd = D >> 4, units = n * upd, half = a.r.half, first = (int)((t * a.upd_magic) >> 20);
+  const int upd = D >> 4, units = n * upd, first = (int)((t * a.upd_magic) >> 20);
   RawVec<XT, 8> ka[UPT], kb[UPT], va[UPT], vb[UPT];
   int tok[UPT], gs[UPT], at_p[UPT], at_q[UPT], pos[UPT];
 #pragma unroll
@@ -158,6 +163,11 @@ __global__ __launch_bounds__(kAppendThreads) void kv_append_kernel(AppendArgs a)
     va[j] = load_vec<XT, 8>(a.v, vrow);
     vb[j] = load_vec<XT, 8>(a.v, vrow + (D >> 1));
   }
+  // the frequencies, once per workgroup, while the tokens are on their way
+#pragma unroll
+  for (int j = 0; j < 2; ++j)
+    if (t + j * TH < half) turns[t + j * TH] = turn_freq(inv[j]);
+  __syncthreads();
   if ((unsigned)page >= (unsigned)a.c.pages) return;
   const size_t at = (size_t)page * a.c.H + h;
   const float kwas = old > 0 ? a.c.ks[at] : 0.0f, vwas = old > 0 ? a.c.vs[at] : 0.0f;
@@ -170,16 +180,17 @@ __global__ __launch_bounds__(kAppendThreads) void kv_append_kernel(AppendArgs a)
     float2 cs[8];
     const bool turn = gs[j] < (half >> 3);
     if (turn) {
+      const Place place = place_of(pos[j], a.r.inverse);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const int pair = unit_pair<8>(gs[j], i, half, a.r.interleaved);
-        if (XT == DT_F32 || j == 0 || a.unit_rest) freq[i] = turn_freq(a.r.inv_freq[pair]);  // else the same pairs as before
-        int p = pos[j];
+        if (XT == DT_F32 || j == 0 || a.unit_rest) freq[i] = turns[pair];  // else the same pairs as before
+        Place p = place;
         if (a.r.pair_axis) {
           const int ax = rotate_axis(a.r, pair);
-          p = ax < 0 ? 0 : (a.r.pos ? a.r.pos[(size_t)ax * a.r.T + row0 + tok[j]] : p);
+          p = place_of(ax < 0 ? 0 : (a.r.pos ? a.r.pos[(size_t)ax * a.r.T + row0 + tok[j]] : pos[j]), a.r.inverse);
         }
-        cs[i] = rotate_cs(p, freq[i], a.r.inverse);
+        cs[i] = rotate_cs(p, freq[i]);
       }
     }
     unpack_vec(ka[j], x[j]);

@@ -75,10 +75,14 @@ __global__ __launch_bounds__(kRaThreads) void rope_axes_kernel(RopeAxesArgs a) {
         rb[s] = load_vec<XT, E>(a.x, row + q);
       }
       if (base == 0) {
-        for (int i = threadIdx.x; i < tn * a.r.half; i += kRaThreads) {
-          const int t = i / a.r.half, pr = i - t * a.r.half, ax = rotate_axis(a.r, pr);
-          const int pos = ax >= 0 ? a.r.pos[(size_t)ax * a.r.T + t0 + t] : 0;
-          cs[i] = rotate_cs(pos, turn_freq(a.r.inv_freq[pr]), a.r.inverse);
+        // a thread keeps one pair, and takes every `together`-th token
+        const int together = kRaThreads / a.r.half, t1 = (int)threadIdx.x / a.r.half, pr = (int)threadIdx.x - t1 * a.r.half;
+        if (t1 < together) {
+          const int ax = rotate_axis(a.r, pr);
+          const TurnFreq f = turn_freq(a.r.inv_freq[pr]);
+          for (int t = t1; t < tn; t += together)
+            cs[t * a.r.half + pr] =
+                rotate_cs(place_of(ax >= 0 ? a.r.pos[(size_t)ax * a.r.T + t0 + t] : 0, a.r.inverse), f);
         }
         __syncthreads();
       }

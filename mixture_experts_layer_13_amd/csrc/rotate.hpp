@@ -3,10 +3,12 @@
 //
 // Pair i of a token turns by positions[axis(i)][token] * inv_freq[i] radians.
 // In fp32 that product is off by half an ulp of the angle: 2^-8 rad at
-// position 2^17 times inv_freq 1, and more beyond.  So it is formed as turns
-// from a frequency of two fp32 terms, and the whole turns are taken off the
-// leading product inside a fused multiply-add (|position| < 2^24 is exact in
-// fp32): only the fraction of a turn, at most 1/2, is ever rounded.
+// position 2^17 times inv_freq 1, and more beyond.  Positions are whole numbers,
+// so the whole turns of a frequency are whole turns of every angle: of
+// inv_freq / 2 pi only the fraction is kept, as 64 bits, and the low 64 bits of
+// its product with the position are the angle's fraction of a turn.  Whole
+// numbers lose nothing, whatever the position and however many the turns (the
+// reduction of an argument by a long 1 / 2 pi: Payne and Hanek, 1983).
 #pragma once
 
 #include "common.hpp"
@@ -21,30 +23,44 @@ struct RotateArgs {
   int interleaved, inverse;
 };
 
-constexpr double kInvTwoPi = 0.15915494309189533577;
-
-// A frequency in turns per position, as two terms.
+// The fraction of a frequency in turns per position, in units of 2^-64.
 struct TurnFreq {
-  float hi, lo;
+  uint32_t hi, lo;
 };
 
+// Within one unit for |inv_freq| <= 2^32: 1 / 2 pi as two doubles (2^-108 of
+// it), the first product's rounding recovered, whole turns off exactly.
 __device__ __forceinline__ TurnFreq turn_freq(float inv_freq) {
-  // 1 / (2 pi) as two fp32 terms; the first product's rounding is recovered
-  constexpr float h = 0.15915494f, l = (float)(kInvTwoPi - (double)h);
-  const float hi = inv_freq * h;
-  return TurnFreq{hi, __builtin_fmaf(inv_freq, l, __builtin_fmaf(inv_freq, h, -hi))};
+#pragma clang fp contract(off)  // what `rest` recovers must have been rounded off
+  constexpr double h = 0x1.45f306dc9c883p-3, l = -0x1.6b01ec5417056p-57;
+  const double f = inv_freq, turns = f * h, rest = __builtin_fma(f, l, __builtin_fma(f, h, -turns));
+  const double top = (turns - __builtin_rint(turns)) * 0x1p32, whole = __builtin_floor(top);
+  const uint64_t u = ((uint64_t)(int64_t)whole << 32) +
+                     (uint64_t)(int64_t)__builtin_rint(__builtin_fma(top - whole, 0x1p32, rest * 0x1p64));
+  return TurnFreq{(uint32_t)(u >> 32), (uint32_t)u};
 }
 
-// {cos, sin} of the angle of position pos.  gfx950's sine and cosine take
-// turns, and on [-1/2, 1/2] are within 2^-22.9 of the exact values (measured
-// at every multiple of 2^-25 there); rounding the fraction adds at most
-// 2^-23.3, and the two products and the sum of a rotation 2^-24 each, so that a
-// rotated value is within 2^-21.7 (|u| + |v|).  A polynomial of the same error
-// takes five times as long, and an append was bound by it.
-__device__ __forceinline__ float2 rotate_cs(int pos, TurnFreq f, int inverse) {
-  const float x = (float)pos;
-  const float t = __builtin_fmaf(x, f.lo, __builtin_fmaf(x, f.hi, -__builtin_rintf(x * f.hi)));
-  return make_float2(__builtin_amdgcn_cosf(t), __builtin_amdgcn_sinf(inverse ? -t : t));
+// A position as its magnitude, and the sign of its angles, with a turn's unit.
+struct Place {
+  uint32_t n;
+  float unit;
+};
+
+__device__ __forceinline__ Place place_of(int pos, int inverse) {
+  return Place{pos < 0 ? 0u - (uint32_t)pos : (uint32_t)pos, (pos < 0) != (inverse != 0) ? -0x1p-32f : 0x1p-32f};
+}
+
+// {cos, sin} of a place's angle.  The fraction of a turn is within 2^-32 of the
+// exact one and rounded once, to fp32 in [-1/2, 1/2].  gfx950's sine and cosine
+// take turns; with that rounding they are within 2^-22.34 of the exact values
+// (measured at every one of the 2^32 fractions).  The two products and the sum of
+// a rotation add at most 2^-23, so that a rotated value is within 2^-21.6
+// (|u| + |v|).  A polynomial of the same error takes five times as long, and an
+// append was bound by it.
+__device__ __forceinline__ float2 rotate_cs(Place p, TurnFreq f) {
+  const uint32_t turn = p.n * f.hi + __umulhi(p.n, f.lo);
+  const float t = (float)(int32_t)turn * p.unit;
+  return make_float2(__builtin_amdgcn_cosf(t), __builtin_amdgcn_sinf(t));
 }
 
 // Axis of pair i; -1 (the pair is left unturned) when the map names none.
