@@ -535,7 +535,8 @@ moe_status moe_kv_append(const moe_kv_cache* cache, const moe_kv_batch* batch, c
  * out        device [T, n_heads, head_dim] of q_dtype, dense (written; rows of
  *            no sequence are left as they were); overlaps no other argument.
  * lse        device f32 [T, n_heads] or NULL (written likewise).
- * sm_scale   within -2^64 and 2^64.
+ * sm_scale   within -2^64 and 2^64; sums of queries times codes, ahead of the
+ *            scales, within -2^100 and 2^100.
  * workspace  device, >= moe_paged_attention_workspace_size() bytes, 16-byte
  *            aligned; no initialisation, not preserved.
  * Limits: n_heads a multiple of n_kv_heads, G <= 128; at most 2^24 row blocks

@@ -168,7 +168,8 @@ __device__ __forceinline__ float page_scale_of(float s) {
 }
 
 // Scale of a page's scores; at least the smallest normal number, so that a
-// hidden score, -infinity, stays that.
+// hidden score, -infinity, stays that.  Where that is above the product (a scale
+// of 0 among them) it takes sums of queries times codes of 2^100 to show.
 __device__ __forceinline__ float score_scale(const AttnArgs& a, float ks) {
   return __builtin_fmaxf(page_scale_of(ks) * a.scale2, 0x1p-126f);
 }

@@ -857,8 +857,7 @@ moe_status moe_paged_attention(const moe_kv_cache* cache, const moe_kv_batch* ba
   a.qs_h = q_stride_h;
   a.nH = n_heads;
   a.G = n_heads / cache->n_kv_heads;
-  // a scale of 0 becomes one too small to tell any two scores apart
-  a.scale2 = __builtin_fmaxf(__builtin_fabsf(sm_scale) * moe::kLog2e, 0x1p-60f);
+  a.scale2 = __builtin_fabsf(sm_scale) * moe::kLog2e;
   a.neg = sm_scale < 0.0f;
   a.causal = causal ? 1 : 0;
   a.window = window;

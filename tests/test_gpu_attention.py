@@ -366,3 +366,20 @@ def test_a_bad_query_of_a_prompt_shows_in_its_row(bad):
         keep = torch.ones(lse.shape, dtype=torch.bool, device="cuda")
         keep[row, 1] = False
         assert torch.equal(out[keep], clean[0][keep]) and torch.equal(lse[keep], clean[1][keep])
+
+
+@pytest.mark.parametrize("q", [[1, 1], [80, 3]])
+@pytest.mark.parametrize("scale", [0.0, 1e-20, -2.0 ** -70])
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_tiny_scales_over_pages_of_the_largest_scale(q, scale, dt):
+    """Page scales of 2^48: a scale of zero weights every token alike, and the
+    smallest others count as they are."""
+    kv = [130, 70]
+    P, tab = A.tables(kv, 16, 1)
+    host = A.random_cache(P, 1, 16, 64, 2)
+    host["k_scales"][:] = 2.0 ** 48
+    x = A.values((sum(q), 4, 64), dt, 3)
+    ref = AO.attention(host, A.f64(x), A.offsets(q), kv, tab, scale)
+    out, lse = attend(host, tab, x, q, kv, scale=scale)
+    torch.cuda.synchronize()
+    A.check_attention(out, lse, ref, dt, 64, f"scale {scale} q{q} {dt}")
