@@ -37,18 +37,14 @@ constexpr long long kCacheBytes = 256LL << 20;  // last-level cache of the MI355
 
 __device__ __forceinline__ int dec_slots(int tiles) { return (tiles + kDecMinTiles - 1) / kDecMinTiles * kDecMinTiles; }
 
-// Tiles of sequence b that this kernel works on (0: none, or another kernel's),
-// rounded up to the shortest run: runs and sequences then both begin at
-// multiples of it, and a shortest run never spans two sequences.
-__device__ __forceinline__ int dec_tiles(const AttnArgs& a, int rows_max, int b) {
+// Shortest runs, of kDecMinTiles tiles, that sequence b takes of this kernel (0:
+// it sees nothing, or is another kernel's): runs and sequences both begin at
+// whole ones, and none spans two sequences.  At most 2^22, so that those of 256
+// sequences, which are scanned at once, stay in 32 bits; tiles would not.
+__device__ __forceinline__ int dec_units(const AttnArgs& a, int rows_max, int b) {
   const Seq s = load_seq(a.b, a.c.lS, b);
   if (s.q <= 0 || s.q > rows_max / a.G) return 0;
-  return dec_slots(view_of(a, s, 0, s.q).n);
-}
-
-__device__ __forceinline__ long long dec_run(long long total, int W) {
-  const long long per = (total + W - 1) / W;
-  return per < kDecMinTiles ? kDecMinTiles : (per + kDecMinTiles - 1) / kDecMinTiles * kDecMinTiles;
+  return dec_slots(view_of(a, s, 0, s.q).n) / kDecMinTiles;
 }
 
 // The first sequence after b that this kernel works on, or B: 64 at a time, as
@@ -57,7 +53,7 @@ __device__ __forceinline__ long long dec_run(long long total, int W) {
 __device__ __forceinline__ int dec_next(const AttnArgs& a, int rows_max, int b) {
   for (++b; b < a.b.B; b += 64) {
     const int i = b + (threadIdx.x & 63);
-    const uint64_t some = __ballot(i < a.b.B && dec_tiles(a, rows_max, i) > 0);
+    const uint64_t some = __ballot(i < a.b.B && dec_units(a, rows_max, i) > 0);
     if (some) return b + __builtin_ctzll(some);
   }
   return a.b.B;
@@ -272,30 +268,30 @@ __device__ __forceinline__ void attn_decode_run(const AttnArgs& a, int w, int h,
   long long left = 1LL << 40, run = 0;
   int2 shared = make_int2(-1, 0);
   if (!OWN) {
-    long long total = 0, begin = 0, before = 0;
+    long long total = 0, before = 0;  // in shortest runs
     int n = 0, e = 0, t;
     for (int base = 0; base < a.b.B; base += kDecThreads) {
-      n = base + (int)threadIdx.x < a.b.B ? dec_tiles(a, ROWS, base + threadIdx.x) : 0;
+      n = base + (int)threadIdx.x < a.b.B ? dec_units(a, ROWS, base + threadIdx.x) : 0;
       e = block_scan<kDecWaves>(n, sh.scan, &t);
       total += t;
       const int own = base + (int)threadIdx.x;  // of the sequences that see nothing, every W-th is this workgroup's
       if (own < a.b.B && n == 0 && own % a.W == w) dec_clear<NS>(a, ROWS, own, h);
     }
-    run = dec_run(total, a.W);
-    begin = w * run;
+    const long long per = total > 0 ? (total + a.W - 1) / a.W : 1, begin = w * per;
     if (begin >= total) {
       if (threadIdx.x == 0) a.part_seq[h * a.W + w] = shared;
       return;
     }
-    left = total - begin < run ? total - begin : run;
+    run = per * kDecMinTiles;
+    left = (total - begin < per ? total - begin : per) * kDecMinTiles;
     for (int base = 0; base < a.b.B && before <= begin; base += kDecThreads) {
       if (a.b.B > kDecThreads) {  // else the one scan above
-        n = base + (int)threadIdx.x < a.b.B ? dec_tiles(a, ROWS, base + threadIdx.x) : 0;
+        n = base + (int)threadIdx.x < a.b.B ? dec_units(a, ROWS, base + threadIdx.x) : 0;
         e = block_scan<kDecWaves>(n, sh.scan, &t);
       }
       if (begin >= before + e - n && begin < before + e) {
         sh.found[0] = base + threadIdx.x;
-        sh.found[1] = (int)(begin - (before + e - n));
+        sh.found[1] = (int)(begin - (before + e - n)) * kDecMinTiles;
       }
       before += t;
     }

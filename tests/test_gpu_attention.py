@@ -383,3 +383,21 @@ def test_tiny_scales_over_pages_of_the_largest_scale(q, scale, dt):
     out, lse = attend(host, tab, x, q, kv, scale=scale)
     torch.cuda.synchronize()
     A.check_attention(out, lse, ref, dt, 64, f"scale {scale} q{q} {dt}")
+
+
+def test_tiles_past_32_bits():
+    """128 sequences of 2^30 tokens, all in one page: 2^31 tiles in one batch.
+    Keys of zero, so that every token weighs the same; values of which one in
+    128 is not zero, so that every sum on the way is exact."""
+    B, D, S, n = 128, 16, 128, 1 << 30
+    kc = torch.zeros(1, 1, S, D, dtype=torch.uint8, device="cuda")
+    vc = torch.zeros(1, 1, S // 16, D, 16, dtype=torch.uint8, device="cuda")
+    vc[0, 0, 3, :, 5] = torch.arange(D, dtype=torch.uint8, device="cuda") % 15 * 8 + 8  # 2^-6 to 2^8
+    one = torch.ones(1, 1, device="cuda")
+    table = torch.zeros(B, n // S, dtype=torch.int32, device="cuda")
+    out, lse = moe.moe_paged_attention(moe.PagedKV(kc, vc, one, one), A.values((B, 1, D), "bf16", 1).cuda(), A.i32([n] * B),
+                                       table, return_lse=True)
+    torch.cuda.synchronize()
+    want = torch.exp2(torch.arange(D, dtype=torch.float64) % 15 - 6 - 7)
+    assert torch.equal(out.cpu().double(), want.expand(B, 1, D))
+    assert (lse.cpu().double() - 30 * np.log(2)).abs().max() <= 2.0 ** -20 * 30
