@@ -309,6 +309,26 @@ __device__ __forceinline__ float attn_probs(const f32x16& sc, float f, float c, 
   return sum;
 }
 
+// Sum of exp2(s f - m) of a lane's 16 tokens by itself, for tiles with values of
+// a scale below 2^kLowScale (an append of zeros leaves 2^-64): beside values of
+// a scale of 2^48, m is up to 2^41 of the largest weight, and such a token's x
+// is under fp32's smallest number from a weight of 2^-21 of it on.  From
+// kLowScale on that takes a weight of 2^-45.
+constexpr float kLowScale = -40.0f;
+__device__ __forceinline__ float attn_weights(const f32x16& sc, float f, float m) {
+  float sum = 0.0f;
+#pragma unroll
+  for (int k = 0; k < 16; ++k) sum += __builtin_amdgcn_exp2f(__builtin_fmaf(sc[k], f, -m));
+  return sum;
+}
+
+// l 2^-below, in two steps: where m rises from values of the smallest scale to
+// some of the largest, 2^-below is no fp32 number but l 2^-below is.
+__device__ __forceinline__ float attn_lower(float l, float below) {
+  const float half = __builtin_amdgcn_exp2f(-0.5f * below);
+  return l * half * half;
+}
+
 // Four values of a row's output from its sums o and l.
 template <int NS>
 __device__ __forceinline__ void attn_store4(const AttnArgs& a, size_t row, int d, const float o[4], float l) {

@@ -61,7 +61,7 @@ __global__ __launch_bounds__(kDecThreads) void attn_join_kernel(AttnArgs a) {
   for (int j = 0; j < ML; ++j) {
     const float f = __builtin_amdgcn_exp2f(ml[j].x - mm);
     weight[threadIdx.x + j * kDecThreads] = f;  // 0 past the last part
-    l += f * ml[j].y;
+    l += attn_lower(ml[j].y, mm - ml[j].x);
   }
   l = wave_sum(l);
   __syncthreads();  // weights written, maxima read

@@ -182,9 +182,10 @@ __device__ __forceinline__ void dec_tile(const AttnArgs& a, const View& vw, int 
   const int t0 = tile * kAttnTile;
   const bool masked = t0 < st.all_lo || t0 + kAttnTile > st.all_hi || __any(t.gone);
   const float f = t.gone ? 1.0f : score_scale(a, t.ks), fv = t.gone ? 1.0f : page_scale_of(t.vs);
-  const float lv = __builtin_amdgcn_logf(fv), rv = __builtin_amdgcn_exp2f(-lv);
+  const float lv = __builtin_amdgcn_logf(fv);
+  float rv = __builtin_amdgcn_exp2f(-lv);
   float top[NR];
-  bool grow = false;
+  bool grow = lv < kLowScale;
 #pragma unroll
   for (int r = 0; r < NR; ++r) {
     if (masked) attn_hide(s[r], t.gone, t0 + 16 * g, st.lo[r], st.hi[r]);
@@ -192,15 +193,20 @@ __device__ __forceinline__ void dec_tile(const AttnArgs& a, const View& vw, int 
     grow |= top[r] > st.m[r] + kMaxSlack;
   }
   if (__any(grow)) {
+    const bool low = __any(lv < kLowScale);
 #pragma unroll
     for (int r = 0; r < NR; ++r) {
       const float m = __builtin_fmaxf(st.m[r], max32(max16(top[r])) - kMaxLow);
-      const float keep = m == -__builtin_inff() ? 1.0f : __builtin_amdgcn_exp2f(st.m[r] - m);
-      st.m[r] = m;
-      st.l[r] *= keep;
+      if (m != -__builtin_inff()) {
+        const float keep = __builtin_amdgcn_exp2f(st.m[r] - m);
+        st.l[r] = attn_lower(st.l[r], m - st.m[r]);
+        st.m[r] = m;
 #pragma unroll
-      for (int n = 0; n < DT / 16; ++n) st.o[r][n] *= keep;
+        for (int n = 0; n < DT / 16; ++n) st.o[r][n] *= keep;
+        if (low) st.l[r] += attn_weights(s[r], f, m);
+      }
     }
+    if (low) rv = 0.0f;
   }
   bf16x8 p[NR][2][NS];
 #pragma unroll
@@ -357,7 +363,7 @@ __device__ __forceinline__ void attn_decode_run(const AttnArgs& a, int w, int h,
 #pragma unroll
         for (int k = 0; k < kDecWaves; ++k) {
           f[k] = __builtin_amdgcn_exp2f(jm[k][col] - base);
-          sum += f[k] * jl[k][col];
+          sum += attn_lower(jl[k][col], base - jm[k][col]);
         }
         const size_t orow = (size_t)(s.q0 + qi) * a.nH + h * a.G + row - qi * a.G;
         const size_t slot = part_slot(a, h, w, skip == 0);

@@ -277,20 +277,25 @@ __global__ __launch_bounds__(kTileThreads, DT <= 128 && NS == 1 ? 2 : 1) void at
     const float top = UNI ? __builtin_fmaf(__builtin_fmaxf(attn_top(sc[0]), attn_top(sc[1])), cf0, lv0)
                           : __builtin_fmaxf(__builtin_fmaf(attn_top(sc[0]), cf0, lv0),
                                             __builtin_fmaf(attn_top(sc[1]), cf1, lv1));
-    if (__any(top > mx + kMaxSlack)) {
+    float rv0 = __builtin_amdgcn_exp2f(-lv0), rv1 = UNI ? rv0 : __builtin_amdgcn_exp2f(-lv1);
+    if (__any(top > mx + kMaxSlack || (UNI ? lv0 : __builtin_fminf(lv0, lv1)) < kLowScale)) {
+      const bool low = __any((UNI ? lv0 : __builtin_fminf(lv0, lv1)) < kLowScale);
       const float mn = __builtin_fmaxf(mx, max32(top) - kMaxLow);
-      const float keep = mn == -__builtin_inff() ? 1.0f : __builtin_amdgcn_exp2f(mx - mn);
-      mx = mn;
-      l *= keep;
+      if (mn != -__builtin_inff()) {
+        const float keep = __builtin_amdgcn_exp2f(mx - mn);
+        l = attn_lower(l, mn - mx);
+        mx = mn;
 #pragma unroll
-      for (int n = 0; n < DT / 32; ++n) o[n] *= keep;
+        for (int n = 0; n < DT / 32; ++n) o[n] *= keep;
+        if (low) l += attn_weights(sc[0], cf0, mx) + attn_weights(sc[1], cf1, mx);
+      }
+      if (low) rv0 = rv1 = 0.0f;
     }
     const float base = mx == -__builtin_inff() ? 0.0f : mx;
     bf16x8 p[2][2][NS];
     const float s0 = attn_probs<NS>(sc[0], cf0, lv0 - base, p[0]);
     const float s1 = attn_probs<NS>(sc[1], UNI ? cf0 : cf1, lv1 - base, p[1]);
-    l += UNI ? __builtin_amdgcn_exp2f(-lv0) * (s0 + s1)
-             : __builtin_amdgcn_exp2f(-lv0) * s0 + __builtin_amdgcn_exp2f(-lv1) * s1;
+    l += UNI ? rv0 * (s0 + s1) : rv0 * s0 + rv1 * s1;
 #pragma unroll
     for (int c = 0; c < 4; ++c)
 #pragma unroll

@@ -401,3 +401,27 @@ def test_tiles_past_32_bits():
     want = torch.exp2(torch.arange(D, dtype=torch.float64) % 15 - 6 - 7)
     assert torch.equal(out.cpu().double(), want.expand(B, 1, D))
     assert (lse.cpu().double() - 30 * np.log(2)).abs().max() <= 2.0 ** -20 * 30
+
+
+@pytest.mark.parametrize("q", [1, 40])
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("S", [16, 64])
+def test_pages_of_zeros_beside_one_of_the_largest_scale(q, dt, S):
+    """40000 tokens of 2^-22.2 of the weight of one whose page has the largest
+    scale, in pages of the smallest (what an append of zeros leaves): they have
+    no part in the sum of values, but 1/120 of the sum of weights."""
+    n, H, D = 40000, 1, 64
+    P, table = A.tables([n], S, 1)
+    host = A.random_cache(P, H, S, D, 2)
+    host["k_codes"][:], host["v_codes"][:] = 0, 0
+    host["k_codes"][table[0, 0], 0, 5, 9] = 0x38  # 1
+    host["v_codes"][table[0, 0], 0, 0, :, 5] = 0x58  # 16
+    host["k_scales"][:], host["v_scales"][:] = 1, AO.MIN_SCALE
+    host["v_scales"][table[0, 0]] = AO.MAX_SCALE
+    x = torch.zeros(q, 2, D, dtype=A.DT[dt])
+    x[:, :, 9] = 1
+    scale = 22.2 * np.log(2)
+    ref = AO.attention(host, A.f64(x), [0, q], [n], table, scale, False)
+    out, lse = attend(host, table, x, [q], [n], causal=False, scale=scale)
+    torch.cuda.synchronize()
+    A.check_attention(out, lse, ref, dt, D, f"zeros beside the largest q{q} {dt} page{S}")
