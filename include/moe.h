@@ -400,11 +400,9 @@ moe_status moe_rope_workspace_size(int32_t T, int32_t n_heads, int32_t head_dim,
 
 /*
  * The attention side of a decoder layer whose experts the calls above run:
- * rotary positions, a paged key/value cache in E4M3 and attention over it
- * ([post], "Triton JIT recompilation elimination", names the fusion of
- * rotation and per-head FP8 codes; the calls below are what such codes are
- * stored in and read by).  The conventions at the top of this file hold for
- * them; their counts (tokens, sequences, pages) are only kernel arguments.
+ * rotary positions, a paged key/value cache in E4M3 and attention over it.
+ * The conventions at the top of this file hold for them; their counts
+ * (tokens, sequences, pages) are only kernel arguments.
  */
 
 /* Rotation of head vectors by position, with one or several axes (text: one;

@@ -17,8 +17,11 @@
 // conversion, and the maximum), at a clock of 1.75 to 2.0 GHz under this load;
 // the two overlap as far as two workgroups a CU allow.  Pages below 64 tokens
 // 560 to 577 us.  Twelve chunks of up to 701 tokens over up to 6001, window 1024,
-// 16 / 4 heads of 64, page 16: 48 us, two or three workgroups a CU, so that a
-// third of the chip waits for the CUs with three; the VALU bounds those.
+// 16 / 4 heads of 64, page 16: 48.5 to 50 us, two or three workgroups a CU, so that
+// the chip waits for the CUs with three; over all of it the VALU issues in 0.37
+// of the cycles and the matrix pipe is busy in 0.14.  f32 queries of heads above
+// 128 spill 75 to 86 registers (4096 tokens, 16 / 4 heads of 256: 494 us, bf16
+// 202, for three times the products).
 #include "attn_decode.hpp"
 #include "launch.hpp"
 

@@ -23,9 +23,11 @@
 // channel (paged.hpp): through LDS, four channels by 16 tokens at a time
 // transposed with byte permutes, where a block of 16 tokens is all new; byte by
 // byte otherwise, which leaves every other token's bytes alone.
-// Measured, page 64, 8 heads of 128, bf16: 65536 tokens at 4.43 TB/s (a copy:
+// Frequencies are made once per workgroup, by one thread each, while the tokens
+// are on their way.
+// Measured, page 64, 8 heads of 128, bf16: 65536 tokens at 4.6 TB/s (a copy:
 // 5.43), bytes and the conversions' VALU together; 8192 tokens (50 MB) in
-// 17.3 us, since its 1032 workgroups are all resident at once and load, then
+// 15.5 us, since its 1032 workgroups are all resident at once and load, then
 // store, in step; one token of each of 64 sequences in 5 us, a chain of table,
 // token, barrier and store.  Keys and values in workgroups of their own take
 // 19 to 21 us for the 8192 tokens, a workgroup over all heads 26.

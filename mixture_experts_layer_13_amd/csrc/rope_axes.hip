@@ -10,9 +10,9 @@
 // (once per token and pair, for every head), and after one barrier rotate and
 // store.  Each thread reads both halves of its pairs before it writes them,
 // which is what allows out == x.
-// Measured: 8192 tokens, 32 heads of 128, bf16, three axes (134 MB): 27.0 us,
-// 4.97 TB/s, a copy's rate (5.43) less the launch; 4099 x 20 x 80, f32, 64
-// turned, interleaved (52 MB): 11.0 us, 4.8 TB/s, with angles per head instead
+// Measured: 8192 tokens, 32 heads of 128, bf16, three axes (134 MB): 27.6 us,
+// 4.87 TB/s, a copy's rate (5.43) less the launch; 4099 x 20 x 80, f32, 64
+// turned, interleaved (52 MB): 11.3 us, 4.6 TB/s, with angles per head instead
 // of per token 20; 64 tokens: 3.8 us, the launch and two trips to memory.
 #include "launch.hpp"
 #include "rotate.hpp"

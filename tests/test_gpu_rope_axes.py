@@ -1,7 +1,8 @@
-"""moe_rope_axes against the fp64 oracle.  Error of a rotated value: the angle
-is within 2^-26 rad of the exact product for |position| < 2^24, sincospi
-within 2 ulp (2^-23), two fp32 roundings follow: at most 2^-21 (|u| + |v|);
-the output type rounds once more by half a step."""
+"""moe_rope_axes against the fp64 oracle.  Error of a rotated value: the angle's
+fraction of a turn is within 2^-32 of the exact one (2^-29.3 rad), rounding it to
+fp32 and the sine and cosine instructions add 2^-22.3, two fp32 roundings of
+2^-24 follow: less than 2^-21 (|u| + |v|); the output type rounds once more by
+half a step."""
 import numpy as np
 import pytest
 import torch
