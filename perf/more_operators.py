@@ -173,7 +173,8 @@ def _to_codes(x, s):
 
 
 def _scale_of(amax):
-    s = (amax / E4M3_MAX).clamp(min=2.0 ** -126)
+    # by a tensor: division by a number would multiply by its rounded reciprocal
+    s = (amax / torch.full_like(amax, E4M3_MAX)).clamp(min=2.0 ** -126)
     return torch.where(amax == 0, 1.0, s)
 
 
