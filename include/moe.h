@@ -555,6 +555,147 @@ moe_status moe_paged_attention(const moe_kv_cache* cache, const moe_kv_batch* ba
 moe_status moe_paged_attention_workspace_size(const moe_kv_cache* cache, int32_t T, int32_t B,
                                               int32_t n_heads, int32_t max_q, size_t* bytes);
 
+/*
+ * Around the experts: tokens into expert order and back (for experts that run
+ * elsewhere, and for training), and experts with block-scaled E4M3 weights.
+ * The conventions at the top of this file hold; row strides are in elements,
+ * at least a row, multiples of 16 bytes, and every value buffer is 16-byte,
+ * every index, weight and scale buffer 4-byte aligned.  An output overlaps no
+ * other argument.
+ */
+
+/* What moe_align_permute wrote, for M tokens of topk pairs f = t * topk + j.
+ *   rows   entries of sorted_pair_ids (at least ceil(rows / block_m) of
+ *          block_expert_ids), and rows of every buffer in expert order: the
+ *          capacity, or fewer where the caller knows that *num_padded fits
+ *          (places from rows on are dropped).
+ * A place holds a pair if sorted_pair_ids is in [0, M * topk) there, else it is
+ * padding.  topk 1..64, M * topk <= 2^26, rows <= 2^26 + 2^18.
+ * Which fields a call reads is said there; the others may be anything. */
+typedef struct {
+  const int32_t* sorted_pair_ids;
+  const int32_t* block_expert_ids;
+  const int32_t* expert_offsets;
+  const int32_t* pair_pos;
+  const int32_t* num_padded;
+  int32_t M, topk, E, block_m, rows;
+} moe_alignment;
+
+/*
+ * rows[pair_pos[f]] = weights[f] * x[t], padding rows zero; rows from
+ * *num_padded on keep what they held, and pairs without a place (-1: the
+ * experts of another rank) go nowhere.  Its gradient, given d_rows:
+ *   dx[t] = sum_j weights[f] * d_rows[pair_pos[f]]
+ *   d_weights[f] = sum_d x[t][d] * d_rows[pair_pos[f]][d]   (0 without a place)
+ * Products and sums in fp32, in the order of j (and a fixed order of d), each
+ * result rounded once.  The same on every run.
+ * x, dx      device [M, K] of x_dtype; rows, d_rows device [rows, K] of
+ *            rows_dtype (MOE_BF16 or MOE_F32, in any combination).
+ * weights    device f32 [M, topk] or NULL (all 1).
+ * d_weights  device f32 [M, topk] or NULL (x is then not read).
+ * K          a multiple of 8 in [8, 65536].   M <= 2^23.
+ * Reads of the alignment: pair_pos; moe_dispatch sorted_pair_ids and num_padded
+ * too.  M == 0 is a no-op.  Errors: MOE_ERR_NULL, MOE_ERR_SHAPE, MOE_ERR_DTYPE,
+ * MOE_ERR_ALIGN, MOE_ERR_HIP.
+ */
+moe_status moe_dispatch(const moe_alignment* alignment, const void* x, int32_t x_dtype, int64_t x_stride, int32_t K,
+                        const float* weights, void* rows, int32_t rows_dtype, int64_t rows_stride, void* stream);
+moe_status moe_dispatch_backward(const moe_alignment* alignment, const void* d_rows, int32_t rows_dtype,
+                                 int64_t d_rows_stride, int32_t K, const void* x, int64_t x_stride,
+                                 const float* weights, void* dx, int32_t x_dtype, int64_t dx_stride,
+                                 float* d_weights, void* stream);
+
+/*
+ * out[t] = sum_j weights[f] * rows[pair_pos[f]] over the pairs with a place.
+ * Its gradient, given d_out:
+ *   d_rows[pair_pos[f]] = weights[f] * d_out[t], padding rows zero (rows from
+ *                         *num_padded on keep what they held)
+ *   d_weights[f] = sum_d d_out[t][d] * rows[pair_pos[f]][d]   (0 without a place)
+ * Types, sizes, limits and errors as in moe_dispatch (out, d_out for x, dx;
+ * moe_combine_backward reads what moe_dispatch reads; without d_weights, rows
+ * is not read).
+ */
+moe_status moe_combine(const moe_alignment* alignment, const void* rows, int32_t rows_dtype, int64_t rows_stride,
+                       int32_t K, const float* weights, void* out, int32_t out_dtype, int64_t out_stride,
+                       void* stream);
+moe_status moe_combine_backward(const moe_alignment* alignment, const void* d_out, int32_t out_dtype,
+                                int64_t d_out_stride, int32_t K, const void* rows, int64_t rows_stride,
+                                const float* weights, void* d_rows, int32_t rows_dtype, int64_t d_rows_stride,
+                                float* d_weights, void* stream);
+
+/*
+ * E4M3 codes with a scale for each block of 128 values along K, of one row
+ * (block_rows 1: activations) or of 128 rows (block_rows 128: weights); the
+ * last block of a row, or of the rows, may be shorter:
+ *   scale = max(fl32(amax / 448), 2^-126), amax over the block's finite
+ *           magnitudes; 1 if amax is 0;
+ *   codes = E4M3(fl32(x / scale)), round to nearest even, saturating (infinities
+ *           too); a NaN gives a NaN code.
+ * gated: the values are SiLU(x[m][k]) * x[m][K + k] in fp32 (x has 2 K values a
+ * row).
+ * x          device [M, K] (gated [M, 2 K]) of x_dtype (MOE_BF16 or MOE_F32).
+ * num_rows   device int32 [1] or NULL: rows from *num_rows on (an alignment's
+ *            num_padded) keep what they held.
+ * codes      device uint8 [M, K], dense (written).
+ * scales     device f32 (written): block (m / block_rows, k / 128) at
+ *            m / block_rows * scale_stride_row + k / 128 * scale_stride_block.
+ * K a multiple of 16 in [16, 65536], M <= 2^27; strides of the scales 1 to
+ * 2^32.  M == 0 is a no-op.  Errors: MOE_ERR_NULL, MOE_ERR_SHAPE,
+ * MOE_ERR_DTYPE, MOE_ERR_ALIGN, MOE_ERR_UNSUPPORTED (gated or num_rows with
+ * block_rows 128), MOE_ERR_HIP.
+ */
+moe_status moe_quantize_blocks(const void* x, int32_t x_dtype, int64_t x_stride, int32_t M, int32_t K, int32_t gated,
+                               int32_t block_rows, const int32_t* num_rows, uint8_t* codes, float* scales,
+                               int64_t scale_stride_row, int64_t scale_stride_block, void* stream);
+
+/*
+ * The product of block-scaled E4M3 matrices, B = ceil(K / 128):
+ *   out[m][n] = sum_{b < B} a_scales[m][b] * w_scales[n / 128][b]
+ *               * sum_{k in block b} a[m][k] * w[n][k]
+ * A block's products are summed exactly in fp32 or to its rounding, the scaled
+ * blocks in fp32 in a fixed order, the result is rounded once; it is the same
+ * on every run.  A NaN code makes its row (of a) or column (of w) NaN.
+ * a          device uint8 [M, K] of E4M3 codes, row stride a_stride bytes
+ *            (a multiple of 16, at most 2^22).
+ * a_scales   device f32: block (m, b) at m * scale_stride_row + b *
+ *            scale_stride_block (strides 1 to 2^20 and 1 to 2^32; consecutive
+ *            rows side by side are read fastest).
+ * w          device uint8 [N, K], dense.   w_scales  device f32
+ *            [ceil(N / 128)][B], dense.  (The transposed matrix with its
+ *            transposed scales gives the gradient of a.)
+ *            A scale of a times one of w: within 2^-126 and 2^102 in magnitude
+ *            (0 where less).
+ * out        device [M, N] of out_dtype (MOE_BF16 or MOE_F32), row stride
+ *            out_stride elements, any alignment of its type (16-byte rows are
+ *            written fastest).
+ * K a multiple of 16 in [16, 65536], N 1..65536, M <= 2^27, M N <= 2^36.
+ * M == 0 is a no-op.  Errors: MOE_ERR_NULL, MOE_ERR_SHAPE, MOE_ERR_DTYPE,
+ * MOE_ERR_ALIGN, MOE_ERR_HIP.
+ */
+moe_status moe_block_matmul(const uint8_t* a, int64_t a_stride, const float* a_scales, int64_t scale_stride_row,
+                            int64_t scale_stride_block, const uint8_t* w, const float* w_scales, int32_t M, int32_t N,
+                            int32_t K, void* out, int32_t out_dtype, int64_t out_stride, void* stream);
+
+/*
+ * The same for the rows of an alignment, each with its expert's weights:
+ * out row p, p < *num_padded, is row (gather ? sorted_pair_ids[p] / topk : p)
+ * of a times w[expert of p]; padding rows are zero, rows from *num_padded on
+ * keep what they held.
+ * a          a_rows rows: the M tokens (gather != 0; a_rows >= M, a_rows *
+ *            a_stride < 2^31, a_rows * scale_stride_row < 2^29) or rows in
+ *            expert order (a_rows >= alignment->rows).
+ * w, w_scales  device [E][N][K] and f32 [E][ceil(N / 128)][B], dense.
+ * out        [alignment->rows, N].
+ * Reads all of the alignment but pair_pos; E 1..1024, block_m as in
+ * moe_align_permute.  M == 0 or rows == 0 is a no-op.  Errors as above;
+ * MOE_ERR_SHAPE also where the tiles of rows x N are more than a grid has.
+ */
+moe_status moe_block_matmul_grouped(const moe_alignment* alignment, const uint8_t* a, int64_t a_stride,
+                                    int32_t a_rows, const float* a_scales, int64_t scale_stride_row,
+                                    int64_t scale_stride_block, const uint8_t* w, const float* w_scales, int32_t N,
+                                    int32_t K, int32_t gather, void* out, int32_t out_dtype, int64_t out_stride,
+                                    void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -1,0 +1,151 @@
+// block_gemm.hpp -- arguments of the block quantisation (quant_blocks.hip) and
+// of the block-scaled E4M3 products (block_gemm.hip, block_rows.hip).
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+namespace moe {
+
+struct QuantArgs {
+  const void* x;
+  long long x_stride;
+  int M, K;                 // K: values of a row of codes (gated: half a row of x)
+  const int32_t* num_rows;  // device, or NULL: rows from there on are left alone
+  uint8_t* codes;           // [M, K]
+  float* scales;
+  long long s_row, s_block;
+};
+
+int launch_quant_blocks(const QuantArgs& a, int dt, bool gated, int block_rows, hipStream_t st);
+
+// out[m, n] = sum_b as[m, b] ws[n / 128, b] sum_{k in block b} a[m, k] w[n, k]
+struct BlockGemmArgs {
+  const uint8_t* a;
+  const float* as;
+  long long a_stride, as_m, as_b;
+  const uint8_t* w;
+  const float* ws;
+  int M, N, K;  // M: rows of a
+  int KB, NB;   // blocks of 128 along K and N
+  void* out;
+  long long out_stride;
+  int vec;      // rows of out can be written 16 bytes at a time
+  // grouped (ids != NULL): out rows in the alignment's order, w [E] of these
+  const int32_t* ids;
+  const int32_t* block_expert;
+  const int32_t* offsets;
+  const int32_t* num_padded;
+  int E, bm, R, pairs, topk;  // topk 0: a is in the alignment's order too
+};
+
+// Rows row0 .. row0 + rows - 1 of out, those of one expert.
+struct RowSpan {
+  int row0, rows, e;
+};
+
+#ifdef __HIPCC__
+typedef float b_f32x4 __attribute__((ext_vector_type(4)));
+typedef int b_i32x4 __attribute__((ext_vector_type(4)));
+typedef int b_i32x8 __attribute__((ext_vector_type(8)));
+typedef __bf16 b_bf16x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 b_bf16x8 __attribute__((ext_vector_type(8)));
+
+// One lane's 32 codes of a block of 128 along K, as an MFMA operand.  E4M3
+// instructions add products by groups of eight, aligned to the group's largest
+// and cut below 2^-13 of its power of two (measured): far inside a bf16 result's
+// rounding (2.7e-5 against 1.7e-3), but not an fp32 result's.  For that the
+// codes become bf16, exactly, whose products are added in fp32, at half the rate.
+template <bool WIDE>
+struct BOperand;
+template <>
+struct BOperand<false> {
+  b_i32x8 v;
+  __device__ __forceinline__ void set(b_i32x4 lo, b_i32x4 hi) {
+    v = b_i32x8{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+  }
+};
+template <>
+struct BOperand<true> {
+  b_bf16x8 v[4];
+  __device__ __forceinline__ void set(b_i32x4 lo, b_i32x4 hi) {
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+      const int c = q < 4 ? lo[q] : hi[q - 4];
+      const b_bf16x2 x = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c, 1.0f, false);
+      const b_bf16x2 y = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c, 1.0f, true);
+      v[q / 2][4 * (q % 2)] = x[0];
+      v[q / 2][4 * (q % 2) + 1] = x[1];
+      v[q / 2][4 * (q % 2) + 2] = y[0];
+      v[q / 2][4 * (q % 2) + 3] = y[1];
+    }
+  }
+};
+
+// The sums of one block of 128 along K, of 16 weight rows and 16 rows of a.
+__device__ __forceinline__ b_f32x4 block_sums(const BOperand<false>& w, const BOperand<false>& a) {
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w.v, a.v, b_f32x4{}, 0, 0, 0, 0, 0, 0);
+}
+__device__ __forceinline__ b_f32x4 block_sums(const BOperand<true>& w, const BOperand<true>& a) {
+  b_f32x4 t = {};
+#pragma unroll
+  for (int q = 0; q < 4; ++q) t = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w.v[q], a.v[q], t, 0, 0, 0);
+  return t;
+}
+
+// Span number i of spans of up to TM rows; rows = 0: none.
+template <int TM>
+__device__ __forceinline__ RowSpan row_span(const BlockGemmArgs& g, int i) {
+  RowSpan s{0, 0, 0};
+  if (!g.ids) {
+    s.row0 = i * TM;
+    s.rows = min(TM, g.M - s.row0);
+    return s;
+  }
+  const int n = min(*g.num_padded, g.R);
+  if (g.bm >= TM) {
+    s.row0 = i * TM;
+    if (s.row0 >= n) return s;
+    s.e = g.block_expert[s.row0 / g.bm];
+    s.rows = min(TM, n - s.row0);
+  } else {
+    // blocks shorter than a span: a span starts where its expert's rows do, or
+    // a whole number of spans behind
+    s.row0 = i * g.bm;
+    if (s.row0 >= n) return s;
+    s.e = g.block_expert[i];
+    if (s.e < 0 || s.e >= g.E) return s;
+    const int from = s.row0 - g.offsets[s.e];
+    if (from % TM) return s;
+    s.rows = min(min(TM, g.offsets[s.e + 1] - s.row0), n - s.row0);
+  }
+  if (s.e < 0 || s.e >= g.E) s.rows = 0;
+  return s;
+}
+
+// The row of a that out row `row` comes from, -1: none (the row is zero).
+__device__ __forceinline__ int source_row(const BlockGemmArgs& g, int row) {
+  if (!g.ids) return row;
+  const int f = g.ids[row];
+  if (f < 0 || f >= g.pairs) return -1;
+  const int at = g.topk ? f / g.topk : row;
+  return at < g.M ? at : -1;
+}
+#endif
+
+// Spans of up to tm rows that row_span<tm> numbers.
+inline long long row_spans(const BlockGemmArgs& g, int tm) {
+  if (!g.ids) return ((long long)g.M + tm - 1) / tm;
+  const int step = g.bm >= tm ? tm : g.bm;
+  return ((long long)g.R + step - 1) / step;
+}
+
+// What a launcher returns, launching nothing, for more tiles than a grid has.
+constexpr int kTooManyTiles = -1;
+constexpr long long kMaxThreads = (1LL << 32) - 1;  // of a grid
+
+// The product, by the kernel that fits (block_gemm.hip); rows: of a span.
+int launch_block_product(const BlockGemmArgs& g, int out_type, hipStream_t st);
+int launch_block_rows(const BlockGemmArgs& g, int out_type, int rows, hipStream_t st);
+
+}  // namespace moe

@@ -11,7 +11,9 @@
 
 #include "../../include/moe.h"
 #include "attention.hpp"
+#include "block_gemm.hpp"
 #include "launch.hpp"
+#include "permute.hpp"
 #include "rotate.hpp"
 
 namespace {
@@ -874,6 +876,248 @@ moe_status moe_paged_attention(const moe_kv_cache* cache, const moe_kv_batch* ba
   const int err = p.tile_units ? moe::launch_attn_tile(a, p.dec_rows, (int)p.tile_units, f32, (hipStream_t)stream)
                                : moe::launch_attn_decode(a, p.dec_rows, f32, (hipStream_t)stream);
   return hip_status(err, "attention launch");
+}
+
+}  // extern "C"
+
+// --------------------- rows in expert order, block-scaled E4M3 products
+
+namespace {
+
+// A row stride (elements of eb bytes) of rows of at least `least` elements.
+moe_status check_row_stride(const char* name, int64_t stride, int64_t least, int eb, int64_t most = 1LL << 32) {
+  if (stride < least || stride > most)
+    return fail(MOE_ERR_SHAPE, "%s row stride %lld must be in [%lld, %lld]", name, (long long)stride, (long long)least,
+                (long long)most);
+  if (stride * eb % 16)
+    return fail(MOE_ERR_ALIGN, "%s row stride %lld must be a multiple of 16 bytes", name, (long long)stride);
+  return MOE_OK;
+}
+
+moe_status check_alignment(const moe_alignment* al) {
+  if (!al) return fail(MOE_ERR_NULL, "alignment is NULL");
+  if (al->M < 0) return fail(MOE_ERR_SHAPE, "M=%d must be >= 0", al->M);
+  if (al->topk < 1 || al->topk > 64) return fail(MOE_ERR_SHAPE, "topk=%d must be in [1, 64]", al->topk);
+  if ((long long)al->M * al->topk > kMaxPairs)
+    return fail(MOE_ERR_SHAPE, "M*topk=%lld exceeds %lld", (long long)al->M * al->topk, kMaxPairs);
+  if (al->rows < 0 || al->rows > kMaxPairs + (1 << 18))
+    return fail(MOE_ERR_SHAPE, "rows=%d must be in [0, 2^26 + 2^18]", al->rows);
+  return MOE_OK;
+}
+
+moe_status check_permute(const moe_alignment* al, int32_t tok_dtype, int32_t rows_dtype, int32_t K) {
+  moe_status s = check_alignment(al);
+  if (s) return s;
+  if (al->M > (1 << 23)) return fail(MOE_ERR_SHAPE, "M=%d must be in [0, 2^23]", al->M);
+  if (K < 8 || K > 65536 || K % 8) return fail(MOE_ERR_SHAPE, "K=%d must be a multiple of 8 in [8, 65536]", K);
+  if (!value_dtype(tok_dtype) || !value_dtype(rows_dtype))
+    return fail(MOE_ERR_DTYPE, "value types must be MOE_F32 or MOE_BF16");
+  return MOE_OK;
+}
+
+// One of the two movements; `scatter`: tokens to rows.
+moe_status permute(const moe_alignment* al, bool scatter, int32_t K, const void* tok, int32_t tok_dtype,
+                   int64_t tok_stride, const void* rows, int32_t rows_dtype, int64_t rows_stride, const float* weights,
+                   void* out, int64_t out_stride, float* dw, void* stream) {
+  moe_status s = check_permute(al, tok_dtype, rows_dtype, K);
+  if (s) return s;
+  const int te = dtype_bytes(tok_dtype), re = dtype_bytes(rows_dtype);
+  const bool reads_tok = scatter || dw, reads_rows = !scatter || dw;
+  if (reads_tok && (s = check_row_stride("token", tok_stride, K, te))) return s;
+  if (reads_rows && (s = check_row_stride("expert row", rows_stride, K, re))) return s;
+  if ((s = check_row_stride("output", out_stride, K, scatter ? re : te))) return s;
+  if (al->M == 0) return ok();
+  if (!al->pair_pos || !out || (reads_tok && !tok) || (reads_rows && !rows && al->rows))
+    return fail(MOE_ERR_NULL, "pair_pos, the inputs and the output are required");
+  if (scatter && (!al->sorted_pair_ids || !al->num_padded) && al->rows)
+    return fail(MOE_ERR_NULL, "sorted_pair_ids and num_padded are required");
+  if ((reads_tok && !aligned(tok, 16)) || (reads_rows && !aligned(rows, 16)) || !aligned(out, 16))
+    return fail(MOE_ERR_ALIGN, "value buffers must be 16-byte aligned");
+  for (const void* q : {(const void*)al->pair_pos, scatter ? (const void*)al->sorted_pair_ids : nullptr,
+                        scatter ? (const void*)al->num_padded : nullptr, (const void*)weights, (const void*)dw})
+    if (!aligned(q, 4)) return fail(MOE_ERR_ALIGN, "index and weight buffers must be 4-byte aligned");
+  moe::PermuteArgs a{};
+  a.sorted_ids = al->sorted_pair_ids;
+  a.pair_pos = al->pair_pos;
+  a.num_padded = al->num_padded;
+  a.M = al->M;
+  a.topk = al->topk;
+  a.P = al->M * al->topk;
+  a.rows = al->rows;
+  a.K = K;
+  a.tok_in = tok;
+  a.tok_in_stride = tok_stride;
+  a.rows_in = rows;
+  a.rows_in_stride = rows_stride;
+  a.tok_out = a.rows_out = out;
+  a.tok_out_stride = a.rows_out_stride = out_stride;
+  a.weights = weights;
+  a.dw = dw;
+  const int err = scatter ? moe::launch_scatter(a, tok_dtype, rows_dtype, (hipStream_t)stream)
+                          : moe::launch_gather(a, tok_dtype, rows_dtype, (hipStream_t)stream);
+  return hip_status(err, scatter ? "dispatch launch" : "combine launch");
+}
+
+// What the two products share.
+moe_status check_block_matmul(int64_t a_stride, int64_t ss_row, int64_t ss_block, int32_t N, int32_t K,
+                              int32_t out_dtype, int64_t out_stride) {
+  if (K < 16 || K > 65536 || K % 16) return fail(MOE_ERR_SHAPE, "K=%d must be a multiple of 16 in [16, 65536]", K);
+  if (N < 1 || N > 65536) return fail(MOE_ERR_SHAPE, "N=%d must be in [1, 65536]", N);
+  if (!value_dtype(out_dtype)) return fail(MOE_ERR_DTYPE, "out_dtype must be MOE_F32 or MOE_BF16");
+  moe_status s = check_row_stride("a", a_stride, K, 1, 1 << 22);
+  if (s) return s;
+  if (ss_row < 1 || ss_row > (1 << 20) || ss_block < 1 || ss_block > (1LL << 32))
+    return fail(MOE_ERR_SHAPE, "scale strides %lld, %lld must be in [1, 2^20] and [1, 2^32]", (long long)ss_row,
+                (long long)ss_block);
+  if (out_stride < N || out_stride > (1LL << 32))
+    return fail(MOE_ERR_SHAPE, "out row stride %lld must be in [N=%d, 2^32]", (long long)out_stride, N);
+  return MOE_OK;
+}
+
+moe_status check_block_buffers(const void* a, const void* a_scales, const void* w, const void* w_scales,
+                               const void* out, int out_bytes) {
+  if (!a || !a_scales || !w || !w_scales || !out)
+    return fail(MOE_ERR_NULL, "a, a_scales, w, w_scales and out are required");
+  if (!aligned(a, 16) || !aligned(w, 16)) return fail(MOE_ERR_ALIGN, "a and w must be 16-byte aligned");
+  if (!aligned(a_scales, 4) || !aligned(w_scales, 4) || !aligned(out, out_bytes))
+    return fail(MOE_ERR_ALIGN, "scales must be 4-byte aligned, out to its type");
+  return MOE_OK;
+}
+
+moe::BlockGemmArgs block_args(const uint8_t* a, int64_t a_stride, const float* a_scales, int64_t ss_row,
+                              int64_t ss_block, const uint8_t* w, const float* w_scales, int32_t M, int32_t N,
+                              int32_t K, void* out, int32_t out_dtype, int64_t out_stride) {
+  moe::BlockGemmArgs g{};
+  g.a = a;
+  g.a_stride = a_stride;
+  g.as = a_scales;
+  g.as_m = ss_row;
+  g.as_b = ss_block;
+  g.w = w;
+  g.ws = w_scales;
+  g.M = M;
+  g.N = N;
+  g.K = K;
+  g.KB = (K + 127) / 128;
+  g.NB = (N + 127) / 128;
+  g.out = out;
+  g.out_stride = out_stride;
+  g.vec = aligned(out, 16) && out_stride * dtype_bytes(out_dtype) % 16 == 0;
+  return g;
+}
+
+moe_status block_status(int err) {
+  if (err == moe::kTooManyTiles) return fail(MOE_ERR_SHAPE, "more tiles of out than one call takes");
+  return hip_status(err, "block product launch");
+}
+
+}  // namespace
+
+extern "C" {
+
+moe_status moe_dispatch(const moe_alignment* alignment, const void* x, int32_t x_dtype, int64_t x_stride, int32_t K,
+                        const float* weights, void* rows, int32_t rows_dtype, int64_t rows_stride, void* stream) {
+  return permute(alignment, true, K, x, x_dtype, x_stride, nullptr, rows_dtype, 0, weights, rows, rows_stride, nullptr,
+                 stream);
+}
+
+moe_status moe_dispatch_backward(const moe_alignment* alignment, const void* d_rows, int32_t rows_dtype,
+                                 int64_t d_rows_stride, int32_t K, const void* x, int64_t x_stride,
+                                 const float* weights, void* dx, int32_t x_dtype, int64_t dx_stride,
+                                 float* d_weights, void* stream) {
+  return permute(alignment, false, K, x, x_dtype, x_stride, d_rows, rows_dtype, d_rows_stride, weights, dx, dx_stride,
+                 d_weights, stream);
+}
+
+moe_status moe_combine(const moe_alignment* alignment, const void* rows, int32_t rows_dtype, int64_t rows_stride,
+                       int32_t K, const float* weights, void* out, int32_t out_dtype, int64_t out_stride,
+                       void* stream) {
+  return permute(alignment, false, K, nullptr, out_dtype, 0, rows, rows_dtype, rows_stride, weights, out, out_stride,
+                 nullptr, stream);
+}
+
+moe_status moe_combine_backward(const moe_alignment* alignment, const void* d_out, int32_t out_dtype,
+                                int64_t d_out_stride, int32_t K, const void* rows, int64_t rows_stride,
+                                const float* weights, void* d_rows, int32_t rows_dtype, int64_t d_rows_stride,
+                                float* d_weights, void* stream) {
+  return permute(alignment, true, K, d_out, out_dtype, d_out_stride, rows, rows_dtype, rows_stride, weights, d_rows,
+                 d_rows_stride, d_weights, stream);
+}
+
+moe_status moe_quantize_blocks(const void* x, int32_t x_dtype, int64_t x_stride, int32_t M, int32_t K, int32_t gated,
+                               int32_t block_rows, const int32_t* num_rows, uint8_t* codes, float* scales,
+                               int64_t scale_stride_row, int64_t scale_stride_block, void* stream) {
+  if (!value_dtype(x_dtype)) return fail(MOE_ERR_DTYPE, "x_dtype must be MOE_F32 or MOE_BF16");
+  if (M < 0 || M > (1 << 27)) return fail(MOE_ERR_SHAPE, "M=%d must be in [0, 2^27]", M);
+  if (K < 16 || K > 65536 || K % 16) return fail(MOE_ERR_SHAPE, "K=%d must be a multiple of 16 in [16, 65536]", K);
+  if (block_rows != 1 && block_rows != 128) return fail(MOE_ERR_SHAPE, "block_rows=%d must be 1 or 128", block_rows);
+  if (block_rows == 128 && (gated || num_rows))
+    return fail(MOE_ERR_UNSUPPORTED, "gated and num_rows need block_rows 1");
+  moe_status s = check_row_stride("x", x_stride, gated ? 2 * (int64_t)K : K, dtype_bytes(x_dtype));
+  if (s) return s;
+  if (scale_stride_row < 1 || scale_stride_row > (1LL << 32) || scale_stride_block < 1 ||
+      scale_stride_block > (1LL << 32))
+    return fail(MOE_ERR_SHAPE, "scale strides %lld, %lld must be in [1, 2^32]", (long long)scale_stride_row,
+                (long long)scale_stride_block);
+  if (M == 0) return ok();
+  if (!x || !codes || !scales) return fail(MOE_ERR_NULL, "x, codes and scales are required");
+  if (!aligned(x, 16) || !aligned(codes, 16)) return fail(MOE_ERR_ALIGN, "x and codes must be 16-byte aligned");
+  if (!aligned(scales, 4) || !aligned(num_rows, 4))
+    return fail(MOE_ERR_ALIGN, "scales and num_rows must be 4-byte aligned");
+  const moe::QuantArgs a{x, x_stride, M, K, num_rows, codes, scales, scale_stride_row, scale_stride_block};
+  return hip_status(moe::launch_quant_blocks(a, x_dtype, gated != 0, block_rows, (hipStream_t)stream),
+                    "block quantisation launch");
+}
+
+moe_status moe_block_matmul(const uint8_t* a, int64_t a_stride, const float* a_scales, int64_t scale_stride_row,
+                            int64_t scale_stride_block, const uint8_t* w, const float* w_scales, int32_t M, int32_t N,
+                            int32_t K, void* out, int32_t out_dtype, int64_t out_stride, void* stream) {
+  moe_status s = check_block_matmul(a_stride, scale_stride_row, scale_stride_block, N, K, out_dtype, out_stride);
+  if (s) return s;
+  if (M < 0 || M > (1 << 27)) return fail(MOE_ERR_SHAPE, "M=%d must be in [0, 2^27]", M);
+  if ((long long)M * N > (1LL << 36)) return fail(MOE_ERR_SHAPE, "M*N=%lld exceeds 2^36", (long long)M * N);
+  if (M == 0) return ok();
+  if ((s = check_block_buffers(a, a_scales, w, w_scales, out, dtype_bytes(out_dtype)))) return s;
+  const moe::BlockGemmArgs g = block_args(a, a_stride, a_scales, scale_stride_row, scale_stride_block, w, w_scales, M,
+                                          N, K, out, out_dtype, out_stride);
+  return block_status(moe::launch_block_product(g, out_dtype, (hipStream_t)stream));
+}
+
+moe_status moe_block_matmul_grouped(const moe_alignment* alignment, const uint8_t* a, int64_t a_stride,
+                                    int32_t a_rows, const float* a_scales, int64_t scale_stride_row,
+                                    int64_t scale_stride_block, const uint8_t* w, const float* w_scales, int32_t N,
+                                    int32_t K, int32_t gather, void* out, int32_t out_dtype, int64_t out_stride,
+                                    void* stream) {
+  moe_status s = check_alignment(alignment);
+  if (s) return s;
+  const moe_alignment& al = *alignment;
+  if ((s = check_block_matmul(a_stride, scale_stride_row, scale_stride_block, N, K, out_dtype, out_stride))) return s;
+  if (al.E < 1 || al.E > 1024) return fail(MOE_ERR_SHAPE, "E=%d must be in [1, 1024]", al.E);
+  if (!valid_block_m(al.block_m)) return fail(MOE_ERR_SHAPE, "block_m=%d must be 16, 32, 64, 128 or 256", al.block_m);
+  if (a_rows < (gather ? al.M : al.rows))
+    return fail(MOE_ERR_SHAPE, "a has %d rows, %d needed", a_rows, gather ? al.M : al.rows);
+  if (gather && ((long long)a_rows * a_stride >= (1LL << 31) || (long long)a_rows * scale_stride_row >= (1LL << 29)))
+    return fail(MOE_ERR_SHAPE, "a_rows=%d times its strides %lld and %lld must be below 2^31 and 2^29", a_rows,
+                (long long)a_stride, (long long)scale_stride_row);
+  if (al.M == 0 || al.rows == 0) return ok();
+  if (!al.sorted_pair_ids || !al.block_expert_ids || !al.expert_offsets || !al.num_padded)
+    return fail(MOE_ERR_NULL, "sorted_pair_ids, block_expert_ids, expert_offsets and num_padded are required");
+  for (const void* q : {(const void*)al.sorted_pair_ids, (const void*)al.block_expert_ids,
+                        (const void*)al.expert_offsets, (const void*)al.num_padded})
+    if (!aligned(q, 4)) return fail(MOE_ERR_ALIGN, "index buffers must be 4-byte aligned");
+  if ((s = check_block_buffers(a, a_scales, w, w_scales, out, dtype_bytes(out_dtype)))) return s;
+  moe::BlockGemmArgs g = block_args(a, a_stride, a_scales, scale_stride_row, scale_stride_block, w, w_scales, a_rows, N,
+                                    K, out, out_dtype, out_stride);
+  g.ids = al.sorted_pair_ids;
+  g.block_expert = al.block_expert_ids;
+  g.offsets = al.expert_offsets;
+  g.num_padded = al.num_padded;
+  g.E = al.E;
+  g.bm = al.block_m;
+  g.R = al.rows;
+  g.pairs = al.M * al.topk;
+  g.topk = gather ? al.topk : 0;
+  return block_status(moe::launch_block_product(g, out_dtype, (hipStream_t)stream));
 }
 
 }  // extern "C"

@@ -22,7 +22,8 @@ EXPORTS = ("moe_status_string", "moe_last_error", "moe_align_capacity", "moe_wor
            "moe_fused_forward_profiled", "moe_fused_forward_noalloc", "moe_route_align", "moe_route_project_topk",
            "moe_route_project_workspace_size", "moe_rope_quantize_per_head", "moe_rope_workspace_size",
            "moe_fused_forward_persistent", "moe_rope_axes", "moe_kv_append", "moe_paged_attention",
-           "moe_paged_attention_workspace_size")
+           "moe_paged_attention_workspace_size", "moe_dispatch", "moe_dispatch_backward", "moe_combine",
+           "moe_combine_backward", "moe_quantize_blocks", "moe_block_matmul", "moe_block_matmul_grouped")
 MOE_QUANT_WORKSPACE_BYTES = 8192
 MOE_WORKSPACE_SCALES_OFFSET = 4096
 MOE_NOALLOC_SCRATCH_BYTES = 64 << 20
@@ -55,6 +56,12 @@ class moe_kv_cache(ctypes.Structure):
 class moe_kv_batch(ctypes.Structure):
     _fields_ = ([(n, ctypes.c_void_p) for n in ("cu_q", "kv_lens", "block_table")] +
                 [(n, ctypes.c_int32) for n in ("B", "T", "max_pages")])
+
+
+class moe_alignment(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_void_p) for n in ("sorted_pair_ids", "block_expert_ids", "expert_offsets", "pair_pos",
+                                                "num_padded")] +
+                [(n, ctypes.c_int32) for n in ("M", "topk", "E", "block_m", "rows")])
 
 
 _lib = None
@@ -118,6 +125,17 @@ def lib():
         L.moe_paged_attention_workspace_size.argtypes = [ctypes.POINTER(moe_kv_cache), i32, i32, i32, i32,
                                                          ctypes.POINTER(sz)]
         L.moe_paged_attention_workspace_size.restype = ctypes.c_int
+        al = ctypes.POINTER(moe_alignment)
+        L.moe_dispatch.argtypes = [al, vp, i32, i64, i32, vp, vp, i32, i64, vp]
+        L.moe_dispatch_backward.argtypes = [al, vp, i32, i64, i32, vp, i64, vp, vp, i32, i64, vp, vp]
+        L.moe_combine.argtypes = [al, vp, i32, i64, i32, vp, vp, i32, i64, vp]
+        L.moe_combine_backward.argtypes = [al, vp, i32, i64, i32, vp, i64, vp, vp, i32, i64, vp, vp]
+        L.moe_quantize_blocks.argtypes = [vp, i32, i64, i32, i32, i32, i32, vp, vp, vp, i64, i64, vp]
+        L.moe_block_matmul.argtypes = [vp, i64, vp, i64, i64, vp, vp, i32, i32, i32, vp, i32, i64, vp]
+        L.moe_block_matmul_grouped.argtypes = [al, vp, i64, i32, vp, i64, i64, vp, vp, i32, i32, i32, vp, i32, i64, vp]
+        for f in (L.moe_dispatch, L.moe_dispatch_backward, L.moe_combine, L.moe_combine_backward,
+                  L.moe_quantize_blocks, L.moe_block_matmul, L.moe_block_matmul_grouped):
+            f.restype = ctypes.c_int
         _lib = L
     return _lib
 
@@ -562,6 +580,238 @@ def moe_fused_forward_persistent(problem, x, w13, w2, topk_weights, alignment, o
         _ptr(alignment.pair_pos), _ptr(alignment.num_padded), _ptr(out), _ptr(workspace),
         workspace.numel() * workspace.element_size(), _ptr(sync),
         sync.numel() * sync.element_size(), _stream(stream)))
+    return out
+
+
+def _rows(t, shape, name, device):
+    """(address, dtype code, row stride) of a [rows, values] tensor of this shape
+    (None: any size) on `device`, the values of a row contiguous."""
+    code = _VALUE_CODES.get(t.dtype)
+    if code is None:
+        raise MoEError(MOE_ERR_DTYPE, f"{name} must be bf16 or f32, not {t.dtype}")
+    if t.dim() != 2 or any(w is not None and w != n for w, n in zip(shape, t.shape)):
+        raise MoEError(MOE_ERR_SHAPE, f"{name} has shape {tuple(t.shape)}, not {tuple(shape)}")
+    st, sv = t.stride()
+    if sv != 1 and t.size(1) > 1:
+        raise MoEError(MOE_ERR_UNSUPPORTED, f"{name}: the values of a row must be contiguous")
+    if t.device != device:
+        raise MoEError(MOE_ERR_UNSUPPORTED, f"{name} is on {t.device}, not on {device}")
+    return t.data_ptr(), code, st if t.size(0) > 1 else t.size(1)
+
+
+def _pairs_f32(t, shape, name, device):
+    """Address of a dense f32 tensor of this shape on `device` (None: None)."""
+    if t is None:
+        return None
+    if t.dtype is not torch.float32:
+        raise MoEError(MOE_ERR_DTYPE, f"{name} must be f32")
+    if t.shape != shape:
+        raise MoEError(MOE_ERR_SHAPE, f"{name} has shape {tuple(t.shape)}, not {tuple(shape)}")
+    if not t.is_contiguous() or t.device != device:
+        raise MoEError(MOE_ERR_UNSUPPORTED, f"{name} must be contiguous and on {device}")
+    return t.data_ptr()
+
+
+def _alignment(al, M, topk, E, device):
+    """The moe_alignment of M tokens and topk pairs a token over al's tensors."""
+    ids = _index(al.sorted_pair_ids, 1, None, "sorted_pair_ids", device)
+    pos = _index(al.pair_pos, 1, None, "pair_pos", device)
+    rows, bm = al.sorted_pair_ids.size(0), al.block_m
+    if al.pair_pos.size(0) < M * topk:
+        raise MoEError(MOE_ERR_SHAPE, f"pair_pos of {al.pair_pos.size(0)} pairs for {M} x {topk}")
+    if bm < 1 or al.block_expert_ids.numel() * bm < rows:
+        raise MoEError(MOE_ERR_SHAPE, f"block_expert_ids of {al.block_expert_ids.numel()} blocks for {rows} rows")
+    if E is not None and al.expert_offsets.numel() != E + 1:
+        raise MoEError(MOE_ERR_SHAPE, f"expert_offsets of {al.expert_offsets.numel()} for {E} experts")
+    return moe_alignment(ids, _index(al.block_expert_ids, 1, None, "block_expert_ids", device),
+                         _index(al.expert_offsets, 1, None, "expert_offsets", device), pos,
+                         _index(al.num_padded, 1, 1, "num_padded", device), M, topk, E or 0, bm, rows)
+
+
+def moe_dispatch(x, alignment, topk, weights=None, out=None, out_dtype=None, stream=None):
+    """x [M, K] bf16/f32 into expert order: rows [rows, K], rows[place of pair] =
+    weight * token; weights f32 [M, topk] or None (1).  Rows of padding are zero,
+    those from num_padded on as they were (in a new tensor: anything)."""
+    dev = x.device
+    xp, xc, xs = _rows(x, (None, None), "x", dev)
+    M, K = x.shape
+    al = _alignment(alignment, M, topk, None, dev)
+    wp = _pairs_f32(weights, (M, topk), "weights", dev)
+    if out is None:
+        out = _made(x, (al.rows, K), out_dtype, stream)
+    op, oc, os_ = _rows(out, (al.rows, K), "out", dev)
+    _run(dev, stream, lib().moe_dispatch, ctypes.byref(al), xp, xc, xs, K, wp, op, oc, os_)
+    return out
+
+
+def moe_dispatch_backward(d_rows, alignment, M, topk, x=None, weights=None, out=None, out_dtype=None, stream=None):
+    """The gradient of moe_dispatch: d_rows [rows, K] -> (dx [M, K], d_weights f32
+    [M, topk], or None without x, which only they need)."""
+    dev = d_rows.device
+    al = _alignment(alignment, M, topk, None, dev)
+    rp, rc, rs = _rows(d_rows, (al.rows, None), "d_rows", dev)
+    K = d_rows.size(1)
+    wp = _pairs_f32(weights, (M, topk), "weights", dev)
+    xp, xc, xs, dw = None, None, 0, None
+    if x is not None:
+        xp, xc, xs = _rows(x, (M, K), "x", dev)
+        dw = _made(d_rows, (M, topk), torch.float32, stream)
+    if out is None:
+        out = _made(d_rows, (M, K), out_dtype or (None if x is None else x.dtype), stream)
+    op, oc, os_ = _rows(out, (M, K), "out", dev)
+    if xc is not None and xc != oc:
+        raise MoEError(MOE_ERR_DTYPE, f"x is {x.dtype}, its gradient {out.dtype}")
+    _run(dev, stream, lib().moe_dispatch_backward, ctypes.byref(al), rp, rc, rs, K, xp, xs, wp, op, oc, os_,
+         None if dw is None else dw.data_ptr())
+    return out, dw
+
+
+def moe_combine(rows, alignment, M, topk, weights=None, out=None, out_dtype=None, stream=None):
+    """rows [rows, K] bf16/f32 in expert order back to tokens: out [M, K], out[t] =
+    the sum of weight * row over the token's pairs; weights as in moe_dispatch."""
+    dev = rows.device
+    al = _alignment(alignment, M, topk, None, dev)
+    rp, rc, rs = _rows(rows, (al.rows, None), "rows", dev)
+    K = rows.size(1)
+    wp = _pairs_f32(weights, (M, topk), "weights", dev)
+    if out is None:
+        out = _made(rows, (M, K), out_dtype, stream)
+    op, oc, os_ = _rows(out, (M, K), "out", dev)
+    _run(dev, stream, lib().moe_combine, ctypes.byref(al), rp, rc, rs, K, wp, op, oc, os_)
+    return out
+
+
+def moe_combine_backward(d_out, alignment, topk, rows=None, weights=None, out=None, out_dtype=None, stream=None):
+    """The gradient of moe_combine: d_out [M, K] -> (d_rows [rows, K], d_weights f32
+    [M, topk], or None without rows, which only they need)."""
+    dev = d_out.device
+    gp, gc, gs = _rows(d_out, (None, None), "d_out", dev)
+    M, K = d_out.shape
+    al = _alignment(alignment, M, topk, None, dev)
+    wp = _pairs_f32(weights, (M, topk), "weights", dev)
+    rp, rc, rs, dw = None, None, 0, None
+    if rows is not None:
+        rp, rc, rs = _rows(rows, (al.rows, K), "rows", dev)
+        dw = _made(d_out, (M, topk), torch.float32, stream)
+    if out is None:
+        out = _made(d_out, (al.rows, K), out_dtype or (None if rows is None else rows.dtype), stream)
+    op, oc, os_ = _rows(out, (al.rows, K), "out", dev)
+    if rc is not None and rc != oc:
+        raise MoEError(MOE_ERR_DTYPE, f"rows are {rows.dtype}, their gradient {out.dtype}")
+    _run(dev, stream, lib().moe_combine_backward, ctypes.byref(al), gp, gc, gs, K, rp, rs, wp, op, oc, os_,
+         None if dw is None else dw.data_ptr())
+    return out, dw
+
+
+_CODES = (torch.float8_e4m3fn, torch.uint8)
+
+
+def moe_quantize_blocks(x, gated=False, block_rows=1, num_rows=None, codes=None, scales=None, stream=None):
+    """x bf16/f32 [M, K] (gated: [M, 2K], the values are SiLU(gate) * up) -> E4M3
+    codes [M, K] and f32 scales, one per row and 128 values: [M, blocks], by
+    default the rows of a block side by side (scales.stride(0) == 1); block_rows
+    128: one per 128 x 128 block, [row blocks, blocks] dense, and x may be [E, N,
+    K], expert by expert.  num_rows int32 [1]: rows from there on are left alone."""
+    dev = x.device
+    if x.dim() == 3:
+        if block_rows != 128:
+            raise MoEError(MOE_ERR_SHAPE, "x of three dimensions needs block_rows 128")
+        E, N, K = x.shape
+        if codes is None:
+            codes = _made(x, (E, N, K), torch.float8_e4m3fn, stream)
+        if scales is None:
+            scales = _made(x, (E, -(-N // 128), -(-K // 128)), torch.float32, stream)
+        for e in range(E):
+            moe_quantize_blocks(x[e], gated, 128, num_rows, codes[e], scales[e], stream)
+        return codes, scales
+    xp, xc, xs = _rows(x, (None, None), "x", dev)
+    M, K = x.size(0), x.size(1) // 2 if gated else x.size(1)
+    SR, SB = -(-M // max(block_rows, 1)), -(-K // 128)
+    if gated and x.size(1) % 2:
+        raise MoEError(MOE_ERR_SHAPE, f"gated x has {x.size(1)} values a row")
+    if codes is None:
+        codes = _made(x, (M, K), torch.float8_e4m3fn, stream)
+    elif codes.dtype not in _CODES:
+        raise MoEError(MOE_ERR_DTYPE, f"codes are {codes.dtype}")
+    elif codes.shape != (M, K) or not codes.is_contiguous() or codes.device != dev:
+        raise MoEError(MOE_ERR_SHAPE, f"codes must be a dense {(M, K)} on {dev}")
+    if scales is None:
+        scales = _made(x, (SB, SR), torch.float32, stream).t() if block_rows == 1 else _made(x, (SR, SB), torch.float32, stream)
+    sp, sr, sb = _scales(scales, SR, SB, "scales", dev)
+    np_ = None if num_rows is None else _index(num_rows, 1, 1, "num_rows", dev)
+    _run(dev, stream, lib().moe_quantize_blocks, xp, xc, xs, M, K, 1 if gated else 0, block_rows, np_, codes.data_ptr(),
+         sp, sr, sb)
+    return codes, scales
+
+
+def _scales(t, rows, blocks, name, device):
+    """(address, row stride, block stride) of f32 scales [rows, blocks]."""
+    if t.dtype is not torch.float32:
+        raise MoEError(MOE_ERR_DTYPE, f"{name} must be f32")
+    if t.shape != (rows, blocks):
+        raise MoEError(MOE_ERR_SHAPE, f"{name} have shape {tuple(t.shape)}, not {(rows, blocks)}")
+    if t.device != device:
+        raise MoEError(MOE_ERR_UNSUPPORTED, f"{name} are on {t.device}, not on {device}")
+    sr, sb = t.stride()
+    # the strides of a dimension of size one are torch's to choose
+    return t.data_ptr(), sr if rows > 1 else 1, sb if blocks > 1 else 1
+
+
+def _codes(t, name, device):
+    if t.dtype not in _CODES:
+        raise MoEError(MOE_ERR_DTYPE, f"{name} must be E4M3 codes, not {t.dtype}")
+    if t.device != device:
+        raise MoEError(MOE_ERR_UNSUPPORTED, f"{name} is on {t.device}, not on {device}")
+    return t.data_ptr()
+
+
+def _block_operands(a, a_scales, w, w_scales, dims):
+    dev = a.device
+    if a.dim() != 2 or w.dim() != dims or w.size(-1) != a.size(1):
+        raise MoEError(MOE_ERR_SHAPE, f"a has shape {tuple(a.shape)}, w {tuple(w.shape)}")
+    M, K = a.shape
+    B = -(-K // 128)
+    if a.stride(1) != 1 or not w.is_contiguous() or not w_scales.is_contiguous():
+        raise MoEError(MOE_ERR_UNSUPPORTED, "the codes of a row must be contiguous, w and w_scales dense")
+    want = (*w.shape[:-2], -(-w.size(-2) // 128), B)
+    if w_scales.dtype is not torch.float32 or w_scales.shape != want or w_scales.device != dev:
+        raise MoEError(MOE_ERR_SHAPE, f"w_scales must be f32 {want} on {dev}")
+    return (_codes(a, "a", dev), a.stride(0) if M > 1 else K, _scales(a_scales, M, B, "a_scales", dev),
+            _codes(w, "w", dev), w_scales.data_ptr())
+
+
+def _block_out(a, rows, N, out, out_dtype, stream):
+    if out is None:
+        out = _made(a, (rows, N), out_dtype, stream)
+    return (out, *_rows(out, (rows, N), "out", a.device))
+
+
+def moe_block_matmul(a, a_scales, w, w_scales, out=None, out_dtype=torch.bfloat16, stream=None):
+    """a [M, K] and w [N, K] of E4M3 codes, a_scales f32 [M, ceil(K / 128)] (any
+    strides), w_scales f32 [ceil(N / 128), ceil(K / 128)] -> out [M, N]."""
+    ap, ast, (sp, sr, sb), wp, wsp = _block_operands(a, a_scales, w, w_scales, 2)
+    out, op, oc, os_ = _block_out(a, a.size(0), w.size(0), out, out_dtype, stream)
+    _run(a.device, stream, lib().moe_block_matmul, ap, ast, sp, sr, sb, wp, wsp, a.size(0), w.size(0), a.size(1), op, oc,
+         os_)
+    return out
+
+
+def moe_block_matmul_grouped(a, a_scales, w, w_scales, alignment, topk=None, M=None, out=None,
+                             out_dtype=torch.bfloat16, stream=None):
+    """The rows of an alignment times their experts' weights w [E, N, K], w_scales
+    f32 [E, ceil(N / 128), ceil(K / 128)] -> out [rows, N].  With topk, a holds
+    tokens (M of them; default: all) and a place reads its pair's token; without,
+    a [rows, K] is in expert order.  Padding rows are zero, those from num_padded
+    on as they were (in a new tensor: anything)."""
+    ap, ast, (sp, sr, sb), wp, wsp = _block_operands(a, a_scales, w, w_scales, 3)
+    E, N, K = w.shape
+    if topk is None:
+        al = _alignment(alignment, alignment.pair_pos.size(0), 1, E, a.device)
+    else:
+        al = _alignment(alignment, a.size(0) if M is None else M, topk, E, a.device)
+    out, op, oc, os_ = _block_out(a, al.rows, N, out, out_dtype, stream)
+    _run(a.device, stream, lib().moe_block_matmul_grouped, ctypes.byref(al), ap, ast, a.size(0), sp, sr, sb, wp, wsp, N, K,
+         0 if topk is None else 1, op, oc, os_)
     return out
 
 
