@@ -11,8 +11,12 @@
 //
 // Operands come through a two-stage LDS ring by direct-to-LDS loads, 128
 // bytes of each row a stage, both scales with them.  Row r's 16-byte column
-// c lies at physical column (c + (r >> 1)) mod 8.
+// c lies at physical column c ^ (r / 2) mod 8: the fragment reads (lane l row
+// l mod 32) find every bank once.
+#include <algorithm>
+
 #include "block_gemm.hpp"
+#include "block_load.hpp"
 #include "common.hpp"
 #include "launch.hpp"
 
@@ -23,142 +27,300 @@ struct BTile {
   static constexpr int kWaves = WN * WM;
   static constexpr int NI = TN / WN / 16, MJ = TM / WM / 16;  // blocks of 16 of a wave
   static constexpr int WLoads = TN / 8 / kWaves, ALoads = TM / 8 / kWaves;  // ring loads of a wave (8 rows each)
+  static constexpr int Loads = WLoads + ALoads + 1;                         // and one of scales
   static constexpr int kCodes = (TN + TM) * 128;
   static constexpr int kStage = kCodes + (TM + 64) * 4;  // codes, scales of the rows of a, of the weight blocks
   static_assert(TN % (8 * kWaves) == 0 && TM % (8 * kWaves) == 0, "whole loads");
   static_assert(128 % (TN / WN) == 0, "a wave's weight rows share their scale");
-  static_assert(TM % 64 == 0 && TM / 64 <= kWaves, "whole loads of the rows' scales");
+  static_assert(TM % 64 == 0 && TM / 64 < kWaves, "a wave for 64 rows' scales, and one more");
+  static_assert(NI % 2 == 0, "two operands of weights in turn");
 };
 
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t b_rsrc(const void* base, uint32_t bytes) {
-  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), (short)0, (int)bytes, 0x00020000);
-}
-__device__ __forceinline__ void b_dma16(__amdgpu_buffer_rsrc_t r, char* dst, uint32_t voff, uint32_t soff) {
-  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)dst, 16, voff, soff, 0, 0);
-}
-__device__ __forceinline__ void b_dma4(__amdgpu_buffer_rsrc_t r, char* dst, uint32_t voff) {
-  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)dst, 4, voff, 0, 0, 0);
+// Tile number blockIdx.x: the workgroups of an XCD (dealt out round-robin) take
+// consecutive tiles, in groups of kGroup spans times all of N, so that the rows
+// and weights that they share meet in that XCD's L2.
+constexpr int kGroup = 4;
+template <int TM>
+__device__ __forceinline__ bool b_tile(const BlockGemmArgs& g, int ntn, int& span, int& nt) {
+  int spans;
+  if (!g.ids) {
+    spans = (g.M + TM - 1) / TM;
+  } else {
+    const int n = min(*g.num_padded, g.R), step = g.bm >= TM ? TM : g.bm;
+    spans = (n + step - 1) / step;
+  }
+  const int total = spans * ntn;
+  if ((int)blockIdx.x >= total) return false;
+  const int xcd = blockIdx.x % 8, per = total / 8, rem = total % 8;
+  const int t = xcd * per + min(xcd, rem) + (int)blockIdx.x / 8;
+  const int grp = t / (kGroup * ntn), r = t % (kGroup * ntn), gs = min(kGroup, spans - grp * kGroup);
+  span = grp * kGroup + r % gs;
+  nt = r / gs;
+  return true;
 }
 
-constexpr uint32_t kNowhere = 0x80000000u;  // past every buffer here: such a load gives zeros
-
-template <int TN, int TM, int WN, int WM, int OT>
+template <int TN, int TM, int WN, int WM, int STAGES, int OT, bool MOVED>
 __global__ __launch_bounds__(WN * WM * 64) void block_gemm_kernel(BlockGemmArgs g, int ntn) {
   using B = BTile<TN, TM, WN, WM>;
-  constexpr int NI = B::NI, MJ = B::MJ;
+  constexpr int NI = B::NI, MJ = B::MJ, S = NI * MJ;
+  constexpr int LAG = 2, RING = 4;  // a step's sums are added LAG steps later
+  static_assert(S % RING == 0 && LAG < RING, "sums of a block's last steps are found by the next block");
+  constexpr bool WIDE = OT == DT_F32;
   __shared__ __attribute__((aligned(16))) char stage0[B::kStage];
   __shared__ __attribute__((aligned(16))) char stage1[B::kStage];
+  __shared__ __attribute__((aligned(16))) char stage2[STAGES > 2 ? B::kStage : 16];
+  __shared__ __attribute__((aligned(16))) char stage3[STAGES > 2 ? B::kStage : 16];
+  static_assert(STAGES == 2 || STAGES == 4, "fragments and scales take turns with every block");
+  static_assert((STAGES - 1) * B::Loads < 64, "counted waits");
   const int lane = threadIdx.x & 63;
   const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wn = wv % WN, wm = wv / WN;
   const int l16 = lane & 15, grp = lane >> 4;
 
-  const RowSpan s = row_span<TM>(g, blockIdx.x / ntn);
+  int span, nt;
+  if (!b_tile<TM>(g, ntn, span, nt)) return;
+  const RowSpan s = row_span<TM>(g, span);
   if (s.rows <= 0) return;
-  const int n0 = (int)(blockIdx.x % ntn) * TN;
+  const int n0 = nt * TN;
 
-  // sources.  Weight rows past N and rows of a past the span lie past their
-  // buffers; the columns past K of a last, partial block are sent there
-  const int nrows = min(TN, g.N - n0);
-  const auto wres = b_rsrc(g.w + ((size_t)s.e * g.N + n0) * g.K, (uint32_t)nrows * g.K);
-  const bool moved = g.ids && g.topk;  // rows of a come from anywhere
-  const uint8_t* abase = moved ? g.a : g.a + (size_t)s.row0 * g.a_stride;
-  const float* asbase = moved ? g.as : g.as + (size_t)s.row0 * g.as_m;
-  const int arows = moved ? g.M : s.rows;
-  const uint32_t abytes = (uint32_t)((size_t)(arows - 1) * g.a_stride + g.K);
-  const auto ares = b_rsrc(abase, abytes);
-  const float* wsbase = g.ws + (size_t)s.e * g.NB * g.KB;
-
-  // this wave's loads: lane l takes row l / 8 of eight, physical column l mod 8
-  uint32_t woff[B::WLoads], aoff[B::ALoads];
+  // Sources.  A load takes eight rows, lane l 16-byte column l mod 8 of row l / 8
+  // as they will lie in LDS; its buffer ends with the last real row of this
+  // wave's, and the columns past K of a last, partial block are sent past every
+  // buffer.
+  const int nrows = min(TN, g.N - n0), w0 = wv * B::WLoads * 8, a0 = wv * B::ALoads * 8;
+  const uint8_t* wbase = g.w + ((size_t)s.e * g.N + n0 + w0) * g.K;
+  const uint32_t wbytes = (uint32_t)max(nrows - w0, 0) * g.K;
+  const uint8_t* abase = MOVED ? g.a : g.a + (size_t)(s.row0 + a0) * g.a_stride;
+  const uint32_t abytes = MOVED         ? (uint32_t)((size_t)(g.M - 1) * g.a_stride + g.K)
+                          : s.rows > a0 ? (uint32_t)((s.rows - a0 - 1) * g.a_stride + g.K)
+                                        : 0u;
+  auto lcol = [&](int odd) { return ((lane ^ (lane >> 4) ^ (4 * odd)) & 7) * 16; };  // of row blocks 2 q + odd
+  uint32_t woff[2], aoff[MOVED ? B::ALoads : 2];
 #pragma unroll
-  for (int q = 0; q < B::WLoads; ++q) {
-    const int r = (wv * B::WLoads + q) * 8 + (lane >> 3);
-    woff[q] = r < nrows ? (uint32_t)r * g.K + (((lane & 7) - (r >> 1)) & 7) * 16 : kNowhere;
-  }
-#pragma unroll
-  for (int q = 0; q < B::ALoads; ++q) {
-    const int r = (wv * B::ALoads + q) * 8 + (lane >> 3);
-    int at = r < s.rows ? source_row(g, s.row0 + r) : -1;
-    if (at >= 0 && !moved) at = r;
-    aoff[q] = at >= 0 ? (uint32_t)(at * g.a_stride) + (((lane & 7) - (r >> 1)) & 7) * 16 : kNowhere;
-  }
-  // scales: wave q takes rows 64 q .. of the tile (any row's where there is
-  // none: its products are not kept), the last wave the weight blocks'
-  uint32_t soff = 0;
-  if (wv * 64 < TM) {
-    const int r = min(wv * 64 + lane, s.rows - 1);
-    int at = max(source_row(g, s.row0 + r), 0);
-    if (!moved) at = r;
-    soff = (uint32_t)(at * g.as_m) * 4;
-  }
-  const uint32_t wsoff = (uint32_t)min(n0 / 128 + lane, g.NB - 1) * g.KB * 4;
-
-  auto fetch = [&](int b, char* stage) {
-    const uint32_t k = (uint32_t)b * 128;
-    const bool cut = (int)k + 128 > g.K;
-#pragma unroll
-    for (int q = 0; q < B::WLoads; ++q) {
-      const int r = (wv * B::WLoads + q) * 8 + (lane >> 3);
-      const bool past = cut && (int)k + (int)((((lane & 7) - (r >> 1)) & 7) * 16) >= g.K;
-      b_dma16(wres, stage + (wv * B::WLoads + q) * 1024, past ? kNowhere : woff[q], k);
-    }
+  for (int q = 0; q < 2; ++q) woff[q] = (uint32_t)(lane >> 3) * g.K + lcol(q);
+  if constexpr (MOVED) {
 #pragma unroll
     for (int q = 0; q < B::ALoads; ++q) {
-      const int r = (wv * B::ALoads + q) * 8 + (lane >> 3);
-      const bool past = cut && (int)k + (int)((((lane & 7) - (r >> 1)) & 7) * 16) >= g.K;
-      b_dma16(ares, stage + TN * 128 + (wv * B::ALoads + q) * 1024, past ? kNowhere : aoff[q], k);
+      const int r = a0 + q * 8 + (lane >> 3);
+      const int at = r < s.rows ? source_row(g, s.row0 + r) : -1;
+      aoff[q] = at >= 0 ? (uint32_t)(at * g.a_stride) + lcol((wv * B::ALoads + q) & 1) : kNowhere;
     }
-    if (wv * 64 < TM) b_dma4(b_rsrc(asbase + (long long)b * g.as_b, 0xffffffffu), stage + B::kCodes + wv * 256, soff);
-    if (wv == B::kWaves - 1) b_dma4(b_rsrc(wsbase + b, 0xffffffffu), stage + B::kCodes + TM * 4, wsoff);
+  } else {
+#pragma unroll
+    for (int q = 0; q < 2; ++q) aoff[q] = (uint32_t)((lane >> 3) * g.a_stride) + lcol(q);
+  }
+  // scales: wave q takes rows 64 q .. of the tile (any row's where there is
+  // none: its products are not kept), the waves behind these the weight blocks'
+  const bool rowscales = wv < TM / 64;
+  uint32_t soff;
+  if (rowscales) {
+    int r = min(wv * 64 + lane, s.rows - 1);
+    if (MOVED) r = max(source_row(g, s.row0 + r), 0);
+    soff = (uint32_t)(r * g.as_m) * 4;
+  } else {
+    soff = (uint32_t)min(n0 / 128 + lane, g.NB - 1) * g.KB * 4;
+  }
+  const float* sbase = rowscales ? (MOVED ? g.as : g.as + (size_t)s.row0 * g.as_m) : g.ws + (size_t)s.e * g.NB * g.KB;
+  const long long sstep = rowscales ? g.as_b : 1;
+  const int sdst = B::kCodes + (rowscales ? wv * 256 : TM * 4);
+
+  // Load v of block b into a stage; of blocks past the last one, nothing (the
+  // buffer is empty).  A buffer's end holds for both offsets together.
+  auto load = [&](auto vc, int b, char* stage) {
+    constexpr int v = decltype(vc)::value;
+    const int k = b * 128;
+    const bool real = b < g.KB;
+    if constexpr (v < B::WLoads) {
+      const int blk = wv * B::WLoads + v, odd = B::WLoads % 2 ? blk & 1 : v & 1;
+      const uint32_t cut = k + lcol(odd) >= g.K ? kNowhere : 0u;
+      b_dma16(b_rsrc(wbase, real ? wbytes : 0u), stage + blk * 1024, (odd ? woff[1] : woff[0]) | cut, v * 8 * g.K + k);
+    } else if constexpr (v < B::WLoads + B::ALoads) {
+      constexpr int q = v - B::WLoads;
+      const int blk = wv * B::ALoads + q, odd = B::ALoads % 2 ? blk & 1 : q & 1;
+      const uint32_t cut = k + lcol(odd) >= g.K ? kNowhere : 0u;
+      const auto res = b_rsrc(abase, real ? abytes : 0u);
+      char* dst = stage + TN * 128 + blk * 1024;
+      if constexpr (MOVED)
+        b_dma16(res, dst, aoff[q] | cut, k);
+      else
+        b_dma16(res, dst, (odd ? aoff[1] : aoff[0]) | cut, q * 8 * (int)g.a_stride + k);
+    } else {
+      b_dma4(b_rsrc(sbase + (long long)b * sstep, real ? kMost : 0u), stage + sdst, soff);
+    }
   };
+
+  // which waves have real rows of a; where none has, there is nothing to multiply
+  bool some = !g.ids, busy = !g.ids;
+  if (g.ids) {
+#pragma unroll
+    for (int q = 0; q < TM / 64; ++q) {
+      const int r = q * 64 + lane;
+      const uint64_t real = __ballot(r < s.rows && source_row(g, s.row0 + r) >= 0);
+      some |= real != 0;
+      constexpr int W = TM / WM;  // a wave's rows: whole multiples of 64, or a part
+      if (W >= 64 ? (q * 64) / W == wm : q == wm * W / 64)
+        busy |= W >= 64 ? real != 0 : (real >> (wm * W % 64) & ((1ull << (W % 64)) - 1)) != 0;
+    }
+  }
+  if (!some) {
+    zero_rows<OT>(g, s, n0, TN, WN * WM * 64);
+    return;
+  }
 
   f32x4 acc[NI][MJ] = {};
   const int nb = (TN / WN) * wn, mb = (TM / WM) * wm;  // this wave's first rows
-  auto multiply = [&](const char* stage) {
+  const int wsat = TM + (n0 % 128 + nb) / 128;
+  BOperand16<WIDE> af[2], bf[2][MJ];
+  float sc[2][MJ] = {};
+  f32x4 t[RING] = {};
+  // a lane's codes of row l16: 16-byte columns grp and 4 + grp
+  const int f0 = l16 * 128 + ((grp ^ (l16 >> 1)) & 7) * 16;
+  const int fa = nb * 128 + f0, fb = (TN + mb) * 128 + f0;
+  auto read_a = [&](int i, const char* stage, BOperand16<WIDE>& o) {
+    const char* p = stage + 16 * i * 128;
+    o.set(ld16(p + fa), ld16(p + (fa ^ 64)));
+  };
+  auto read_b = [&](int j, const char* stage, BOperand16<WIDE>& o) {
+    const char* p = stage + 16 * j * 128;
+    o.set(ld16(p + fb), ld16(p + (fb ^ 64)));
+  };
+  auto read_s = [&](const char* stage, float (&o)[MJ]) {
     const float* as = reinterpret_cast<const float*>(stage + B::kCodes);
-    const float ws = as[TM + (n0 % 128 + nb) / 128];
-    BOperand<OT == DT_F32> bf[MJ];
-    float sc[MJ];
+    const float ws = as[wsat];
+#pragma unroll
+    for (int j = 0; j < MJ; ++j) o[j] = as[mb + 16 * j + l16] * ws;
+  };
+  // Block b, in stage cur (P: its parity).  Its steps are an MFMA each, the
+  // additions of LAG steps before under it.  The wave's reads of cur end a row
+  // block before its products do; there, behind a barrier that all of block
+  // b + 1 (in nxt) has landed for, cur is free for block b + STAGES and the first
+  // fragments of block b + 1 are read under the last products.  The loads into
+  // the stage of block b - 1 (prv), begun behind its barrier, end here, spread
+  // out: a bunch of them would hold up the wave's MFMAs at the issue.
+  constexpr int EARLY = B::Loads - (S - MJ) > 2 ? B::Loads - (S - MJ) : 2;
+  constexpr int GAP = (S - MJ) / (B::Loads - EARLY) >= 2 ? 2 : 1;
+  static_assert((B::Loads - EARLY - 1) * GAP < S - MJ, "all loads of a block come before its barrier");
+  auto add = [&](auto qc, float f) {  // the sums of step q, of this block or the last
+    constexpr int q = (decltype(qc)::value + S) % S;
+#pragma unroll
+    for (int v = 0; v < 4; ++v)
+      acc[q / MJ][q % MJ][v] = __builtin_fmaf(t[q % RING][v], f, acc[q / MJ][q % MJ][v]);
+  };
+  auto block = [&](auto par, int b, char* cur, char* nxt, char* prv) {
+    constexpr int P = decltype(par)::value;
+    b_for<0, S>([&](auto qc) {
+      constexpr int q = decltype(qc)::value, i = q / MJ, j = q % MJ;
+      if constexpr (q == S - MJ) {
+        b_wait_vmcnt<(STAGES - 2) * B::Loads>();
+        b_barrier();
+        read_s(nxt, sc[P ^ 1]);
+      }
+      t[q % RING] = block_sums16(af[i & 1], bf[P][j]);
+      if constexpr (j == 0 && i + 1 < NI) read_a(i + 1, cur, af[(i + 1) & 1]);
+      if constexpr (i == NI - 1) {
+        if constexpr (j == 0) read_a(0, nxt, af[0]);
+        read_b(j, nxt, bf[P ^ 1][j]);
+        b_for<j * EARLY / MJ, (j + 1) * EARLY / MJ>([&](auto v) { load(v, b + STAGES, cur); });
+      } else if constexpr (q % GAP == 0 && q / GAP < B::Loads - EARLY) {
+        load(std::integral_constant<int, EARLY + q / GAP>{}, b + STAGES - 1, prv);
+      }
+      constexpr int d = (q + S - LAG) % S;
+      add(std::integral_constant<int, d>{}, q >= LAG ? sc[P][d % MJ] : sc[P ^ 1][d % MJ]);
+      __builtin_amdgcn_sched_barrier(0);
+    });
+  };
+
+  constexpr int kAhead = (STAGES - 2) * B::Loads + EARLY;  // loads behind block 0's
+  b_for<0, B::Loads>([&](auto v) { load(v, 0, stage0); });
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_sched_barrier(0);
+  if constexpr (STAGES > 2) {
+    b_for<0, B::Loads>([&](auto v) { load(v, 1, stage1); });
+    b_for<0, B::Loads>([&](auto v) { load(v, 2, stage2); });
+  }
+  b_for<0, EARLY>([&](auto v) { load(v, STAGES - 1, STAGES > 2 ? stage3 : stage1); });
+  b_wait_vmcnt<kAhead>();  // block 0
+  b_barrier();
+  read_s(stage0, sc[0]);
+  read_a(0, stage0, af[0]);
+#pragma unroll
+  for (int j = 0; j < MJ; ++j) read_b(j, stage0, bf[0][j]);
+  const std::integral_constant<int, 0> even{};
+  const std::integral_constant<int, 1> odd{};
+  int b = 0;
+  if (!busy) {  // none of this wave's rows of a is real: it loads and keeps the barriers
+    b_for<EARLY, B::Loads>([&](auto v) { load(v, STAGES - 1, STAGES > 2 ? stage3 : stage1); });
+    for (; b < g.KB; ++b) {
+      b_wait_vmcnt<(STAGES - 2) * B::Loads>();
+      b_barrier();
+      char* const cur = b % STAGES == 0 ? stage0 : b % STAGES == 1 ? stage1 : b % STAGES == 2 ? stage2 : stage3;
+      b_for<0, B::Loads>([&](auto v) { load(v, b + STAGES, cur); });
+    }
+    b_wait_vmcnt<0>();
+  }
+  // whole turns of the ring, then what is left, once: a path from one stage's
+  // block to its own next would make the compiler wait for loads before its reads
+  for (; b + STAGES <= g.KB; b += STAGES) {
+    if constexpr (STAGES == 2) {
+      block(even, b, stage0, stage1, stage1);
+      block(odd, b + 1, stage1, stage0, stage0);
+    } else {
+      block(even, b, stage0, stage1, stage3);
+      block(odd, b + 1, stage1, stage2, stage0);
+      block(even, b + 2, stage2, stage3, stage1);
+      block(odd, b + 3, stage3, stage0, stage2);
+    }
+  }
+  if (b < g.KB) {
+    block(even, b, stage0, stage1, STAGES == 2 ? stage1 : stage3);
+    if constexpr (STAGES > 2) {
+      if (b + 1 < g.KB) {
+        block(odd, b + 1, stage1, stage2, stage0);
+        if (b + 2 < g.KB) block(even, b + 2, stage2, stage3, stage1);
+      }
+    }
+  }
+  b_wait_vmcnt<0>();  // no load may land after the workgroup's LDS is released
+  auto rest = [&](const float (&f)[MJ]) {
+    b_for<S - LAG, S>([&](auto q) { add(q, f[q % MJ]); });
+  };
+  if (g.KB & 1)
+    rest(sc[0]);
+  else
+    rest(sc[1]);
+
+  // Value v of lane l of block (i, j): column 16 i + 4 (l / 16) + v of row
+  // 16 j + l mod 16.  bf16 rows go through this wave's part of LDS (behind a
+  // barrier: the others may still read theirs), 16-byte column c of row r at
+  // c ^ r, so that a store writes whole row pieces of the wave.
+  constexpr int WTN = TN / WN, WTM = TM / WM;
+  b_barrier();
+  if (OT == DT_BF16 && g.vec && n0 + nb + WTN <= g.N) {
+    constexpr int kRowBytes = WTN * 2, kPieces = kRowBytes / 16, kRowsAtOnce = 64 / kPieces;
+    static_assert(WTM * kRowBytes * (B::kWaves / 2) <= B::kStage, "half of the waves in each of two stages");
+    char* mine = (wv < B::kWaves / 2 ? stage0 : stage1) + (wv % (B::kWaves / 2)) * WTM * kRowBytes;
 #pragma unroll
     for (int j = 0; j < MJ; ++j) {
       const int r = mb + 16 * j + l16;
-      const char* p = stage + TN * 128 + r * 128;
-      const i32x4 lo = ld16(p + ((grp + (r >> 1)) & 7) * 16), hi = ld16(p + ((grp + 4 + (r >> 1)) & 7) * 16);
-      bf[j].set(lo, hi);
-      sc[j] = as[r] * ws;
-    }
+      const bool real = r < s.rows && source_row(g, s.row0 + r) >= 0;
 #pragma unroll
-    for (int i = 0; i < NI; ++i) {
-      const int r = nb + 16 * i + l16;
-      const char* p = stage + r * 128;
-      const i32x4 lo = ld16(p + ((grp + (r >> 1)) & 7) * 16), hi = ld16(p + ((grp + 4 + (r >> 1)) & 7) * 16);
-      BOperand<OT == DT_F32> af;
-      af.set(lo, hi);
-#pragma unroll
-      for (int j = 0; j < MJ; ++j) {
-        const f32x4 t = block_sums(af, bf[j]);
-#pragma unroll
-        for (int v = 0; v < 4; ++v) acc[i][j][v] = __builtin_fmaf(t[v], sc[j], acc[i][j][v]);
+      for (int i = 0; i < NI; ++i) {
+        const f32x4 v = real ? acc[i][j] : f32x4{};
+        const int c = (2 * i + (grp >> 1)) ^ (l16 & (kPieces - 1));
+        *reinterpret_cast<uint2*>(mine + (16 * j + l16) * kRowBytes + c * 16 + (grp & 1) * 8) =
+            make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
       }
     }
-  };
-
-  fetch(0, stage0);
-  for (int b = 0; b < g.KB; b += 2) {
-    __builtin_amdgcn_s_waitcnt(0);
-    __syncthreads();
-    if (b + 1 < g.KB) fetch(b + 1, stage1);
-    multiply(stage0);
-    if (b + 1 >= g.KB) break;
-    __builtin_amdgcn_s_waitcnt(0);
-    __syncthreads();
-    if (b + 2 < g.KB) fetch(b + 2, stage0);
-    multiply(stage1);
+    const int c = lane % kPieces;
+#pragma unroll
+    for (int q = 0; q < WTM / kRowsAtOnce; ++q) {
+      const int r = q * kRowsAtOnce + lane / kPieces;
+      const i32x4 v = ld16(mine + r * kRowBytes + (c ^ (r & 15 & (kPieces - 1))) * 16);
+      if (mb + r < s.rows)
+        st16(reinterpret_cast<uint16_t*>(g.out) + (size_t)(s.row0 + mb + r) * g.out_stride + n0 + nb + c * 8, v);
+    }
+    return;
   }
-
-  // value v of lane l of block (i, j): column 16 i + 4 (l / 16) + v of row
-  // 16 j + l mod 16
 #pragma unroll
   for (int j = 0; j < MJ; ++j) {
     const int r = mb + 16 * j + l16;
@@ -166,42 +328,69 @@ __global__ __launch_bounds__(WN * WM * 64) void block_gemm_kernel(BlockGemmArgs 
     const bool real = source_row(g, s.row0 + r) >= 0;
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
-      const f32x4 t = real ? acc[i][j] : f32x4{};
+      const f32x4 v = real ? acc[i][j] : f32x4{};
       const int n = n0 + nb + 16 * i + 4 * grp;
       const size_t at = (size_t)(s.row0 + r) * g.out_stride + n;
       if constexpr (OT == DT_BF16) {
         uint16_t* p = reinterpret_cast<uint16_t*>(g.out) + at;
         if (g.vec && n + 4 <= g.N)
-          *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16x2(t[0], t[1]), pack_bf16x2(t[2], t[3]));
+          *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
         else
-          for (int c = 0; c < 4 && n + c < g.N; ++c) p[c] = (uint16_t)f32_to_bf16_bits(t[c]);
+          for (int c = 0; c < 4 && n + c < g.N; ++c) p[c] = (uint16_t)f32_to_bf16_bits(v[c]);
       } else {
         float* p = reinterpret_cast<float*>(g.out) + at;
         if (g.vec && n + 4 <= g.N)
-          *reinterpret_cast<f32x4*>(p) = t;
+          *reinterpret_cast<f32x4*>(p) = v;
         else
-          for (int c = 0; c < 4 && n + c < g.N; ++c) p[c] = t[c];
+          for (int c = 0; c < 4 && n + c < g.N; ++c) p[c] = v[c];
       }
     }
   }
 }
 
-template <int TN, int TM, int WN, int WM>
-static int block_gemm_launch(const BlockGemmArgs& g, int ot, hipStream_t st) {
+template <int TN, int TM, int WN, int WM, int STAGES, int OT>
+static int block_gemm_launch(const BlockGemmArgs& g, hipStream_t st) {
   BlockGemmArgs c = g;
   int ntn = (g.N + TN - 1) / TN;
   const long long tiles = row_spans(g, TM) * ntn;
   if (tiles * WN * WM * 64 > kMaxThreads) return kTooManyTiles;
   void* args[] = {&c, &ntn};
-  return (int)hipLaunchKernel(ot == DT_BF16 ? (void*)block_gemm_kernel<TN, TM, WN, WM, DT_BF16>
-                                            : (void*)block_gemm_kernel<TN, TM, WN, WM, DT_F32>,
+  return (int)hipLaunchKernel(g.ids && g.topk ? (void*)block_gemm_kernel<TN, TM, WN, WM, STAGES, OT, true>
+                                              : (void*)block_gemm_kernel<TN, TM, WN, WM, STAGES, OT, false>,
                               dim3((unsigned)tiles), dim3(WN * WM * 64), args, 0, st);
 }
 
+// Which kernel: by the workgroups that each makes of the call, against the
+// compute units.  us for N = K = 4096, bf16 out, in a graph:
+//   M            128   256   512  1024  2048  4096
+//   few rows    11.0  17.1  29.2
+//   64 x 64     13.4  13.5  21.9  39.6
+//   64 x 128    18.2  18.0  18.6  33.9
+//   128 x 128   23.9  23.6  23.7  24.4  53.3  99.3   (four stages, one a CU)
+//   128 x 128   32.3  32.0  32.2  32.5  43.4  87.3   (two stages, two a CU)
+//   256 x 256   51.1  52.0  51.2  50.9  52.3  65.2
+// fp32 out (operands twice as wide, half the rate): 64 x 64 17.1 at 1037 x 1544 x
+// 2000 (128 x 128 21.6), 256 x 128 262 at 8192 x 4096 x 4096 (128 x 128 312).
 int launch_block_product(const BlockGemmArgs& g, int ot, hipStream_t st) {
-  const int rows = g.ids ? g.bm : g.M;
-  if (rows <= 64) return launch_block_rows(g, ot, rows, st);
-  return block_gemm_launch<128, 128, 2, 2>(g, ot, st);
+  const long long cu = device_cu_count();
+  // rows of a batch, or of the average expert
+  const long long m = g.ids ? (std::min(g.pairs, g.R) + g.E - 1) / g.E : g.M;
+  auto tiles = [&](int tn, int tm) { return ((long long)g.N + tn - 1) / tn * spans_estimate(g, tm); };
+  if (m <= 64 || tiles(32, 64) <= cu) return launch_block_rows(g, ot, (int)std::min(m, 64LL), st);
+  if (ot == DT_F32) {
+    if (tiles(64, 64) <= 2 * cu) return block_gemm_launch<64, 64, 2, 2, 4, DT_F32>(g, st);
+    if (tiles(128, 128) <= cu) return block_gemm_launch<128, 128, 2, 4, 4, DT_F32>(g, st);
+    return block_gemm_launch<256, 128, 4, 2, 2, DT_F32>(g, st);
+  }
+  if (tiles(64, 64) <= cu) return block_gemm_launch<64, 64, 2, 2, 4, DT_BF16>(g, st);
+  if (tiles(64, 128) <= cu) return block_gemm_launch<64, 128, 2, 2, 4, DT_BF16>(g, st);
+  const long long t = tiles(128, 128);
+  if (t <= cu) return block_gemm_launch<128, 128, 2, 4, 4, DT_BF16>(g, st);
+  // rounds over the chip, in hundredths of the larger tile's
+  const long long last = t % (2 * cu), large = (tiles(256, 256) + cu - 1) / cu * 100;
+  const long long small = t / (2 * cu) * 67 + (last == 0 ? 0 : last <= cu ? 50 : 67);
+  if (small < large) return block_gemm_launch<128, 128, 2, 4, 2, DT_BF16>(g, st);
+  return block_gemm_launch<256, 256, 2, 4, 2, DT_BF16>(g, st);
 }
 
 }  // namespace moe

@@ -51,48 +51,51 @@ typedef int b_i32x8 __attribute__((ext_vector_type(8)));
 typedef __bf16 b_bf16x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 b_bf16x8 __attribute__((ext_vector_type(8)));
 
-// One lane's 32 codes of a block of 128 along K, as an MFMA operand.  E4M3
+// One lane's 32 codes of a block of 128 along K as an MFMA operand.  E4M3
 // instructions add products by groups of eight, aligned to the group's largest
 // and cut below 2^-13 of its power of two (measured): far inside a bf16 result's
-// rounding (2.7e-5 against 1.7e-3), but not an fp32 result's.  For that the
-// codes become bf16, exactly, whose products are added in fp32, at half the rate.
+// rounding (2.7e-5 against 1.7e-3), but not an fp32 result's.  For that (WIDE)
+// the codes become bf16, exactly, whose products are added in fp32, at half the
+// rate (7.7e-8).
 template <bool WIDE>
-struct BOperand;
+struct BOperand16;
 template <>
-struct BOperand<false> {
+struct BOperand16<false> {
   b_i32x8 v;
   __device__ __forceinline__ void set(b_i32x4 lo, b_i32x4 hi) {
     v = b_i32x8{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
   }
 };
+__device__ __forceinline__ void b_widen(b_i32x4 c, b_bf16x8& lo, b_bf16x8& hi) {
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    const b_bf16x2 x = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c[q], 1.0f, false);
+    const b_bf16x2 y = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c[q], 1.0f, true);
+    b_bf16x8& o = q < 2 ? lo : hi;
+    o[4 * (q % 2)] = x[0];
+    o[4 * (q % 2) + 1] = x[1];
+    o[4 * (q % 2) + 2] = y[0];
+    o[4 * (q % 2) + 3] = y[1];
+  }
+}
 template <>
-struct BOperand<true> {
+struct BOperand16<true> {
   b_bf16x8 v[4];
   __device__ __forceinline__ void set(b_i32x4 lo, b_i32x4 hi) {
-#pragma unroll
-    for (int q = 0; q < 8; ++q) {
-      const int c = q < 4 ? lo[q] : hi[q - 4];
-      const b_bf16x2 x = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c, 1.0f, false);
-      const b_bf16x2 y = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c, 1.0f, true);
-      v[q / 2][4 * (q % 2)] = x[0];
-      v[q / 2][4 * (q % 2) + 1] = x[1];
-      v[q / 2][4 * (q % 2) + 2] = y[0];
-      v[q / 2][4 * (q % 2) + 3] = y[1];
-    }
+    b_widen(lo, v[0], v[1]);
+    b_widen(hi, v[2], v[3]);
   }
 };
-
-// The sums of one block of 128 along K, of 16 weight rows and 16 rows of a.
-__device__ __forceinline__ b_f32x4 block_sums(const BOperand<false>& w, const BOperand<false>& a) {
+// The sums of one block, of 16 weight rows and 16 rows of a.
+__device__ __forceinline__ b_f32x4 block_sums16(const BOperand16<false>& w, const BOperand16<false>& a) {
   return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w.v, a.v, b_f32x4{}, 0, 0, 0, 0, 0, 0);
 }
-__device__ __forceinline__ b_f32x4 block_sums(const BOperand<true>& w, const BOperand<true>& a) {
+__device__ __forceinline__ b_f32x4 block_sums16(const BOperand16<true>& w, const BOperand16<true>& a) {
   b_f32x4 t = {};
 #pragma unroll
   for (int q = 0; q < 4; ++q) t = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w.v[q], a.v[q], t, 0, 0, 0);
   return t;
 }
-
 // Span number i of spans of up to TM rows; rows = 0: none.
 template <int TM>
 __device__ __forceinline__ RowSpan row_span(const BlockGemmArgs& g, int i) {
@@ -131,6 +134,24 @@ __device__ __forceinline__ int source_row(const BlockGemmArgs& g, int row) {
   const int at = g.topk ? f / g.topk : row;
   return at < g.M ? at : -1;
 }
+
+// Zeros for the columns n0 .. n0 + cols - 1 of a span none of whose rows is real.
+template <int OT>
+__device__ __forceinline__ void zero_rows(const BlockGemmArgs& g, const RowSpan& s, int n0, int cols, int threads) {
+  constexpr int V = OT == 1 ? 8 : 4;  // values in 16 bytes
+  const int n1 = min(n0 + cols, g.N), w = g.vec ? (n1 - n0) / V : 0, rest = n1 - n0 - w * V;
+  for (int q = threadIdx.x; q < s.rows * w; q += threads) {
+    const size_t at = (size_t)(s.row0 + q / w) * g.out_stride + n0 + q % w * V;
+    *reinterpret_cast<b_i32x4*>(reinterpret_cast<char*>(g.out) + at * (16 / V)) = b_i32x4{};
+  }
+  for (int q = threadIdx.x; q < s.rows * rest; q += threads) {
+    const size_t at = (size_t)(s.row0 + q / rest) * g.out_stride + n0 + w * V + q % rest;
+    if constexpr (OT == 1)
+      reinterpret_cast<uint16_t*>(g.out)[at] = 0;
+    else
+      reinterpret_cast<float*>(g.out)[at] = 0.0f;
+  }
+}
 #endif
 
 // Spans of up to tm rows that row_span<tm> numbers.
@@ -138,6 +159,15 @@ inline long long row_spans(const BlockGemmArgs& g, int tm) {
   if (!g.ids) return ((long long)g.M + tm - 1) / tm;
   const int step = g.bm >= tm ? tm : g.bm;
   return ((long long)g.R + step - 1) / step;
+}
+
+// About how many of these have real rows: an expert's pairs end in one that is half
+// empty on the average.
+inline long long spans_estimate(const BlockGemmArgs& g, int tm) {
+  if (!g.ids) return row_spans(g, tm);
+  const long long pairs = g.pairs < g.R ? g.pairs : g.R, most = row_spans(g, tm);
+  const long long n = pairs / tm + (g.E < pairs ? g.E : pairs) / 2 + 1;
+  return n < most ? n : most;
 }
 
 // What a launcher returns, launching nothing, for more tiles than a grid has.

@@ -141,6 +141,69 @@ def test_grouped(M, k, E, bm, N, K, keep, gather, dt):
     assert (out[:n].cpu().float().numpy()[pad] == 0).all() and (out[n:] == 3).all()
 
 
+def on_gpu(a, sa, w, sw):
+    """The product and the magnitudes' sum in 64 bits, block by block on the GPU."""
+    v = torch.from_numpy(BO.e4m3_values()).to(B.DEV)
+    out = torch.zeros(a.shape[0], w.shape[0], dtype=torch.float64, device=B.DEV)
+    mass = torch.zeros_like(out)
+    rows = torch.arange(w.shape[0], device=B.DEV) // 128
+    for b in range(sw.shape[1]):
+        c = slice(b * 128, b * 128 + 128)
+        x = v[a[:, c].long()] * sa[:, b, None].double()
+        y = (v[w[:, c].long()] * sw[rows, b, None].double()).t().contiguous()
+        out += x @ y
+        mass += x.abs() @ y.abs()
+    return out, mass
+
+
+def near(got, out, mass, dt, K):
+    """As product_bound, with all of a group's magnitudes for its largest."""
+    n = 128 + 3 + -(-K // 128)
+    tol = ((7 * 2.0 ** -13 if dt == "bf16" else 0) + n * B.U) * mass + B.HALF_STEP[dt] * out.abs() * (1 + 2.0 ** -7) + 1e-38
+    worst = ((got.double() - out).abs() / tol).max().item()
+    assert worst <= 1, worst
+
+
+LARGE = [(1000, 4000, "bf16"), (2000, 4010, "bf16"), (4000, 4090, "bf16"), (4097, 4104, "bf16"), (300, 4001, "bf16"),
+         (600, 4000, "bf16"), (1000, 4001, "f32"), (2500, 4004, "f32"), (700, 3000, "f32")]
+
+
+@pytest.mark.parametrize("K", [16, 144, 272, 656])
+@pytest.mark.parametrize("M,N,dt", LARGE)
+def test_large(M, N, dt, K):
+    """Sizes for each of the tile kernels, their blocks from one on, odd and even."""
+    a, sa, w, sw = (B.dev(x) for x in operands(M, N, K, M + K))
+    got = moe.moe_block_matmul(a, sa.t().contiguous().t(), w, sw, out_dtype=B.DT[dt])
+    near(got, *on_gpu(a, sa, w, sw), dt, K)
+
+
+@pytest.mark.parametrize("gather", [True, False])
+@pytest.mark.parametrize("M,k,E,bm,N,K,keep,dt", [
+    (3000, 2, 3, 256, 2100, 272, 1.0, "bf16"), (3000, 2, 3, 16, 2100, 144, 0.9, "bf16"), (5000, 4, 5, 128, 1030, 400, 0.7, "bf16"),
+    (900, 8, 64, 256, 520, 272, 1.0, "bf16"), (900, 8, 64, 16, 520, 272, 0.3, "bf16"), (2000, 2, 4, 64, 2100, 272, 1.0, "f32"),
+    (700, 1, 2, 128, 4100, 528, 1.0, "f32")])
+def test_grouped_large(M, k, E, bm, N, K, keep, dt, gather):
+    ids, al, pos, n = B.aligned(M, k, E, bm, M + N, keep)
+    R = al.sorted_pair_ids.numel()
+    a, sa, w, sw = (B.dev(x) for x in operands(M if gather else R, N, K, M + N + K, E))
+    out = torch.full((R, N), 3.0, dtype=B.DT[dt], device=B.DEV)
+    if not gather:
+        pad = torch.ones(R, dtype=torch.bool, device=B.DEV)
+        pad[torch.from_numpy(pos[pos >= 0]).to(B.DEV).long()] = False
+        a[pad], sa[pad] = 0x7F, float("nan")
+    moe.moe_block_matmul_grouped(a, sa.t().contiguous().t(), w, sw, al, topk=k if gather else None, out=out)
+    off = al.expert_offsets.cpu().numpy()
+    for e in range(E):
+        p = torch.arange(off[e], off[e + 1], device=B.DEV)
+        f = al.sorted_pair_ids[p].long()
+        real = f < M * k
+        assert (out[p[~real]] == 0).all()
+        if real.any():
+            at = f[real] // k if gather else p[real]
+            near(out[p[real]], *on_gpu(a[at], sa[at], w[e], sw[e]), dt, K)
+    assert (out[n:] == 3).all()
+
+
 def test_grouped_rows_trimmed_and_odd_strides():
     M, k, E, bm, N, K = 90, 2, 5, 32, 65, 144
     ids, al, pos, n = B.aligned(M, k, E, bm, 4)
