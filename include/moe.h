@@ -593,7 +593,7 @@ typedef struct {
  *            rows_dtype (MOE_BF16 or MOE_F32, in any combination).
  * weights    device f32 [M, topk] or NULL (all 1).
  * d_weights  device f32 [M, topk] or NULL (x is then not read).
- * K          a multiple of 8 in [8, 65536].   M <= 2^23.
+ * K          a multiple of 8 in [8, 65536].   M <= 2^22.
  * Reads of the alignment: pair_pos; moe_dispatch sorted_pair_ids and num_padded
  * too.  M == 0 is a no-op.  Errors: MOE_ERR_NULL, MOE_ERR_SHAPE, MOE_ERR_DTYPE,
  * MOE_ERR_ALIGN, MOE_ERR_HIP.
@@ -639,8 +639,8 @@ moe_status moe_combine_backward(const moe_alignment* alignment, const void* d_ou
  * codes      device uint8 [M, K], dense (written).
  * scales     device f32 (written): block (m / block_rows, k / 128) at
  *            m / block_rows * scale_stride_row + k / 128 * scale_stride_block.
- * K a multiple of 16 in [16, 65536], M <= 2^27; strides of the scales 1 to
- * 2^32.  M == 0 is a no-op.  Errors: MOE_ERR_NULL, MOE_ERR_SHAPE,
+ * K a multiple of 16 in [16, 65536], M <= 2^27, M ceil(K / 128) <= 2^28; strides
+ * of the scales 1 to 2^32.  M == 0 is a no-op.  Errors: MOE_ERR_NULL, MOE_ERR_SHAPE,
  * MOE_ERR_DTYPE, MOE_ERR_ALIGN, MOE_ERR_UNSUPPORTED (gated or num_rows with
  * block_rows 128), MOE_ERR_HIP.
  */

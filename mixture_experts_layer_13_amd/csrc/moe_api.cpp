@@ -908,7 +908,7 @@ moe_status check_alignment(const moe_alignment* al) {
 moe_status check_permute(const moe_alignment* al, int32_t tok_dtype, int32_t rows_dtype, int32_t K) {
   moe_status s = check_alignment(al);
   if (s) return s;
-  if (al->M > (1 << 23)) return fail(MOE_ERR_SHAPE, "M=%d must be in [0, 2^23]", al->M);
+  if (al->M > (1 << 22)) return fail(MOE_ERR_SHAPE, "M=%d must be in [0, 2^22]", al->M);
   if (K < 8 || K > 65536 || K % 8) return fail(MOE_ERR_SHAPE, "K=%d must be a multiple of 8 in [8, 65536]", K);
   if (!value_dtype(tok_dtype) || !value_dtype(rows_dtype))
     return fail(MOE_ERR_DTYPE, "value types must be MOE_F32 or MOE_BF16");
@@ -1064,6 +1064,8 @@ moe_status moe_quantize_blocks(const void* x, int32_t x_dtype, int64_t x_stride,
   if (!aligned(x, 16) || !aligned(codes, 16)) return fail(MOE_ERR_ALIGN, "x and codes must be 16-byte aligned");
   if (!aligned(scales, 4) || !aligned(num_rows, 4))
     return fail(MOE_ERR_ALIGN, "scales and num_rows must be 4-byte aligned");
+  if ((long long)M * ((K + 127) / 128) > (1LL << 28))
+    return fail(MOE_ERR_SHAPE, "M=%d rows of %d blocks exceed 2^28 blocks", M, (K + 127) / 128);
   const moe::QuantArgs a{x, x_stride, M, K, num_rows, codes, scales, scale_stride_row, scale_stride_block};
   return hip_status(moe::launch_quant_blocks(a, x_dtype, gated != 0, block_rows, (hipStream_t)stream),
                     "block quantisation launch");

@@ -18,21 +18,17 @@
 
 namespace moe {
 
-constexpr int kPermWave = 4;  // waves of a workgroup
+constexpr int kPermWaves = 8;  // most waves of a workgroup
+constexpr int kPairs = 8;      // pairs whose rows a thread has in flight
 
+// VEC consecutive values of a row as they lie in memory, at most 16 bytes.
 template <int DT, int VEC>
-__device__ __forceinline__ void load_vec(const void* base, size_t at, float (&v)[VEC]) {
-  if constexpr (DT == DT_F32) {
-#pragma unroll
-    for (int q = 0; q < VEC / 4; ++q) {
-      const i32x4 d = ld16(reinterpret_cast<const float*>(base) + at + 4 * q);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) v[4 * q + i] = __int_as_float(d[i]);
-    }
-  } else {
-    uint32_t d[VEC / 2];
-    const uint16_t* p = reinterpret_cast<const uint16_t*>(base) + at;
-    if constexpr (VEC == 8) {
+struct Raw8 {
+  static constexpr int kWords = VEC * (DT == DT_F32 ? 4 : 2) / 4;
+  uint32_t d[kWords];
+  __device__ __forceinline__ void load(const void* base, size_t at) {
+    const char* p = reinterpret_cast<const char*>(base) + at * (DT == DT_F32 ? 4 : 2);
+    if constexpr (kWords == 4) {
       const i32x4 r = ld16(p);
 #pragma unroll
       for (int i = 0; i < 4; ++i) d[i] = (uint32_t)r[i];
@@ -41,22 +37,19 @@ __device__ __forceinline__ void load_vec(const void* base, size_t at, float (&v)
       d[0] = r.x;
       d[1] = r.y;
     }
-#pragma unroll
-    for (int i = 0; i < VEC / 2; ++i) {
-      v[2 * i] = __uint_as_float(d[i] << 16);
-      v[2 * i + 1] = __uint_as_float(d[i] & 0xffff0000u);
-    }
   }
-}
+  __device__ __forceinline__ float value(int i) const {
+    if constexpr (DT == DT_F32) return __uint_as_float(d[i]);
+    return __uint_as_float(i & 1 ? d[i / 2] & 0xffff0000u : d[i / 2] << 16);
+  }
+};
 
 template <int DT, int VEC>
 __device__ __forceinline__ void store_vec(void* base, size_t at, const float (&v)[VEC]) {
   if constexpr (DT == DT_F32) {
-#pragma unroll
-    for (int q = 0; q < VEC / 4; ++q)
-      st16(reinterpret_cast<float*>(base) + at + 4 * q,
-           i32x4{__float_as_int(v[4 * q]), __float_as_int(v[4 * q + 1]), __float_as_int(v[4 * q + 2]),
-                 __float_as_int(v[4 * q + 3])});
+    static_assert(VEC == 4, "16 bytes");
+    st16(reinterpret_cast<float*>(base) + at,
+         i32x4{__float_as_int(v[0]), __float_as_int(v[1]), __float_as_int(v[2]), __float_as_int(v[3])});
   } else {
     uint16_t* p = reinterpret_cast<uint16_t*>(base) + at;
     if constexpr (VEC == 8)
@@ -67,127 +60,143 @@ __device__ __forceinline__ void store_vec(void* base, size_t at, const float (&v
   }
 }
 
-// Sum over the workgroup of G values per lane; thread i < G gets value i.
-template <int G>
-__device__ __forceinline__ float group_sums(float (&v)[G], float (*lds)[G]) {
-  const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
+// Places and weights of the pairs j0 .. j0 + kPairs - 1 of token t; -1: none.
+struct Places {
+  int p[kPairs];
+  float w[kPairs];
+  __device__ __forceinline__ Places(const PermuteArgs& a, int t, int j0) {
 #pragma unroll
-  for (int i = 0; i < G; ++i) {
-    const float s = wave_sum(v[i]);
-    if (lane == 0) lds[wv][i] = s;
+    for (int j = 0; j < kPairs; ++j) {
+      const size_t f = (size_t)t * a.topk + min(j0 + j, a.topk - 1);
+      const int at = a.pair_pos[f];
+      p[j] = j0 + j < a.topk && at >= 0 && at < a.rows ? at : -1;
+      w[j] = a.weights ? a.weights[f] : 1.0f;
+    }
+  }
+};
+
+// The workgroup's sums of dot, to the pairs j0 .. of token t.  A wave's eight sums
+// take ten exchanges: lanes 32, 16 and 8 apart first deal the values out among
+// each other, then those of one value meet (48 if each were summed by itself).
+__device__ __forceinline__ void store_dots(const PermuteArgs& a, int t, int j0, const float (&dot)[kPairs]) {
+  static_assert(kPairs == 8, "three halvings");
+  __shared__ float part[kPermWaves][kPairs];
+  const int lane = threadIdx.x & 63, waves = blockDim.x >> 6;
+  float v[kPairs];
+#pragma unroll
+  for (int j = 0; j < kPairs; ++j) v[j] = dot[j];
+#pragma unroll
+  for (int n = kPairs / 2, m = 32; n > 0; n /= 2, m /= 2)
+#pragma unroll
+    for (int j = 0; j < n; ++j) {
+      const float keep = lane & m ? v[j + n] : v[j], give = lane & m ? v[j] : v[j + n];
+      v[j] = keep + __shfl_xor(give, m, kWave);
+    }
+#pragma unroll
+  for (int m = 4; m > 0; m /= 2) v[0] += __shfl_xor(v[0], m, kWave);
+  if ((lane & 7) == 0) part[threadIdx.x >> 6][lane >> 3] = v[0];  // bits 5, 4, 3 of the lane: 4, 2, 1 of the pair
+  __syncthreads();
+  if ((int)threadIdx.x < min(kPairs, a.topk - j0)) {
+    float s = 0.0f;
+    for (int q = 0; q < waves; ++q) s += part[q][threadIdx.x];
+    a.dw[(size_t)t * a.topk + j0 + threadIdx.x] = s;
   }
   __syncthreads();
-  float s = 0.0f;
-  if (threadIdx.x < G)
-    for (int q = 0; q < kPermWave; ++q) s += lds[q][threadIdx.x];
-  __syncthreads();
-  return s;
 }
 
-// Place of pair f among rows rows, -1 if it has none.
-__device__ __forceinline__ int pair_place(const PermuteArgs& a, int f) {
-  const int p = a.pair_pos[f];
-  return p >= 0 && p < a.rows ? p : -1;
+template <int XT, int RT>
+constexpr int perm_vec() {
+  return XT == DT_BF16 && RT == DT_BF16 ? 8 : 4;
 }
 
-// Token to rows.  Workgroups below M: token blockIdx.x, the vectors of this
-// blockIdx.y; the others zero the rows of no pair, 16 rows each.
+// Token to rows.  Workgroups below M: token blockIdx.x (the vectors of part
+// blockIdx.y); the others zero the rows of no pair among 32.
 template <int XT, int RT, bool DOT>
-__global__ __launch_bounds__(kPermWave * 64) void scatter_kernel(PermuteArgs a) {
-  constexpr int VEC = XT == DT_BF16 && RT == DT_BF16 ? 8 : 4;
-  constexpr int G = 8;
+__global__ __launch_bounds__(kPermWaves * 64) void scatter_kernel(PermuteArgs a) {
+  constexpr int VEC = perm_vec<XT, RT>();
   const int n = a.K / VEC, step = gridDim.y * blockDim.x;
   const int v0 = blockIdx.y * blockDim.x + threadIdx.x;
   if ((int)blockIdx.x >= a.M) {
-    const int r0 = ((int)blockIdx.x - a.M) * 16;
-    const int end = min(min(r0 + 16, a.rows), *a.num_padded);
-    for (int r = r0; r < end; ++r) {
-      const int f = a.sorted_ids[r];
-      if (f >= 0 && f < a.P) continue;
-      const float z[VEC] = {};
-      for (int v = v0; v < n; v += step) store_vec<RT, VEC>(a.rows_out, (size_t)r * a.rows_out_stride + (size_t)v * VEC, z);
+    const int r0 = ((int)blockIdx.x - a.M) * 32, l = threadIdx.x & 31;
+    const int end = min(a.rows, *a.num_padded);
+    const int f = r0 + l < end ? a.sorted_ids[r0 + l] : 0;
+    uint32_t empty = (uint32_t)__ballot(r0 + l < end && !(f >= 0 && f < a.P));
+    const float z[VEC] = {};
+    for (; empty; empty &= empty - 1) {
+      const size_t r = r0 + __builtin_ctz(empty);
+      for (int v = v0; v < n; v += step) store_vec<RT, VEC>(a.rows_out, r * a.rows_out_stride + (size_t)v * VEC, z);
     }
     return;
   }
   const int t = blockIdx.x;
-  __shared__ float sums[kPermWave][G];
-  for (int j0 = 0; j0 < a.topk; j0 += G) {
-    int p[G];
-    float w[G], dot[G] = {};
-#pragma unroll
-    for (int j = 0; j < G; ++j) {
-      const int f = t * a.topk + j0 + j;
-      p[j] = j0 + j < a.topk ? pair_place(a, f) : -1;
-      w[j] = a.weights && p[j] >= 0 ? a.weights[f] : 1.0f;
-    }
+  for (int j0 = 0; j0 < a.topk; j0 += kPairs) {
+    const Places at(a, t, j0);
+    float dot[kPairs] = {};
     for (int v = v0; v < n; v += step) {
-      float x[VEC];
-      load_vec<XT, VEC>(a.tok_in, (size_t)t * a.tok_in_stride + (size_t)v * VEC, x);
-      float r[DOT ? G : 1][VEC];
+      Raw8<XT, VEC> x;
+      x.load(a.tok_in, (size_t)t * a.tok_in_stride + (size_t)v * VEC);
+      Raw8<RT, VEC> r[DOT ? kPairs : 1];
       if constexpr (DOT) {
 #pragma unroll
-        for (int j = 0; j < G; ++j)
-          if (p[j] >= 0) load_vec<RT, VEC>(a.rows_in, (size_t)p[j] * a.rows_in_stride + (size_t)v * VEC, r[j]);
+        for (int j = 0; j < kPairs; ++j)
+          if (at.p[j] >= 0) r[j].load(a.rows_in, (size_t)at.p[j] * a.rows_in_stride + (size_t)v * VEC);
       }
 #pragma unroll
-      for (int j = 0; j < G; ++j)
-        if (p[j] >= 0) {
+      for (int j = 0; j < kPairs; ++j)
+        if (at.p[j] >= 0) {
           float y[VEC];
 #pragma unroll
           for (int i = 0; i < VEC; ++i) {
-            y[i] = w[j] * x[i];
-            if constexpr (DOT) dot[j] = __builtin_fmaf(x[i], r[j][i], dot[j]);
+            y[i] = at.w[j] * x.value(i);
+            if constexpr (DOT) dot[j] = __builtin_fmaf(x.value(i), r[j].value(i), dot[j]);
           }
-          store_vec<RT, VEC>(a.rows_out, (size_t)p[j] * a.rows_out_stride + (size_t)v * VEC, y);
+          store_vec<RT, VEC>(a.rows_out, (size_t)at.p[j] * a.rows_out_stride + (size_t)v * VEC, y);
         }
     }
-    if constexpr (DOT) {
-      const float s = group_sums<G>(dot, sums);
-      if ((int)threadIdx.x < G && j0 + (int)threadIdx.x < a.topk) a.dw[(size_t)t * a.topk + j0 + threadIdx.x] = s;
-    }
+    if constexpr (DOT) store_dots(a, t, j0, dot);
   }
 }
 
 // Rows to token.
 template <int XT, int RT, bool DOT>
-__global__ __launch_bounds__(kPermWave * 64) void gather_kernel(PermuteArgs a) {
-  constexpr int VEC = XT == DT_BF16 && RT == DT_BF16 ? 8 : 4;
-  constexpr int G = 8;
+__global__ __launch_bounds__(kPermWaves * 64) void gather_kernel(PermuteArgs a) {
+  constexpr int VEC = perm_vec<XT, RT>();
   const int n = a.K / VEC, step = gridDim.y * blockDim.x;
   const int v0 = blockIdx.y * blockDim.x + threadIdx.x;
   const int t = blockIdx.x;
-  __shared__ float sums[kPermWave][G];
-  for (int j0 = 0; j0 < (DOT ? a.topk : 1); j0 += G) {
-    float dot[G] = {};
-    for (int v = v0; v < n; v += step) {
-      float x[VEC], acc[VEC] = {};
-      if constexpr (DOT) load_vec<XT, VEC>(a.tok_in, (size_t)t * a.tok_in_stride + (size_t)v * VEC, x);
-      // the sum takes all pairs in the first round; the products G pairs a round
-      for (int g = j0; g < (j0 ? min(j0 + G, a.topk) : a.topk); g += G) {
-        float r[G][VEC];
-        int p[G];
+  // acc += the rows of `at` at vector v, dot += their products with x
+  auto take = [&](const Places& at, int v, float (&acc)[VEC], bool products, float (&dot)[kPairs]) {
+    Raw8<RT, VEC> r[kPairs];
+    Raw8<XT, VEC> x;
+    if (DOT && products) x.load(a.tok_in, (size_t)t * a.tok_in_stride + (size_t)v * VEC);
 #pragma unroll
-        for (int j = 0; j < G; ++j) {
-          p[j] = g + j < a.topk ? pair_place(a, t * a.topk + g + j) : -1;
-          if (p[j] >= 0) load_vec<RT, VEC>(a.rows_in, (size_t)p[j] * a.rows_in_stride + (size_t)v * VEC, r[j]);
+    for (int j = 0; j < kPairs; ++j)
+      if (at.p[j] >= 0) r[j].load(a.rows_in, (size_t)at.p[j] * a.rows_in_stride + (size_t)v * VEC);
+#pragma unroll
+    for (int j = 0; j < kPairs; ++j)
+      if (at.p[j] >= 0) {
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) {
+          acc[i] = __builtin_fmaf(at.w[j], r[j].value(i), acc[i]);
+          if (DOT && products) dot[j] = __builtin_fmaf(x.value(i), r[j].value(i), dot[j]);
         }
-#pragma unroll
-        for (int j = 0; j < G; ++j)
-          if (p[j] >= 0) {
-            const float w = a.weights ? a.weights[(size_t)t * a.topk + g + j] : 1.0f;
-#pragma unroll
-            for (int i = 0; i < VEC; ++i) {
-              acc[i] = __builtin_fmaf(w, r[j][i], acc[i]);
-              if constexpr (DOT)
-                if (g == j0) dot[j] = __builtin_fmaf(x[i], r[j][i], dot[j]);
-            }
-          }
       }
-      if (j0 == 0) store_vec<XT, VEC>(a.tok_out, (size_t)t * a.tok_out_stride + (size_t)v * VEC, acc);
-    }
-    if constexpr (DOT) {
-      const float s = group_sums<G>(dot, sums);
-      if ((int)threadIdx.x < G && j0 + (int)threadIdx.x < a.topk) a.dw[(size_t)t * a.topk + j0 + threadIdx.x] = s;
+  };
+  const Places first(a, t, 0);
+  float dot[kPairs] = {}, unused[kPairs];
+  for (int v = v0; v < n; v += step) {
+    float acc[VEC] = {};
+    take(first, v, acc, true, dot);
+    for (int j0 = kPairs; j0 < a.topk; j0 += kPairs) take(Places(a, t, j0), v, acc, false, unused);
+    store_vec<XT, VEC>(a.tok_out, (size_t)t * a.tok_out_stride + (size_t)v * VEC, acc);
+  }
+  if constexpr (DOT) {
+    store_dots(a, t, 0, dot);
+    for (int j0 = kPairs; j0 < a.topk; j0 += kPairs) {
+      const Places at(a, t, j0);
+      float more[kPairs] = {}, acc[VEC] = {};
+      for (int v = v0; v < n; v += step) take(at, v, acc, true, more);
+      store_dots(a, t, j0, more);
     }
   }
 }
@@ -205,22 +214,28 @@ static void* gather_of(int xt, int rt) {
   return rt == DT_BF16 ? (void*)gather_kernel<DT_F32, DT_BF16, DOT> : (void*)gather_kernel<DT_F32, DT_F32, DOT>;
 }
 
-int launch_scatter(const PermuteArgs& a, int xt, int rt, hipStream_t st) {
-  const int vec = xt == DT_BF16 && rt == DT_BF16 ? 8 : 4, parts = (a.K / vec + 255) / 256;
-  const unsigned y = a.dw ? 1 : (unsigned)parts;
+// A token's vectors over as few rounds of a workgroup of up to eight waves as will
+// do; of few tokens without products, each wave's over a workgroup of its own.
+static int permute_launch(const void* kernel, const PermuteArgs& a, int xt, int rt, long long groups, hipStream_t st) {
+  const int vec = xt == DT_BF16 && rt == DT_BF16 ? 8 : 4;
+  const int chunks = (a.K / vec + 63) / 64, rounds = (chunks + kPermWaves - 1) / kPermWaves;
+  int waves = (chunks + rounds - 1) / rounds, parts = 1;
+  if (!a.dw && (long long)a.M * waves < 4 * device_cu_count()) {
+    parts = chunks;
+    waves = 1;
+  }
   PermuteArgs c = a;
   void* args[] = {&c};
-  return (int)hipLaunchKernel(a.dw ? scatter_of<true>(xt, rt) : scatter_of<false>(xt, rt),
-                              dim3((unsigned)(a.M + (a.rows + 15) / 16), y), dim3(kPermWave * 64), args, 0, st);
+  return (int)hipLaunchKernel(kernel, dim3((unsigned)groups, (unsigned)parts), dim3(waves * 64), args, 0, st);
+}
+
+int launch_scatter(const PermuteArgs& a, int xt, int rt, hipStream_t st) {
+  return permute_launch(a.dw ? scatter_of<true>(xt, rt) : scatter_of<false>(xt, rt), a, xt, rt,
+                        a.M + ((long long)a.rows + 31) / 32, st);
 }
 
 int launch_gather(const PermuteArgs& a, int xt, int rt, hipStream_t st) {
-  const int vec = xt == DT_BF16 && rt == DT_BF16 ? 8 : 4, parts = (a.K / vec + 255) / 256;
-  const unsigned y = a.dw ? 1 : (unsigned)parts;
-  PermuteArgs c = a;
-  void* args[] = {&c};
-  return (int)hipLaunchKernel(a.dw ? gather_of<true>(xt, rt) : gather_of<false>(xt, rt), dim3((unsigned)a.M, y),
-                              dim3(kPermWave * 64), args, 0, st);
+  return permute_launch(a.dw ? gather_of<true>(xt, rt) : gather_of<false>(xt, rt), a, xt, rt, a.M, st);
 }
 
 }  // namespace moe

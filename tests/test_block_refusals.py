@@ -44,7 +44,7 @@ def combine_bwd(a="default", g=F, ot=BF, gs=64, K=64, rows=F, rs=64, w=None, dr=
     return moe.lib().moe_combine_backward(ref(al() if a == "default" else a), g, ot, gs, K, rows, rs, w, dr, rt, drs, dw, None)
 
 
-BAD_ALIGNMENT = [(dict(M=-1), SHAPE), (dict(M=(1 << 23) + 1, topk=1), SHAPE), (dict(topk=0), SHAPE), (dict(topk=65), SHAPE),
+BAD_ALIGNMENT = [(dict(M=-1), SHAPE), (dict(M=(1 << 22) + 1, topk=1), SHAPE), (dict(topk=0), SHAPE), (dict(topk=65), SHAPE),
                  (dict(M=1 << 22, topk=17), SHAPE), (dict(rows=-1), SHAPE), (dict(rows=(1 << 26) + (1 << 18) + 1), SHAPE),
                  (dict(pair_pos=None), NULL), (dict(pair_pos=ODD4), ALIGN)]
 BAD_PLACES = [(dict(sorted_pair_ids=None), NULL), (dict(num_padded=None), NULL), (dict(sorted_pair_ids=ODD4), ALIGN),
@@ -90,7 +90,7 @@ def quant(x=F, xt=BF, xs=256, M=9, K=256, gated=0, br=1, n=None, codes=F, scales
     (dict(K=65552, xs=65552), SHAPE), (dict(br=2), SHAPE), (dict(br=0), SHAPE), (dict(br=128, gated=1, xs=512), UNSUP),
     (dict(br=128, n=F), UNSUP), (dict(gated=1), SHAPE), (dict(xs=250), SHAPE), (dict(xs=260), ALIGN), (dict(sr=0), SHAPE),
     (dict(sb=0), SHAPE), (dict(x=None), NULL), (dict(codes=None), NULL), (dict(scales=None), NULL), (dict(x=ODD16), ALIGN),
-    (dict(codes=ODD16), ALIGN), (dict(scales=ODD4), ALIGN), (dict(n=ODD4), ALIGN), (dict(M=0, x=None, codes=None), OK),
+    (dict(codes=ODD16), ALIGN), (dict(scales=ODD4), ALIGN), (dict(n=ODD4), ALIGN), (dict(M=1 << 20, K=65536, xs=65536), SHAPE), (dict(M=0, x=None, codes=None), OK),
 ])
 def test_quantize_refusals(kw, status):
     assert quant(**kw) == status
