@@ -583,20 +583,22 @@ def moe_fused_forward_persistent(problem, x, w13, w2, topk_weights, alignment, o
     return out
 
 
-def _rows(t, shape, name, device):
-    """(address, dtype code, row stride) of a [rows, values] tensor of this shape
-    (None: any size) on `device`, the values of a row contiguous."""
+def _rows(t, rows, values, name, device):
+    """(address, dtype code, row stride) of a [rows, values] tensor (None: any
+    number) on `device`, the values of a row contiguous."""
     code = _VALUE_CODES.get(t.dtype)
     if code is None:
         raise MoEError(MOE_ERR_DTYPE, f"{name} must be bf16 or f32, not {t.dtype}")
-    if t.dim() != 2 or any(w is not None and w != n for w, n in zip(shape, t.shape)):
-        raise MoEError(MOE_ERR_SHAPE, f"{name} has shape {tuple(t.shape)}, not {tuple(shape)}")
+    shape = t.shape
+    if len(shape) != 2 or (rows is not None and shape[0] != rows) or (values is not None and shape[1] != values):
+        raise MoEError(MOE_ERR_SHAPE, f"{name} has shape {tuple(shape)}, not {(rows, values)}")
     st, sv = t.stride()
-    if sv != 1 and t.size(1) > 1:
+    if sv != 1 and shape[1] > 1:
         raise MoEError(MOE_ERR_UNSUPPORTED, f"{name}: the values of a row must be contiguous")
     if t.device != device:
         raise MoEError(MOE_ERR_UNSUPPORTED, f"{name} is on {t.device}, not on {device}")
-    return t.data_ptr(), code, st if t.size(0) > 1 else t.size(1)
+    # the stride of a dimension of size one is torch's to choose
+    return t.data_ptr(), code, st if shape[0] > 1 else shape[1]
 
 
 def _pairs_f32(t, shape, name, device):
@@ -612,20 +614,30 @@ def _pairs_f32(t, shape, name, device):
     return t.data_ptr()
 
 
-def _alignment(al, M, topk, E, device):
-    """The moe_alignment of M tokens and topk pairs a token over al's tensors."""
-    ids = _index(al.sorted_pair_ids, 1, None, "sorted_pair_ids", device)
-    pos = _index(al.pair_pos, 1, None, "pair_pos", device)
-    rows, bm = al.sorted_pair_ids.size(0), al.block_m
+def _places(al, M, topk, device, padding):
+    """The moe_alignment of M tokens of topk pairs as far as the movements read it
+    (padding: with what tells padding rows), and its rows."""
+    pos, rows = _index(al.pair_pos, 1, None, "pair_pos", device), al.sorted_pair_ids.size(0)
     if al.pair_pos.size(0) < M * topk:
         raise MoEError(MOE_ERR_SHAPE, f"pair_pos of {al.pair_pos.size(0)} pairs for {M} x {topk}")
-    if bm < 1 or al.block_expert_ids.numel() * bm < rows:
-        raise MoEError(MOE_ERR_SHAPE, f"block_expert_ids of {al.block_expert_ids.numel()} blocks for {rows} rows")
-    if E is not None and al.expert_offsets.numel() != E + 1:
-        raise MoEError(MOE_ERR_SHAPE, f"expert_offsets of {al.expert_offsets.numel()} for {E} experts")
-    return moe_alignment(ids, _index(al.block_expert_ids, 1, None, "block_expert_ids", device),
-                         _index(al.expert_offsets, 1, None, "expert_offsets", device), pos,
-                         _index(al.num_padded, 1, 1, "num_padded", device), M, topk, E or 0, bm, rows)
+    if not padding:
+        return moe_alignment(None, None, None, pos, None, M, topk, 0, 0, rows), rows
+    ids = _index(al.sorted_pair_ids, 1, None, "sorted_pair_ids", device)
+    used = _index(al.num_padded, 1, 1, "num_padded", device)
+    return moe_alignment(ids, None, None, pos, used, M, topk, 0, 0, rows), rows
+
+
+def _segments(al, M, topk, E, device):
+    """The moe_alignment of M * topk pairs and E experts as far as the products
+    read it, and its rows."""
+    ids = _index(al.sorted_pair_ids, 1, None, "sorted_pair_ids", device)
+    rows, bm = al.sorted_pair_ids.size(0), al.block_m
+    blocks = _index(al.block_expert_ids, 1, None, "block_expert_ids", device)
+    if bm < 1 or al.block_expert_ids.size(0) * bm < rows:
+        raise MoEError(MOE_ERR_SHAPE, f"block_expert_ids of {al.block_expert_ids.size(0)} blocks for {rows} rows")
+    offsets = _index(al.expert_offsets, 1, E + 1, "expert_offsets", device)
+    used = _index(al.num_padded, 1, 1, "num_padded", device)
+    return moe_alignment(ids, blocks, offsets, None, used, M, topk, E, bm, rows), rows
 
 
 def moe_dispatch(x, alignment, topk, weights=None, out=None, out_dtype=None, stream=None):
@@ -633,14 +645,14 @@ def moe_dispatch(x, alignment, topk, weights=None, out=None, out_dtype=None, str
     weight * token; weights f32 [M, topk] or None (1).  Rows of padding are zero,
     those from num_padded on as they were (in a new tensor: anything)."""
     dev = x.device
-    xp, xc, xs = _rows(x, (None, None), "x", dev)
+    xp, xc, xs = _rows(x, None, None, "x", dev)
     M, K = x.shape
-    al = _alignment(alignment, M, topk, None, dev)
-    wp = _pairs_f32(weights, (M, topk), "weights", dev)
+    al, rows = _places(alignment, M, topk, dev, True)
+    wp = None if weights is None else _pairs_f32(weights, (M, topk), "weights", dev)
     if out is None:
-        out = _made(x, (al.rows, K), out_dtype, stream)
-    op, oc, os_ = _rows(out, (al.rows, K), "out", dev)
-    _run(dev, stream, lib().moe_dispatch, ctypes.byref(al), xp, xc, xs, K, wp, op, oc, os_)
+        out = _made(x, (rows, K), out_dtype, stream)
+    op, oc, ost = _rows(out, rows, K, "out", dev)
+    _run(dev, stream, lib().moe_dispatch, al, xp, xc, xs, K, wp, op, oc, ost)
     return out
 
 
@@ -648,21 +660,21 @@ def moe_dispatch_backward(d_rows, alignment, M, topk, x=None, weights=None, out=
     """The gradient of moe_dispatch: d_rows [rows, K] -> (dx [M, K], d_weights f32
     [M, topk], or None without x, which only they need)."""
     dev = d_rows.device
-    al = _alignment(alignment, M, topk, None, dev)
-    rp, rc, rs = _rows(d_rows, (al.rows, None), "d_rows", dev)
+    al, rows = _places(alignment, M, topk, dev, False)
+    rp, rc, rs = _rows(d_rows, rows, None, "d_rows", dev)
     K = d_rows.size(1)
-    wp = _pairs_f32(weights, (M, topk), "weights", dev)
-    xp, xc, xs, dw = None, None, 0, None
+    wp = None if weights is None else _pairs_f32(weights, (M, topk), "weights", dev)
+    xp, xc, xs, dw, dwp = None, None, 0, None, None
     if x is not None:
-        xp, xc, xs = _rows(x, (M, K), "x", dev)
+        xp, xc, xs = _rows(x, M, K, "x", dev)
         dw = _made(d_rows, (M, topk), torch.float32, stream)
+        dwp = dw.data_ptr()
     if out is None:
         out = _made(d_rows, (M, K), out_dtype or (None if x is None else x.dtype), stream)
-    op, oc, os_ = _rows(out, (M, K), "out", dev)
+    op, oc, ost = _rows(out, M, K, "out", dev)
     if xc is not None and xc != oc:
         raise MoEError(MOE_ERR_DTYPE, f"x is {x.dtype}, its gradient {out.dtype}")
-    _run(dev, stream, lib().moe_dispatch_backward, ctypes.byref(al), rp, rc, rs, K, xp, xs, wp, op, oc, os_,
-         None if dw is None else dw.data_ptr())
+    _run(dev, stream, lib().moe_dispatch_backward, al, rp, rc, rs, K, xp, xs, wp, op, oc, ost, dwp)
     return out, dw
 
 
@@ -670,14 +682,14 @@ def moe_combine(rows, alignment, M, topk, weights=None, out=None, out_dtype=None
     """rows [rows, K] bf16/f32 in expert order back to tokens: out [M, K], out[t] =
     the sum of weight * row over the token's pairs; weights as in moe_dispatch."""
     dev = rows.device
-    al = _alignment(alignment, M, topk, None, dev)
-    rp, rc, rs = _rows(rows, (al.rows, None), "rows", dev)
+    al, n = _places(alignment, M, topk, dev, False)
+    rp, rc, rs = _rows(rows, n, None, "rows", dev)
     K = rows.size(1)
-    wp = _pairs_f32(weights, (M, topk), "weights", dev)
+    wp = None if weights is None else _pairs_f32(weights, (M, topk), "weights", dev)
     if out is None:
         out = _made(rows, (M, K), out_dtype, stream)
-    op, oc, os_ = _rows(out, (M, K), "out", dev)
-    _run(dev, stream, lib().moe_combine, ctypes.byref(al), rp, rc, rs, K, wp, op, oc, os_)
+    op, oc, ost = _rows(out, M, K, "out", dev)
+    _run(dev, stream, lib().moe_combine, al, rp, rc, rs, K, wp, op, oc, ost)
     return out
 
 
@@ -685,21 +697,21 @@ def moe_combine_backward(d_out, alignment, topk, rows=None, weights=None, out=No
     """The gradient of moe_combine: d_out [M, K] -> (d_rows [rows, K], d_weights f32
     [M, topk], or None without rows, which only they need)."""
     dev = d_out.device
-    gp, gc, gs = _rows(d_out, (None, None), "d_out", dev)
+    gp, gc, gs = _rows(d_out, None, None, "d_out", dev)
     M, K = d_out.shape
-    al = _alignment(alignment, M, topk, None, dev)
-    wp = _pairs_f32(weights, (M, topk), "weights", dev)
-    rp, rc, rs, dw = None, None, 0, None
+    al, n = _places(alignment, M, topk, dev, True)
+    wp = None if weights is None else _pairs_f32(weights, (M, topk), "weights", dev)
+    rp, rc, rs, dw, dwp = None, None, 0, None, None
     if rows is not None:
-        rp, rc, rs = _rows(rows, (al.rows, K), "rows", dev)
+        rp, rc, rs = _rows(rows, n, K, "rows", dev)
         dw = _made(d_out, (M, topk), torch.float32, stream)
+        dwp = dw.data_ptr()
     if out is None:
-        out = _made(d_out, (al.rows, K), out_dtype or (None if rows is None else rows.dtype), stream)
-    op, oc, os_ = _rows(out, (al.rows, K), "out", dev)
+        out = _made(d_out, (n, K), out_dtype or (None if rows is None else rows.dtype), stream)
+    op, oc, ost = _rows(out, n, K, "out", dev)
     if rc is not None and rc != oc:
         raise MoEError(MOE_ERR_DTYPE, f"rows are {rows.dtype}, their gradient {out.dtype}")
-    _run(dev, stream, lib().moe_combine_backward, ctypes.byref(al), gp, gc, gs, K, rp, rs, wp, op, oc, os_,
-         None if dw is None else dw.data_ptr())
+    _run(dev, stream, lib().moe_combine_backward, al, gp, gc, gs, K, rp, rs, wp, op, oc, ost, dwp)
     return out, dw
 
 
@@ -724,23 +736,30 @@ def moe_quantize_blocks(x, gated=False, block_rows=1, num_rows=None, codes=None,
         for e in range(E):
             moe_quantize_blocks(x[e], gated, 128, num_rows, codes[e], scales[e], stream)
         return codes, scales
-    xp, xc, xs = _rows(x, (None, None), "x", dev)
-    M, K = x.size(0), x.size(1) // 2 if gated else x.size(1)
-    SR, SB = -(-M // max(block_rows, 1)), -(-K // 128)
-    if gated and x.size(1) % 2:
-        raise MoEError(MOE_ERR_SHAPE, f"gated x has {x.size(1)} values a row")
+    xp, xc, xs = _rows(x, None, None, "x", dev)
+    M, K = x.shape
+    if gated:
+        if K % 2:
+            raise MoEError(MOE_ERR_SHAPE, f"gated x has {K} values a row")
+        K //= 2
+    SR, SB = M if block_rows == 1 else -(-M // max(block_rows, 1)), -(-K // 128)
     if codes is None:
         codes = _made(x, (M, K), torch.float8_e4m3fn, stream)
     elif codes.dtype not in _CODES:
         raise MoEError(MOE_ERR_DTYPE, f"codes are {codes.dtype}")
     elif codes.shape != (M, K) or not codes.is_contiguous() or codes.device != dev:
         raise MoEError(MOE_ERR_SHAPE, f"codes must be a dense {(M, K)} on {dev}")
-    if scales is None:
-        scales = _made(x, (SB, SR), torch.float32, stream).t() if block_rows == 1 else _made(x, (SR, SB), torch.float32, stream)
-    sp, sr, sb = _scales(scales, SR, SB, "scales", dev)
-    np_ = None if num_rows is None else _index(num_rows, 1, 1, "num_rows", dev)
-    _run(dev, stream, lib().moe_quantize_blocks, xp, xc, xs, M, K, 1 if gated else 0, block_rows, np_, codes.data_ptr(),
-         sp, sr, sb)
+    if scales is not None:
+        sp, sr, sb = _scales(scales, SR, SB, "scales", dev)
+    elif block_rows == 1:
+        made = _made(x, (SB, SR), torch.float32, stream)
+        scales, sp, sr, sb = made.t(), made.data_ptr(), 1, SR or 1
+    else:
+        scales = _made(x, (SR, SB), torch.float32, stream)
+        sp, sr, sb = scales.data_ptr(), SB, 1
+    limit = None if num_rows is None else _index(num_rows, 1, 1, "num_rows", dev)
+    _run(dev, stream, lib().moe_quantize_blocks, xp, xc, xs, M, K, 1 if gated else 0, block_rows, limit,
+         codes.data_ptr(), sp, sr, sb)
     return codes, scales
 
 
@@ -757,42 +776,35 @@ def _scales(t, rows, blocks, name, device):
     return t.data_ptr(), sr if rows > 1 else 1, sb if blocks > 1 else 1
 
 
-def _codes(t, name, device):
-    if t.dtype not in _CODES:
-        raise MoEError(MOE_ERR_DTYPE, f"{name} must be E4M3 codes, not {t.dtype}")
-    if t.device != device:
-        raise MoEError(MOE_ERR_UNSUPPORTED, f"{name} is on {t.device}, not on {device}")
-    return t.data_ptr()
-
-
 def _block_operands(a, a_scales, w, w_scales, dims):
-    dev = a.device
-    if a.dim() != 2 or w.dim() != dims or w.size(-1) != a.size(1):
-        raise MoEError(MOE_ERR_SHAPE, f"a has shape {tuple(a.shape)}, w {tuple(w.shape)}")
+    """(M, N, K, addresses and strides of a, its scales, w and its scales)."""
+    dev, wshape = a.device, w.shape
+    if a.dim() != 2 or len(wshape) != dims or wshape[-1] != a.size(1):
+        raise MoEError(MOE_ERR_SHAPE, f"a has shape {tuple(a.shape)}, w {tuple(wshape)}")
     M, K = a.shape
-    B = -(-K // 128)
-    if a.stride(1) != 1 or not w.is_contiguous() or not w_scales.is_contiguous():
+    N, B = wshape[-2], -(-K // 128)
+    if a.dtype not in _CODES or w.dtype not in _CODES:
+        raise MoEError(MOE_ERR_DTYPE, f"a and w must be E4M3 codes, not {a.dtype} and {w.dtype}")
+    st, sv = a.stride()
+    if sv != 1 or not w.is_contiguous() or not w_scales.is_contiguous():
         raise MoEError(MOE_ERR_UNSUPPORTED, "the codes of a row must be contiguous, w and w_scales dense")
-    want = (*w.shape[:-2], -(-w.size(-2) // 128), B)
-    if w_scales.dtype is not torch.float32 or w_scales.shape != want or w_scales.device != dev:
-        raise MoEError(MOE_ERR_SHAPE, f"w_scales must be f32 {want} on {dev}")
-    return (_codes(a, "a", dev), a.stride(0) if M > 1 else K, _scales(a_scales, M, B, "a_scales", dev),
-            _codes(w, "w", dev), w_scales.data_ptr())
-
-
-def _block_out(a, rows, N, out, out_dtype, stream):
-    if out is None:
-        out = _made(a, (rows, N), out_dtype, stream)
-    return (out, *_rows(out, (rows, N), "out", a.device))
+    if w.device != dev or w_scales.device != dev:
+        raise MoEError(MOE_ERR_UNSUPPORTED, f"w and w_scales must be on {dev}")
+    want = (-(-N // 128), B) if dims == 2 else (wshape[0], -(-N // 128), B)
+    if w_scales.dtype is not torch.float32 or w_scales.shape != want:
+        raise MoEError(MOE_ERR_SHAPE, f"w_scales must be f32 {want}")
+    return M, N, K, a.data_ptr(), st if M > 1 else K, _scales(a_scales, M, B, "a_scales", dev), w.data_ptr(), w_scales.data_ptr()
 
 
 def moe_block_matmul(a, a_scales, w, w_scales, out=None, out_dtype=torch.bfloat16, stream=None):
     """a [M, K] and w [N, K] of E4M3 codes, a_scales f32 [M, ceil(K / 128)] (any
     strides), w_scales f32 [ceil(N / 128), ceil(K / 128)] -> out [M, N]."""
-    ap, ast, (sp, sr, sb), wp, wsp = _block_operands(a, a_scales, w, w_scales, 2)
-    out, op, oc, os_ = _block_out(a, a.size(0), w.size(0), out, out_dtype, stream)
-    _run(a.device, stream, lib().moe_block_matmul, ap, ast, sp, sr, sb, wp, wsp, a.size(0), w.size(0), a.size(1), op, oc,
-         os_)
+    dev = a.device
+    M, N, K, ap, ast, (sp, sr, sb), wp, wsp = _block_operands(a, a_scales, w, w_scales, 2)
+    if out is None:
+        out = _made(a, (M, N), out_dtype, stream)
+    op, oc, ost = _rows(out, M, N, "out", dev)
+    _run(dev, stream, lib().moe_block_matmul, ap, ast, sp, sr, sb, wp, wsp, M, N, K, op, oc, ost)
     return out
 
 
@@ -803,15 +815,17 @@ def moe_block_matmul_grouped(a, a_scales, w, w_scales, alignment, topk=None, M=N
     tokens (M of them; default: all) and a place reads its pair's token; without,
     a [rows, K] is in expert order.  Padding rows are zero, those from num_padded
     on as they were (in a new tensor: anything)."""
-    ap, ast, (sp, sr, sb), wp, wsp = _block_operands(a, a_scales, w, w_scales, 3)
-    E, N, K = w.shape
+    dev = a.device
+    A, N, K, ap, ast, (sp, sr, sb), wp, wsp = _block_operands(a, a_scales, w, w_scales, 3)
     if topk is None:
-        al = _alignment(alignment, alignment.pair_pos.size(0), 1, E, a.device)
+        al, rows = _segments(alignment, alignment.pair_pos.size(0), 1, w.size(0), dev)
     else:
-        al = _alignment(alignment, a.size(0) if M is None else M, topk, E, a.device)
-    out, op, oc, os_ = _block_out(a, al.rows, N, out, out_dtype, stream)
-    _run(a.device, stream, lib().moe_block_matmul_grouped, ctypes.byref(al), ap, ast, a.size(0), sp, sr, sb, wp, wsp, N, K,
-         0 if topk is None else 1, op, oc, os_)
+        al, rows = _segments(alignment, A if M is None else M, topk, w.size(0), dev)
+    if out is None:
+        out = _made(a, (rows, N), out_dtype, stream)
+    op, oc, ost = _rows(out, rows, N, "out", dev)
+    _run(dev, stream, lib().moe_block_matmul_grouped, al, ap, ast, A, sp, sr, sb, wp, wsp, N, K,
+         0 if topk is None else 1, op, oc, ost)
     return out
 
 
@@ -902,6 +916,58 @@ class FusedMoE:
                               self.alignment, self.out, self.workspace, self.w13_scale,
                               self.w2_scale, self.a1_scale, self.a2_scale, stream, events)
         return self.out
+
+
+class BlockMoE:
+    """The layer of FusedMoE with block-scaled E4M3 weights (moe_quantize_blocks
+    with block_rows 128 makes them): route and align, activations to E4M3 by token
+    and 128 channels, gate/up product, SiLU(gate) * up to E4M3, down product,
+    weighted combine.  w13 [E, 2N, K] and w2 [E, K, N] of codes, their scales f32
+    [E, ceil(2N / 128), ceil(K / 128)] and [E, ceil(K / 128), ceil(N / 128)].  The
+    products' results are held in bf16: a rounding of 2^-8 ahead of E4M3's 2^-4, or
+    of the sum over a token's experts.  Buffers are allocated once for M tokens and
+    reused, so that nothing is allocated or synchronised per call and the sequence
+    can be captured into a HIP graph; calls of one object, and replays of graphs
+    that hold them, must not overlap in time, and out holds until the next."""
+
+    def __init__(self, M, K, N, E, topk, w13, w13_scales, w2, w2_scales, block_m=None, out_dtype=torch.bfloat16,
+                 renormalize=True, device="cuda"):
+        if w13.shape != (E, 2 * N, K) or w2.shape != (E, K, N):
+            raise MoEError(MOE_ERR_SHAPE, f"w13 has shape {tuple(w13.shape)}, w2 {tuple(w2.shape)}")
+        if block_m is None:
+            # the products' tiles: rows of 16 to 64 for few tokens, then up to 256
+            block_m = 16 if M * topk <= 64 * E else (256 if M * topk >= 512 * E else 128)
+        self.M, self.topk, self.block_m, self.renormalize = M, topk, block_m, renormalize
+        self.w13, self.w13_scales, self.w2, self.w2_scales = w13, w13_scales, w2, w2_scales
+        like = dict(dtype=torch.bfloat16, device=device)
+        # the alignment's part of a workspace does not depend on the layer's sizes
+        problem = make_problem(M, 128, 128, E, topk, block_m, torch.bfloat16, torch.bfloat16, torch.bfloat16)
+        self.workspace = torch.empty(max(moe_workspace_size(problem), 16), dtype=torch.uint8, device=device)
+        self.topk_ids = torch.empty(M, topk, dtype=torch.int32, device=device)
+        self.topk_weights = torch.empty(M, topk, device=device)
+        self.alignment = alloc_alignment(M, topk, E, block_m, device)
+        rows = self.alignment.sorted_pair_ids.size(0)
+        codes = dict(dtype=torch.float8_e4m3fn, device=device)
+        self.x_codes, self.x_scales = torch.empty(M, K, **codes), torch.empty(-(-K // 128), M, device=device).t()
+        self.gate_up = torch.empty(rows, 2 * N, **like)
+        self.h_codes, self.h_scales = torch.empty(rows, N, **codes), torch.empty(-(-N // 128), rows, device=device).t()
+        self.y = torch.empty(rows, K, **like)
+        self.out = torch.empty(M, K, dtype=out_dtype, device=device)
+
+    def __call__(self, x, logits, stream=None):
+        """x [M, K] bf16/f32, logits f32 [M, E] -> out [M, K], this object's buffer."""
+        if x.shape[0] != self.M or logits.shape[0] != self.M:
+            raise MoEError(MOE_ERR_SHAPE, f"{x.shape[0]} tokens and {logits.shape[0]} rows of logits, buffers for {self.M}")
+        al = self.alignment
+        moe_route_align(logits, self.topk, self.renormalize, self.block_m, self.workspace, self.topk_ids,
+                        self.topk_weights, al, stream)
+        moe_quantize_blocks(x, codes=self.x_codes, scales=self.x_scales, stream=stream)
+        moe_block_matmul_grouped(self.x_codes, self.x_scales, self.w13, self.w13_scales, al, topk=self.topk,
+                                 out=self.gate_up, stream=stream)
+        moe_quantize_blocks(self.gate_up, gated=True, num_rows=al.num_padded, codes=self.h_codes, scales=self.h_scales,
+                            stream=stream)
+        moe_block_matmul_grouped(self.h_codes, self.h_scales, self.w2, self.w2_scales, al, out=self.y, stream=stream)
+        return moe_combine(self.y, al, self.M, self.topk, weights=self.topk_weights, out=self.out, stream=stream)
 
 
 class PagedAttention:

@@ -157,7 +157,9 @@ def test_binding_refusals():
     refused(DTYPE, moe.moe_dispatch, x, good, 2, weights=w.double())
     refused(UNSUP, moe.moe_dispatch, x, good, 2, weights=torch.zeros(2, 9).t())
     refused(SHAPE, moe.moe_dispatch, x, good, 2, out=rows[:63])
-    refused(SHAPE, moe.moe_dispatch, x, moe.Alignment(i32(64), i32(3), i32(5), i32(18), i32(1), 16), 2)
+    refused(SHAPE, moe.moe_block_matmul_grouped, torch.zeros(9, 64, dtype=torch.uint8), torch.zeros(9, 1),
+            torch.zeros(4, 8, 64, dtype=torch.uint8), torch.zeros(4, 1, 1),
+            moe.Alignment(i32(64), i32(3), i32(5), i32(18), i32(1), 16), topk=2)
     refused(DTYPE, moe.moe_dispatch, x, moe.Alignment(i32(64).long(), i32(4), i32(5), i32(18), i32(1), 16), 2)
     refused(SHAPE, moe.moe_combine, rows[:60], good, 9, 2)
     refused(DTYPE, moe.moe_dispatch_backward, rows, good, 9, 2, x=x, out=x.bfloat16())
