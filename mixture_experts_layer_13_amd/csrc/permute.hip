@@ -157,18 +157,75 @@ __global__ __launch_bounds__(kPermWaves * 64) void scatter_kernel(PermuteArgs a)
   }
 }
 
-// Rows to token.
-template <int XT, int RT, bool DOT>
+// Rows to token.  The token's pairs that have a place are listed first (of a rank's
+// experts few are left), and their rows loaded four at a time for two vectors a
+// thread, whatever topk is.
+constexpr int kListed = 4;
+
+template <int XT, int RT>
 __global__ __launch_bounds__(kPermWaves * 64) void gather_kernel(PermuteArgs a) {
   constexpr int VEC = perm_vec<XT, RT>();
+  __shared__ int place[64];
+  __shared__ float weight[64];
   const int n = a.K / VEC, step = gridDim.y * blockDim.x;
   const int v0 = blockIdx.y * blockDim.x + threadIdx.x;
   const int t = blockIdx.x;
+  int kept;
+  {
+    const int lane = threadIdx.x & 63;
+    const size_t f = (size_t)t * a.topk + min(lane, a.topk - 1);
+    const int p = a.pair_pos[f];
+    const float w = a.weights ? a.weights[f] : 1.0f;
+    const bool has = lane < a.topk && p >= 0 && p < a.rows;
+    const uint64_t all = __ballot(has);
+    kept = __popcll(all);
+    if (has && threadIdx.x < 64) {
+      const int at = __popcll(all & lanemask_lt(lane));
+      place[at] = p;
+      weight[at] = w;
+    }
+  }
+  __syncthreads();
+  for (int v = v0; v < n; v += 2 * step) {
+    const int w = min(v + step, n - 1);  // the second vector, or one that is not stored
+    float acc[2][VEC] = {};
+    for (int i = 0; i < kept; i += kListed) {
+      Raw8<RT, VEC> r[kListed][2];
+      float wt[kListed];
+#pragma unroll
+      for (int q = 0; q < kListed; ++q) {
+        const int at = min(i + q, kept - 1);
+        const size_t row = (size_t)__builtin_amdgcn_readfirstlane(place[at]) * a.rows_in_stride;
+        wt[q] = weight[at];
+        if (i + q < kept) {
+          r[q][0].load(a.rows_in, row + (size_t)v * VEC);
+          r[q][1].load(a.rows_in, row + (size_t)w * VEC);
+        }
+      }
+#pragma unroll
+      for (int q = 0; q < kListed; ++q)
+        if (i + q < kept)
+#pragma unroll
+          for (int c = 0; c < VEC; ++c) {
+            acc[0][c] = __builtin_fmaf(wt[q], r[q][0].value(c), acc[0][c]);
+            acc[1][c] = __builtin_fmaf(wt[q], r[q][1].value(c), acc[1][c]);
+          }
+    }
+    store_vec<XT, VEC>(a.tok_out, (size_t)t * a.tok_out_stride + (size_t)v * VEC, acc[0]);
+    if (v + step < n) store_vec<XT, VEC>(a.tok_out, (size_t)t * a.tok_out_stride + (size_t)w * VEC, acc[1]);
+  }
+}
+
+// The same with the products for the weights' gradient.
+template <int XT, int RT>
+__global__ __launch_bounds__(kPermWaves * 64) void gather_dot_kernel(PermuteArgs a) {
+  constexpr int VEC = perm_vec<XT, RT>();
+  const int n = a.K / VEC, step = blockDim.x, t = blockIdx.x;
   // acc += the rows of `at` at vector v, dot += their products with x
   auto take = [&](const Places& at, int v, float (&acc)[VEC], bool products, float (&dot)[kPairs]) {
     Raw8<RT, VEC> r[kPairs];
     Raw8<XT, VEC> x;
-    if (DOT && products) x.load(a.tok_in, (size_t)t * a.tok_in_stride + (size_t)v * VEC);
+    if (products) x.load(a.tok_in, (size_t)t * a.tok_in_stride + (size_t)v * VEC);
 #pragma unroll
     for (int j = 0; j < kPairs; ++j)
       if (at.p[j] >= 0) r[j].load(a.rows_in, (size_t)at.p[j] * a.rows_in_stride + (size_t)v * VEC);
@@ -178,26 +235,24 @@ __global__ __launch_bounds__(kPermWaves * 64) void gather_kernel(PermuteArgs a) 
 #pragma unroll
         for (int i = 0; i < VEC; ++i) {
           acc[i] = __builtin_fmaf(at.w[j], r[j].value(i), acc[i]);
-          if (DOT && products) dot[j] = __builtin_fmaf(x.value(i), r[j].value(i), dot[j]);
+          if (products) dot[j] = __builtin_fmaf(x.value(i), r[j].value(i), dot[j]);
         }
       }
   };
   const Places first(a, t, 0);
   float dot[kPairs] = {}, unused[kPairs];
-  for (int v = v0; v < n; v += step) {
+  for (int v = threadIdx.x; v < n; v += step) {
     float acc[VEC] = {};
     take(first, v, acc, true, dot);
     for (int j0 = kPairs; j0 < a.topk; j0 += kPairs) take(Places(a, t, j0), v, acc, false, unused);
     store_vec<XT, VEC>(a.tok_out, (size_t)t * a.tok_out_stride + (size_t)v * VEC, acc);
   }
-  if constexpr (DOT) {
-    store_dots(a, t, 0, dot);
-    for (int j0 = kPairs; j0 < a.topk; j0 += kPairs) {
-      const Places at(a, t, j0);
-      float more[kPairs] = {}, acc[VEC] = {};
-      for (int v = v0; v < n; v += step) take(at, v, acc, true, more);
-      store_dots(a, t, j0, more);
-    }
+  store_dots(a, t, 0, dot);
+  for (int j0 = kPairs; j0 < a.topk; j0 += kPairs) {
+    const Places at(a, t, j0);
+    float more[kPairs] = {}, acc[VEC] = {};
+    for (int v = threadIdx.x; v < n; v += step) take(at, v, acc, true, more);
+    store_dots(a, t, j0, more);
   }
 }
 
@@ -207,19 +262,24 @@ static void* scatter_of(int xt, int rt) {
     return rt == DT_BF16 ? (void*)scatter_kernel<DT_BF16, DT_BF16, DOT> : (void*)scatter_kernel<DT_BF16, DT_F32, DOT>;
   return rt == DT_BF16 ? (void*)scatter_kernel<DT_F32, DT_BF16, DOT> : (void*)scatter_kernel<DT_F32, DT_F32, DOT>;
 }
-template <bool DOT>
 static void* gather_of(int xt, int rt) {
+  if (xt == DT_BF16) return rt == DT_BF16 ? (void*)gather_kernel<DT_BF16, DT_BF16> : (void*)gather_kernel<DT_BF16, DT_F32>;
+  return rt == DT_BF16 ? (void*)gather_kernel<DT_F32, DT_BF16> : (void*)gather_kernel<DT_F32, DT_F32>;
+}
+static void* gather_dot_of(int xt, int rt) {
   if (xt == DT_BF16)
-    return rt == DT_BF16 ? (void*)gather_kernel<DT_BF16, DT_BF16, DOT> : (void*)gather_kernel<DT_BF16, DT_F32, DOT>;
-  return rt == DT_BF16 ? (void*)gather_kernel<DT_F32, DT_BF16, DOT> : (void*)gather_kernel<DT_F32, DT_F32, DOT>;
+    return rt == DT_BF16 ? (void*)gather_dot_kernel<DT_BF16, DT_BF16> : (void*)gather_dot_kernel<DT_BF16, DT_F32>;
+  return rt == DT_BF16 ? (void*)gather_dot_kernel<DT_F32, DT_BF16> : (void*)gather_dot_kernel<DT_F32, DT_F32>;
 }
 
-// A token's vectors over as few rounds of a workgroup of up to eight waves as will
-// do; of few tokens without products, each wave's over a workgroup of its own.
-static int permute_launch(const void* kernel, const PermuteArgs& a, int xt, int rt, long long groups, hipStream_t st) {
+// A token's vectors, `each` to a thread, over as few rounds of a workgroup of up to
+// eight waves as will do; of few tokens without products, each wave's over a
+// workgroup of its own.
+static int permute_launch(const void* kernel, const PermuteArgs& a, int xt, int rt, int each, long long groups,
+                          hipStream_t st) {
   const int vec = xt == DT_BF16 && rt == DT_BF16 ? 8 : 4;
-  const int chunks = (a.K / vec + 63) / 64, rounds = (chunks + kPermWaves - 1) / kPermWaves;
-  int waves = (chunks + rounds - 1) / rounds, parts = 1;
+  const int chunks = (a.K / vec + 63) / 64, rounds = (chunks + each * kPermWaves - 1) / (each * kPermWaves);
+  int waves = (chunks + rounds * each - 1) / (rounds * each), parts = 1;
   if (!a.dw && (long long)a.M * waves < 4 * device_cu_count()) {
     parts = chunks;
     waves = 1;
@@ -230,12 +290,12 @@ static int permute_launch(const void* kernel, const PermuteArgs& a, int xt, int 
 }
 
 int launch_scatter(const PermuteArgs& a, int xt, int rt, hipStream_t st) {
-  return permute_launch(a.dw ? scatter_of<true>(xt, rt) : scatter_of<false>(xt, rt), a, xt, rt,
+  return permute_launch(a.dw ? scatter_of<true>(xt, rt) : scatter_of<false>(xt, rt), a, xt, rt, 1,
                         a.M + ((long long)a.rows + 31) / 32, st);
 }
 
 int launch_gather(const PermuteArgs& a, int xt, int rt, hipStream_t st) {
-  return permute_launch(a.dw ? gather_of<true>(xt, rt) : gather_of<false>(xt, rt), a, xt, rt, a.M, st);
+  return permute_launch(a.dw ? gather_dot_of(xt, rt) : gather_of(xt, rt), a, xt, rt, a.dw ? 1 : 2, a.M, st);
 }
 
 }  // namespace moe
