@@ -926,8 +926,8 @@ moe_status permute(const moe_alignment* al, bool scatter, int32_t K, const void*
   if (reads_tok && (s = check_row_stride("token", tok_stride, K, te))) return s;
   if (reads_rows && (s = check_row_stride("expert row", rows_stride, K, re))) return s;
   if ((s = check_row_stride("output", out_stride, K, scatter ? re : te))) return s;
-  if (al->M == 0) return ok();
-  if (!al->pair_pos || !out || (reads_tok && !tok) || (reads_rows && !rows && al->rows))
+  if (al->M == 0 || (scatter && al->rows == 0 && !dw)) return ok();
+  if (!al->pair_pos || (!out && !(scatter && al->rows == 0)) || (reads_tok && !tok) || (reads_rows && !rows && al->rows))
     return fail(MOE_ERR_NULL, "pair_pos, the inputs and the output are required");
   if (scatter && (!al->sorted_pair_ids || !al->num_padded) && al->rows)
     return fail(MOE_ERR_NULL, "sorted_pair_ids and num_padded are required");

@@ -808,17 +808,18 @@ def moe_block_matmul(a, a_scales, w, w_scales, out=None, out_dtype=torch.bfloat1
     return out
 
 
-def moe_block_matmul_grouped(a, a_scales, w, w_scales, alignment, topk=None, M=None, out=None,
+def moe_block_matmul_grouped(a, a_scales, w, w_scales, alignment, topk=None, M=None, pairs=None, out=None,
                              out_dtype=torch.bfloat16, stream=None):
     """The rows of an alignment times their experts' weights w [E, N, K], w_scales
     f32 [E, ceil(N / 128), ceil(K / 128)] -> out [rows, N].  With topk, a holds
     tokens (M of them; default: all) and a place reads its pair's token; without,
-    a [rows, K] is in expert order.  Padding rows are zero, those from num_padded
-    on as they were (in a new tensor: anything)."""
+    a [rows, K] is in expert order, of `pairs` pairs (default: pair_pos's size;
+    less where the buffers were made for more tokens).  Padding rows are zero,
+    those from num_padded on as they were (in a new tensor: anything)."""
     dev = a.device
     A, N, K, ap, ast, (sp, sr, sb), wp, wsp = _block_operands(a, a_scales, w, w_scales, 3)
     if topk is None:
-        al, rows = _segments(alignment, alignment.pair_pos.size(0), 1, w.size(0), dev)
+        al, rows = _segments(alignment, alignment.pair_pos.size(0) if pairs is None else pairs, 1, w.size(0), dev)
     else:
         al, rows = _segments(alignment, A if M is None else M, topk, w.size(0), dev)
     if out is None:

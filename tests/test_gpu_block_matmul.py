@@ -219,6 +219,29 @@ def test_grouped_rows_trimmed_and_odd_strides():
         assert (out[rows:] == 3).all() and (out[:, N:] == 3).all()
 
 
+@pytest.mark.parametrize("bm", [16, 128])
+def test_grouped_buffers_made_for_more_tokens(bm):
+    """An alignment's buffers used again for fewer tokens: their padding marks are
+    fewer pairs than the buffers hold."""
+    M, k, E, N, K = 30, 2, 4, 96, 144
+    big = moe.alloc_alignment(200, k, E, bm, B.DEV)
+    ids, al, pos, n = B.aligned(M, k, E, bm, 5)
+    ws = torch.empty(moe.moe_workspace_size(moe.make_problem(M, 128, 128, E, k, bm, *[torch.bfloat16] * 3)), dtype=torch.uint8,
+                     device=B.DEV)
+    moe.moe_align_permute(B.dev(ids.astype(np.int32)), E, bm, ws, alignment=big)
+    R = big.sorted_pair_ids.numel()
+    a, sa, w, sw = operands(R, N, K, 3, E)
+    want = moe.moe_block_matmul_grouped(B.fp8(a)[:al.sorted_pair_ids.numel()], B.dev(sa)[:al.sorted_pair_ids.numel()], B.fp8(w),
+                                        B.dev(sw), al)
+    got = moe.moe_block_matmul_grouped(B.fp8(a), B.dev(sa), B.fp8(w), B.dev(sw), big, pairs=M * k)
+    assert torch.equal(got[:n], want[:n])
+    pad = np.ones(n, bool)
+    pad[pos[pos >= 0]] = False
+    assert pad.any() and (got[:n].cpu().float().numpy()[pad] == 0).all()
+    tok = moe.moe_block_matmul_grouped(B.fp8(a)[:200], B.dev(sa)[:200], B.fp8(w), B.dev(sw), big, topk=k, M=M)
+    assert (tok[:n].cpu().float().numpy()[pad] == 0).all()
+
+
 def test_results_repeat_and_streams():
     a, sa, w, sw = operands(300, 512, 1024, 6)
     args = (B.fp8(a), B.dev(sa), B.fp8(w), B.dev(sw))

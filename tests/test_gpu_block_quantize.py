@@ -154,3 +154,14 @@ def test_scales_in_any_layout():
 def test_no_rows():
     c, s = moe.moe_quantize_blocks(torch.empty(0, 256, device=B.DEV))
     assert c.shape == (0, 256) and s.shape == (0, 2)
+
+
+def test_offsets_past_32_bits():
+    """More than 2^31 values: the last rows as by themselves."""
+    M, K = 300000, 8192
+    x = torch.randn(M, K, dtype=torch.bfloat16, device=B.DEV)
+    codes, scales = moe.moe_quantize_blocks(x)
+    assert codes.numel() > 2 ** 31
+    c, s = moe.moe_quantize_blocks(x[-40:])
+    assert torch.equal(codes[-40:].view(torch.uint8), c.view(torch.uint8)) and torch.equal(scales[-40:], s)
+    check(x[-40:].cpu(), c, s)

@@ -231,3 +231,18 @@ def test_other_streams_and_a_graph():
         for j, (a, b) in enumerate(zip(held, eager)):
             m = n if j == 1 else None
             assert torch.equal(a[:m], b[:m]), (i, j)
+
+
+def test_no_rows_at_all():
+    """An alignment cut to nothing: tokens get zeros, weights the gradient 0."""
+    M, K, k = 6, 64, 2
+    i32 = lambda n, v=0: torch.full((n,), v, dtype=torch.int32, device=B.DEV)
+    al = moe.Alignment(i32(0), i32(0), i32(4), i32(M * k, -1), i32(1), 16)
+    x = B.values((M, K), "f32", 1).to(B.DEV)
+    rows = moe.moe_dispatch(x, al, k)
+    assert rows.shape == (0, K)
+    assert (moe.moe_combine(rows, al, M, k) == 0).all()
+    d_rows, dw = moe.moe_combine_backward(x, al, k, rows=rows)
+    assert d_rows.shape == (0, K) and (dw == 0).all()
+    dx, dw = moe.moe_dispatch_backward(rows, al, M, k, x=x)
+    assert (dx == 0).all() and (dw == 0).all()
