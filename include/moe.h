@@ -686,7 +686,7 @@ moe_status moe_block_matmul(const uint8_t* a, int64_t a_stride, const float* a_s
  *            expert order (a_rows >= alignment->rows).
  * w, w_scales  device [E][N][K] and f32 [E][ceil(N / 128)][B], dense.
  * out        [alignment->rows, N].
- * Reads all of the alignment but pair_pos; E 1..1024, block_m as in
+ * Wants all of the alignment but pair_pos; E 1..1024, block_m as in
  * moe_align_permute.  M == 0 or rows == 0 is a no-op.  Errors as above;
  * MOE_ERR_SHAPE also where the tiles of rows x N are more than a grid has.
  */

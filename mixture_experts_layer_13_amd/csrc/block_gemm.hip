@@ -40,15 +40,7 @@ struct BTile {
 // consecutive tiles, in groups of kGroup spans times all of N, so that the rows
 // and weights that they share meet in that XCD's L2.
 constexpr int kGroup = 4;
-template <int TM>
-__device__ __forceinline__ bool b_tile(const BlockGemmArgs& g, int ntn, int& span, int& nt) {
-  int spans;
-  if (!g.ids) {
-    spans = (g.M + TM - 1) / TM;
-  } else {
-    const int n = min(*g.num_padded, g.R), step = g.bm >= TM ? TM : g.bm;
-    spans = (n + step - 1) / step;
-  }
+__device__ __forceinline__ bool b_tile(int spans, int ntn, int& span, int& nt) {
   const int total = spans * ntn;
   if ((int)blockIdx.x >= total) return false;
   const int xcd = blockIdx.x % 8, per = total / 8, rem = total % 8;
@@ -78,8 +70,9 @@ __global__ __launch_bounds__(WN * WM * 64) void block_gemm_kernel(BlockGemmArgs 
   const int l16 = lane & 15, grp = lane >> 4;
 
   int span, nt;
-  if (!b_tile<TM>(g, ntn, span, nt)) return;
-  const RowSpan s = row_span<TM>(g, span);
+  const RowSpans<TM> all(g);
+  if (!b_tile(all.total, ntn, span, nt)) return;
+  const RowSpan s = all.at(g, span);
   if (s.rows <= 0) return;
   const int n0 = nt * TN;
 

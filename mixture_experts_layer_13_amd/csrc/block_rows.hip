@@ -39,7 +39,7 @@ __global__ __launch_bounds__(WAVES * 64) void block_rows_kernel(BlockGemmArgs g,
   __shared__ __attribute__((aligned(16))) char parts[R::kParts > R::kOne ? R::kParts : 16];
   const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int l16 = lane & 15, grp = lane >> 4;
-  const RowSpan s = row_span<16 * MB>(g, blockIdx.x / ntn);
+  const RowSpan s = RowSpans<16 * MB>(g).at(g, blockIdx.x / ntn);
   if (s.rows <= 0) return;
   const int n0 = (int)(blockIdx.x % ntn) * 16 * NB;
 
