@@ -364,25 +364,37 @@ static int block_gemm_launch(const BlockGemmArgs& g, hipStream_t st) {
 //   256 x 256   51.1  52.0  51.2  50.9  52.3  65.2
 // fp32 out (operands twice as wide, half the rate): 64 x 64 17.1 at 1037 x 1544 x
 // 2000 (128 x 128 21.6), 256 x 128 262 at 8192 x 4096 x 4096 (128 x 128 312).
+// Rows of experts, of uneven numbers (falling like 1 / (rank + 3)), by their average:
+// us for 64 experts x 2048 x 4096 | 16 x 1408 x 2048
+//   rows           8            16           32           64          128          256          512
+//   few (16)    113 | 13.1   139 | 15.8   200 | 21     343 | 29
+//   few (32)    115 | 13.7   129 | 14.6   159 | 18     254 | 26
+//   64 x 64     122 | 12.8   132 | 13.3   133 | 13.5   157 | 13.3   242 | 23     413 | 38
+//   128 x 128   140 | 12.8   141 | 13.0   157 | 13.8   147 | 14.3   187 | 16     287 | 28   (four stages)
+//   128 x 128                142 | 15.9   166 | 16.2   165 | 17.2   183 | 18     279 | 25     485 | 44
+//   256 x 256                147 | 21.4   149 | 22.4   190 | 23.0   196 | 29     217 | 31     358 | 36
 int launch_block_product(const BlockGemmArgs& g, int ot, hipStream_t st) {
   const long long cu = device_cu_count();
   // rows of a batch, or of the average expert
   const long long m = g.ids ? (std::min(g.pairs, g.R) + g.E - 1) / g.E : g.M;
   auto tiles = [&](int tn, int tm) { return ((long long)g.N + tn - 1) / tn * spans_estimate(g, tm); };
-  if (m <= 64 || tiles(32, 64) <= cu) return launch_block_rows(g, ot, (int)std::min(m, 64LL), st);
+  if (tiles(32, 64) <= cu || (!g.ids && m <= 64)) return launch_block_rows(g, ot, (int)std::min(m, 64LL), st);
+  if (g.ids && m <= 16) return launch_block_rows(g, ot, m <= 8 ? 16 : 32, st);
   if (ot == DT_F32) {
-    if (tiles(64, 64) <= 2 * cu) return block_gemm_launch<64, 64, 2, 2, 4, DT_F32>(g, st);
+    if (tiles(64, 64) <= 2 * cu || m <= 96) return block_gemm_launch<64, 64, 2, 2, 4, DT_F32>(g, st);
     if (tiles(128, 128) <= cu) return block_gemm_launch<128, 128, 2, 4, 4, DT_F32>(g, st);
     return block_gemm_launch<256, 128, 4, 2, 2, DT_F32>(g, st);
   }
-  if (tiles(64, 64) <= cu) return block_gemm_launch<64, 64, 2, 2, 4, DT_BF16>(g, st);
-  if (tiles(64, 128) <= cu) return block_gemm_launch<64, 128, 2, 2, 4, DT_BF16>(g, st);
   const long long t = tiles(128, 128);
-  if (t <= cu) return block_gemm_launch<128, 128, 2, 4, 4, DT_BF16>(g, st);
-  // rounds over the chip, in hundredths of the larger tile's
-  const long long last = t % (2 * cu), large = (tiles(256, 256) + cu - 1) / cu * 100;
+  if (g.ids ? m <= 48 : tiles(64, 64) <= cu) return block_gemm_launch<64, 64, 2, 2, 4, DT_BF16>(g, st);
+  if (!g.ids && tiles(64, 128) <= cu) return block_gemm_launch<64, 128, 2, 2, 4, DT_BF16>(g, st);
+  if (t <= cu || (g.ids && m <= 96)) return block_gemm_launch<128, 128, 2, 4, 4, DT_BF16>(g, st);
+  // rounds over the chip, in hundredths of the larger tile's; experts' last tiles, of
+  // less work than the others, fill the larger tile's last round
+  const long long last = t % (2 * cu), n = tiles(256, 256);
+  const long long large = g.ids ? std::max(100LL, n * 100 / cu) : (n + cu - 1) / cu * 100;
   const long long small = t / (2 * cu) * 67 + (last == 0 ? 0 : last <= cu ? 50 : 67);
-  if (small < large) return block_gemm_launch<128, 128, 2, 4, 2, DT_BF16>(g, st);
+  if (small < large || (g.ids && m < 192)) return block_gemm_launch<128, 128, 2, 4, 2, DT_BF16>(g, st);
   return block_gemm_launch<256, 256, 2, 4, 2, DT_BF16>(g, st);
 }
 
