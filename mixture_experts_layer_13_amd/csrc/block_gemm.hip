@@ -70,8 +70,8 @@ __global__ __launch_bounds__(WN * WM * 64) void block_gemm_kernel(BlockGemmArgs 
   const int l16 = lane & 15, grp = lane >> 4;
 
   int span, nt;
-  const RowSpans<TM> all(g);
-  if (!b_tile(all.total, ntn, span, nt)) return;
+  RowSpans<TM> all;
+  if (!b_tile(all.total(g), ntn, span, nt)) return;
   const RowSpan s = all.at(g, span);
   if (s.rows <= 0) return;
   const int n0 = nt * TN;
@@ -91,11 +91,13 @@ __global__ __launch_bounds__(WN * WM * 64) void block_gemm_kernel(BlockGemmArgs 
   uint32_t woff[2], aoff[MOVED ? B::ALoads : 2];
 #pragma unroll
   for (int q = 0; q < 2; ++q) woff[q] = (uint32_t)(lane >> 3) * g.K + lcol(q);
+  auto source = [&](int r) { return r < s.rows ? source_row(g, s.row0 + r, g.ids ? g.ids[s.row0 + r] : 0) : -1; };
   if constexpr (MOVED) {
+    static_assert(B::ALoads <= 8, "a lane for each row that this wave loads");
+    const int mine = source(a0 + (lane & (8 * B::ALoads - 1)));
 #pragma unroll
     for (int q = 0; q < B::ALoads; ++q) {
-      const int r = a0 + q * 8 + (lane >> 3);
-      const int at = r < s.rows ? source_row(g, s.row0 + r) : -1;
+      const int at = __shfl(mine, q * 8 + (lane >> 3), kWave);
       aoff[q] = at >= 0 ? (uint32_t)(at * g.a_stride) + lcol((wv * B::ALoads + q) & 1) : kNowhere;
     }
   } else {
@@ -108,7 +110,7 @@ __global__ __launch_bounds__(WN * WM * 64) void block_gemm_kernel(BlockGemmArgs 
   uint32_t soff;
   if (rowscales) {
     int r = min(wv * 64 + lane, s.rows - 1);
-    if (MOVED) r = max(source_row(g, s.row0 + r), 0);
+    if (MOVED) r = max(source(r), 0);
     soff = (uint32_t)(r * g.as_m) * 4;
   } else {
     soff = (uint32_t)min(n0 / 128 + lane, g.NB - 1) * g.KB * 4;
@@ -142,26 +144,13 @@ __global__ __launch_bounds__(WN * WM * 64) void block_gemm_kernel(BlockGemmArgs 
     }
   };
 
-  // which waves have real rows of a; where none has, there is nothing to multiply
-  bool some = !g.ids, busy = !g.ids;
-  if (g.ids) {
-#pragma unroll
-    for (int q = 0; q < TM / 64; ++q) {
-      const int r = q * 64 + lane;
-      const uint64_t real = __ballot(r < s.rows && source_row(g, s.row0 + r) >= 0);
-      some |= real != 0;
-      constexpr int W = TM / WM;  // a wave's rows: whole multiples of 64, or a part
-      if (W >= 64 ? (q * 64) / W == wm : q == wm * W / 64)
-        busy |= W >= 64 ? real != 0 : (real >> (wm * W % 64) & ((1ull << (W % 64)) - 1)) != 0;
-    }
-  }
-  if (!some) {
-    zero_rows<OT>(g, s, n0, TN, WN * WM * 64);
-    return;
-  }
+  // which of this wave's rows are real
+  constexpr int WTN = TN / WN, WTM = TM / WM;
+  static_assert(WTM <= 64, "a bit for each");
+  const uint64_t real = __ballot((lane & (WTM - 1)) == lane && source(WTM * wm + lane) >= 0);
 
   f32x4 acc[NI][MJ] = {};
-  const int nb = (TN / WN) * wn, mb = (TM / WM) * wm;  // this wave's first rows
+  const int nb = WTN * wn, mb = WTM * wm;  // this wave's first rows
   const int wsat = TM + (n0 % 128 + nb) / 128;
   BOperand16<WIDE> af[2], bf[2][MJ];
   float sc[2][MJ] = {};
@@ -241,7 +230,7 @@ __global__ __launch_bounds__(WN * WM * 64) void block_gemm_kernel(BlockGemmArgs 
   const std::integral_constant<int, 0> even{};
   const std::integral_constant<int, 1> odd{};
   int b = 0;
-  if (!busy) {  // none of this wave's rows of a is real: it loads and keeps the barriers
+  if (!real) {  // none of this wave's rows of a is real: it loads and keeps the barriers
     b_for<EARLY, B::Loads>([&](auto v) { load(v, STAGES - 1, STAGES > 2 ? stage3 : stage1); });
     for (; b < g.KB; ++b) {
       b_wait_vmcnt<(STAGES - 2) * B::Loads>();
@@ -286,7 +275,7 @@ __global__ __launch_bounds__(WN * WM * 64) void block_gemm_kernel(BlockGemmArgs 
   // 16 j + l mod 16.  bf16 rows go through this wave's part of LDS (behind a
   // barrier: the others may still read theirs), 16-byte column c of row r at
   // c ^ r, so that a store writes whole row pieces of the wave.
-  constexpr int WTN = TN / WN, WTM = TM / WM;
+  zero_rows<OT>(g, s, n0, TN, WN * WM * 64);
   b_barrier();
   if (OT == DT_BF16 && g.vec && n0 + nb + WTN <= g.N) {
     constexpr int kRowBytes = WTN * 2, kPieces = kRowBytes / 16, kRowsAtOnce = 64 / kPieces;
@@ -294,11 +283,10 @@ __global__ __launch_bounds__(WN * WM * 64) void block_gemm_kernel(BlockGemmArgs 
     char* mine = (wv < B::kWaves / 2 ? stage0 : stage1) + (wv % (B::kWaves / 2)) * WTM * kRowBytes;
 #pragma unroll
     for (int j = 0; j < MJ; ++j) {
-      const int r = mb + 16 * j + l16;
-      const bool real = r < s.rows && source_row(g, s.row0 + r) >= 0;
+      const bool kept = real >> (16 * j + l16) & 1;
 #pragma unroll
       for (int i = 0; i < NI; ++i) {
-        const f32x4 v = real ? acc[i][j] : f32x4{};
+        const f32x4 v = kept ? acc[i][j] : f32x4{};
         const int c = (2 * i + (grp >> 1)) ^ (l16 & (kPieces - 1));
         *reinterpret_cast<uint2*>(mine + (16 * j + l16) * kRowBytes + c * 16 + (grp & 1) * 8) =
             make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
@@ -314,25 +302,54 @@ __global__ __launch_bounds__(WN * WM * 64) void block_gemm_kernel(BlockGemmArgs 
     }
     return;
   }
+  // Rows that do not begin on 16 bytes: 16 at a time through LDS as well, a lane a
+  // column, so that a store writes 64 values in a row (3766 x 6429 x 400 fp32 100 us
+  // with each lane its four, 62).
+  if (!g.vec) {
+    constexpr int kRow = WTN + 4, kCols = WTN < 64 ? WTN : 64;
+    static_assert(16 * kRow * 4 * (B::kWaves / 2) <= B::kStage, "half of the waves in each of two stages");
+    float* mine =
+        reinterpret_cast<float*>((wv < B::kWaves / 2 ? stage0 : stage1) + (wv % (B::kWaves / 2)) * 16 * kRow * 4);
+#pragma unroll
+    for (int j = 0; j < MJ; ++j) {
+      const bool kept = real >> (16 * j + l16) & 1;
+#pragma unroll
+      for (int i = 0; i < NI; ++i)
+        *reinterpret_cast<f32x4*>(mine + l16 * kRow + 16 * i + 4 * grp) = kept ? acc[i][j] : f32x4{};
+#pragma unroll
+      for (int q = 0; q < 16 * WTN / 64; ++q) {
+        const int r = q * 64 / WTN + (WTN < 64 ? lane / kCols : 0), c = q * 64 % WTN + lane % kCols;
+        const float v = mine[r * kRow + c];
+        if (mb + 16 * j + r < s.rows && n0 + nb + c < g.N) {
+          const size_t at = (size_t)(s.row0 + mb + 16 * j + r) * g.out_stride + n0 + nb + c;
+          if constexpr (OT == DT_BF16)
+            reinterpret_cast<uint16_t*>(g.out)[at] = (uint16_t)f32_to_bf16_bits(v);
+          else
+            reinterpret_cast<float*>(g.out)[at] = v;
+        }
+      }
+    }
+    return;
+  }
 #pragma unroll
   for (int j = 0; j < MJ; ++j) {
     const int r = mb + 16 * j + l16;
     if (r >= s.rows) continue;
-    const bool real = source_row(g, s.row0 + r) >= 0;
+    const bool kept = real >> (16 * j + l16) & 1;
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
-      const f32x4 v = real ? acc[i][j] : f32x4{};
+      const f32x4 v = kept ? acc[i][j] : f32x4{};
       const int n = n0 + nb + 16 * i + 4 * grp;
       const size_t at = (size_t)(s.row0 + r) * g.out_stride + n;
       if constexpr (OT == DT_BF16) {
         uint16_t* p = reinterpret_cast<uint16_t*>(g.out) + at;
-        if (g.vec && n + 4 <= g.N)
+        if (n + 4 <= g.N)
           *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
         else
           for (int c = 0; c < 4 && n + c < g.N; ++c) p[c] = (uint16_t)f32_to_bf16_bits(v[c]);
       } else {
         float* p = reinterpret_cast<float*>(g.out) + at;
-        if (g.vec && n + 4 <= g.N)
+        if (n + 4 <= g.N)
           *reinterpret_cast<f32x4*>(p) = v;
         else
           for (int c = 0; c < 4 && n + c < g.N; ++c) p[c] = v[c];

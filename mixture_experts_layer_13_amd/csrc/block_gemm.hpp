@@ -41,9 +41,10 @@ struct BlockGemmArgs {
   int E, bm, R, pairs, topk;  // topk 0: a is in the alignment's order too
 };
 
-// Rows row0 .. row0 + rows - 1 of out, those of one expert.
+// Rows row0 .. row0 + rows - 1 of out, those of one expert; the `empty` rows behind
+// them are padding that no other span has.
 struct RowSpan {
-  int row0, rows, e;
+  int row0, rows, e, empty;
 };
 
 #ifdef __HIPCC__
@@ -110,84 +111,105 @@ __device__ __forceinline__ int b_sum_to(int v) {
 }
 
 // The spans of up to TM rows that the rows fall into, none of two experts, in order.
-// Of blocks no shorter than a span these are whole parts of a block.  Else an expert's
-// begin with its first row, and lane l counts those of the experts l c to
-// l c + c - 1, c = ceil(E / 64).  (Numbering the blocks, and leaving those that start
-// no span, gave every second workgroup nothing to do where blocks are half a span:
-// half of the shader engines, to which they are dealt in turn, stood idle.  64
-// experts of 1024 rows x 2048 x 4096 in blocks of 128 907 us, of 16 1956, now both
-// 615 as in blocks of 256.)
+// An expert's begin with its first row; those of padding alone, which blocks longer
+// than a span can end in, are left to the last one with rows (`empty`).  They are
+// counted by 64 experts at a time, a lane each; where blocks are as long as spans,
+// span i is block i.
+// (One span for every TM rows, or for every block, cost the workgroups that only
+// found out that there is nothing to do their slots on the chip, and worse where they
+// came in a pattern: every second one means half of the shader engines, to which
+// workgroups are dealt in turn.  64 experts of 1024 rows x 2048 x 4096 in blocks of
+// 128 907 us, of 16 1956, now both 587 as in blocks of 256; 49 experts of 149 rows x
+// 680 x 3872 in blocks of 256 78 -> 47.)
 template <int TM>
 struct RowSpans {
-  int total, c, before, count, from, to;
-  __device__ __forceinline__ explicit RowSpans(const BlockGemmArgs& g) {
-    if (!g.ids || g.bm >= TM) {
-      total = ((g.ids ? min(*g.num_padded, g.R) : g.M) + TM - 1) / TM;
-      return;
+  int from, to, count, before;  // this lane's expert of the 64 looked at
+  // Looks at the experts e0 .. e0 + 63, `ahead` spans being those of the experts
+  // before; returns the spans with these.
+  __device__ __forceinline__ int look(const BlockGemmArgs& g, int e0, int ahead) {
+    const int e = e0 + (threadIdx.x & 63);
+    from = min(g.offsets[min(e, g.E)], g.R);
+    to = min(g.offsets[min(e + 1, g.E)], g.R);
+    count = (to - from + TM - 1) / TM;
+    if (g.bm > TM && count > 0) {
+      // the spans of its last block up to the last one whose first row is a pair's
+      const int parts = g.bm / TM;
+      int last = (count - 1) / parts * parts, end = min(count, last + parts);
+      for (int step = parts > 4 ? parts / 4 : 1;; step = 1) {
+        int more = 0;
+#pragma unroll
+        for (int k = 1; k <= 3; ++k) {
+          const int c = last + k * step, f = g.ids[from + min(c, count - 1) * TM];
+          more += c < end && f >= 0 && f < g.pairs;
+        }
+        last += more * step;
+        end = min(end, last + step);
+        if (step == 1) break;
+      }
+      count = last + 1;
     }
-    const int lane = threadIdx.x & 63;
-    c = (g.E + 63) >> 6;
-    count = 0;
-    to = min(g.offsets[min(lane * c, g.E)], g.R);
-    for (int q = 1; q <= c; ++q) {
-      from = to;
-      to = min(g.offsets[min(lane * c + q, g.E)], g.R);
-      count += (to - from + TM - 1) / TM;
-    }
-    const int upto = b_sum_to(count);
+    const int upto = ahead + b_sum_to(count);
     before = upto - count;
-    total = __builtin_amdgcn_readlane(upto, 63);
+    return __builtin_amdgcn_readlane(upto, 63);
   }
-  // span number i; rows = 0: none
-  __device__ __forceinline__ RowSpan at(const BlockGemmArgs& g, int i) const {
-    RowSpan s{0, 0, 0};
-    if (i >= total) return s;
-    if (!g.ids || g.bm >= TM) {
+  static __device__ __forceinline__ bool plain(const BlockGemmArgs& g) { return !g.ids || g.bm == TM; }
+  static __device__ __forceinline__ int rows(const BlockGemmArgs& g) {
+    return g.ids ? min(*g.num_padded, g.R) : g.M;
+  }
+  // How many there are.
+  __device__ __forceinline__ int total(const BlockGemmArgs& g) {
+    if (plain(g)) return (rows(g) + TM - 1) / TM;
+    int n = 0;
+    for (int e0 = 0; e0 < g.E; e0 += 64) n = look(g, e0, n);
+    return n;
+  }
+  // Span number i, less than the grid's; rows = 0: none.
+  __device__ __forceinline__ RowSpan at(const BlockGemmArgs& g, int i) {
+    RowSpan s{0, 0, 0, 0};
+    if (plain(g)) {
       s.row0 = i * TM;
-      s.rows = min(TM, (g.ids ? min(*g.num_padded, g.R) : g.M) - s.row0);
-      if (g.ids) s.e = g.block_expert[s.row0 / g.bm];
+      if (g.ids) s.e = g.block_expert[i];  // (asked for along with the number of rows)
+      s.rows = max(min(TM, rows(g) - s.row0), 0);
       if (s.e < 0 || (g.ids && s.e >= g.E)) s.rows = 0;
       return s;
     }
-    const int own = __builtin_ctzll(__ballot(i >= before && i < before + count));
-    int k = i - __builtin_amdgcn_readlane(before, own);  // the span of these experts
-    int b = __builtin_amdgcn_readlane(from, own), e = __builtin_amdgcn_readlane(to, own);
-    s.e = own * c;
-    if (c > 1) {
-      for (;; ++s.e) {
-        b = min(g.offsets[s.e], g.R);
-        e = min(g.offsets[s.e + 1], g.R);
-        const int n = (e - b + TM - 1) / TM;
-        if (k < n) break;
-        k -= n;
-      }
+    for (int e0 = 0, n = 0; e0 < g.E; e0 += 64) {
+      n = look(g, e0, n);
+      if (i >= n) continue;
+      const int own = __builtin_ctzll(__ballot(i >= before && i < before + count));
+      const int k = i - __builtin_amdgcn_readlane(before, own);
+      s.e = e0 + own;
+      s.row0 = __builtin_amdgcn_readlane(from, own) + k * TM;
+      const int left = __builtin_amdgcn_readlane(to, own) - s.row0;
+      s.rows = min(TM, left);
+      if (k == __builtin_amdgcn_readlane(count, own) - 1) s.empty = left - s.rows;
+      break;
     }
-    s.row0 = b + k * TM;
-    s.rows = min(TM, e - s.row0);
     return s;
   }
 };
 
-// The row of a that out row `row` comes from, -1: none (the row is zero).
-__device__ __forceinline__ int source_row(const BlockGemmArgs& g, int row) {
+// The row of a that out row `row`, of pair f, comes from, -1: none (the row is zero).
+__device__ __forceinline__ int source_row(const BlockGemmArgs& g, int row, int f) {
   if (!g.ids) return row;
-  const int f = g.ids[row];
   if (f < 0 || f >= g.pairs) return -1;
   const int at = g.topk ? f / g.topk : row;
   return at < g.M ? at : -1;
 }
 
-// Zeros for the columns n0 .. n0 + cols - 1 of a span none of whose rows is real.
+// Zeros for the columns n0 .. n0 + cols - 1 of a span's rows of padding.
 template <int OT>
 __device__ __forceinline__ void zero_rows(const BlockGemmArgs& g, const RowSpan& s, int n0, int cols, int threads) {
+  if (s.empty <= 0) return;
+  const int row0 = s.row0 + s.rows;
   constexpr int V = OT == 1 ? 8 : 4;  // values in 16 bytes
   const int n1 = min(n0 + cols, g.N), w = g.vec ? (n1 - n0) / V : 0, rest = n1 - n0 - w * V;
-  for (int q = threadIdx.x; q < s.rows * w; q += threads) {
-    const size_t at = (size_t)(s.row0 + q / w) * g.out_stride + n0 + q % w * V;
+  for (int q = threadIdx.x; q < s.empty * w; q += threads) {
+    const size_t at = (size_t)(row0 + q / w) * g.out_stride + n0 + q % w * V;
     *reinterpret_cast<b_i32x4*>(reinterpret_cast<char*>(g.out) + at * (16 / V)) = b_i32x4{};
   }
-  for (int q = threadIdx.x; q < s.rows * rest; q += threads) {
-    const size_t at = (size_t)(s.row0 + q / rest) * g.out_stride + n0 + w * V + q % rest;
+  for (int q = threadIdx.x; q < s.empty * rest; q += threads) {
+    const size_t at = (size_t)(row0 + q / rest) * g.out_stride + n0 + w * V + q % rest;
     if constexpr (OT == 1)
       reinterpret_cast<uint16_t*>(g.out)[at] = 0;
     else
@@ -198,9 +220,13 @@ __device__ __forceinline__ void zero_rows(const BlockGemmArgs& g, const RowSpan&
 
 // At most so many spans of up to tm rows.
 inline long long row_spans(const BlockGemmArgs& g, int tm) {
-  if (!g.ids || g.bm >= tm) return ((long long)(g.ids ? g.R : g.M) + tm - 1) / tm;
+  if (!g.ids) return ((long long)g.M + tm - 1) / tm;
+  const long long n = ((long long)g.R + tm - 1) / tm;
+  if (g.bm == tm) return n;
+  // the experts' pairs, and their rows
+  const long long of_pairs = (g.pairs + (long long)std::min(g.E, g.pairs) * (tm - 1)) / tm;
   const long long experts = std::min<long long>(g.E, ((long long)g.R + g.bm - 1) / g.bm);
-  return (g.R + experts * (tm - 1)) / tm;
+  return std::min(of_pairs, g.bm > tm ? n : (g.R + experts * (tm - 1)) / tm);
 }
 
 // About how many of these have real rows: an expert's pairs end in one that is half

@@ -39,17 +39,14 @@ __global__ __launch_bounds__(WAVES * 64) void block_rows_kernel(BlockGemmArgs g,
   __shared__ __attribute__((aligned(16))) char parts[R::kParts > R::kOne ? R::kParts : 16];
   const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int l16 = lane & 15, grp = lane >> 4;
-  const RowSpan s = RowSpans<16 * MB>(g).at(g, blockIdx.x / ntn);
+  const int span = blockIdx.x / ntn, n0 = (int)(blockIdx.x % ntn) * 16 * NB;
+  // of blocks that are spans: the pairs are asked for before what the span is has come
+  int pair = g.ids && g.bm == 16 * MB ? g.ids[min(span * 16 * MB + lane, g.R - 1)] : 0;
+  const RowSpan s = RowSpans<16 * MB>().at(g, span);
   if (s.rows <= 0) return;
-  const int n0 = (int)(blockIdx.x % ntn) * 16 * NB;
-
-  if (g.ids) {
-    const bool real = lane < s.rows && source_row(g, s.row0 + lane) >= 0;
-    if (__ballot(real) == 0) {  // padding only
-      zero_rows<OT>(g, s, n0, 16 * NB, WAVES * 64);
-      return;
-    }
-  }
+  if (g.ids && g.bm != 16 * MB) pair = g.ids[min(s.row0 + lane, g.R - 1)];
+  const int source = lane < s.rows ? source_row(g, s.row0 + lane, pair) : -1;  // of row `lane` of the span
+  const uint64_t real = __ballot(source >= 0);
 
   // sources, as in the tile kernel (block_gemm.hip)
   const int nrows = min(16 * NB, g.N - n0);
@@ -65,13 +62,10 @@ __global__ __launch_bounds__(WAVES * 64) void block_rows_kernel(BlockGemmArgs g,
   uint32_t aoff[2 * MB], soff;
   b_for<0, 2 * MB>([&](auto q) {
     const int r = 8 * q + (lane >> 3);
-    const int at = r < s.rows ? source_row(g, s.row0 + r) : -1;
+    const int at = __shfl(source, r, kWave);
     aoff[q] = at >= 0 ? (uint32_t)((moved ? at : r) * g.a_stride) + lcol(q & 1) : kNowhere;
   });
-  {
-    const int r = min(lane, s.rows - 1), at = max(source_row(g, s.row0 + r), 0);
-    soff = (uint32_t)((moved ? at : r) * g.as_m) * 4;
-  }
+  soff = (uint32_t)((moved ? max(source, 0) : min(lane, s.rows - 1)) * g.as_m) * 4;
   char* const own0 = ring0 + wv * R::kStage;
   char* const own1 = ring1 + wv * R::kStage;
   char* const own2 = ring2 + (STAGES > 2 ? wv * R::kStage : 0);
@@ -134,6 +128,7 @@ __global__ __launch_bounds__(WAVES * 64) void block_rows_kernel(BlockGemmArgs g,
     if constexpr (STAGES > 3) step(b + 3 * WAVES, own3);
   }
   b_wait_vmcnt<0>();  // no load may land in what follows
+  zero_rows<OT>(g, s, n0, 16 * NB, WAVES * 64);
   if constexpr (R::kParts <= R::kOne) __syncthreads();
   f32x4(*part)[NB * MB][64] = reinterpret_cast<f32x4(*)[NB * MB][64]>(R::kParts > R::kOne ? parts : ring0);
 #pragma unroll
@@ -150,7 +145,7 @@ __global__ __launch_bounds__(WAVES * 64) void block_rows_kernel(BlockGemmArgs g,
     for (int v = 1; v < WAVES; ++v) t += part[v][blk][ln];
     const int r = 16 * j + (ln & 15), n = n0 + 16 * i + 4 * (ln >> 4);
     if (r >= s.rows) continue;
-    if (source_row(g, s.row0 + r) < 0) t = f32x4{};
+    if (!(real >> r & 1)) t = f32x4{};
     const size_t at = (size_t)(s.row0 + r) * g.out_stride + n;
     if constexpr (OT == DT_BF16) {
       uint16_t* p = reinterpret_cast<uint16_t*>(g.out) + at;

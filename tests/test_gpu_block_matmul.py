@@ -141,6 +141,15 @@ def test_grouped(M, k, E, bm, N, K, keep, gather, dt):
     assert (out[:n].cpu().float().numpy()[pad] == 0).all() and (out[n:] == 3).all()
 
 
+@pytest.mark.parametrize("gather", [True, False])
+@pytest.mark.parametrize("bm", [16, 32, 64, 128, 256])
+@pytest.mark.parametrize("M,k,E", [(1, 1, 65), (30, 3, 64), (40, 4, 130), (260, 6, 70), (500, 8, 66), (9, 8, 1024)])
+def test_many_experts(M, k, E, bm, gather):
+    """More experts than a wave has lanes, most of them with few rows or none, in
+    blocks shorter and longer than the kernels' spans."""
+    test_grouped(M, k, E, bm, 40, 144, 0.9, gather, "bf16")
+
+
 def on_gpu(a, sa, w, sw):
     """The product and the magnitudes' sum in 64 bits, block by block on the GPU."""
     v = torch.from_numpy(BO.e4m3_values()).to(B.DEV)
