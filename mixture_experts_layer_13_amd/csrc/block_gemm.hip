@@ -152,17 +152,18 @@ __global__ __launch_bounds__(WN * WM * 64) void block_gemm_kernel(BlockGemmArgs 
   f32x4 acc[NI][MJ] = {};
   const int nb = WTN * wn, mb = WTM * wm;  // this wave's first rows
   const int wsat = TM + (n0 % 128 + nb) / 128;
-  BOperand16<WIDE> af[2], bf[2][MJ];
+  BOperand16<false> af[2], bf[2][MJ];  // codes as read
+  BOperand16<WIDE> wa, wb[MJ];         // WIDE: those at hand, converted before their first product
   float sc[2][MJ] = {};
   f32x4 t[RING] = {};
   // a lane's codes of row l16: 16-byte columns grp and 4 + grp
   const int f0 = l16 * 128 + ((grp ^ (l16 >> 1)) & 7) * 16;
   const int fa = nb * 128 + f0, fb = (TN + mb) * 128 + f0;
-  auto read_a = [&](int i, const char* stage, BOperand16<WIDE>& o) {
+  auto read_a = [&](int i, const char* stage, BOperand16<false>& o) {
     const char* p = stage + 16 * i * 128;
     o.set(ld16(p + fa), ld16(p + (fa ^ 64)));
   };
-  auto read_b = [&](int j, const char* stage, BOperand16<WIDE>& o) {
+  auto read_b = [&](int j, const char* stage, BOperand16<false>& o) {
     const char* p = stage + 16 * j * 128;
     o.set(ld16(p + fb), ld16(p + (fb ^ 64)));
   };
@@ -197,7 +198,13 @@ __global__ __launch_bounds__(WN * WM * 64) void block_gemm_kernel(BlockGemmArgs 
         b_barrier();
         read_s(nxt, sc[P ^ 1]);
       }
-      t[q % RING] = block_sums16(af[i & 1], bf[P][j]);
+      if constexpr (WIDE) {
+        if constexpr (j == 0) wa.set(af[i & 1]);
+        if constexpr (i == 0) wb[j].set(bf[P][j]);
+        t[q % RING] = block_sums16(wa, wb[j]);
+      } else {
+        t[q % RING] = block_sums16(af[i & 1], bf[P][j]);
+      }
       if constexpr (j == 0 && i + 1 < NI) read_a(i + 1, cur, af[(i + 1) & 1]);
       if constexpr (i == NI - 1) {
         if constexpr (j == 0) read_a(0, nxt, af[0]);

@@ -88,6 +88,9 @@ struct BOperand16<true> {
     b_widen(lo, v[0], v[1]);
     b_widen(hi, v[2], v[3]);
   }
+  __device__ __forceinline__ void set(const BOperand16<false>& c) {
+    set(__builtin_shufflevector(c.v, c.v, 0, 1, 2, 3), __builtin_shufflevector(c.v, c.v, 4, 5, 6, 7));
+  }
 };
 // The sums of one block, of 16 weight rows and 16 rows of a.
 __device__ __forceinline__ b_f32x4 block_sums16(const BOperand16<false>& w, const BOperand16<false>& a) {
