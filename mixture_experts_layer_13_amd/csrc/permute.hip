@@ -289,13 +289,21 @@ static int permute_launch(const void* kernel, const PermuteArgs& a, int xt, int 
   return (int)hipLaunchKernel(kernel, dim3((unsigned)groups, (unsigned)parts), dim3(waves * 64), args, 0, st);
 }
 
+// One vector a thread where its pairs' rows are many, two where they are few: smaller
+// workgroups, of which more fit.  us with one | two: dispatch backward of 8192 tokens
+// x 4096 bf16 topk 1 54.5 | 33.4, 3 69.5 | 59.8, 8 128.8 | 132.7; of 5003 x 1032 fp32
+// topk 3 26.3 | 20.1; combine backward of 16384 x 2048 bf16 topk 1 76.8 | 49.9, 3
+// 116.8 | 96.7, 8 213.6 | 227.4; dispatch of 16384 x 4096 bf16 topk 1 84.7 | 54.9, 3
+// 140.0 | 106.9.
+static int vectors_each(const PermuteArgs& a) { return a.topk <= 4 ? 2 : 1; }
+
 int launch_scatter(const PermuteArgs& a, int xt, int rt, hipStream_t st) {
-  return permute_launch(a.dw ? scatter_of<true>(xt, rt) : scatter_of<false>(xt, rt), a, xt, rt, 1,
+  return permute_launch(a.dw ? scatter_of<true>(xt, rt) : scatter_of<false>(xt, rt), a, xt, rt, vectors_each(a),
                         a.M + ((long long)a.rows + 31) / 32, st);
 }
 
 int launch_gather(const PermuteArgs& a, int xt, int rt, hipStream_t st) {
-  return permute_launch(a.dw ? gather_dot_of(xt, rt) : gather_of(xt, rt), a, xt, rt, a.dw ? 1 : 2, a.M, st);
+  return permute_launch(a.dw ? gather_dot_of(xt, rt) : gather_of(xt, rt), a, xt, rt, a.dw ? vectors_each(a) : 2, a.M, st);
 }
 
 }  // namespace moe
