@@ -601,6 +601,27 @@ def _rows(t, rows, values, name, device):
     return t.data_ptr(), code, st if shape[0] > 1 else shape[1]
 
 
+def _made_rows(like, rows, values, dtype, stream, columns=False):
+    """_made of [rows, values], a row's values side by side (columns: a column's)."""
+    if stream is None:  # half the time of new_empty with a dtype, and a third of it with t()
+        return torch.empty_strided((rows, values), (1, rows or 1) if columns else (values, 1), dtype=dtype,
+                                   device=like.device)
+    t = _made(like, (values, rows) if columns else (rows, values), dtype, stream)
+    return t.t() if columns else t
+
+
+def _out(out, like, rows, values, dtype, stream):
+    """(out, address, dtype code, row stride) of a given [rows, values], or of one
+    made of this type."""
+    if out is not None:
+        return out, *_rows(out, rows, values, "out", like.device)
+    code = _VALUE_CODES.get(dtype)
+    if code is None:
+        raise MoEError(MOE_ERR_DTYPE, f"out must be bf16 or f32, not {dtype}")
+    out = _made_rows(like, rows, values, dtype, stream)
+    return out, out.data_ptr(), code, values
+
+
 def _pairs_f32(t, shape, name, device):
     """Address of a dense f32 tensor of this shape on `device` (None: None)."""
     if t is None:
@@ -649,9 +670,7 @@ def moe_dispatch(x, alignment, topk, weights=None, out=None, out_dtype=None, str
     M, K = x.shape
     al, rows = _places(alignment, M, topk, dev, True)
     wp = None if weights is None else _pairs_f32(weights, (M, topk), "weights", dev)
-    if out is None:
-        out = _made(x, (rows, K), out_dtype, stream)
-    op, oc, ost = _rows(out, rows, K, "out", dev)
+    out, op, oc, ost = _out(out, x, rows, K, out_dtype or x.dtype, stream)
     _run(dev, stream, lib().moe_dispatch, al, xp, xc, xs, K, wp, op, oc, ost)
     return out
 
@@ -667,11 +686,9 @@ def moe_dispatch_backward(d_rows, alignment, M, topk, x=None, weights=None, out=
     xp, xc, xs, dw, dwp = None, None, 0, None, None
     if x is not None:
         xp, xc, xs = _rows(x, M, K, "x", dev)
-        dw = _made(d_rows, (M, topk), torch.float32, stream)
+        dw = _made_rows(d_rows, M, topk, torch.float32, stream)
         dwp = dw.data_ptr()
-    if out is None:
-        out = _made(d_rows, (M, K), out_dtype or (None if x is None else x.dtype), stream)
-    op, oc, ost = _rows(out, M, K, "out", dev)
+    out, op, oc, ost = _out(out, d_rows, M, K, out_dtype or (d_rows if x is None else x).dtype, stream)
     if xc is not None and xc != oc:
         raise MoEError(MOE_ERR_DTYPE, f"x is {x.dtype}, its gradient {out.dtype}")
     _run(dev, stream, lib().moe_dispatch_backward, al, rp, rc, rs, K, xp, xs, wp, op, oc, ost, dwp)
@@ -686,9 +703,7 @@ def moe_combine(rows, alignment, M, topk, weights=None, out=None, out_dtype=None
     rp, rc, rs = _rows(rows, n, None, "rows", dev)
     K = rows.size(1)
     wp = None if weights is None else _pairs_f32(weights, (M, topk), "weights", dev)
-    if out is None:
-        out = _made(rows, (M, K), out_dtype, stream)
-    op, oc, ost = _rows(out, M, K, "out", dev)
+    out, op, oc, ost = _out(out, rows, M, K, out_dtype or rows.dtype, stream)
     _run(dev, stream, lib().moe_combine, al, rp, rc, rs, K, wp, op, oc, ost)
     return out
 
@@ -704,11 +719,9 @@ def moe_combine_backward(d_out, alignment, topk, rows=None, weights=None, out=No
     rp, rc, rs, dw, dwp = None, None, 0, None, None
     if rows is not None:
         rp, rc, rs = _rows(rows, n, K, "rows", dev)
-        dw = _made(d_out, (M, topk), torch.float32, stream)
+        dw = _made_rows(d_out, M, topk, torch.float32, stream)
         dwp = dw.data_ptr()
-    if out is None:
-        out = _made(d_out, (n, K), out_dtype or (None if rows is None else rows.dtype), stream)
-    op, oc, ost = _rows(out, n, K, "out", dev)
+    out, op, oc, ost = _out(out, d_out, n, K, out_dtype or (d_out if rows is None else rows).dtype, stream)
     if rc is not None and rc != oc:
         raise MoEError(MOE_ERR_DTYPE, f"rows are {rows.dtype}, their gradient {out.dtype}")
     _run(dev, stream, lib().moe_combine_backward, al, gp, gc, gs, K, rp, rs, wp, op, oc, ost, dwp)
@@ -744,7 +757,7 @@ def moe_quantize_blocks(x, gated=False, block_rows=1, num_rows=None, codes=None,
         K //= 2
     SR, SB = M if block_rows == 1 else -(-M // max(block_rows, 1)), -(-K // 128)
     if codes is None:
-        codes = _made(x, (M, K), torch.float8_e4m3fn, stream)
+        codes = _made_rows(x, M, K, torch.float8_e4m3fn, stream)
     elif codes.dtype not in _CODES:
         raise MoEError(MOE_ERR_DTYPE, f"codes are {codes.dtype}")
     elif codes.shape != (M, K) or not codes.is_contiguous() or codes.device != dev:
@@ -752,10 +765,10 @@ def moe_quantize_blocks(x, gated=False, block_rows=1, num_rows=None, codes=None,
     if scales is not None:
         sp, sr, sb = _scales(scales, SR, SB, "scales", dev)
     elif block_rows == 1:
-        made = _made(x, (SB, SR), torch.float32, stream)
-        scales, sp, sr, sb = made.t(), made.data_ptr(), 1, SR or 1
+        scales = _made_rows(x, SR, SB, torch.float32, stream, True)
+        sp, sr, sb = scales.data_ptr(), 1, SR or 1
     else:
-        scales = _made(x, (SR, SB), torch.float32, stream)
+        scales = _made_rows(x, SR, SB, torch.float32, stream)
         sp, sr, sb = scales.data_ptr(), SB, 1
     limit = None if num_rows is None else _index(num_rows, 1, 1, "num_rows", dev)
     _run(dev, stream, lib().moe_quantize_blocks, xp, xc, xs, M, K, 1 if gated else 0, block_rows, limit,
@@ -801,9 +814,7 @@ def moe_block_matmul(a, a_scales, w, w_scales, out=None, out_dtype=torch.bfloat1
     strides), w_scales f32 [ceil(N / 128), ceil(K / 128)] -> out [M, N]."""
     dev = a.device
     M, N, K, ap, ast, (sp, sr, sb), wp, wsp = _block_operands(a, a_scales, w, w_scales, 2)
-    if out is None:
-        out = _made(a, (M, N), out_dtype, stream)
-    op, oc, ost = _rows(out, M, N, "out", dev)
+    out, op, oc, ost = _out(out, a, M, N, out_dtype, stream)
     _run(dev, stream, lib().moe_block_matmul, ap, ast, sp, sr, sb, wp, wsp, M, N, K, op, oc, ost)
     return out
 
@@ -822,9 +833,7 @@ def moe_block_matmul_grouped(a, a_scales, w, w_scales, alignment, topk=None, M=N
         al, rows = _segments(alignment, alignment.pair_pos.size(0) if pairs is None else pairs, 1, w.size(0), dev)
     else:
         al, rows = _segments(alignment, A if M is None else M, topk, w.size(0), dev)
-    if out is None:
-        out = _made(a, (rows, N), out_dtype, stream)
-    op, oc, ost = _rows(out, rows, N, "out", dev)
+    out, op, oc, ost = _out(out, a, rows, N, out_dtype, stream)
     _run(dev, stream, lib().moe_block_matmul_grouped, al, ap, ast, A, sp, sr, sb, wp, wsp, N, K,
          0 if topk is None else 1, op, oc, ost)
     return out
