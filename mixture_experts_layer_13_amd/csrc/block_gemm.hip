@@ -37,17 +37,36 @@ struct BTile {
 };
 
 // Tile number blockIdx.x: the workgroups of an XCD (dealt out round-robin) take
-// consecutive tiles, in groups of kGroup spans times all of N, so that the rows
-// and weights that they share meet in that XCD's L2.
+// consecutive tiles, in groups of spans times all of N, so that the rows and weights
+// that they share meet in that XCD's L2: of a batch kGroup spans, of experts kGroup
+// or up to as many again less one, none of two experts.
 constexpr int kGroup = 4;
-__device__ __forceinline__ bool b_tile(int spans, int ntn, int& span, int& nt) {
-  const int total = spans * ntn;
+template <int TM>
+__device__ __forceinline__ bool b_tile(const BlockGemmArgs& g, int ntn, RowSpan& s, int& nt) {
+  RowSpans<TM> all;
+  const int spans = g.ids ? all.total(g) : (g.M + TM - 1) / TM, total = spans * ntn;
   if ((int)blockIdx.x >= total) return false;
   const int xcd = blockIdx.x % 8, per = total / 8, rem = total % 8;
   const int t = xcd * per + min(xcd, rem) + (int)blockIdx.x / 8;
-  const int grp = t / (kGroup * ntn), r = t % (kGroup * ntn), gs = min(kGroup, spans - grp * kGroup);
-  span = grp * kGroup + r % gs;
+  if (!g.ids) {
+    const int grp = t / (kGroup * ntn), r = t % (kGroup * ntn), gs = min(kGroup, spans - grp * kGroup);
+    nt = r / gs;
+    s = all.at(g, grp * kGroup + r % gs);
+    return true;
+  }
+  const auto x = all.expert_of(g, t / ntn, true);
+  // its spans in groups of `small`, and of one more the first `more`
+  const int groups = max(x.spans / kGroup, 1), small = x.spans / groups, more = x.spans % groups;
+  int u = t - x.span * ntn, at = more * (small + 1);
+  const bool large = u < at * ntn;
+  const int gs = large ? small + 1 : small;
+  if (large)
+    at = 0;
+  else
+    u -= at * ntn;
+  const int r = u % (gs * ntn);
   nt = r / gs;
+  s = all.span(x, at + u / (gs * ntn) * gs + r % gs);
   return true;
 }
 
@@ -69,10 +88,9 @@ __global__ __launch_bounds__(WN * WM * 64) void block_gemm_kernel(BlockGemmArgs 
   const int wn = wv % WN, wm = wv / WN;
   const int l16 = lane & 15, grp = lane >> 4;
 
-  int span, nt;
-  RowSpans<TM> all;
-  if (!b_tile(all.total(g), ntn, span, nt)) return;
-  const RowSpan s = all.at(g, span);
+  RowSpan s;
+  int nt;
+  if (!b_tile<TM>(g, ntn, s, nt)) return;
   if (s.rows <= 0) return;
   const int n0 = nt * TN;
 

@@ -116,8 +116,8 @@ __device__ __forceinline__ int b_sum_to(int v) {
 // The spans of up to TM rows that the rows fall into, none of two experts, in order.
 // An expert's begin with its first row; those of padding alone, which blocks longer
 // than a span can end in, are left to the last one with rows (`empty`).  They are
-// counted by 64 experts at a time, a lane each; where blocks are as long as spans,
-// span i is block i.
+// counted by 64 experts at a time, a lane each; to the few-row kernel, whose blocks are
+// mostly as long as its spans, span i is block i then.
 // (One span for every TM rows, or for every block, cost the workgroups that only
 // found out that there is nothing to do their slots on the chip, and worse where they
 // came in a pattern: every second one means half of the shader engines, to which
@@ -155,39 +155,44 @@ struct RowSpans {
     before = upto - count;
     return __builtin_amdgcn_readlane(upto, 63);
   }
-  static __device__ __forceinline__ bool plain(const BlockGemmArgs& g) { return !g.ids || g.bm == TM; }
-  static __device__ __forceinline__ int rows(const BlockGemmArgs& g) {
-    return g.ids ? min(*g.num_padded, g.R) : g.M;
-  }
-  // How many there are.
+  // How many there are (of experts).
   __device__ __forceinline__ int total(const BlockGemmArgs& g) {
-    if (plain(g)) return (rows(g) + TM - 1) / TM;
     int n = 0;
     for (int e0 = 0; e0 < g.E; e0 += 64) n = look(g, e0, n);
     return n;
   }
+  // The expert e of span i, its rows [first, end) and spans [span, span + spans);
+  // known: total() has just been asked.  e < 0: there is none.
+  struct Expert {
+    int e, first, end, span, spans;
+  };
+  __device__ __forceinline__ Expert expert_of(const BlockGemmArgs& g, int i, bool known) {
+    for (int e0 = 0, n = 0; e0 < g.E; e0 += 64) {
+      if (!known || g.E > 64) {
+        n = look(g, e0, n);
+        if (i >= n) continue;
+      }
+      const int own = __builtin_ctzll(__ballot(i >= before && i < before + count));
+      return {e0 + own, __builtin_amdgcn_readlane(from, own), __builtin_amdgcn_readlane(to, own),
+              __builtin_amdgcn_readlane(before, own), __builtin_amdgcn_readlane(count, own)};
+    }
+    return {-1, 0, 0, 0, 0};
+  }
+  // An expert's span number k.
+  static __device__ __forceinline__ RowSpan span(const Expert& x, int k) {
+    const int row0 = x.first + k * TM, left = x.end - row0;
+    return {row0, min(TM, left), x.e, k == x.spans - 1 ? max(left - TM, 0) : 0};
+  }
   // Span number i, less than the grid's; rows = 0: none.
   __device__ __forceinline__ RowSpan at(const BlockGemmArgs& g, int i) {
-    RowSpan s{0, 0, 0, 0};
-    if (plain(g)) {
-      s.row0 = i * TM;
-      if (g.ids) s.e = g.block_expert[i];  // (asked for along with the number of rows)
-      s.rows = max(min(TM, rows(g) - s.row0), 0);
-      if (s.e < 0 || (g.ids && s.e >= g.E)) s.rows = 0;
-      return s;
+    if (g.ids && g.bm != TM) {
+      const Expert x = expert_of(g, i, false);
+      return x.e < 0 ? RowSpan{0, 0, 0, 0} : span(x, i - x.span);
     }
-    for (int e0 = 0, n = 0; e0 < g.E; e0 += 64) {
-      n = look(g, e0, n);
-      if (i >= n) continue;
-      const int own = __builtin_ctzll(__ballot(i >= before && i < before + count));
-      const int k = i - __builtin_amdgcn_readlane(before, own);
-      s.e = e0 + own;
-      s.row0 = __builtin_amdgcn_readlane(from, own) + k * TM;
-      const int left = __builtin_amdgcn_readlane(to, own) - s.row0;
-      s.rows = min(TM, left);
-      if (k == __builtin_amdgcn_readlane(count, own) - 1) s.empty = left - s.rows;
-      break;
-    }
+    RowSpan s{i * TM, 0, 0, 0};
+    if (g.ids) s.e = g.block_expert[i];  // (asked for along with the number of rows)
+    s.rows = max(min(TM, (g.ids ? min(*g.num_padded, g.R) : g.M) - s.row0), 0);
+    if (s.e < 0 || (g.ids && s.e >= g.E)) s.rows = 0;
     return s;
   }
 };
@@ -225,11 +230,10 @@ __device__ __forceinline__ void zero_rows(const BlockGemmArgs& g, const RowSpan&
 inline long long row_spans(const BlockGemmArgs& g, int tm) {
   if (!g.ids) return ((long long)g.M + tm - 1) / tm;
   const long long n = ((long long)g.R + tm - 1) / tm;
-  if (g.bm == tm) return n;
   // the experts' pairs, and their rows
   const long long of_pairs = (g.pairs + (long long)std::min(g.E, g.pairs) * (tm - 1)) / tm;
   const long long experts = std::min<long long>(g.E, ((long long)g.R + g.bm - 1) / g.bm);
-  return std::min(of_pairs, g.bm > tm ? n : (g.R + experts * (tm - 1)) / tm);
+  return std::min(of_pairs, g.bm >= tm ? n : (g.R + experts * (tm - 1)) / tm);
 }
 
 // About how many of these have real rows: an expert's pairs end in one that is half
