@@ -9,10 +9,22 @@
 // one fused multiply-add each, the scale of the token (a lane's column) times
 // that of the weight block (the same for all of a wave).
 //
-// Operands come through a two-stage LDS ring by direct-to-LDS loads, 128
-// bytes of each row a stage, both scales with them.  Row r's 16-byte column
-// c lies at physical column c ^ (r / 2) mod 8: the fragment reads (lane l row
-// l mod 32) find every bank once.
+// Operands come through an LDS ring of two or four stages by direct-to-LDS
+// loads, 128 bytes of each row a stage, both scales with them.  Row r's 16-byte
+// column c lies at physical column c ^ (r / 2) mod 8: the fragment reads (lane l
+// row l mod 16, columns l / 16 and 4 more) find every bank once (no conflicts
+// counted in the loop).
+//
+// What bounds it: 8192 x 4096 x 7168 takes 197 to 230 us by the card (2.1 to 2.4
+// PFLOP/s; a library's product with one scale for each tensor 186), the matrix pipe
+// busy 0.58 of the cycles at 1.78 GHz, the clock that full load leaves: 32 compute
+// units alone take 1.36 us for a 256 x 256 x 128 block, the whole chip 1.75.  Hence
+// 256 x 256 (the fewest LDS and L2 bytes a product) where there are enough rows, one
+// fused multiply-add a sum and block, and nothing else in the loop.  Measured and
+// slower: 32 x 32 x 64 instructions (225 us against 211), all fragments of a block
+// read ahead, the stage's two operands freed apart with a second barrier.
+// Few tiles: a four-stage ring, one workgroup a compute unit; two stages of 128 x 128
+// leave room for two workgroups, whose barriers and ends overlap.
 #include <algorithm>
 
 #include "block_gemm.hpp"

