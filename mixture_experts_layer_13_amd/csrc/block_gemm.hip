@@ -312,7 +312,7 @@ __global__ __launch_bounds__(WN * WM * 64) void block_gemm_kernel(BlockGemmArgs 
   // 16 j + l mod 16.  bf16 rows go through this wave's part of LDS (behind a
   // barrier: the others may still read theirs), 16-byte column c of row r at
   // c ^ r, so that a store writes whole row pieces of the wave.
-  zero_rows<OT>(g, s, n0, TN, WN * WM * 64);
+  zero_rows<OT, TN>(g, s, n0, WN * WM * 64);
   b_barrier();
   if (OT == DT_BF16 && g.vec && n0 + nb + WTN <= g.N) {
     constexpr int kRowBytes = WTN * 2, kPieces = kRowBytes / 16, kRowsAtOnce = 64 / kPieces;
@@ -432,23 +432,33 @@ int launch_block_product(const BlockGemmArgs& g, int ot, hipStream_t st) {
   // rows of a batch, or of the average expert
   const long long m = g.ids ? (std::min(g.pairs, g.R) + g.E - 1) / g.E : g.M;
   auto tiles = [&](int tn, int tm) { return ((long long)g.N + tn - 1) / tn * spans_estimate(g, tm); };
-  if (tiles(32, 64) <= cu || (!g.ids && m <= 64)) return launch_block_rows(g, ot, (int)std::min(m, 64LL), st);
-  if (g.ids && m <= 16) return launch_block_rows(g, ot, m <= 8 ? 16 : 32, st);
+  if (tiles(32, 64) <= cu || (!g.ids && m <= 64 && g.KB > 4)) return launch_block_rows(g, ot, (int)std::min(m, 64LL), st);
+  if (g.ids && m <= 16 && g.KB > 4) return launch_block_rows(g, ot, m <= 8 ? 16 : 32, st);
+  // rounds of tiles over the chip, of `two` (hundredths of a 256 x 256 tile's time)
+  // with two on a compute unit, of `one` with one; where two do not fit, one round
+  auto rounds = [&](int tn, int tm, int one, int two) {
+    const long long t = tiles(tn, tm), last = t % (2 * cu);
+    if (!two) return t <= cu ? one : 1LL << 30;
+    return t / (2 * cu) * two + (last == 0 ? 0 : last <= cu ? one : two);
+  };
   if (ot == DT_F32) {
-    if (tiles(64, 64) <= 2 * cu || m <= 96) return block_gemm_launch<64, 64, 2, 2, 4, DT_F32>(g, st);
-    if (tiles(128, 128) <= cu) return block_gemm_launch<128, 128, 2, 4, 4, DT_F32>(g, st);
+    const long long a = rounds(64, 64, 19, 27), b = (tiles(128, 128) + cu - 1) / cu * 41, c = (tiles(256, 128) + cu - 1) / cu * 66;
+    if (g.N <= 64 || (g.ids && m <= 96) || (a <= b && a <= c)) return block_gemm_launch<64, 64, 2, 2, 4, DT_F32>(g, st);
+    if (b <= c) return block_gemm_launch<128, 128, 2, 4, 4, DT_F32>(g, st);
     return block_gemm_launch<256, 128, 4, 2, 2, DT_F32>(g, st);
   }
-  const long long t = tiles(128, 128);
-  if (g.ids ? m <= 48 : tiles(64, 64) <= cu) return block_gemm_launch<64, 64, 2, 2, 4, DT_BF16>(g, st);
-  if (!g.ids && tiles(64, 128) <= cu) return block_gemm_launch<64, 128, 2, 2, 4, DT_BF16>(g, st);
-  if (t <= cu || (g.ids && m <= 96)) return block_gemm_launch<128, 128, 2, 4, 4, DT_BF16>(g, st);
-  // rounds over the chip, in hundredths of the larger tile's; experts' last tiles, of
-  // less work than the others, fill the larger tile's last round
-  const long long last = t % (2 * cu), n = tiles(256, 256);
-  const long long large = g.ids ? std::max(100LL, n * 100 / cu) : (n + cu - 1) / cu * 100;
-  const long long small = t / (2 * cu) * 67 + (last == 0 ? 0 : last <= cu ? 50 : 67);
-  if (small < large || (g.ids && m < 192)) return block_gemm_launch<128, 128, 2, 4, 2, DT_BF16>(g, st);
+  if (g.N <= 64 || (g.ids && m <= 48)) return block_gemm_launch<64, 64, 2, 2, 4, DT_BF16>(g, st);
+  if (g.ids && m <= 96) return block_gemm_launch<128, 128, 2, 4, 4, DT_BF16>(g, st);
+  // experts' last tiles, of less work than the others, fill the last of several rounds
+  const long long n = tiles(256, 256);
+  const long long t256 = g.ids && m < 192 ? 1LL << 30 : g.ids && n >= 2 * cu ? n * 100 / cu : (n + cu - 1) / cu * 100;
+  const long long t64 = tiles(64, 64) <= 2 * cu ? rounds(64, 64, 21, 31) : 1LL << 30, t64x128 = rounds(64, 128, 28, 0);
+  const long long t128one = rounds(128, 128, 37, 0), t128 = rounds(128, 128, 50, 67);
+  const long long best = std::min({t64, t64x128, t128one, t128, t256});
+  if (best == t64) return block_gemm_launch<64, 64, 2, 2, 4, DT_BF16>(g, st);
+  if (best == t64x128) return block_gemm_launch<64, 128, 2, 2, 4, DT_BF16>(g, st);
+  if (best == t128one) return block_gemm_launch<128, 128, 2, 4, 4, DT_BF16>(g, st);
+  if (best == t128) return block_gemm_launch<128, 128, 2, 4, 2, DT_BF16>(g, st);
   return block_gemm_launch<256, 256, 2, 4, 2, DT_BF16>(g, st);
 }
 

@@ -205,16 +205,23 @@ __device__ __forceinline__ int source_row(const BlockGemmArgs& g, int row, int f
   return at < g.M ? at : -1;
 }
 
-// Zeros for the columns n0 .. n0 + cols - 1 of a span's rows of padding.
-template <int OT>
-__device__ __forceinline__ void zero_rows(const BlockGemmArgs& g, const RowSpan& s, int n0, int cols, int threads) {
-  if (s.empty <= 0) return;
-  const int row0 = s.row0 + s.rows;
+// Zeros for a span's rows of padding, in a tile of COLS columns from n0 on: pieces of
+// at least 256 bytes, by the workgroup of a piece's first tile (tiles side by side
+// are on different XCDs, whose half lines do not meet before memory).
+template <int OT, int COLS>
+__device__ __forceinline__ void zero_rows(const BlockGemmArgs& g, const RowSpan& s, int n0, int threads) {
   constexpr int V = OT == 1 ? 8 : 4;  // values in 16 bytes
-  const int n1 = min(n0 + cols, g.N), w = g.vec ? (n1 - n0) / V : 0, rest = n1 - n0 - w * V;
-  for (int q = threadIdx.x; q < s.empty * w; q += threads) {
-    const size_t at = (size_t)(row0 + q / w) * g.out_stride + n0 + q % w * V;
-    *reinterpret_cast<b_i32x4*>(reinterpret_cast<char*>(g.out) + at * (16 / V)) = b_i32x4{};
+  constexpr int kPiece = COLS > 16 * V ? COLS : 16 * V;
+  if (s.empty <= 0 || n0 % kPiece) return;
+  const int row0 = s.row0 + s.rows;
+  const int n1 = min(n0 + kPiece, g.N), w = g.vec ? (n1 - n0) / V : 0, rest = n1 - n0 - w * V;
+  if (w) {  // a thread keeps its column: one division
+    const int step = threads / w, c = (int)threadIdx.x % w;
+    for (int r = (int)threadIdx.x / w; r < s.empty; r += step) {
+      if ((int)threadIdx.x >= step * w) break;
+      const size_t at = (size_t)(row0 + r) * g.out_stride + n0 + c * V;
+      *reinterpret_cast<b_i32x4*>(reinterpret_cast<char*>(g.out) + at * (16 / V)) = b_i32x4{};
+    }
   }
   for (int q = threadIdx.x; q < s.empty * rest; q += threads) {
     const size_t at = (size_t)(row0 + q / rest) * g.out_stride + n0 + w * V + q % rest;

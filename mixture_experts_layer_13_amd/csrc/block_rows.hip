@@ -134,7 +134,7 @@ __global__ __launch_bounds__(WAVES * 64) void block_rows_kernel(BlockGemmArgs g,
     if constexpr (STAGES > 3) step(b + 3 * WAVES, own3);
   }
   b_wait_vmcnt<0>();  // no load may land in what follows
-  zero_rows<OT>(g, s, n0, 16 * NB, WAVES * 64);
+  zero_rows<OT, 16 * NB>(g, s, n0, WAVES * 64);
   if constexpr (R::kParts <= R::kOne) __syncthreads();
   f32x4(*part)[NB * MB][64] = reinterpret_cast<f32x4(*)[NB * MB][64]>(R::kParts > R::kOne ? parts : ring0);
 #pragma unroll
