@@ -82,7 +82,7 @@ __device__ __forceinline__ bool b_tile(const BlockGemmArgs& g, int ntn, RowSpan&
   return true;
 }
 
-template <int TN, int TM, int WN, int WM, int STAGES, int OT, bool MOVED>
+template <int TN, int TM, int WN, int WM, int STAGES, int OT, bool MOVED, bool PAST>
 __global__ __launch_bounds__(WN * WM * 64) void block_gemm_kernel(BlockGemmArgs g, int ntn) {
   using B = BTile<TN, TM, WN, WM>;
   constexpr int NI = B::NI, MJ = B::MJ, S = NI * MJ;
@@ -158,7 +158,7 @@ __global__ __launch_bounds__(WN * WM * 64) void block_gemm_kernel(BlockGemmArgs 
     if constexpr (v < B::WLoads) {
       const int blk = wv * B::WLoads + v, odd = B::WLoads % 2 ? blk & 1 : v & 1;
       const uint32_t cut = k + lcol(odd) >= g.K ? kNowhere : 0u;
-      b_dma16(b_rsrc(wbase, real ? wbytes : 0u), stage + blk * 1024, (odd ? woff[1] : woff[0]) | cut, v * 8 * g.K + k);
+      b_dma16<PAST ? kPastCaches : 0>(b_rsrc(wbase, real ? wbytes : 0u), stage + blk * 1024, (odd ? woff[1] : woff[0]) | cut, v * 8 * g.K + k);
     } else if constexpr (v < B::WLoads + B::ALoads) {
       constexpr int q = v - B::WLoads;
       const int blk = wv * B::ALoads + q, odd = B::ALoads % 2 ? blk & 1 : q & 1;
@@ -395,20 +395,20 @@ __global__ __launch_bounds__(WN * WM * 64) void block_gemm_kernel(BlockGemmArgs 
   }
 }
 
-template <int TN, int TM, int WN, int WM, int STAGES, int OT>
+template <int TN, int TM, int WN, int WM, int STAGES, int OT, bool PAST = false>
 static int block_gemm_launch(const BlockGemmArgs& g, hipStream_t st) {
   BlockGemmArgs c = g;
   int ntn = (g.N + TN - 1) / TN;
   const long long tiles = row_spans(g, TM) * ntn;
   if (tiles * WN * WM * 64 > kMaxThreads) return kTooManyTiles;
   void* args[] = {&c, &ntn};
-  return (int)hipLaunchKernel(g.ids && g.topk ? (void*)block_gemm_kernel<TN, TM, WN, WM, STAGES, OT, true>
-                                              : (void*)block_gemm_kernel<TN, TM, WN, WM, STAGES, OT, false>,
+  return (int)hipLaunchKernel(g.ids && g.topk ? (void*)block_gemm_kernel<TN, TM, WN, WM, STAGES, OT, true, PAST>
+                                              : (void*)block_gemm_kernel<TN, TM, WN, WM, STAGES, OT, false, PAST>,
                               dim3((unsigned)tiles), dim3(WN * WM * 64), args, 0, st);
 }
 
 // Which kernel: by the workgroups that each makes of the call, against the
-// compute units.  us for N = K = 4096, bf16 out, in a graph:
+// compute units, and the time of a round of them.  us for N = K = 4096, bf16 out, in a graph:
 //   M            128   256   512  1024  2048  4096
 //   few rows    11.0  17.1  29.2
 //   64 x 64     13.4  13.5  21.9  39.6
@@ -432,8 +432,20 @@ int launch_block_product(const BlockGemmArgs& g, int ot, hipStream_t st) {
   // rows of a batch, or of the average expert
   const long long m = g.ids ? (std::min(g.pairs, g.R) + g.E - 1) / g.E : g.M;
   auto tiles = [&](int tn, int tm) { return ((long long)g.N + tn - 1) / tn * spans_estimate(g, tm); };
-  if (tiles(32, 64) <= cu || (!g.ids && m <= 64 && g.KB > 4)) return launch_block_rows(g, ot, (int)std::min(m, 64LL), st);
-  if (g.ids && m <= 16 && g.KB > 4) return launch_block_rows(g, ot, m <= 8 ? 16 : 32, st);
+  if (tiles(32, 64) <= cu || (!g.ids && m <= 64)) return launch_block_rows(g, ot, (int)std::min(m, 64LL), st);
+  if (g.ids && m <= 16) {
+    // Tiles of 64 x 64 are fewer workgroups, which counts where each has to look its
+    // rows up.  us of few rows | 64 x 64 past the caches, 64 experts x 2048, average 2, 8
+    // and 12 rows: K 512 in blocks of 16 16 | 17, 29 | 27, 32 | 29, of 256 33 | 25, 60 | 40,
+    // 66 | 40; K 4096 53 | 63, 103 | 99, 114 | 106, of 256 76 | 77, 149 | 123, 164 | 131.
+    if (m <= (ot == DT_F32 ? 12 : 8) && (g.bm == 16 || tiles(64, 64) <= cu)) return launch_block_rows(g, ot, 16, st);
+    const bool past = weights_past_caches(g);
+    if (ot == DT_F32)
+      return past ? block_gemm_launch<64, 64, 2, 2, 4, DT_F32, true>(g, st)
+                  : block_gemm_launch<64, 64, 2, 2, 4, DT_F32>(g, st);
+    return past ? block_gemm_launch<64, 64, 2, 2, 4, DT_BF16, true>(g, st)
+                : block_gemm_launch<64, 64, 2, 2, 4, DT_BF16>(g, st);
+  }
   // rounds of tiles over the chip, of `two` (hundredths of a 256 x 256 tile's time)
   // with two on a compute unit, of `one` with one; where two do not fit, one round
   auto rounds = [&](int tn, int tm, int one, int two) {

@@ -252,6 +252,14 @@ inline long long spans_estimate(const BlockGemmArgs& g, int tm) {
   return n < most ? n : most;
 }
 
+// Whether weights that are read about once go past the caches: 64 MiB and more would
+// only push others out (of the MALL's 256 MiB).  The few-row kernel, us: 537 MB 101.7
+// -> 99.7, 67 MB 15.9 -> 15.2; 134 MB 27.5 -> 28.8 where the MALL holds them, 57 -> 33
+// where it is full of another kernel's writes; 8 MB that it holds 5.6 -> 6.9.
+inline bool weights_past_caches(const BlockGemmArgs& g) {
+  return (long long)(g.ids ? g.E : 1) * g.N * g.K >= 64LL << 20;
+}
+
 // What a launcher returns, launching nothing, for more tiles than a grid has.
 constexpr int kTooManyTiles = -1;
 constexpr long long kMaxThreads = (1LL << 32) - 1;  // of a grid

@@ -180,12 +180,9 @@ static int block_rows_start(const BlockGemmArgs& g, hipStream_t st) {
                               dim3(WAVES * 64), args, 0, st);
 }
 
-// Weights of 64 MiB and more would only push others out of the caches (256 MiB of
-// MALL): 537 MB 101.7 -> 99.7 us, 67 MB 15.9 -> 15.2; 8 MB that the MALL holds
-// 5.6 -> 6.9.
 template <int NB, int MB, int WAVES, int STAGES>
 static int block_rows_launch(const BlockGemmArgs& g, int ot, hipStream_t st) {
-  const bool past = (long long)(g.ids ? g.E : 1) * g.N * g.K >= 64LL << 20;
+  const bool past = weights_past_caches(g);
   if (ot == DT_BF16)
     return past ? block_rows_start<NB, MB, WAVES, STAGES, true, DT_BF16>(g, st)
                 : block_rows_start<NB, MB, WAVES, STAGES, false, DT_BF16>(g, st);
