@@ -4,7 +4,8 @@
 //
 // A workgroup computes TN columns of out (weight rows) x TM rows of a; its
 // WN x WM waves own (TN / WN) x (TM / WM) each, weights on the MFMA row
-// operand.  One 16x16x128 MFMA starts from zero and holds a whole block of
+// operand.  With KS > 1 there are so many sets of waves, each with a ring of its own
+// and every KS-th block along K; their sums are added in order.  One 16x16x128 MFMA starts from zero and holds a whole block of
 // 128 along K, so its four results a lane are added to the accumulators with
 // one fused multiply-add each, the scale of the token (a lane's column) times
 // that of the weight block (the same for all of a wave).
@@ -82,21 +83,27 @@ __device__ __forceinline__ bool b_tile(const BlockGemmArgs& g, int ntn, RowSpan&
   return true;
 }
 
-template <int TN, int TM, int WN, int WM, int STAGES, int OT, bool MOVED, bool PAST>
-__global__ __launch_bounds__(WN * WM * 64) void block_gemm_kernel(BlockGemmArgs g, int ntn) {
+template <int TN, int TM, int WN, int WM, int STAGES, int KS, int OT, bool MOVED, bool PAST>
+__global__ __launch_bounds__(KS * WN * WM * 64) void block_gemm_kernel(BlockGemmArgs g, int ntn) {
   using B = BTile<TN, TM, WN, WM>;
   constexpr int NI = B::NI, MJ = B::MJ, S = NI * MJ;
   constexpr int LAG = 2, RING = 4;  // a step's sums are added LAG steps later
   static_assert(S % RING == 0 && LAG < RING, "sums of a block's last steps are found by the next block");
   constexpr bool WIDE = OT == DT_F32;
-  __shared__ __attribute__((aligned(16))) char stage0[B::kStage];
-  __shared__ __attribute__((aligned(16))) char stage1[B::kStage];
-  __shared__ __attribute__((aligned(16))) char stage2[STAGES > 2 ? B::kStage : 16];
-  __shared__ __attribute__((aligned(16))) char stage3[STAGES > 2 ? B::kStage : 16];
+  __shared__ __attribute__((aligned(16))) char ring0[KS * B::kStage];
+  __shared__ __attribute__((aligned(16))) char ring1[KS * B::kStage];
+  __shared__ __attribute__((aligned(16))) char ring2[STAGES > 2 ? KS * B::kStage : 16];
+  __shared__ __attribute__((aligned(16))) char ring3[STAGES > 2 ? KS * B::kStage : 16];
   static_assert(STAGES == 2 || STAGES == 4, "fragments and scales take turns with every block");
   static_assert((STAGES - 1) * B::Loads < 64, "counted waits");
   const int lane = threadIdx.x & 63;
-  const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int part = KS > 1 ? wave / B::kWaves : 0, wv = wave - part * B::kWaves;
+  char* const stage0 = ring0 + part * B::kStage;
+  char* const stage1 = ring1 + part * B::kStage;
+  char* const stage2 = ring2 + (STAGES > 2 ? part * B::kStage : 0);
+  char* const stage3 = ring3 + (STAGES > 2 ? part * B::kStage : 0);
+  const int steps = (g.KB + KS - 1) / KS;  // blocks of each part, the last one's perhaps past the end
   const int wn = wv % WN, wm = wv / WN;
   const int l16 = lane & 15, grp = lane >> 4;
 
@@ -149,10 +156,11 @@ __global__ __launch_bounds__(WN * WM * 64) void block_gemm_kernel(BlockGemmArgs 
   const long long sstep = rowscales ? g.as_b : 1;
   const int sdst = B::kCodes + (rowscales ? wv * 256 : TM * 4);
 
-  // Load v of block b into a stage; of blocks past the last one, nothing (the
-  // buffer is empty).  A buffer's end holds for both offsets together.
-  auto load = [&](auto vc, int b, char* stage) {
+  // Load v of this part's block number `step` into a stage; of blocks past the last
+  // one, zeros (the buffer is empty).  A buffer's end holds for both offsets together.
+  auto load = [&](auto vc, int step, char* stage) {
     constexpr int v = decltype(vc)::value;
+    const int b = step * KS + part;
     const int k = b * 128;
     const bool real = b < g.KB;
     if constexpr (v < B::WLoads) {
@@ -269,7 +277,7 @@ __global__ __launch_bounds__(WN * WM * 64) void block_gemm_kernel(BlockGemmArgs 
   int b = 0;
   if (!real) {  // none of this wave's rows of a is real: it loads and keeps the barriers
     b_for<EARLY, B::Loads>([&](auto v) { load(v, STAGES - 1, STAGES > 2 ? stage3 : stage1); });
-    for (; b < g.KB; ++b) {
+    for (; b < steps; ++b) {
       b_wait_vmcnt<(STAGES - 2) * B::Loads>();
       b_barrier();
       char* const cur = b % STAGES == 0 ? stage0 : b % STAGES == 1 ? stage1 : b % STAGES == 2 ? stage2 : stage3;
@@ -279,7 +287,7 @@ __global__ __launch_bounds__(WN * WM * 64) void block_gemm_kernel(BlockGemmArgs 
   }
   // whole turns of the ring, then what is left, once: a path from one stage's
   // block to its own next would make the compiler wait for loads before its reads
-  for (; b + STAGES <= g.KB; b += STAGES) {
+  for (; b + STAGES <= steps; b += STAGES) {
     if constexpr (STAGES == 2) {
       block(even, b, stage0, stage1, stage1);
       block(odd, b + 1, stage1, stage0, stage0);
@@ -290,12 +298,12 @@ __global__ __launch_bounds__(WN * WM * 64) void block_gemm_kernel(BlockGemmArgs 
       block(odd, b + 3, stage3, stage0, stage2);
     }
   }
-  if (b < g.KB) {
+  if (b < steps) {
     block(even, b, stage0, stage1, STAGES == 2 ? stage1 : stage3);
     if constexpr (STAGES > 2) {
-      if (b + 1 < g.KB) {
+      if (b + 1 < steps) {
         block(odd, b + 1, stage1, stage2, stage0);
-        if (b + 2 < g.KB) block(even, b + 2, stage2, stage3, stage1);
+        if (b + 2 < steps) block(even, b + 2, stage2, stage3, stage1);
       }
     }
   }
@@ -303,10 +311,26 @@ __global__ __launch_bounds__(WN * WM * 64) void block_gemm_kernel(BlockGemmArgs 
   auto rest = [&](const float (&f)[MJ]) {
     b_for<S - LAG, S>([&](auto q) { add(q, f[q % MJ]); });
   };
-  if (g.KB & 1)
+  if (steps & 1)
     rest(sc[0]);
   else
     rest(sc[1]);
+
+  if constexpr (KS > 1) {  // the parts' sums, in order, to the first one's waves
+    static_assert((KS - 1) * B::kWaves * S * 1024 <= KS * B::kStage, "sums in one ring");
+    f32x4* sums = reinterpret_cast<f32x4*>(ring0) + lane;
+    b_barrier();
+    if (part) {
+#pragma unroll
+      for (int q = 0; q < S; ++q) sums[(((part - 1) * B::kWaves + wv) * S + q) * 64] = acc[q / MJ][q % MJ];
+    }
+    b_barrier();
+    if (part) return;
+#pragma unroll
+    for (int p = 0; p < KS - 1; ++p)
+#pragma unroll
+      for (int q = 0; q < S; ++q) acc[q / MJ][q % MJ] += sums[((p * B::kWaves + wv) * S + q) * 64];
+  }
 
   // Value v of lane l of block (i, j): column 16 i + 4 (l / 16) + v of row
   // 16 j + l mod 16.  bf16 rows go through this wave's part of LDS (behind a
@@ -395,16 +419,16 @@ __global__ __launch_bounds__(WN * WM * 64) void block_gemm_kernel(BlockGemmArgs 
   }
 }
 
-template <int TN, int TM, int WN, int WM, int STAGES, int OT, bool PAST = false>
+template <int TN, int TM, int WN, int WM, int STAGES, int OT, bool PAST = false, int KS = 1>
 static int block_gemm_launch(const BlockGemmArgs& g, hipStream_t st) {
   BlockGemmArgs c = g;
   int ntn = (g.N + TN - 1) / TN;
   const long long tiles = row_spans(g, TM) * ntn;
-  if (tiles * WN * WM * 64 > kMaxThreads) return kTooManyTiles;
+  if (tiles * KS * WN * WM * 64 > kMaxThreads) return kTooManyTiles;
   void* args[] = {&c, &ntn};
-  return (int)hipLaunchKernel(g.ids && g.topk ? (void*)block_gemm_kernel<TN, TM, WN, WM, STAGES, OT, true, PAST>
-                                              : (void*)block_gemm_kernel<TN, TM, WN, WM, STAGES, OT, false, PAST>,
-                              dim3((unsigned)tiles), dim3(WN * WM * 64), args, 0, st);
+  return (int)hipLaunchKernel(g.ids && g.topk ? (void*)block_gemm_kernel<TN, TM, WN, WM, STAGES, KS, OT, true, PAST>
+                                              : (void*)block_gemm_kernel<TN, TM, WN, WM, STAGES, KS, OT, false, PAST>,
+                              dim3((unsigned)tiles), dim3(KS * WN * WM * 64), args, 0, st);
 }
 
 // Which kernel: by the workgroups that each makes of the call, against the
@@ -416,8 +440,16 @@ static int block_gemm_launch(const BlockGemmArgs& g, hipStream_t st) {
 //   128 x 128   23.9  23.6  23.7  24.4  53.3  99.3   (four stages, one a CU)
 //   128 x 128   32.3  32.0  32.2  32.5  43.4  87.3   (two stages, two a CU)
 //   256 x 256   51.1  52.0  51.2  50.9  52.3  65.2
-// fp32 out (operands twice as wide, half the rate): 64 x 64 17.1 at 1037 x 1544 x
-// 2000 (128 x 128 21.6), 256 x 128 262 at 8192 x 4096 x 4096 (128 x 128 312).
+// fp32 out (operands twice as wide, half the rate; in two parts: waves that share out
+// the blocks of K, as conversions and waits of more waves overlap):
+//   M                       200   512  1024  2048  4096 | 1037 x 1544 x 2000
+//   64 x 64                20.2  29.8  55.6   104   200   17.2
+//   64 x 64, two parts     16.6  32.6  61.1                19.5
+//   64 x 128, two parts    23.2  25.6  48.9                14.1
+//   128 x 128              35.2  35.6  41.1  80.3   158   20.6
+//   128 x 128, two parts   30.7  32.2  36.7  76.4   143   18.5
+//   256 x 128              57.7  57.2  58.1  67.1   134   29.3
+// (with M = 200 and K = 512 one part 5.7, two 6.2; 2000 x 2000 x 400 11.7 and 14.5.)
 // Rows of experts, of uneven numbers (falling like 1 / (rank + 3)), by their average:
 // us for 64 experts x 2048 x 4096 | 16 x 1408 x 2048
 //   rows           8            16           32           64          128          256          512
@@ -454,9 +486,19 @@ int launch_block_product(const BlockGemmArgs& g, int ot, hipStream_t st) {
     return t / (2 * cu) * two + (last == 0 ? 0 : last <= cu ? one : two);
   };
   if (ot == DT_F32) {
-    const long long a = rounds(64, 64, 19, 27), b = (tiles(128, 128) + cu - 1) / cu * 41, c = (tiles(256, 128) + cu - 1) / cu * 66;
-    if (g.N <= 64 || (g.ids && m <= 96) || (a <= b && a <= c)) return block_gemm_launch<64, 64, 2, 2, 4, DT_F32>(g, st);
-    if (b <= c) return block_gemm_launch<128, 128, 2, 4, 4, DT_F32>(g, st);
+    const long long none = 1LL << 30, a = rounds(64, 64, 19, 27);
+    const long long b = (tiles(128, 128) + cu - 1) / cu * 41, c = (tiles(256, 128) + cu - 1) / cu * 66;
+    if (g.ids && m <= 96) return block_gemm_launch<64, 64, 2, 2, 4, DT_F32>(g, st);
+    // in two parts along K where that is one round and K is long
+    const bool parts = g.KB >= 12;
+    const long long a2 = parts ? rounds(64, 64, 16, 0) : none, b2 = parts ? rounds(128, 128, 37, 0) : none;
+    const long long d2 = parts ? rounds(64, 128, 25, 0) : none;
+    const long long best = std::min({a2, d2, a, b2, b, c});
+    if (best == a2) return block_gemm_launch<64, 64, 2, 2, 4, DT_F32, false, 2>(g, st);
+    if (best == d2) return block_gemm_launch<64, 128, 2, 2, 2, DT_F32, false, 2>(g, st);
+    if (best == a || g.N <= 64) return block_gemm_launch<64, 64, 2, 2, 4, DT_F32>(g, st);
+    if (best == b2) return block_gemm_launch<128, 128, 2, 2, 2, DT_F32, false, 2>(g, st);
+    if (best == b) return block_gemm_launch<128, 128, 2, 4, 4, DT_F32>(g, st);
     return block_gemm_launch<256, 128, 4, 2, 2, DT_F32>(g, st);
   }
   if (g.N <= 64 || (g.ids && m <= 48)) return block_gemm_launch<64, 64, 2, 2, 4, DT_BF16>(g, st);

@@ -186,6 +186,13 @@ def test_large(M, N, dt, K):
     near(got, *on_gpu(a, sa, w, sw), dt, K)
 
 
+@pytest.mark.parametrize("K", [1536, 1552, 1680, 1920, 4000])
+@pytest.mark.parametrize("M,N", [(200, 4000), (70, 4001), (500, 4090), (1000, 4004), (1000, 4001), (1037, 1544)])
+def test_long_k_in_fp32(M, N, K):
+    """Sizes whose blocks along K are shared out, evenly and unevenly."""
+    test_large(M, N, "f32", K)
+
+
 @pytest.mark.parametrize("gather", [True, False])
 @pytest.mark.parametrize("M,k,E,bm,N,K,keep,dt", [
     (3000, 2, 3, 256, 2100, 272, 1.0, "bf16"), (3000, 2, 3, 16, 2100, 144, 0.9, "bf16"), (5000, 4, 5, 128, 1030, 400, 0.7, "bf16"),
@@ -211,6 +218,12 @@ def test_grouped_large(M, k, E, bm, N, K, keep, dt, gather):
             at = f[real] // k if gather else p[real]
             near(out[p[real]], *on_gpu(a[at], sa[at], w[e], sw[e]), dt, K)
     assert (out[n:] == 3).all()
+
+
+@pytest.mark.parametrize("gather", [True, False])
+@pytest.mark.parametrize("M,k,E,bm,N,K", [(700, 1, 3, 64, 1000, 1680), (900, 2, 4, 256, 1001, 1552), (1500, 2, 3, 16, 2050, 1920)])
+def test_grouped_long_k_in_fp32(M, k, E, bm, N, K, gather):
+    test_grouped_large(M, k, E, bm, N, K, 0.9, "f32", gather)
 
 
 def test_grouped_rows_trimmed_and_odd_strides():
