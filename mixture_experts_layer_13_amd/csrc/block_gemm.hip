@@ -4,11 +4,12 @@
 //
 // A workgroup computes TN columns of out (weight rows) x TM rows of a; its
 // WN x WM waves own (TN / WN) x (TM / WM) each, weights on the MFMA row
-// operand.  With KS > 1 there are so many sets of waves, each with a ring of its own
-// and every KS-th block along K; their sums are added in order.  One 16x16x128 MFMA starts from zero and holds a whole block of
-// 128 along K, so its four results a lane are added to the accumulators with
-// one fused multiply-add each, the scale of the token (a lane's column) times
-// that of the weight block (the same for all of a wave).
+// operand.  With KS > 1 there are so many sets of waves, each with a ring of
+// its own and every KS-th block along K; their sums are added in order.  One
+// 16x16x128 MFMA starts from zero and holds a whole block of 128 along K, so
+// its four results a lane are added to the accumulators with one fused
+// multiply-add each, the scale of the token (a lane's column) times that of
+// the weight block (the same for all of a wave).
 //
 // Operands come through an LDS ring of two or four stages by direct-to-LDS
 // loads, 128 bytes of each row a stage, both scales with them.  Row r's 16-byte
@@ -166,7 +167,8 @@ __global__ __launch_bounds__(KS * WN * WM * 64) void block_gemm_kernel(BlockGemm
     if constexpr (v < B::WLoads) {
       const int blk = wv * B::WLoads + v, odd = B::WLoads % 2 ? blk & 1 : v & 1;
       const uint32_t cut = k + lcol(odd) >= g.K ? kNowhere : 0u;
-      b_dma16<PAST ? kPastCaches : 0>(b_rsrc(wbase, real ? wbytes : 0u), stage + blk * 1024, (odd ? woff[1] : woff[0]) | cut, v * 8 * g.K + k);
+      b_dma16<PAST ? kPastCaches : 0>(b_rsrc(wbase, real ? wbytes : 0u), stage + blk * 1024,
+                                      (odd ? woff[1] : woff[0]) | cut, v * 8 * g.K + k);
     } else if constexpr (v < B::WLoads + B::ALoads) {
       constexpr int q = v - B::WLoads;
       const int blk = wv * B::ALoads + q, odd = B::ALoads % 2 ? blk & 1 : q & 1;

@@ -83,8 +83,8 @@ __global__ __launch_bounds__(WAVES * 64) void block_rows_kernel(BlockGemmArgs g,
     const bool real = b < g.KB;
     const uint32_t cut0 = k + lcol(0) >= g.K ? kNowhere : 0u, cut1 = k + lcol(1) >= g.K ? kNowhere : 0u;
     b_for<0, 2 * NB>([&](auto q) {
-      b_dma16<PAST ? kPastCaches : 0>(b_rsrc(wbase, real ? wbytes : 0u), stage + q * 1024, (woff + lcol(q & 1)) | (q & 1 ? cut1 : cut0),
-              q * 8 * g.K + k);
+      b_dma16<PAST ? kPastCaches : 0>(b_rsrc(wbase, real ? wbytes : 0u), stage + q * 1024,
+                                      (woff + lcol(q & 1)) | (q & 1 ? cut1 : cut0), q * 8 * g.K + k);
     });
     b_for<0, 2 * MB>([&](auto q) {
       b_dma16(b_rsrc(abase, real ? abytes : 0u), stage + NB * 2048 + q * 1024, aoff[q] | (q & 1 ? cut1 : cut0), k);

@@ -268,7 +268,8 @@ static void* scatter_of(int xt, int rt) {
   return rt == DT_BF16 ? (void*)scatter_kernel<DT_F32, DT_BF16, DOT> : (void*)scatter_kernel<DT_F32, DT_F32, DOT>;
 }
 static void* gather_of(int xt, int rt) {
-  if (xt == DT_BF16) return rt == DT_BF16 ? (void*)gather_kernel<DT_BF16, DT_BF16> : (void*)gather_kernel<DT_BF16, DT_F32>;
+  if (xt == DT_BF16)
+    return rt == DT_BF16 ? (void*)gather_kernel<DT_BF16, DT_BF16> : (void*)gather_kernel<DT_BF16, DT_F32>;
   return rt == DT_BF16 ? (void*)gather_kernel<DT_F32, DT_BF16> : (void*)gather_kernel<DT_F32, DT_F32>;
 }
 static void* gather_dot_of(int xt, int rt) {
@@ -308,7 +309,8 @@ int launch_scatter(const PermuteArgs& a, int xt, int rt, hipStream_t st) {
 }
 
 int launch_gather(const PermuteArgs& a, int xt, int rt, hipStream_t st) {
-  return permute_launch(a.dw ? gather_dot_of(xt, rt) : gather_of(xt, rt), a, xt, rt, a.dw ? vectors_each(a) : 2, a.M, st);
+  return permute_launch(a.dw ? gather_dot_of(xt, rt) : gather_of(xt, rt), a, xt, rt, a.dw ? vectors_each(a) : 2, a.M,
+                        st);
 }
 
 }  // namespace moe

@@ -117,7 +117,8 @@ __device__ __forceinline__ uint2 codes8_fast(const float (&v)[8], float s) {
   if (__builtin_expect(!e4m3_fast_scale(s, r) || !(least >= 0x1p-9f), 0)) return codes8(v, s);
 #pragma unroll
   for (int i = 0; i < 8; ++i) q[i] = __builtin_amdgcn_fmed3f(q[i], -448.0f, 448.0f);
-  int lo = __builtin_amdgcn_cvt_pk_fp8_f32(q[0], q[1], 0, false), hi = __builtin_amdgcn_cvt_pk_fp8_f32(q[4], q[5], 0, false);
+  int lo = __builtin_amdgcn_cvt_pk_fp8_f32(q[0], q[1], 0, false);
+  int hi = __builtin_amdgcn_cvt_pk_fp8_f32(q[4], q[5], 0, false);
   lo = __builtin_amdgcn_cvt_pk_fp8_f32(q[2], q[3], lo, true);
   hi = __builtin_amdgcn_cvt_pk_fp8_f32(q[6], q[7], hi, true);
   return make_uint2((uint32_t)lo, (uint32_t)hi);
@@ -215,8 +216,9 @@ int launch_quant_blocks(const QuantArgs& a, int dt, bool gated, int block_rows, 
   uint32_t inv22 = ((1u << 22) + KB - 1) / KB;
   uint64_t inv64 = KB == 1 ? 0 : ~0ull / KB + 1;
   void* args[] = {&c, &KB, &inv22, &inv64};
-  const void* k = dt == DT_F32 ? (gated ? (void*)quant_rows_kernel<DT_F32, true> : (void*)quant_rows_kernel<DT_F32, false>)
-                               : (gated ? (void*)quant_rows_kernel<DT_BF16, true> : (void*)quant_rows_kernel<DT_BF16, false>);
+  const void* k = dt == DT_F32 ? gated ? (void*)quant_rows_kernel<DT_F32, true> : (void*)quant_rows_kernel<DT_F32, false>
+                  : gated      ? (void*)quant_rows_kernel<DT_BF16, true>
+                               : (void*)quant_rows_kernel<DT_BF16, false>;
   const long long groups = ((long long)a.M * KB + 31) / 32;
   if (groups * 256 > kMaxThreads) return kTooManyTiles;
   return (int)hipLaunchKernel(k, dim3((unsigned)groups), dim3(256), args, 0, st);
