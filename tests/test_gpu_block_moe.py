@@ -127,3 +127,10 @@ def test_a_training_step_around_the_experts():
     dx, _ = moe.moe_dispatch_backward(drows, al, M, k, out_dtype=torch.float32)
     for name, got, ref, m, adds in zip(("out", "dx", "dw", "dp"), (out, dx, dw, dp), want, mass, (K + k, N + k, M, K + N)):
         assert ((got.cpu().double() - ref).abs() <= (adds + 8) * B.U * m).all(), name
+
+
+def test_no_tokens():
+    L = layer(1, 256, 128, 4, 2)
+    none = moe.BlockMoE(0, 256, 128, 4, 2, L.w13, L.w13_scales, L.w2, L.w2_scales)
+    out = none(torch.empty(0, 256, dtype=torch.bfloat16, device=B.DEV), torch.empty(0, 4, device=B.DEV))
+    assert out.shape == (0, 256)
