@@ -21,6 +21,10 @@ struct QuantArgs {
 
 int launch_quant_blocks(const QuantArgs& a, int dt, bool gated, int block_rows, hipStream_t st);
 
+// A gathered call's rows times the stride of their scales, and of their codes, at
+// most: a lane's byte offsets into them stay below 2^31.
+constexpr long long kMostScales = (1LL << 29) - 1, kMostCodes = (1LL << 31) - 1;
+
 // out[m, n] = sum_b as[m, b] ws[n / 128, b] sum_{k in block b} a[m, k] w[n, k]
 struct BlockGemmArgs {
   const uint8_t* a;

@@ -6,6 +6,8 @@
 
 #include <type_traits>
 
+#include "block_gemm.hpp"
+
 namespace moe {
 
 // f(0), f(1), .. f(B - 1), as constants.
@@ -31,8 +33,10 @@ __device__ __forceinline__ void b_dma4(__amdgpu_buffer_rsrc_t r, char* dst, uint
 
 constexpr uint32_t kNowhere = 0x80000000u;  // past every buffer here: such a load gives zeros
 // A buffer whose loads are all inside what it stands for (not all ones: a choice
-// between those and nothing is made lane by lane, and the load looped over).
-constexpr uint32_t kMost = 0x7fffff00u;
+// between those and nothing is made lane by lane, and the load looped over).  The
+// farthest are a gathered call's scales: a_rows times their stride is below 2^29.
+constexpr uint32_t kMost = 0x7ffffffcu;
+static_assert(4 * kMostScales <= kMost && kMost < kNowhere, "a row's scale may lie that far");
 
 template <int N>
 __device__ __forceinline__ void b_wait_vmcnt() {

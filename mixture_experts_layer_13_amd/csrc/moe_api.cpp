@@ -1098,7 +1098,7 @@ moe_status moe_block_matmul_grouped(const moe_alignment* alignment, const uint8_
   if (!valid_block_m(al.block_m)) return fail(MOE_ERR_SHAPE, "block_m=%d must be 16, 32, 64, 128 or 256", al.block_m);
   if (a_rows < (gather ? al.M : al.rows))
     return fail(MOE_ERR_SHAPE, "a has %d rows, %d needed", a_rows, gather ? al.M : al.rows);
-  if (gather && ((long long)a_rows * a_stride >= (1LL << 31) || (long long)a_rows * scale_stride_row >= (1LL << 29)))
+  if (gather && ((long long)a_rows * a_stride > moe::kMostCodes || (long long)a_rows * scale_stride_row > moe::kMostScales))
     return fail(MOE_ERR_SHAPE, "a_rows=%d times its strides %lld and %lld must be below 2^31 and 2^29", a_rows,
                 (long long)a_stride, (long long)scale_stride_row);
   if (al.M == 0 || al.rows == 0) return ok();

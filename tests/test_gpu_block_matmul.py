@@ -296,3 +296,21 @@ def test_offsets_past_32_bits():
     assert ids.max() * N * K > 2 ** 31
     one = moe.moe_block_matmul(a[t:t + 1], sa[t:t + 1], w[ids.max()], sw[ids.max()])
     B.within(got[pos[t * 2 + j]], B.f64(one[0]), 2 * B.HALF_STEP["bf16"] * np.abs(B.f64(one[0])), "last expert")
+
+
+@pytest.mark.parametrize("rows,N", [(16, 96), (64, 8448)])
+def test_gathered_scales_at_the_largest_offset(rows, N):
+    """Tokens whose scales lie up to the limit on a_rows times their stride, for the
+    few-row kernel and a tile's: the last one's are 2^31 - 64 bytes from the first."""
+    M, K, stride = (1 << 26) - 1, 16, 8
+    a, sa, w, sw = operands(rows, N, K, 3, 1)
+    wide = torch.empty(M, stride, device=B.DEV)
+    wide[-rows:, :1] = B.dev(sa)
+    tokens = torch.empty(M, K, dtype=torch.uint8, device=B.DEV)
+    tokens[-rows:] = B.dev(a)
+    i32 = lambda v: torch.tensor(v, dtype=torch.int32, device=B.DEV)
+    al = moe.Alignment(torch.arange(M - rows, M, dtype=torch.int32, device=B.DEV), i32([0]), i32([0, rows]), i32([0]), i32([rows]),
+                       rows)
+    got = moe.moe_block_matmul_grouped(tokens, wide[:, :1], B.fp8(w), B.dev(sw), al, topk=1, out_dtype=torch.float32)
+    ref = BO.matmul(a, sa, w[0], sw[0])
+    B.within(got, ref[0], B.product_bound(*ref, "f32", K), f"{rows} last tokens")
