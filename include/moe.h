@@ -570,7 +570,8 @@ moe_status moe_paged_attention_workspace_size(const moe_kv_cache* cache, int32_t
  *          capacity, or fewer where the caller knows that *num_padded fits
  *          (places from rows on are dropped).
  * A place holds a pair if sorted_pair_ids is in [0, M * topk) there, else it is
- * padding.  topk 1..64, M * topk <= 2^26, rows <= 2^26 + 2^18.
+ * padding (marked M * topk: in buffers made for more tokens, M is still that of
+ * the call that filled them).  topk 1..64, M * topk <= 2^26, rows <= 2^26 + 2^18.
  * Which fields a call reads is said there; the others may be anything. */
 typedef struct {
   const int32_t* sorted_pair_ids;

@@ -496,6 +496,9 @@ class Alignment:
     pair_pos: torch.Tensor
     num_padded: torch.Tensor
     block_m: int
+    # M * topk of the routing that was last written here (moe_align_permute,
+    # moe_route_align), which may be fewer than the buffers hold; None: not known
+    pairs: int | None = None
 
 
 def alloc_alignment(M, topk, E, block_m, device):
@@ -515,6 +518,7 @@ def moe_align_permute(topk_ids, E, block_m, workspace, alignment=None, stream=No
                                    _ptr(al.num_padded), _ptr(workspace),
                                    workspace.numel() * workspace.element_size(),
                                    _stream(stream)))
+    al.pairs = M * topk
     return al
 
 
@@ -533,6 +537,7 @@ def moe_route_align(logits, topk, renormalize, block_m, workspace, topk_ids=None
                                  _ptr(al.block_expert_ids), _ptr(al.expert_offsets),
                                  _ptr(al.pair_pos), _ptr(al.num_padded), _ptr(workspace),
                                  workspace.numel() * workspace.element_size(), _stream(stream)))
+    al.pairs = M * topk
     return topk_ids, topk_weights, al
 
 
@@ -823,16 +828,24 @@ def moe_block_matmul_grouped(a, a_scales, w, w_scales, alignment, topk=None, M=N
                              out_dtype=torch.bfloat16, stream=None):
     """The rows of an alignment times their experts' weights w [E, N, K], w_scales
     f32 [E, ceil(N / 128), ceil(K / 128)] -> out [rows, N].  With topk, a holds
-    tokens (M of them; default: all) and a place reads its pair's token; without,
-    a [rows, K] is in expert order, of `pairs` pairs (default: pair_pos's size;
-    less where the buffers were made for more tokens).  Padding rows are zero,
-    those from num_padded on as they were (in a new tensor: anything)."""
+    tokens (M of them, or more) and a place reads its pair's token; without, a
+    [rows, K] is in expert order, of `pairs` pairs.  By default these are those of
+    the alignment (alignment.pairs), or where it does not know them all that a or
+    pair_pos holds.  Padding rows are zero, those from num_padded on as they were
+    (in a new tensor: anything)."""
     dev = a.device
     A, N, K, ap, ast, (sp, sr, sb), wp, wsp = _block_operands(a, a_scales, w, w_scales, 3)
+    known = alignment.pairs
     if topk is None:
-        al, rows = _segments(alignment, alignment.pair_pos.size(0) if pairs is None else pairs, 1, w.size(0), dev)
+        if pairs is None:
+            pairs = alignment.pair_pos.size(0) if known is None else known
+        al, rows = _segments(alignment, pairs, 1, w.size(0), dev)
     else:
-        al, rows = _segments(alignment, A if M is None else M, topk, w.size(0), dev)
+        if M is None:
+            M = A if known is None else known // max(topk, 1)
+            if known is not None and M * topk != known:
+                raise MoEError(MOE_ERR_SHAPE, f"an alignment of {known} pairs, topk {topk}")
+        al, rows = _segments(alignment, M, topk, w.size(0), dev)
     out, op, oc, ost = _out(out, a, rows, N, out_dtype, stream)
     _run(dev, stream, lib().moe_block_matmul_grouped, al, ap, ast, A, sp, sr, sb, wp, wsp, N, K,
          0 if topk is None else 1, op, oc, ost)

@@ -205,3 +205,17 @@ def test_oracle_closed_forms():
     rows = BO.dispatch(x, pos, 1, 6)
     assert np.array_equal(BO.combine(rows, pos, 1, 4)[0], x) and (rows[[2, 4]] == 0).all()
     assert np.allclose(BO.pair_dots(x, rows, pos, 1)[0][:, 0], (x * x).sum(1))
+
+
+def test_pairs_of_an_alignment():
+    """An alignment that knows its pairs: whole tokens of topk, and as many in a."""
+    i32 = lambda n: torch.zeros(n, dtype=torch.int32)
+    known = moe.Alignment(i32(64), i32(4), i32(5), i32(40), i32(1), 16, 18)
+    assert known.pairs == 18 and moe.Alignment(i32(64), i32(4), i32(5), i32(40), i32(1), 16).pairs is None
+    w = torch.zeros(4, 8, 64, dtype=torch.uint8), torch.zeros(4, 1, 1)
+    a = lambda rows: (torch.zeros(rows, 64, dtype=torch.uint8), torch.zeros(rows, 1))
+    refused(SHAPE, moe.moe_block_matmul_grouped, *a(9), *w, known, topk=4)  # 4.5 tokens
+    refused(SHAPE, moe.moe_block_matmul_grouped, *a(9), *w, known, topk=0)
+    refused(UNSUP, moe.moe_block_matmul_grouped, *a(9), *w, known, topk=2)  # (right, but on the host)
+    # the library: fewer tokens than the alignment's, fewer rows than its places
+    assert grouped(g=al(M=9), rows=8) == SHAPE and grouped(g=al(rows=64), rows=63, gather=0) == SHAPE

@@ -314,3 +314,50 @@ def test_gathered_scales_at_the_largest_offset(rows, N):
     got = moe.moe_block_matmul_grouped(tokens, wide[:, :1], B.fp8(w), B.dev(sw), al, topk=1, out_dtype=torch.float32)
     ref = BO.matmul(a, sa, w[0], sw[0])
     B.within(got, ref[0], B.product_bound(*ref, "f32", K), f"{rows} last tokens")
+
+
+def reused(k, E, bm, M, capacity, seed):
+    """An alignment of M tokens in buffers made for more: (Alignment, real places, rows in use)."""
+    al = moe.alloc_alignment(capacity, k, E, bm, B.DEV)
+    ids, own, pos, n = B.aligned(M, k, E, bm, seed)
+    ws = torch.empty(moe.moe_workspace_size(moe.make_problem(M, 128, 128, E, k, bm, *[torch.bfloat16] * 3)), dtype=torch.uint8,
+                     device=B.DEV)
+    moe.moe_align_permute(B.dev(ids.astype(np.int32)), E, bm, ws, alignment=al)
+    return al, ws, pos, n
+
+
+@pytest.mark.parametrize("bm", [16, 256])
+@pytest.mark.parametrize("N", [96, 8300])
+def test_grouped_of_reused_buffers_by_default(N, bm):
+    """The call without the number of its pairs or tokens, a and the alignment's
+    buffers made for more: padding is zero, every expert's rows are written."""
+    M, k, E, K, capacity = 30, 2, 4, 144, 200
+    al, ws, pos, n = reused(k, E, bm, M, capacity, 5)
+    R = al.sorted_pair_ids.numel()
+    a, sa, w, sw = operands(max(R, capacity), N, K, 3, E)
+    real = np.zeros(R, bool)
+    real[pos] = True
+    ordered, tokens = a[:R].copy(), a[:capacity].copy()
+    ordered[~real], tokens[M:] = 0x7F, 0x7F  # NaN in what no pair reads
+    W = (B.fp8(w), B.dev(sw))
+    for args, given, more in (((B.fp8(ordered), B.dev(sa[:R]), *W), dict(pairs=M * k), {}),
+                              ((B.fp8(tokens), B.dev(sa[:capacity]), *W), dict(topk=k, M=M), dict(topk=k))):
+        want = moe.moe_block_matmul_grouped(*args, al, **given)
+        out = torch.full((R, N), 3.0, dtype=torch.bfloat16, device=B.DEV)
+        moe.moe_block_matmul_grouped(*args, al, out=out, **more)
+        assert torch.equal(out[:n], want[:n]) and torch.isfinite(want[:n]).all()
+        assert (out[:n][torch.from_numpy(~real[:n]).to(B.DEV)] == 0).all() and (out[n:] == 3).all()
+
+
+def test_pairs_of_the_last_alignment_count():
+    """What a product takes for its pairs is what the buffers were last filled with."""
+    k, E, bm, N, K = 2, 4, 64, 96, 144
+    al, ws, pos, n = reused(k, E, bm, 30, 200, 5)
+    assert al.pairs == 60
+    moe.moe_route_align(B.values((11, E), "f32", 1).to(B.DEV), k, True, bm, ws, alignment=al)
+    assert al.pairs == 22
+    R, n = al.sorted_pair_ids.numel(), int(al.num_padded)
+    a, sa, w, sw = operands(R, N, K, 3, E)
+    got = moe.moe_block_matmul_grouped(B.fp8(a), B.dev(sa), B.fp8(w), B.dev(sw), al)
+    pad = (al.sorted_pair_ids[:n] >= 22).cpu().numpy()
+    assert pad.sum() == n - 22 and (got[:n].cpu().float().numpy()[pad] == 0).all()
