@@ -653,9 +653,16 @@ moe_status moe_quantize_blocks(const void* x, int32_t x_dtype, int64_t x_stride,
  * The product of block-scaled E4M3 matrices, B = ceil(K / 128):
  *   out[m][n] = sum_{b < B} a_scales[m][b] * w_scales[n / 128][b]
  *               * sum_{k in block b} a[m][k] * w[n][k]
- * A block's products are summed exactly in fp32 or to its rounding, the scaled
- * blocks in fp32 in a fixed order, the result is rounded once; it is the same
- * on every run.  A NaN code makes its row (of a) or column (of w) NaN.
+ * The scaled blocks are added in fp32 in a fixed order and the result is rounded
+ * once; it is the same on every run.  How a block's products are added goes by
+ * out_dtype:
+ *   MOE_F32   in fp32 (at half the rate).
+ *   MOE_BF16  each eight consecutive ones aligned to the largest of them, and what
+ *             lies below 2^-13 of its power of two cut off: the eight are off by up
+ *             to 7 * 2^-13 of that product, times the scales.  Of random values
+ *             that is 3e-5 of a result (measured), far inside bf16's rounding; where
+ *             large products cancel, small ones beside them can be lost.
+ * A NaN code makes its row (of a) or column (of w) NaN.
  * a          device uint8 [M, K] of E4M3 codes, row stride a_stride bytes
  *            (a multiple of 16, at most 2^22).
  * a_scales   device f32: block (m, b) at m * scale_stride_row + b *

@@ -816,7 +816,9 @@ def _block_operands(a, a_scales, w, w_scales, dims):
 
 def moe_block_matmul(a, a_scales, w, w_scales, out=None, out_dtype=torch.bfloat16, stream=None):
     """a [M, K] and w [N, K] of E4M3 codes, a_scales f32 [M, ceil(K / 128)] (any
-    strides), w_scales f32 [ceil(N / 128), ceil(K / 128)] -> out [M, N]."""
+    strides), w_scales f32 [ceil(N / 128), ceil(K / 128)] -> out [M, N].  An f32 out
+    adds all products in fp32; a bf16 one cuts each eight below 2^-13 of the largest
+    (include/moe.h)."""
     dev = a.device
     M, N, K, ap, ast, (sp, sr, sb), wp, wsp = _block_operands(a, a_scales, w, w_scales, 2)
     out, op, oc, ost = _out(out, a, M, N, out_dtype, stream)
@@ -948,7 +950,8 @@ class BlockMoE:
     weighted combine.  w13 [E, 2N, K] and w2 [E, K, N] of codes, their scales f32
     [E, ceil(2N / 128), ceil(K / 128)] and [E, ceil(K / 128), ceil(N / 128)].  The
     products' results are held in bf16: a rounding of 2^-8 ahead of E4M3's 2^-4, or
-    of the sum over a token's experts.  Buffers are allocated once for M tokens and
+    of the sum over a token's experts; each eight of their products are cut below
+    2^-13 of the largest, as for any bf16 result of moe_block_matmul.  Buffers are allocated once for M tokens and
     reused, so that nothing is allocated or synchronised per call and the sequence
     can be captured into a HIP graph; calls of one object, and replays of graphs
     that hold them, must not overlap in time, and out holds until the next."""

@@ -361,3 +361,26 @@ def test_pairs_of_the_last_alignment_count():
     got = moe.moe_block_matmul_grouped(B.fp8(a), B.dev(sa), B.fp8(w), B.dev(sw), al)
     pad = (al.sorted_pair_ids[:n] >= 22).cpu().numpy()
     assert pad.sum() == n - 22 and (got[:n].cpu().float().numpy()[pad] == 0).all()
+
+
+@pytest.mark.parametrize("M,N,K", [(3, 40, 272), (64, 7168, 256), (300, 513, 272), (700, 4000, 144)])
+def test_groups_that_cancel(M, N, K):
+    """Eight products in a row of 448^2, -448^2 and six of 1 to 9.  Whole numbers
+    below 2^24 are exact in fp32 whatever the order; a bf16 result may lose what lies
+    below 2^-13 of the largest."""
+    r = np.random.RandomState(M + N)
+    code = BO.e4m3_code(np.float32([1, 2, 3]))
+    a, w = code[r.randint(0, 3, (M, K))], code[r.randint(0, 3, (N, K))]
+    at = np.arange(0, K, 8)
+    big = BO.e4m3_code(np.float32([448, -448]))
+    a[:, at], a[:, at + 1], w[:, at], w[:, at + 1] = big[0], big[0], big[0], big[1]
+    sa, sw = np.ones((M, -(-K // 128)), np.float32), np.ones((-(-N // 128), -(-K // 128)), np.float32)
+    args = (B.fp8(a), B.dev(sa), B.fp8(w), B.dev(sw))
+    v = BO.e4m3_values()
+    want = v[a] @ v[w].T
+    assert want.max() < 9 * K and want.min() > 0
+    assert np.array_equal(B.f64(moe.moe_block_matmul(*args, out_dtype=torch.float32)), want)
+    cut = K // 8 * 7 * 2.0 ** -13 * 448 ** 2
+    got = moe.moe_block_matmul(*args)
+    B.within(got, want, cut + (want + cut) * B.HALF_STEP["bf16"], "groups that cancel")
+    assert torch.equal(got, moe.moe_block_matmul(*args))
