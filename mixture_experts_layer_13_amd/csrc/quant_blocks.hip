@@ -59,34 +59,54 @@ __device__ __forceinline__ float block_scale(float amax) {
   return amax > 0.0f ? fmaxf(amax / 448.0f, 1.17549435e-38f) : 1.0f;
 }
 
-// v = SiLU(v) * w, v / (1 + e^-v) * w.  The exponent in two parts (a gate of 10
-// would lose four bits of e^-v to the rounding of v log2 e, and with them codes at
-// a border): log2 e to 16 bits times a bf16 gate is exact, of an fp32 gate's
-// product the rest comes from a fused multiply-add; the quotient with one
-// correction: within two ulps.  Gates beyond 80 in the ordinary way, whose limits
-// are right.
+// e^v.  The exponent in two parts (an argument of 10 would lose four bits of the
+// result to the rounding of v log2 e, and with them codes at a border): log2 e to 16
+// bits times a bf16 value, or its half, is exact, of an fp32 value's product the rest
+// comes from a fused multiply-add.  In u = 2^-24: the hardware's 2, this addition's 1
+// and, for bf16, v^2 / 5000 that the first order leaves out: 4.3 at 80.
 template <int DT>
-__device__ __forceinline__ void gate8(float (&v)[8], const float (&w)[8]) {
+__device__ __forceinline__ float exp_near(float v) {
   constexpr float kHi = DT == DT_F32 ? 1.44269502162933349609f : 1.442687988281250f;
   constexpr float kLo = DT == DT_F32 ? 1.334975816e-08f : 4.888495152e-06f;  // (log2 e - kHi) ln 2
   constexpr float kLn2 = 0.693147180559945309417f;
+  const float t = v * kHi;
+  float low = v * kLo;
+  if constexpr (DT == DT_F32) low = __builtin_fmaf(__builtin_fmaf(v, kHi, -t), kLn2, low);
+  const float e = __builtin_amdgcn_exp2f(t);
+  return __builtin_fmaf(e, low, e);
+}
+
+// SiLU(v) = v / (1 + e^-v), the quotient with one correction: within 7 u (with the
+// product and the scale behind it 3.4 measured).  Beyond 80, where 1 + e^-80 is 1, it
+// is v or v e^v, the power as a square since it may be subnormal: within 9 u where it
+// is not (-inf gives the formula's NaN).
+template <int DT>
+__device__ __forceinline__ float silu_near(float v) {
+  const float d = 1.0f + exp_near<DT>(-v);
+  const float r = __builtin_amdgcn_rcpf(d), q = v * r;
+  return __builtin_fmaf(__builtin_fmaf(-q, d, v), r, q);
+}
+template <int DT>
+__device__ __forceinline__ float silu_far(float v) {
+  const float e = exp_near<DT>(0.5f * v);
+  return v > 0.0f ? v : v * e * e;
+}
+
+// v = SiLU(v) * w.  A value does not depend on the gates beside it.
+template <int DT>
+__device__ __forceinline__ void gate8(float (&v)[8], const float (&w)[8]) {
+  constexpr float kNear = 80.0f;
   float most = 0.0f;
 #pragma unroll
   for (int i = 0; i < 8; ++i) most = fmaxf(most, __builtin_fabsf(v[i]));
-  if (__builtin_expect(!(most <= 80.0f), 0)) {  // (a NaN's way does not matter)
+  if (__builtin_expect(!(most <= kNear), 0)) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = silu(v[i]) * w[i];
+    for (int i = 0; i < 8; ++i)
+      v[i] = (__builtin_fabsf(v[i]) <= kNear ? silu_near<DT>(v[i]) : silu_far<DT>(v[i])) * w[i];
     return;
   }
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float t = -v[i] * kHi;
-    float low = -v[i] * kLo;
-    if constexpr (DT == DT_F32) low = __builtin_fmaf(__builtin_fmaf(-v[i], kHi, -t), kLn2, low);
-    const float e = __builtin_amdgcn_exp2f(t), d = 1.0f + __builtin_fmaf(e, low, e);
-    const float r = __builtin_amdgcn_rcpf(d), q = v[i] * r;
-    v[i] = __builtin_fmaf(__builtin_fmaf(-q, d, v[i]), r, q) * w[i];
-  }
+  for (int i = 0; i < 8; ++i) v[i] = silu_near<DT>(v[i]) * w[i];
 }
 
 // Codes of eight values, little-endian.

@@ -165,3 +165,37 @@ def test_offsets_past_32_bits():
     c, s = moe.moe_quantize_blocks(x[-40:])
     assert torch.equal(codes[-40:].view(torch.uint8), c.view(torch.uint8)) and torch.equal(scales[-40:], s)
     check(x[-40:].cpu(), c, s)
+
+
+def one_of_a_block(gates, ups, dt, other, place):
+    """A row for each gate: its pair alone in a block of 128, beside gates `other` of ups 0."""
+    x = torch.zeros(len(gates), 256)
+    x[:, :128] = other
+    x[:, place], x[:, 128 + place] = gates, ups
+    return x.to(B.DT[dt])
+
+
+@pytest.mark.parametrize("place", [0, 5, 127])
+@pytest.mark.parametrize("other", [0.0, -3.0, 100.0, -100.0])
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_a_gate_beside_others(dt, other, place):
+    """SiLU(g) u alone in its block shows in the scale.  In u = 2^-24: the
+    hardware's exponential 2 (1 ulp), the correction of its argument 1, and up to 1.3
+    of its second order, 1 + e 1, the quotient 1.5, the product with up 1, the scale
+    1: 9.  From -80 down, SiLU is the gate times two equal exponentials: 3.4 each, two
+    products, the product with up and the scale 1 each, 11; from 80 up it is the gate.
+    Whatever the gates beside it are."""
+    g = torch.cat([torch.linspace(-80, 80, 641), torch.linspace(-87, -80.5, 53), torch.linspace(81, 1000, 30)])
+    x = one_of_a_block(g, torch.full_like(g, 1000.0), dt, other, place)
+    codes, scales = moe.moe_quantize_blocks(x.to(B.DEV), gated=True)
+    z, up = B.f64(x[:, place]), B.f64(x[:, 128 + place])
+    h = np.abs(z / (1 + np.exp(-z)) * up)
+    zero = h == 0
+    s = B.f64(scales)[:, 0]
+    assert (s[zero] == 1).all()
+    off = np.abs(s * 448 - h)[~zero] / (B.U * h[~zero])
+    z = z[~zero]
+    for name, part, bound in (("near", np.abs(z) <= 80, 9), ("below", z < -80, 11), ("above", z > 80, 2)):
+        print(f"  {name} {dt} beside {other}: {off[part].max():.2f} u of {bound}", flush=True)
+    for name, part, bound in (("near", np.abs(z) <= 80, 9), ("below", z < -80, 11), ("above", z > 80, 2)):
+        assert off[part].max() <= bound * (1 + 2.0 ** -20), name
