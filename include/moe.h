@@ -631,7 +631,7 @@ moe_status moe_combine_backward(const moe_alignment* alignment, const void* d_ou
  *   scale = max(fl32(amax / 448), 2^-126), amax over the block's finite
  *           magnitudes; 1 if amax is 0;
  *   codes = E4M3(fl32(x / scale)), round to nearest even, saturating (infinities
- *           too); a NaN gives a NaN code.
+ *           too); a NaN of either sign gives the code 0x7f.
  * gated: the values are SiLU(x[m][k]) * x[m][K + k] in fp32 (x has 2 K values a
  * row).
  * x          device [M, K] (gated [M, 2 K]) of x_dtype (MOE_BF16 or MOE_F32).

@@ -114,10 +114,11 @@ __device__ __forceinline__ uint2 codes8(const float (&v)[8], float s) {
   const float r = 1.0f / s;
   const bool fast = e4m3_fast_scale(s, r);
   uint32_t lo = e4m3_codes4(v[0], v[1], v[2], v[3], s, r, fast), hi = e4m3_codes4(v[4], v[5], v[6], v[7], s, r, fast);
+  // (those of NaN are saturated ones here, of either sign)
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    if (v[i] != v[i]) lo |= 0x7fu << (8 * i);
-    if (v[4 + i] != v[4 + i]) hi |= 0x7fu << (8 * i);
+    if (v[i] != v[i]) lo = (lo & ~(0xffu << (8 * i))) | 0x7fu << (8 * i);
+    if (v[4 + i] != v[4 + i]) hi = (hi & ~(0xffu << (8 * i))) | 0x7fu << (8 * i);
   }
   return make_uint2(lo, hi);
 }

@@ -199,3 +199,28 @@ def test_a_gate_beside_others(dt, other, place):
         print(f"  {name} {dt} beside {other}: {off[part].max():.2f} u of {bound}", flush=True)
     for name, part, bound in (("near", np.abs(z) <= 80, 9), ("below", z < -80, 11), ("above", z > 80, 2)):
         assert off[part].max() <= bound * (1 + 2.0 ** -20), name
+
+
+def special(rows):
+    """Blocks (128 wide) of zeros, of their negatives, of subnormals, at the smallest
+    scale, with infinities, with one NaN, of NaN, of infinities, of large values."""
+    x = B.values((rows, 9 * 128), "f32", 1)
+    b = [x[:, 128 * i:128 * i + 128] for i in range(9)]
+    b[0][:], b[1][:], b[2][:], b[3][:] = 0, -0.0, 2.0 ** -140, -2.0 ** -126
+    b[4][rows // 2, 2:4] = torch.tensor([float("inf"), -float("inf")])
+    b[5][rows // 3, 12] = float("nan")
+    b[5][rows - 1, 100] = -float("nan")
+    b[6][:], b[7][:] = float("nan"), -float("inf")
+    b[8][0, 0] = 3.4e38
+    return x
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("block_rows", [1, 128])
+def test_special_values_to_the_last_byte(block_rows, dt):
+    """Both forms, whole bytes: a NaN's code is 0x7f whatever its sign."""
+    x = special(150).to(B.DT[dt])
+    codes, scales = moe.moe_quantize_blocks(x.to(B.DEV), block_rows=block_rows)
+    c, s = BO.quantize(x.float().numpy(), block_rows)
+    assert np.array_equal(scales.cpu().numpy(), s)
+    assert np.array_equal(codes.view(torch.uint8).cpu().numpy(), c)
