@@ -749,8 +749,13 @@ def moe_quantize_blocks(x, gated=False, block_rows=1, num_rows=None, codes=None,
         E, N, K = x.shape
         if codes is None:
             codes = _made(x, (E, N, K), torch.float8_e4m3fn, stream)
+        elif codes.shape != (E, N, K):
+            raise MoEError(MOE_ERR_SHAPE, f"codes have shape {tuple(codes.shape)}, not {(E, N, K)}")
+        blocks = (E, -(-N // 128), -(-K // 128))
         if scales is None:
-            scales = _made(x, (E, -(-N // 128), -(-K // 128)), torch.float32, stream)
+            scales = _made(x, blocks, torch.float32, stream)
+        elif scales.shape != blocks:
+            raise MoEError(MOE_ERR_SHAPE, f"scales have shape {tuple(scales.shape)}, not {blocks}")
         for e in range(E):
             moe_quantize_blocks(x[e], gated, 128, num_rows, codes[e], scales[e], stream)
         return codes, scales

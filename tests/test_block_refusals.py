@@ -219,3 +219,15 @@ def test_pairs_of_an_alignment():
     refused(UNSUP, moe.moe_block_matmul_grouped, *a(9), *w, known, topk=2)  # (right, but on the host)
     # the library: fewer tokens than the alignment's, fewer rows than its places
     assert grouped(g=al(M=9), rows=8) == SHAPE and grouped(g=al(rows=64), rows=63, gather=0) == SHAPE
+
+
+@pytest.mark.parametrize("codes,scales", [((3, 200, 144), None), ((1, 200, 144), None), ((200, 144), None), ((2, 200, 160), None),
+                                          (None, (3, 2, 2)), (None, (1, 2, 2)), (None, (2, 2)), (None, (2, 2, 1))])
+def test_buffers_for_the_codes_of_experts(codes, scales):
+    """Refused as a whole, not after the first experts (or, of too many, never)."""
+    made = {}
+    if codes:
+        made["codes"] = torch.zeros(codes, dtype=torch.uint8)
+    if scales:
+        made["scales"] = torch.zeros(scales)
+    refused(SHAPE, moe.moe_quantize_blocks, torch.zeros(2, 200, 144), block_rows=128, **made)
