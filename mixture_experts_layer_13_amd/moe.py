@@ -518,7 +518,7 @@ def moe_align_permute(topk_ids, E, block_m, workspace, alignment=None, stream=No
                                    _ptr(al.num_padded), _ptr(workspace),
                                    workspace.numel() * workspace.element_size(),
                                    _stream(stream)))
-    al.pairs = M * topk
+    al.pairs, al.block_m = M * topk, block_m
     return al
 
 
@@ -537,7 +537,7 @@ def moe_route_align(logits, topk, renormalize, block_m, workspace, topk_ids=None
                                  _ptr(al.block_expert_ids), _ptr(al.expert_offsets),
                                  _ptr(al.pair_pos), _ptr(al.num_padded), _ptr(workspace),
                                  workspace.numel() * workspace.element_size(), _stream(stream)))
-    al.pairs = M * topk
+    al.pairs, al.block_m = M * topk, block_m
     return topk_ids, topk_weights, al
 
 

@@ -384,3 +384,19 @@ def test_groups_that_cancel(M, N, K):
     got = moe.moe_block_matmul(*args)
     B.within(got, want, cut + (want + cut) * B.HALF_STEP["bf16"], "groups that cancel")
     assert torch.equal(got, moe.moe_block_matmul(*args))
+
+
+@pytest.mark.parametrize("M", [8, 50])
+def test_grouped_of_buffers_filled_with_other_blocks(M):
+    """Buffers made for blocks of 16 and many tokens, filled with blocks of 64: the
+    product goes by those."""
+    k, E, N, K = 2, 4, 96, 144
+    al, ws, pos, n = reused(k, E, 16, 20, 300, 5)
+    ids, own, pos, n = B.aligned(M, k, E, 64, 8)
+    assert n <= al.sorted_pair_ids.numel() and n // 64 <= al.block_expert_ids.numel()
+    ws = torch.empty(moe.moe_workspace_size(moe.make_problem(M, 128, 128, E, k, 64, *[torch.bfloat16] * 3)), dtype=torch.uint8,
+                     device=B.DEV)
+    moe.moe_align_permute(B.dev(ids.astype(np.int32)), E, 64, ws, alignment=al)
+    a, sa, w, sw = operands(M, N, K, 3, E)
+    args = (B.fp8(a), B.dev(sa), B.fp8(w), B.dev(sw))
+    assert torch.equal(moe.moe_block_matmul_grouped(*args, al, topk=k)[:n], moe.moe_block_matmul_grouped(*args, own, topk=k)[:n])
