@@ -561,7 +561,8 @@ moe_status moe_paged_attention_workspace_size(const moe_kv_cache* cache, int32_t
  * The conventions at the top of this file hold; row strides are in elements,
  * at least a row, multiples of 16 bytes, and every value buffer is 16-byte,
  * every index, weight and scale buffer 4-byte aligned.  An output overlaps no
- * other argument.
+ * other argument (MOE_ERR_SHAPE; columns of one matrix do not, and of buffers with
+ * different row strides the caller sees to it).
  */
 
 /* What moe_align_permute wrote, for M tokens of topk pairs f = t * topk + j.

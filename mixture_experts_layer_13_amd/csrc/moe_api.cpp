@@ -894,6 +894,48 @@ moe_status check_row_stride(const char* name, int64_t stride, int64_t least, int
   return MOE_OK;
 }
 
+// A buffer: `rows` pieces of `len` bytes, `stride` (at least len) apart.
+struct Region {
+  const void* base;
+  long long rows, len, stride;
+};
+
+Region dense(const void* p, long long bytes) { return {p, 1, bytes, bytes}; }
+
+// Scales [rows, blocks] where one of their strides is 1, else nothing.
+Region scale_region(const void* p, long long rows, long long blocks, long long row_stride, long long block_stride) {
+  if (block_stride == 1 && row_stride >= blocks) return {p, rows, blocks * 4, row_stride * 4};
+  if (row_stride == 1 && block_stride >= rows) return {p, blocks, rows * 4, block_stride * 4};
+  return dense(nullptr, 0);
+}
+
+// Whether two buffers have a byte in common.  Columns of one matrix do not; of pieces
+// with different distances it is not found out (false).
+bool overlap(const Region& x, const Region& y) {
+  if (!x.base || !y.base || x.rows < 1 || y.rows < 1 || x.len < 1 || y.len < 1) return false;
+  const long long at = (long long)((intptr_t)y.base - (intptr_t)x.base);  // of y, from x
+  const long long xs = (x.rows - 1) * x.stride + x.len, ys = (y.rows - 1) * y.stride + y.len;
+  if (at >= xs || at + ys <= 0) return false;
+  const bool whole_x = xs == x.rows * x.len, whole_y = ys == y.rows * y.len;
+  if (whole_x && whole_y) return true;
+  if (whole_y) return overlap(y, x);
+  if (whole_x) {  // the first piece of y that ends behind the start of x
+    const long long i = at + y.len > 0 ? 0 : (-at - y.len) / y.stride + 1;
+    return i < y.rows && at + i * y.stride < xs;
+  }
+  if (x.stride != y.stride) return false;
+  // y's piece j begins `in` behind the start of x's piece j + k
+  const long long k = at / x.stride - (at % x.stride < 0), in = at - k * x.stride;
+  auto any = [&](long long d) { return d < x.rows && d + y.rows > 0; };  // a j with both pieces j and j + d
+  return (in < x.len && any(k)) || (in + y.len > x.stride && any(k + 1));
+}
+
+moe_status check_apart(const char* name, const Region& out, std::initializer_list<Region> others) {
+  for (const Region& r : others)
+    if (overlap(out, r)) return fail(MOE_ERR_SHAPE, "%s overlaps another argument", name);
+  return MOE_OK;
+}
+
 moe_status check_alignment(const moe_alignment* al) {
   if (!al) return fail(MOE_ERR_NULL, "alignment is NULL");
   if (al->M < 0) return fail(MOE_ERR_SHAPE, "M=%d must be >= 0", al->M);
@@ -936,6 +978,16 @@ moe_status permute(const moe_alignment* al, bool scatter, int32_t K, const void*
   for (const void* q : {(const void*)al->pair_pos, scatter ? (const void*)al->sorted_pair_ids : nullptr,
                         scatter ? (const void*)al->num_padded : nullptr, (const void*)weights, (const void*)dw})
     if (!aligned(q, 4)) return fail(MOE_ERR_ALIGN, "index and weight buffers must be 4-byte aligned");
+  const long long M = al->M, R = al->rows, pairs = M * al->topk;
+  const Region places = dense(al->pair_pos, pairs * 4), w = dense(weights, pairs * 4);
+  const Region ids = dense(scatter ? al->sorted_pair_ids : nullptr, R * 4);
+  const Region used = dense(scatter ? al->num_padded : nullptr, 4);
+  const Region tokens{reads_tok ? tok : nullptr, M, K * te, tok_stride * te};
+  const Region from{reads_rows ? rows : nullptr, R, K * re, rows_stride * re};
+  const Region to{out, scatter ? R : M, K * (scatter ? re : te), out_stride * (scatter ? re : te)};
+  if ((s = check_apart("output", to, {tokens, from, w, places, ids, used})) ||
+      (s = check_apart("d_weights", dense(dw, pairs * 4), {to, tokens, from, w, places, ids, used})))
+    return s;
   moe::PermuteArgs a{};
   a.sorted_ids = al->sorted_pair_ids;
   a.pair_pos = al->pair_pos;
@@ -983,6 +1035,12 @@ moe_status check_block_buffers(const void* a, const void* a_scales, const void* 
     return fail(MOE_ERR_ALIGN, "scales must be 4-byte aligned, out to its type");
   return MOE_OK;
 }
+
+Region out_region(const void* out, int32_t rows, int32_t N, int32_t dtype, int64_t stride) {
+  const long long eb = dtype_bytes(dtype);
+  return {out, rows, N * eb, stride * eb};
+}
+long long scale_bytes(int32_t N, int32_t K) { return (N + 127) / 128 * ((K + 127) / 128) * 4LL; }
 
 moe::BlockGemmArgs block_args(const uint8_t* a, int64_t a_stride, const float* a_scales, int64_t ss_row,
                               int64_t ss_block, const uint8_t* w, const float* w_scales, int32_t M, int32_t N,
@@ -1066,6 +1124,12 @@ moe_status moe_quantize_blocks(const void* x, int32_t x_dtype, int64_t x_stride,
     return fail(MOE_ERR_ALIGN, "scales and num_rows must be 4-byte aligned");
   if ((long long)M * ((K + 127) / 128) > (1LL << 28))
     return fail(MOE_ERR_SHAPE, "M=%d rows of %d blocks exceed 2^28 blocks", M, (K + 127) / 128);
+  const long long B = (K + 127) / 128, eb = dtype_bytes(x_dtype);
+  const Region from{x, M, (gated ? 2LL : 1LL) * K * eb, x_stride * eb}, limit = dense(num_rows, 4);
+  const Region to = scale_region(scales, (M + block_rows - 1LL) / block_rows, B, scale_stride_row, scale_stride_block);
+  if ((s = check_apart("codes", dense(codes, (long long)M * K), {from, limit, to})) ||
+      (s = check_apart("scales", to, {from, limit})))
+    return s;
   const moe::QuantArgs a{x, x_stride, M, K, num_rows, codes, scales, scale_stride_row, scale_stride_block};
   return hip_status(moe::launch_quant_blocks(a, x_dtype, gated != 0, block_rows, (hipStream_t)stream),
                     "block quantisation launch");
@@ -1080,6 +1144,10 @@ moe_status moe_block_matmul(const uint8_t* a, int64_t a_stride, const float* a_s
   if ((long long)M * N > (1LL << 36)) return fail(MOE_ERR_SHAPE, "M*N=%lld exceeds 2^36", (long long)M * N);
   if (M == 0) return ok();
   if ((s = check_block_buffers(a, a_scales, w, w_scales, out, dtype_bytes(out_dtype)))) return s;
+  if ((s = check_apart("out", out_region(out, M, N, out_dtype, out_stride),
+                       {Region{a, M, K, a_stride}, scale_region(a_scales, M, (K + 127) / 128, scale_stride_row, scale_stride_block),
+                        dense(w, (long long)N * K), dense(w_scales, scale_bytes(N, K))})))
+    return s;
   const moe::BlockGemmArgs g = block_args(a, a_stride, a_scales, scale_stride_row, scale_stride_block, w, w_scales, M,
                                           N, K, out, out_dtype, out_stride);
   return block_status(moe::launch_block_product(g, out_dtype, (hipStream_t)stream));
@@ -1108,6 +1176,14 @@ moe_status moe_block_matmul_grouped(const moe_alignment* alignment, const uint8_
                         (const void*)al.expert_offsets, (const void*)al.num_padded})
     if (!aligned(q, 4)) return fail(MOE_ERR_ALIGN, "index buffers must be 4-byte aligned");
   if ((s = check_block_buffers(a, a_scales, w, w_scales, out, dtype_bytes(out_dtype)))) return s;
+  const long long wbytes = (long long)al.E * N * K, blocks = ((long long)al.rows + al.block_m - 1) / al.block_m;
+  if ((s = check_apart("out", out_region(out, al.rows, N, out_dtype, out_stride),
+                       {Region{a, a_rows, K, a_stride},
+                        scale_region(a_scales, a_rows, (K + 127) / 128, scale_stride_row, scale_stride_block),
+                        dense(w, wbytes), dense(w_scales, al.E * scale_bytes(N, K)), dense(al.sorted_pair_ids, al.rows * 4LL),
+                        dense(al.block_expert_ids, blocks * 4), dense(al.expert_offsets, (al.E + 1) * 4LL),
+                        dense(al.num_padded, 4)})))
+    return s;
   moe::BlockGemmArgs g = block_args(a, a_stride, a_scales, scale_stride_row, scale_stride_block, w, w_scales, a_rows, N,
                                     K, out, out_dtype, out_stride);
   g.ids = al.sorted_pair_ids;

@@ -231,3 +231,38 @@ def test_buffers_for_the_codes_of_experts(codes, scales):
     if scales:
         made["scales"] = torch.zeros(scales)
     refused(SHAPE, moe.moe_quantize_blocks, torch.zeros(2, 200, 144), block_rows=128, **made)
+
+
+P = F + (1 << 30)  # apart from F for every call here
+
+
+@pytest.mark.parametrize("call,kw", [
+    # 9 tokens of 64 bf16: 1152 bytes, 64 rows: 8192; weights, places: 72; marks: 256
+    (dispatch, dict(a=al(), x=P, rows=P)), (dispatch, dict(x=P + 8176, rows=P)), (dispatch, dict(x=P, rows=P + 1136)),
+    (dispatch, dict(x=F, rows=P, w=P + 16)), (dispatch, dict(a=al(pair_pos=P), rows=P)),
+    (dispatch, dict(a=al(sorted_pair_ids=P + 8188), rows=P)), (dispatch, dict(a=al(num_padded=P), rows=P)),
+    (dispatch, dict(x=P, xs=128, rows=P + 112, rs=128)), (dispatch, dict(x=P + 128 * 2, xs=128, rows=P + 112, rs=128)),
+    (dispatch, dict(x=P, xs=1024, rows=P + 8192, rs=64)), (dispatch, dict(x=P + 8176 - 4 * 2048, xs=1024, rows=P, rs=64)),
+    (dispatch_bwd, dict(dr=F, x=P, dx=P, dw=P + (1 << 20))), (dispatch_bwd, dict(dr=P, x=F, dx=P + 8000, dw=P + (1 << 20))),
+    (dispatch_bwd, dict(dr=F, x=F, dx=P, dw=P + 1148)), (dispatch_bwd, dict(dr=F, x=F, dx=P, dw=F + 1000)),
+    (dispatch_bwd, dict(a=al(pair_pos=P), dx=P + (1 << 20), dw=P + 68)),
+    (dispatch_bwd, dict(w=P, dx=P + (1 << 20), dw=P)),
+    (combine, dict(rows=P, out=P)), (combine, dict(rows=P, out=P + 8176)), (combine, dict(w=P, out=P)),
+    (combine_bwd, dict(g=P, rows=F, dr=P, dw=P + (1 << 20))), (combine_bwd, dict(g=F, rows=P, dr=P, dw=P + (1 << 20))),
+    (combine_bwd, dict(g=F, rows=F, dr=P, dw=P)),
+    # 9 rows of 256 bf16: 4608 bytes, their codes 2304, scales 72
+    (quant, dict(x=P, codes=P, scales=P + (1 << 20))), (quant, dict(x=P, codes=P + 4592, scales=P + (1 << 20))),
+    (quant, dict(x=F, codes=P, scales=P + 2300)), (quant, dict(x=P, codes=P + (1 << 20), scales=P + 4604)),
+    (quant, dict(x=F, codes=P, scales=P - 60, sr=2, sb=1)), (quant, dict(x=F, codes=P, scales=P + 2300, sr=100, sb=1)),
+    (quant, dict(x=F, n=P, codes=P, scales=P + (1 << 20))), (quant, dict(x=F, n=P + 4, codes=P + (1 << 20), scales=P)),
+    (quant, dict(gated=1, xs=512, x=P, codes=P + 9200, scales=P + (1 << 20))),
+    # 9 rows of 256 codes: 2304 bytes; out 9 x 100 bf16: 1800; w 25600
+    (matmul, dict(a=P, out=P)), (matmul, dict(sa=P, out=P)), (matmul, dict(w=P, out=P + 25596)), (matmul, dict(sw=P + 1796, out=P)),
+    (matmul, dict(a=P, ast=4096, out=P + 4096)), (matmul, dict(sa=P + 1600, sr=1, sb=50, out=P, os=100)),
+    (grouped, dict(a=P, out=P)), (grouped, dict(sa=P, out=P)), (grouped, dict(w=P, out=P + 4 * 25600 - 4)),
+    (grouped, dict(sw=P + 64 * 200 - 4, out=P)), (grouped, dict(a=P, rows=64, gather=0, out=P + 64 * 256 - 16)),
+    *((grouped, dict(g=al(**{n: P + 12796}), out=P)) for n in ("sorted_pair_ids", "block_expert_ids", "expert_offsets", "num_padded")),
+])
+def test_outputs_that_overlap_inputs(call, kw):
+    assert call(**kw) == SHAPE, kw
+    assert "overlaps" in moe.moe_last_error()

@@ -134,3 +134,36 @@ def test_no_tokens():
     none = moe.BlockMoE(0, 256, 128, 4, 2, L.w13, L.w13_scales, L.w2, L.w2_scales)
     out = none(torch.empty(0, 256, dtype=torch.bfloat16, device=B.DEV), torch.empty(0, 4, device=B.DEV))
     assert out.shape == (0, 256)
+
+
+def test_outputs_beside_inputs_in_one_matrix():
+    """Columns of one matrix, and what ends where another begins, do not overlap."""
+    M, K, E, k, bm = 40, 64, 4, 2, 16
+    ids, al, pos, n = B.aligned(M, k, E, bm, 3)
+    R = al.sorted_pair_ids.numel()
+    x = B.values((M, K), "bf16", 1).to(B.DEV)
+    rows = moe.moe_dispatch(x, al, k)
+    out = moe.moe_combine(rows, al, M, k)
+    wide = torch.full((R, 3 * K), 7.0, dtype=torch.bfloat16, device=B.DEV)
+    wide[:M, K:2 * K] = x
+    moe.moe_dispatch(wide[:M, K:2 * K], al, k, out=wide[:, :K])
+    assert torch.equal(wide[:n, :K], rows[:n]) and torch.equal(wide[:M, K:2 * K], x)
+    moe.moe_combine(wide[:, :K], al, M, k, out=wide[:M, 2 * K:])
+    assert torch.equal(wide[:M, 2 * K:], out) and (wide[M:, K:] == 7).all()
+    line = torch.empty((R + M) * K, dtype=torch.bfloat16, device=B.DEV)
+    line[:M * K] = x.view(-1)
+    moe.moe_dispatch(line[:M * K].view(M, K), al, k, out=line[M * K:].view(R, K))
+    assert torch.equal(line[M * K:].view(R, K)[:n], rows[:n])
+    h = B.values((M, 256), "f32", 2).to(B.DEV)
+    codes, scales = moe.moe_quantize_blocks(h)
+    raw = torch.empty(M * 256 + M * 8, dtype=torch.uint8, device=B.DEV)
+    c, s = raw[:M * 256].view(M, 256), raw[M * 256:].view(torch.float32).view(2, M).t()
+    moe.moe_quantize_blocks(h, codes=c, scales=s)
+    assert torch.equal(c, codes.view(torch.uint8)) and torch.equal(s, scales)
+    w = B.values((96, 256), "f32", 3).to(B.DEV)
+    wc, ws = moe.moe_quantize_blocks(w, block_rows=128)
+    both = torch.zeros(M, 256 + 96 * 2, dtype=torch.uint8, device=B.DEV)
+    both[:, :256] = c
+    y = both.view(torch.bfloat16)[:, 128:]
+    moe.moe_block_matmul(both[:, :256], scales, wc, ws, out=y)
+    assert torch.equal(y, moe.moe_block_matmul(codes, scales, wc, ws)) and torch.equal(both[:, :256], c)
