@@ -672,8 +672,8 @@ moe_status moe_quantize_blocks(const void* x, int32_t x_dtype, int64_t x_stride,
  * w          device uint8 [N, K], dense.   w_scales  device f32
  *            [ceil(N / 128)][B], dense.  (The transposed matrix with its
  *            transposed scales gives the gradient of a.)
- *            A scale of a times one of w: within 2^-126 and 2^102 in magnitude
- *            (0 where less).
+ *            A scale of a times one of w: at most 2^102 in magnitude, rounded as
+ *            an fp32 number (below 2^-126 to a multiple of 2^-149).
  * out        device [M, N] of out_dtype (MOE_BF16 or MOE_F32), row stride
  *            out_stride elements, any alignment of its type (16-byte rows are
  *            written fastest).

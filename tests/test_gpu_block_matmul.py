@@ -400,3 +400,21 @@ def test_grouped_of_buffers_filled_with_other_blocks(M):
     a, sa, w, sw = operands(M, N, K, 3, E)
     args = (B.fp8(a), B.dev(sa), B.fp8(w), B.dev(sw))
     assert torch.equal(moe.moe_block_matmul_grouped(*args, al, topk=k)[:n], moe.moe_block_matmul_grouped(*args, own, topk=k)[:n])
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("M,N", [(3, 40), (300, 256)])
+def test_products_of_small_scales(M, N, dt):
+    """Two scales' product rounded as fp32, subnormal ones too: sums of 128 ones, which
+    are exact, times 1.5 and 1.25 times powers of two down to 2^-160."""
+    K = 256
+    one = np.full((M, K), 0x38, np.uint8), np.full((N, K), 0x38, np.uint8)
+    e = -np.arange(100, 161)
+    for at in range(0, len(e), 3):
+        sa = np.full((M, 2), 1.5 * 2.0 ** -75, np.float32)
+        sa[:, 1] *= np.float32(1.25)
+        sw = np.full((-(-N // 128), 2), 2.0 ** (e[at] + 75), np.float32)
+        both = (sa[0].astype(np.float64) * sw[0]).astype(np.float32).astype(np.float64)
+        want = (128 * both[0] + 128 * both[1]).astype(np.float32)
+        got = moe.moe_block_matmul(B.fp8(one[0]), B.dev(sa), B.fp8(one[1]), B.dev(sw), out_dtype=B.DT[dt])
+        assert (got == torch.tensor(want).to(B.DT[dt]).to(B.DEV)).all(), (e[at], got[0, 0].item(), want)
