@@ -167,3 +167,54 @@ def test_outputs_beside_inputs_in_one_matrix():
     y = both.view(torch.bfloat16)[:, 128:]
     moe.moe_block_matmul(both[:, :256], scales, wc, ws, out=y)
     assert torch.equal(y, moe.moe_block_matmul(codes, scales, wc, ws)) and torch.equal(both[:, :256], c)
+
+
+@pytest.mark.parametrize("M,K,N,E,k,dt", [(5, 256, 144, 8, 3, "f32"), (150, 272, 256, 4, 2, "bf16"), (64, 128, 64, 40, 8, "f32")])
+def test_the_layer_from_end_to_end(M, K, N, E, k, dt):
+    """Against the layer in 64 bits, from tokens that E4M3 holds exactly and down
+    weights of one value a row, so that no bound is a sum of unlike terms: the
+    products' bounds, |SiLU'| <= 1.1, the codes of SiLU(gate) * up 2^-4 of a value or
+    half a smallest step of its block, bf16 results 2^-8."""
+    r = np.random.RandomState(M)
+    v = BO.e4m3_values()
+    small = np.flatnonzero(np.isfinite(v) & (np.abs(v) <= 4))
+    x = v[small[r.randint(0, len(small), (M, K))]]
+    x[:, ::128] = 448  # the scale is 1; no weight reads these
+    w13 = r.randn(E, 2 * N, K) * 0.2
+    w13[:, :, ::128] = 0
+    w2 = np.zeros((E, K, N))
+    col = r.randint(0, N, (E, K))
+    w2[np.arange(E)[:, None], np.arange(K), col] = r.randn(E, K)
+    c13, s13 = moe.moe_quantize_blocks(B.dev(w13.astype(np.float32)), block_rows=128)
+    c2, s2 = moe.moe_quantize_blocks(B.dev(w2.astype(np.float32)), block_rows=128)
+    m = moe.BlockMoE(M, K, N, E, k, c13, s13, c2, s2, out_dtype=B.DT[dt])
+    logits = B.values((M, E), "f32", 6)
+    out = m(B.dev(x.astype(np.float32)).to(B.DT[dt]), logits.to(B.DEV))
+    host = lambda t: (t.view(torch.uint8) if t.dtype == torch.float8_e4m3fn else t).cpu().numpy()
+    c13, s13, c2, s2 = (host(t) for t in (c13, s13, c2, s2))
+    ids, wts = oracle.route_topk(logits.numpy(), k, True)
+    xc, one = BO.e4m3_code(x.astype(np.float32)), np.ones((M, -(-K // 128)), np.float32)
+    want, tol, swapped = np.zeros((M, K)), np.zeros((M, K)), np.zeros((M, K))
+    for e in range(E):
+        t, j = np.nonzero(ids == e)
+        if not len(t):
+            continue
+        ref = BO.matmul(xc[t], one[t], c13[e], s13[e])
+        off = B.product_bound(*ref, "bf16", K)
+        (g, u), (dg, du) = np.split(ref[0], 2, 1), np.split(off, 2, 1)
+        silu = g / (1 + np.exp(-g))
+        h = silu * u
+        dh = 1.1 * dg * (np.abs(u) + du) + np.abs(silu) * du
+        top = np.pad(np.abs(h) + dh, ((0, 0), (0, -N % 128))).reshape(len(t), -1, 128).max(2) / 448
+        step = np.maximum((np.abs(h) + dh) * 2.0 ** -4, np.repeat(top, 128, 1)[:, :N] * 2.0 ** -10)
+        dh += step * (1 + 2.0 ** -10) + 2.0 ** -17 * np.abs(h)
+        W = v[c2[e]] * np.repeat(np.repeat(s2[e].astype(np.float64), 128, 0)[:K], 128, 1)[:, :N]
+        y, dy = h @ W.T, dh @ np.abs(W).T
+        dy += (np.abs(y) + dy) * (B.HALF_STEP["bf16"] * (1 + 2.0 ** -7) + 2.0 ** -12)
+        p = wts[t, j].astype(np.float64)[:, None]
+        want[t] += p * y
+        swapped[t] += p * ((u / (1 + np.exp(-u)) * g) @ W.T)
+        tol[t] += p * (dy + np.abs(y) * 2.0 ** -20)
+    tol += (np.abs(want) + tol) * B.HALF_STEP[dt] * (1 + 2.0 ** -7)
+    B.within(out, want, tol, "the layer")
+    assert (np.abs(swapped - want) > 2 * tol).mean() > 0.5  # gate and up the other way round would show
