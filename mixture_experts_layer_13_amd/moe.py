@@ -969,7 +969,7 @@ class BlockMoE:
             # the products' tiles do not depend on it, and more of it is more padding:
             # 64 tokens 176 us (of 256: 254), 8192 1171 (1200)
             block_m = 16
-        self.M, self.topk, self.block_m, self.renormalize = M, topk, block_m, renormalize
+        self.M, self.E, self.topk, self.block_m, self.renormalize = M, E, topk, block_m, renormalize
         self.w13, self.w13_scales, self.w2, self.w2_scales = w13, w13_scales, w2, w2_scales
         like = dict(dtype=torch.bfloat16, device=device)
         # the alignment's part of a workspace does not depend on the layer's sizes
@@ -988,9 +988,17 @@ class BlockMoE:
 
     def __call__(self, x, logits, stream=None):
         """x [M, K] bf16/f32, logits f32 [M, E] -> out [M, K], this object's buffer."""
-        if x.shape[0] != self.M or logits.shape[0] != self.M:
-            raise MoEError(MOE_ERR_SHAPE, f"{x.shape[0]} tokens and {logits.shape[0]} rows of logits, buffers for {self.M}")
-        al = self.alignment
+        dev, al = self.out.device, self.alignment
+        if x.shape[0] != self.M:
+            raise MoEError(MOE_ERR_SHAPE, f"{x.shape[0]} tokens, buffers for {self.M}")
+        if x.device != dev:
+            raise MoEError(MOE_ERR_UNSUPPORTED, f"x is on {x.device}, not on {dev}")
+        _pairs_f32(logits, (self.M, self.E), "logits", dev)  # (the routing takes them as such)
+        if dev.type != "cuda":
+            raise MoEError(MOE_ERR_UNSUPPORTED, f"tensors are on {dev}, not on a GPU")
+        if dev.index != torch._C._cuda_getDevice():
+            with torch.cuda.device(dev):
+                return self(x, logits, stream)
         moe_route_align(logits, self.topk, self.renormalize, self.block_m, self.workspace, self.topk_ids,
                         self.topk_weights, al, stream)
         moe_quantize_blocks(x, codes=self.x_codes, scales=self.x_scales, stream=stream)

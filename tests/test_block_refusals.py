@@ -266,3 +266,21 @@ P = F + (1 << 30)  # apart from F for every call here
 def test_outputs_that_overlap_inputs(call, kw):
     assert call(**kw) == SHAPE, kw
     assert "overlaps" in moe.moe_last_error()
+
+
+def test_layer_refusals():
+    """Logits of another type, number or place would be read (and places written)
+    past their ends; nothing is launched before all of them are looked at."""
+    M, K, N, E, k = 9, 128, 64, 4, 2
+    codes, scales = lambda *s: torch.zeros(s, dtype=torch.uint8), lambda *s: torch.zeros(s)
+    layer = moe.BlockMoE(M, K, N, E, k, codes(E, 2 * N, K), scales(E, 1, 1), codes(E, K, N), scales(E, 1, 1), device="cpu")
+    x, logits = torch.zeros(M, K), torch.zeros(M, E)
+    refused(DTYPE, layer, x, logits.bfloat16())
+    refused(SHAPE, layer, x, torch.zeros(M, E + 1))
+    refused(SHAPE, layer, x, logits[:8])
+    refused(SHAPE, layer, x[:8], logits)
+    refused(UNSUP, layer, x, torch.zeros(E, M).t())
+    refused(UNSUP, layer, x, logits.to("meta"))
+    refused(UNSUP, layer, x.to("meta"), logits)
+    refused(UNSUP, layer, x, logits)  # on the host
+    refused(SHAPE, moe.BlockMoE, M, K, N, E, k, codes(E, N, K), scales(E, 1, 1), codes(E, K, N), scales(E, 1, 1), device="cpu")
