@@ -300,9 +300,10 @@ def test_offsets_past_32_bits():
 
 @pytest.mark.parametrize("rows,N", [(16, 96), (64, 8448)])
 def test_gathered_scales_at_the_largest_offset(rows, N):
-    """Tokens whose scales lie up to the limit on a_rows times their stride, for the
-    few-row kernel and a tile's: the last one's are 2^31 - 64 bytes from the first."""
-    M, K, stride = (1 << 26) - 1, 16, 8
+    """Tokens whose codes and scales lie up to the limits on a_rows times their strides,
+    for the few-row kernel and a tile's: the last one's are 2^31 - 64 bytes from the
+    first."""
+    M, K, stride = (1 << 26) - 1, 32, 8
     a, sa, w, sw = operands(rows, N, K, 3, 1)
     wide = torch.empty(M, stride, device=B.DEV)
     wide[-rows:, :1] = B.dev(sa)
