@@ -17,8 +17,8 @@
 // row l mod 16, columns l / 16 and 4 more) find every bank once (no conflicts
 // counted in the loop).
 //
-// What bounds it: 8192 x 4096 x 7168 takes 197 to 230 us by the card (2.1 to 2.4
-// PFLOP/s; a library's product with one scale for each tensor 186), the matrix pipe
+// What bounds it: 8192 x 4096 x 7168 takes 197 to 240 us by the card and its heat (2.0
+// to 2.4 PFLOP/s; a library's product with one scale for each tensor 186), the matrix pipe
 // busy 0.58 of the cycles at 1.78 GHz, the clock that full load leaves: 32 compute
 // units alone take 1.36 us for a 256 x 256 x 128 block, the whole chip 1.75.  Hence
 // 256 x 256 (the fewest LDS and L2 bytes a product) where there are enough rows, one
