@@ -496,8 +496,9 @@ class Alignment:
     pair_pos: torch.Tensor
     num_padded: torch.Tensor
     block_m: int
-    # M * topk of the routing that was last written here (moe_align_permute,
-    # moe_route_align), which may be fewer than the buffers hold; None: not known
+    # M * topk of the call that last filled the buffers (moe_align_permute,
+    # moe_route_align; a graph's replay is not seen), which may be fewer than they
+    # hold; None: not known
     pairs: int | None = None
 
 
